@@ -76,7 +76,9 @@ typedef enum mla_device_error {
   MLA_DEV_BAD_BLOCK_ID = 3,  /* a block-table entry needed for a visible token is < 0 or >= num_blocks */
   MLA_DEV_LEN_BOUND = 4,     /* a length exceeds the static bound (table width * page size) */
   MLA_DEV_BAD_SUBPAGE = 5,   /* the decode met a sub-page id outside the cache */
-  MLA_DEV_WAIT_TIMEOUT = 6   /* an in-kernel wait gave up; the CTA returned without its result */
+  MLA_DEV_WAIT_TIMEOUT = 6,  /* an in-kernel wait gave up; the CTA returned without its result */
+  MLA_DEV_NO_FREE_BLOCK = 7, /* the free ring held fewer blocks than the requests needed */
+  MLA_DEV_BAD_FREE_RING = 8  /* ring state outside [0, num_blocks], or more blocks returned than the pool has */
 } mla_device_error;
 
 /* Sub-page size P for a physical block size: the largest power of two dividing
@@ -341,6 +343,90 @@ mla_status mla_write_kv(int num_reqs, int num_rows, const int32_t *seq_lens,
                         int block_table_stride, int num_blocks, int block_size,
                         void *kv_cache, int kv_dtype, float kv_scale,
                         int64_t num_cache_rows, mla_stream_t stream);
+
+/* Arguments of mla_update_block_tables (host struct, read during the call). */
+typedef struct mla_table_args {
+  int num_reqs;             /* B, 0 <= B <= 16384 */
+  int num_rows;             /* T: capacity of slot_map; qo_indptr[B] <= T */
+  const int32_t *prev_lens; /* [B] tokens whose blocks each request holds now (0: none) */
+  const int32_t *seq_lens;  /* [B] tokens L_b after this step, its qlen_b new ones included (0: finished) */
+  const int32_t *qo_indptr; /* [B+1] */
+  int world_size, rank, interleave; /* the shard these tables belong to; 1, 0, 1 unsharded */
+  int block_size;
+  int num_blocks;           /* C: blocks of the pool, and capacity of the free ring */
+  int32_t *block_table;     /* [B, block_table_stride], in and out */
+  int block_table_stride;
+  int32_t *free_ring;       /* [C] ids of free blocks, in and out */
+  const int32_t *ring_in;   /* {head, count}: the free ids are free_ring[(head + i) % C], i < count */
+  int32_t *ring_out;        /* {head, count} after the call; must not be ring_in */
+  int32_t *slot_map;        /* [T] cache row of every new token */
+} mla_table_args;
+
+/* Block tables and slot map of a step, made on the device from the requests'
+ * lengths (no counterpart in the pages, whose host allocates the blocks).
+ * With loc(n) the tokens of the first n positions that shard `rank` holds
+ * (as mla_shard_row_view counts them; n unsharded), request b holds
+ * held_b = cdiv(loc(prev_lens[b]), block_size) blocks and needs
+ * need_b = cdiv(loc(seq_lens[b]), block_size).  Blocks come from the front of
+ * the ring and go back to its end, both in request order: with take_b =
+ * max(need_b - held_b, 0), rel_b = max(held_b - need_b, 0) and exclusive
+ * prefix sums off_b, roff_b of them,
+ *     block_table[b][held_b + i] = free_ring[(head + off_b + i) % C],  i < take_b
+ *     free_ring[(head + count + roff_b + i) % C] = block_table[b][need_b + i],  i < rel_b
+ *     ring_out = {(head + t) % C, count - t + sum rel},  t = min(sum take, count).
+ * Blocks returned by this call are dealt from the next call on.  Table entries
+ * a request keeps, and those past need_b, are not written: calling again with
+ * the same inputs gives the same result.
+ *     slot_map[qo_indptr[b] + t] = block_table[b][j / block_size] * block_size + j % block_size
+ * for new token t at global position g = L_b - qlen_b + t, j its local index,
+ * when this shard owns g, and -1 otherwise; rows from qo_indptr[B] on get -1.
+ * Requests with qlen 0 (finished, or waiting) are allowed here.
+ * Returns MLA_ERR_UNSUPPORTED for B > 16384.  Device checks (nothing faults):
+ * MLA_DEV_BAD_INDPTR and MLA_DEV_BAD_FREE_RING (nothing is dealt or returned,
+ * ring_out = ring_in, every slot -1), MLA_DEV_BAD_QLEN (qlen > L, or a negative
+ * length, read as 0: that request's slots are -1), MLA_DEV_LEN_BOUND (need
+ * clipped to the table's width, slots past it -1), MLA_DEV_NO_FREE_BLOCK
+ * (entries the ring could not serve are -1, and so are their tokens' slots),
+ * MLA_DEV_BAD_BLOCK_ID (an id outside the pool in the ring or table: -1). */
+mla_status mla_update_block_tables(const mla_table_args *a, mla_stream_t stream);
+
+/* Quantising write of new latent rows into an e4m3 cache with one float32
+ * scale per block of scale_block consecutive cache rows (kv_scales
+ * [num_cache_rows / scale_block]; a row's values are scale * code).  Row r of
+ * kv_new [T, 576] bf16 goes to cache row slot_map[r] (-1: not written).
+ * scale_block G is a power of two, 1 <= G <= 64, dividing block_size.  For a
+ * scale block that receives rows, f is the first offset written in it:
+ *     want  = 2^k, the smallest with max |x| <= 448 * 2^k over its new rows
+ *             (finite values only), k >= -100
+ *     scale = want if f == 0, else max(old scale, want)
+ *     code  = e4m3(x / scale), the quotient in float32, nearest even, saturating
+ *             (+-inf: +-448, NaN stays NaN);
+ * and when the scale grew, the codes of the f rows before are rewritten as
+ * e4m3(code * old / scale).  Rows after the new ones are left as they were.
+ * A power of two costs e4m3 no precision (its steps are relative) and makes
+ * that rewriting exact but for codes that become subnormal, so a block filled
+ * token by token ends like one filled at once.
+ * slot_map comes from mla_update_block_tables or is made alike: slots
+ * distinct, and the rows of one scale block ascending by one with only -1 rows
+ * between them.  Device check: MLA_DEV_BAD_BLOCK_ID (a slot >= num_cache_rows
+ * or < -1: the row is not written). */
+mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, const int32_t *slot_map,
+                               void *kv_cache, float *kv_scales, int scale_block,
+                               int64_t num_cache_rows, mla_stream_t stream);
+
+/* mla_decode_verify over an e4m3 cache with one scale per block of scale_block
+ * rows, as mla_write_kv_scaled writes it: token j in cache row n has
+ * k_j = kv_scales[n / scale_block] * code, v_j = its first 512 values.
+ * a->kv_dtype must be MLA_KV_FP8_E4M3 and a->kv_scale is ignored; the scales
+ * may be any positive finite values (below 2^-100 they count as 2^-100).
+ * scale_block is a power of two, 1 <= scale_block <= min(64, page_size);
+ * num_cache_rows a multiple of it.  No flags are taken
+ * (MLA_ERR_UNSUPPORTED).  A NaN code reaches the rows that see
+ * its token and no other row.  Workspace, partial layout, outputs, errors and
+ * device checks are those of mla_decode_verify. */
+mla_status mla_decode_verify_scaled(const mla_decode_args *a, const float *kv_scales,
+                                    int scale_block, void *workspace, size_t workspace_bytes,
+                                    mla_stream_t stream);
 
 /* The same decode / verify as mla_decode_verify, for callers that cannot
  * allocate device memory where they make the call -- serving runtimes that

@@ -25,26 +25,6 @@ std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode{nullptr};
 
 __device__ __forceinline__ void dev_error(int *err, int code) { atomicCAS(err, 0, code); }
 
-// Round-robin count of window w on rank r of W (interleave 1): positions
-// g < w with g mod W == r, i.e. floor((w - 1 - r) / W) + 1 when w - 1 - r >= 0.
-// [vLLM #51705 digest, _build_dcp_verify_row_view snippet; sglang #34432,
-// g(j) = j * W + r]
-__device__ __forceinline__ int rr_count(int w, int W, int r) {
-  const int top = w - 1 - r;
-  return top >= 0 ? top / W + 1 : 0;
-}
-// Interleave I > 1 (runs of I consecutive positions dealt to the ranks in
-// turn; the pages stop at I = 1): I positions per full cycle of I * W plus
-// the rank's part of the last, partial cycle.
-__device__ __forceinline__ int il_count(int w, int W, int r, int I) {
-  if (I == 1) return rr_count(w, W, r);
-  if (w <= 0) return 0;
-  const int64_t cycle = static_cast<int64_t>(I) * W;
-  int64_t rem = w % cycle - static_cast<int64_t>(r) * I;
-  rem = rem < 0 ? 0 : (rem > I ? I : rem);
-  return static_cast<int>((w / cycle) * I + rem);
-}
-
 // Request owning row r: the b with qo_indptr[b] <= r < qo_indptr[b+1].
 __device__ __forceinline__ int find_request(const int32_t *ind, int B, int r) {
   int lo = 0, hi = B;  // invariant: ind[lo] <= r < ind[hi] when indptr is valid
@@ -578,6 +558,45 @@ mla_status mla_decode_verify(const mla_decode_args *a, void *workspace, size_t w
   m.out = a->out;
   m.lse = a->lse;
   return launch_merge(m, s);
+}
+
+mla_status mla_decode_verify_scaled(const mla_decode_args *a, const float *kv_scales, int scale_block,
+                                    void *workspace, size_t workspace_bytes, mla_stream_t stream) {
+  if (a == nullptr || kv_scales == nullptr) {
+    set_error("mla_decode_verify_scaled: null argument struct or kv_scales");
+    return MLA_ERR_INVALID_ARG;
+  }
+  mla_decode_args s = *a;
+  s.kv_scale = 1.0f;  // the scales are the cache's own
+  mla_status st = check_decode_args(&s);
+  if (st != MLA_OK) return st;
+  if (s.kv_dtype != MLA_KV_FP8_E4M3 || s.flags != 0) {
+    set_error("mla_decode_verify_scaled: needs an e4m3 cache (kv_dtype %d) and no flags (0x%x)",
+              s.kv_dtype, s.flags);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (scale_block < 1 || scale_block > 64 || scale_block > s.page_size || (scale_block & (scale_block - 1)) != 0) {
+    set_error("mla_decode_verify_scaled: scale_block %d unsupported (power of two up to 64 and the page size %d)",
+              scale_block, s.page_size);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (s.num_cache_rows % scale_block != 0) {
+    set_error("mla_decode_verify_scaled: %lld cache rows are not whole scale blocks of %d",
+              (long long)s.num_cache_rows, scale_block);
+    return MLA_ERR_INVALID_ARG;
+  }
+  const WorkspaceLayout lay = decode_workspace_layout(s);
+  if (workspace == nullptr || workspace_bytes < lay.total || !is_aligned(workspace, 256)) {
+    set_error("mla_decode_verify_scaled: workspace of %zu bytes (256-byte aligned) needed, got %zu at %p",
+              lay.total, workspace_bytes, workspace);
+    return MLA_ERR_WORKSPACE;
+  }
+  int *err = device_error_word();
+  if (err == nullptr) return MLA_ERR_CUDA;
+  DecodeLaunch d{};
+  d.a = &s;
+  d.err = err;
+  return launch_decode_scaled(d, kv_scales, scale_block, reinterpret_cast<cudaStream_t>(stream));
 }
 
 mla_status mla_merge_segments(const mla_merge_args *a, mla_stream_t stream) {

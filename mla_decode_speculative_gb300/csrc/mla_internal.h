@@ -41,6 +41,25 @@ __device__ __forceinline__ void grid_dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Positions g < w that rank r of W holds.  Interleave 1: g mod W == r, i.e.
+// floor((w - 1 - r) / W) + 1 when w - 1 - r >= 0 [vLLM #51705 digest,
+// _build_dcp_verify_row_view snippet; sglang #34432, g(j) = j * W + r].
+__device__ __forceinline__ int rr_count(int w, int W, int r) {
+  const int top = w - 1 - r;
+  return top >= 0 ? top / W + 1 : 0;
+}
+// Interleave I > 1 (runs of I consecutive positions dealt to the ranks in
+// turn; the pages stop at I = 1): I positions per full cycle of I * W plus
+// the rank's part of the last, partial cycle.
+__device__ __forceinline__ int il_count(int w, int W, int r, int I) {
+  if (I == 1) return rr_count(w, W, r);
+  if (w <= 0) return 0;
+  const int64_t cycle = static_cast<int64_t>(I) * W;
+  int64_t rem = w % cycle - static_cast<int64_t>(r) * I;
+  rem = rem < 0 ? 0 : (rem > I ? I : rem);
+  return static_cast<int>((w / cycle) * I + rem);
+}
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                               Args... args) {
@@ -96,6 +115,10 @@ WorkspaceLayout decode_workspace_layout(const mla_decode_args &a);
 // split-K parts into out / lse itself (balanced split), so no merge launch
 // must follow.
 mla_status launch_decode(const DecodeLaunch &d, cudaStream_t stream, bool *merged);
+
+// The decode over an e4m3 cache with a scale per block of rows (arguments and
+// workspace as launch_decode; scale_block a power of two up to 64).
+mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, int scale_block, cudaStream_t stream);
 
 struct MergeLaunch {
   int mode;

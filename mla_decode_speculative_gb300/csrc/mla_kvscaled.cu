@@ -1,0 +1,326 @@
+// mla_kvscaled.cu -- quantising write of new latent rows into an e4m3 cache
+// with one power-of-two scale per block of G cache rows (mla_write_kv_scaled).
+//
+// A unit is one scale block that receives rows: its first new row (offset f in
+// the block) leads it, the rows that follow it in the block belong to it, and
+// the f rows before it were written by earlier calls.  The unit's threads load
+// all of its new rows at once (at most 64 rows of 72 16-byte pieces, 18 pieces
+// a thread), reduce max |x|, choose the scale, and write the codes from the
+// registers that still hold the rows: each value is read once and each code
+// written once, which is the whole traffic unless a scale grows (the earlier
+// rows' codes are then read and rewritten).
+//
+// Scale: 2^k, the smallest with max |x| <= 448 * 2^k.  With max |x| = m 2^e,
+// m in [1, 2), and 448 = 1.75 * 2^8, that is k = e - 8, plus one when m > 1.75;
+// both come from the bf16 bits, and x / 2^k is exact.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "mla_internal.h"
+
+namespace mla {
+namespace {
+
+constexpr int kRowPieces = 72;   // 16-byte pieces (8 values) of a new row
+constexpr int kMaxGroup = 64;    // rows of a scale block at most
+constexpr int kHeld = 18;        // pieces a thread holds: 64 rows over 256 threads, 8 rows over 32
+constexpr int kMinExp = -100;
+constexpr int kThreads = 256;
+
+struct WriteScaledParams {
+  const uint4 *x;
+  const int32_t *slots;
+  uint2 *cache;
+  float *scales;
+  int *err;
+  int num_rows, log_g, num_cache_rows;
+  int window;  // rows whose units one CTA (or warp) writes
+};
+
+// Largest |x| of a packed pair and what was seen so far (NaN is passed over).
+__device__ __forceinline__ __nv_bfloat162 pair_max(__nv_bfloat162 m, uint32_t v) {
+  return __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v)));
+}
+
+// bits of the larger of two bf16 magnitudes
+__device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
+  const uint32_t u = *reinterpret_cast<const uint32_t *>(&m);
+  return max(u & 0xffffu, u >> 16);
+}
+
+// The exponent k of the scale for a largest magnitude given as bf16 bits.
+__device__ __forceinline__ int scale_exp(uint32_t bits) {
+  const int k = static_cast<int>(bits >> 7) - 127 - 8 + ((bits & 0x7f) > 0x60 ? 1 : 0);
+  return bits == 0 ? kMinExp : max(k, kMinExp);
+}
+
+__device__ __forceinline__ float pow2f(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+
+__device__ __forceinline__ uint32_t quantise4(uint32_t a, uint32_t b, float inv, float scale, bool exact) {
+  float2 lo = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  float2 hi = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+  if (exact) {
+    lo = make_float2(lo.x * inv, lo.y * inv);
+    hi = make_float2(hi.x * inv, hi.y * inv);
+  } else {  // a scale that another writer chose: divide
+    lo = make_float2(lo.x / scale, lo.y / scale);
+    hi = make_float2(hi.x / scale, hi.y / scale);
+  }
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3)) |
+         (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16);
+}
+
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes >> (16 * h)), __NV_E4M3);
+    float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r));
+    f = make_float2(f.x * ratio, f.y * ratio);
+    out |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << (16 * h);
+  }
+  return out;
+}
+
+// One unit by `kTeam` threads (a warp, or the whole CTA): rows[0 .. n) are its
+// new rows, ascending; first_slot is rows[0]'s cache row.
+template <int kTeam>
+__device__ __forceinline__ void write_unit(const WriteScaledParams &p, const int *rows, int n, int first_slot, int t,
+                                           uint32_t *team_max) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  const int pieces = n * kRowPieces;
+  uint4 v[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = t + i * kTeam;
+    if (c < pieces) v[i] = p.x[static_cast<int64_t>(rows[c / kRowPieces]) * kRowPieces + c % kRowPieces];
+  }
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
+  __nv_bfloat162 m = zero;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (t + i * kTeam < pieces) m = pair_max(pair_max(pair_max(pair_max(m, v[i].x), v[i].y), v[i].z), v[i].w);
+  uint32_t top = max_bits(m);
+  if (top >= 0x7f80) {  // an infinity among them: only finite values count
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (t + i * kTeam < pieces) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+      }
+  }
+  top = __reduce_max_sync(kAll, top);
+  if (kTeam > 32) {
+    if ((t & 31) == 0) team_max[t >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTeam / 32; ++w) top = max(top, team_max[w]);
+  }
+  const int f = first_slot & ((1 << p.log_g) - 1), block = first_slot >> p.log_g;
+  const float want = pow2f(scale_exp(top));
+  const float old = f > 0 ? p.scales[block] : want;
+  const float scale = f > 0 ? fmaxf(old, want) : want;
+  const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
+  const float inv = 1.0f / scale;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = t + i * kTeam;
+    if (c < pieces) {
+      const int row = c / kRowPieces;  // the unit's slots follow one another
+      p.cache[static_cast<int64_t>(first_slot + row) * kRowPieces + c % kRowPieces] =
+          make_uint2(quantise4(v[i].x, v[i].y, inv, scale, exact), quantise4(v[i].z, v[i].w, inv, scale, exact));
+    }
+  }
+  if (f > 0 && scale > old) {
+    const float ratio = old / scale;
+    uint2 *prior = p.cache + static_cast<int64_t>(first_slot - f) * kRowPieces;
+    for (int c = t; c < f * kRowPieces; c += kTeam) {
+      const uint2 u = prior[c];
+      prior[c] = make_uint2(rescale4(u.x, ratio), rescale4(u.y, ratio));
+    }
+  }
+  if (kTeam > 32) __syncthreads();  // every thread has read the old scale
+  else __syncwarp();
+  if (t == 0) p.scales[block] = scale;
+}
+
+// Leaders among rows r0 .. r0 + 31 (a warp): the row of lane l opens a unit.
+// A row whose nearest earlier row with a slot lies in the same scale block
+// follows a leader; rows without a slot (another shard's) are passed over.
+__device__ __forceinline__ uint32_t leaders(const WriteScaledParams &p, int r0, int r_end, int lane, int &slot) {
+  const int r = r0 + lane;
+  slot = r < r_end ? p.slots[r] : -1;
+  if (slot >= p.num_cache_rows || slot < -1) {
+    atomicCAS(p.err, 0, MLA_DEV_BAD_BLOCK_ID);
+    slot = -1;
+  }
+  const uint32_t have = __ballot_sync(0xffffffffu, slot >= 0);
+  if (have == 0) return 0;
+  // the nearest earlier slot: in these 32 rows, or before them
+  const uint32_t below = have & ((1u << lane) - 1u);
+  int prev = __shfl_sync(0xffffffffu, slot, below ? 31 - __clz(below) : 0);
+  const int head_slot = __shfl_sync(0xffffffffu, slot, __ffs(have) - 1);
+  int before = -1;
+  if ((head_slot & ((1 << p.log_g) - 1)) != 0)
+    for (int b0 = r0 - 32; b0 > -32 && before < 0; b0 -= 32) {
+      const int s = b0 + lane >= 0 ? p.slots[b0 + lane] : -1;
+      const uint32_t got = __ballot_sync(0xffffffffu, s >= 0 && s < p.num_cache_rows);
+      if (got) before = __shfl_sync(0xffffffffu, s, 31 - __clz(got));
+    }
+  if (below == 0) prev = before;
+  const bool lead = slot >= 0 && (prev < 0 || (prev >> p.log_g) != (slot >> p.log_g));
+  return __ballot_sync(0xffffffffu, lead);
+}
+
+// The rows of the unit that row r0 leads (a warp), into rows[]; returns how many.
+__device__ __forceinline__ int members(const WriteScaledParams &p, int r0, int first_slot, int lane, int *rows) {
+  const int block = first_slot >> p.log_g;
+  const int room = (1 << p.log_g) - (first_slot & ((1 << p.log_g) - 1));
+  int n = 0;
+  for (int b0 = r0; b0 < p.num_rows && n < room; b0 += 32) {
+    const int r = b0 + lane;
+    const int s = r < p.num_rows ? p.slots[r] : -1;
+    const bool valid = s >= 0 && s < p.num_cache_rows;
+    const uint32_t other = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) != block);
+    const uint32_t upto = other ? (1u << (__ffs(other) - 1)) - 1u : 0xffffffffu;
+    const uint32_t mine = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) == block) & upto;
+    const int at = n + __popc(mine & ((1u << lane) - 1u));
+    if ((mine >> lane & 1u) && at < room) rows[at] = r;
+    n = min(n + __popc(mine), room);
+    if (other) break;
+  }
+  __syncwarp();
+  return n;
+}
+
+// A CTA per unit: scale blocks of more than 8 rows.
+__global__ void __launch_bounds__(kThreads) write_scaled_cta(const WriteScaledParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ int s_lead[kMaxGroup], s_slot[kMaxGroup], s_rows[kMaxGroup], s_n, s_units;
+  __shared__ uint32_t s_max[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r0 = blockIdx.x * p.window, r_end = min(p.num_rows, r0 + p.window);
+  if (warp == 0) {
+    int units = 0;
+    for (int w0 = r0; w0 < r_end; w0 += 32) {
+      int slot;
+      const uint32_t lead = leaders(p, w0, r_end, lane, slot);
+      if (lead >> lane & 1u) {
+        const int at = units + __popc(lead & ((1u << lane) - 1u));
+        s_lead[at] = w0 + lane;
+        s_slot[at] = slot;
+      }
+      units += __popc(lead);
+    }
+    if (lane == 0) s_units = units;
+  }
+  __syncthreads();
+  const int units = s_units;
+  for (int u = 0; u < units; ++u) {
+    if (warp == 0) {
+      const int n = members(p, s_lead[u], s_slot[u], lane, s_rows);
+      if (lane == 0) s_n = n;
+    }
+    __syncthreads();
+    write_unit<kThreads>(p, s_rows, s_n, s_slot[u], tid, s_max);
+    __syncthreads();
+  }
+}
+
+// A warp per unit: scale blocks of up to 8 rows.
+__global__ void __launch_bounds__(kThreads) write_scaled_warp(const WriteScaledParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ int s_rows[kThreads / 32][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp) * p.window;
+  if (r0 >= p.num_rows) return;
+  const int r_end = static_cast<int>(min(static_cast<int64_t>(p.num_rows), r0 + p.window));
+  int slot;
+  uint32_t lead = leaders(p, static_cast<int>(r0), r_end, lane, slot);
+  while (lead) {
+    const int l = __ffs(lead) - 1;
+    lead &= lead - 1;
+    const int first_slot = __shfl_sync(0xffffffffu, slot, l);
+    const int n = members(p, static_cast<int>(r0) + l, first_slot, lane, s_rows[warp]);
+    write_unit<32>(p, s_rows[warp], n, first_slot, lane, nullptr);
+    __syncwarp();
+  }
+}
+
+std::atomic<int> g_write_sms[64];
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, const int32_t *slot_map, void *kv_cache,
+                                          float *kv_scales, int scale_block, int64_t num_cache_rows,
+                                          mla_stream_t stream) {
+  if (num_rows < 0 || num_cache_rows < 1 || num_cache_rows > INT32_MAX || kv_cache == nullptr || kv_scales == nullptr ||
+      (num_rows > 0 && (kv_new == nullptr || slot_map == nullptr))) {
+    set_error("mla_write_kv_scaled: bad sizes or null pointers (T=%d, %lld cache rows)", num_rows,
+              (long long)num_cache_rows);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (scale_block < 1 || scale_block > kMaxGroup || (scale_block & (scale_block - 1)) != 0) {
+    set_error("mla_write_kv_scaled: scale_block %d unsupported (power of two in [1, %d])", scale_block, kMaxGroup);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  if (num_cache_rows % scale_block != 0) {
+    set_error("mla_write_kv_scaled: %lld cache rows are not whole scale blocks of %d", (long long)num_cache_rows,
+              scale_block);
+    return MLA_ERR_INVALID_ARG;
+  }
+  if ((reinterpret_cast<uintptr_t>(kv_new) | reinterpret_cast<uintptr_t>(kv_cache)) % 16 != 0) {
+    set_error("mla_write_kv_scaled: kv_new and kv_cache must be 16-byte aligned");
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (num_rows == 0) return MLA_OK;
+  int *err = device_error_word();
+  if (err == nullptr) return MLA_ERR_CUDA;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  int sms = g_write_sms[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(SM count)");
+    g_write_sms[dev].store(sms, std::memory_order_relaxed);
+  }
+  WriteScaledParams p{};
+  p.x = static_cast<const uint4 *>(kv_new);
+  p.slots = slot_map;
+  p.cache = static_cast<uint2 *>(kv_cache);
+  p.scales = kv_scales;
+  p.err = err;
+  p.num_rows = num_rows;
+  p.log_g = __builtin_ctz(static_cast<unsigned>(scale_block));
+  p.num_cache_rows = static_cast<int>(num_cache_rows);
+  const bool by_cta = scale_block > 8;
+  // rows per team: one while the GPU holds a team for every row, then as many
+  // as keep it at two full waves, within the list of leaders (64) or a warp
+  const int teams = sms * (by_cta ? 8 : 64);
+  const int most = by_cta ? kMaxGroup : 32;
+  int window = num_rows / teams;
+  window = window < 1 ? 1 : (window > most ? most : window);
+  p.window = window;
+  const int per_cta = by_cta ? window : window * (kThreads / 32);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_rows) + per_cta - 1) / per_cta));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  e = by_cta ? launch_pdl(write_scaled_cta, grid, dim3(kThreads), 0, s, p)
+             : launch_pdl(write_scaled_warp, grid, dim3(kThreads), 0, s, p);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "write_kv_scaled launch");
+}

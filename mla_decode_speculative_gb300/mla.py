@@ -38,7 +38,7 @@ MLA_DECODE_FUSED_MERGE = 4
 
 DEVICE_ERRORS = {0: "MLA_DEV_OK", 1: "MLA_DEV_BAD_INDPTR", 2: "MLA_DEV_BAD_QLEN",
                  3: "MLA_DEV_BAD_BLOCK_ID", 4: "MLA_DEV_LEN_BOUND", 5: "MLA_DEV_BAD_SUBPAGE",
-                 6: "MLA_DEV_WAIT_TIMEOUT"}
+                 6: "MLA_DEV_WAIT_TIMEOUT", 7: "MLA_DEV_NO_FREE_BLOCK", 8: "MLA_DEV_BAD_FREE_RING"}
 
 
 class MLAError(RuntimeError):
@@ -69,11 +69,23 @@ class MergeArgs(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
+class TableArgs(ctypes.Structure):
+    _fields_ = [("num_reqs", ctypes.c_int), ("num_rows", ctypes.c_int),
+                ("prev_lens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("qo_indptr", ctypes.c_void_p), ("world_size", ctypes.c_int),
+                ("rank", ctypes.c_int), ("interleave", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("num_blocks", ctypes.c_int),
+                ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int),
+                ("free_ring", ctypes.c_void_p), ("ring_in", ctypes.c_void_p),
+                ("ring_out", ctypes.c_void_p), ("slot_map", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 EXPORTS = ("mla_page_size", "mla_plan_rows", "mla_shard_row_view", "mla_shard_row_views",
            "mla_decode_verify_workspace",
-           "mla_decode_verify", "mla_decode_verify_noalloc", "mla_write_kv", "mla_merge_segments", "mla_get_device_error",
+           "mla_decode_verify", "mla_decode_verify_noalloc", "mla_write_kv", "mla_merge_segments",
+           "mla_update_block_tables", "mla_write_kv_scaled", "mla_decode_verify_scaled", "mla_get_device_error",
            "mla_last_error_string", "mla_status_string", "mla_abi_version")
 
 
@@ -113,6 +125,12 @@ def lib():
         L.mla_write_kv.argtypes = [c_int, c_int, i32p, i32p, vp, c_int, c_int, c_int, i32p, c_int,
                                    c_int, c_int, vp, c_int, ctypes.c_float, ctypes.c_int64, vp]
         L.mla_write_kv.restype = c_int
+        L.mla_update_block_tables.argtypes = [ctypes.POINTER(TableArgs), vp]
+        L.mla_update_block_tables.restype = c_int
+        L.mla_write_kv_scaled.argtypes = [c_int, vp, i32p, vp, vp, c_int, ctypes.c_int64, vp]
+        L.mla_write_kv_scaled.restype = c_int
+        L.mla_decode_verify_scaled.argtypes = [ctypes.POINTER(DecodeArgs), vp, c_int, vp, ctypes.c_size_t, vp]
+        L.mla_decode_verify_scaled.restype = c_int
         L.mla_merge_segments.argtypes = [ctypes.POINTER(MergeArgs), vp]
         L.mla_merge_segments.restype = c_int
         L.mla_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
@@ -413,6 +431,99 @@ def write_kv(seq_lens, qo_indptr, kv_new, kv_cache, block_table, num_blocks, blo
                               MLA_KV_FP8_E4M3 if fp8 else MLA_KV_BF16, float(kv_scale),
                               int(kv_cache.numel() // D_QK), _stream(stream)), "mla_write_kv")
     return kv_cache
+
+
+def _here(*tensors):
+    """The tensors' one device must be the current one: the library launches there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def update_block_tables(prev_lens, seq_lens, qo_indptr, block_table, free_ring, ring_in, block_size,
+                        num_rows, ring_out=None, slot_map=None, world_size=1, rank=0, interleave=1,
+                        stream=None):
+    """mla_update_block_tables: blocks for the requests that grow from prev_lens to seq_lens
+    tokens, blocks back from those that shrink, and the new tokens' cache rows.  All int32:
+    prev_lens, seq_lens [B], qo_indptr [B + 1], block_table [B, width] (updated), free_ring
+    [num_blocks] (updated), ring_in [2] = (head, count).  Returns (slot_map [num_rows],
+    ring_out [2])."""
+    B = int(seq_lens.shape[0])
+    _here(prev_lens, seq_lens, qo_indptr, block_table, free_ring, ring_in, ring_out, slot_map)
+    if block_table.dim() != 2 or block_table.shape[0] != B or prev_lens.shape[0] != B or \
+            qo_indptr.shape[0] != B + 1 or ring_in.numel() != 2:
+        raise ValueError("prev_lens, seq_lens [B], qo_indptr [B + 1], block_table [B, width], ring_in [2]")
+    if ring_out is None:
+        ring_out = torch.empty_like(ring_in)
+    if slot_map is None:
+        slot_map = torch.empty(num_rows, dtype=torch.int32, device=seq_lens.device)
+    if slot_map.numel() < num_rows or ring_out.numel() != 2:
+        raise ValueError("slot_map holds fewer than num_rows entries, or ring_out is not [2]")
+    i32 = torch.int32
+    a = TableArgs(B, int(num_rows), _ptr(prev_lens, i32, "prev_lens"), _ptr(seq_lens, i32, "seq_lens"),
+                  _ptr(qo_indptr, i32, "qo_indptr"), int(world_size), int(rank), int(interleave),
+                  int(block_size), int(free_ring.numel()), _ptr(block_table, i32, "block_table"),
+                  int(block_table.shape[1]), _ptr(free_ring, i32, "free_ring"),
+                  _ptr(ring_in, i32, "ring_in"), _ptr(ring_out, i32, "ring_out"),
+                  _ptr(slot_map, i32, "slot_map"))
+    _check(lib().mla_update_block_tables(ctypes.byref(a), _stream(stream)), "mla_update_block_tables")
+    return slot_map, ring_out
+
+
+def _check_scaled(kv_cache, kv_scales, scale_block):
+    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 2 or kv_cache.shape[1] != D_QK:
+        raise ValueError("kv_cache must be [N, 576] uint8 (e4m3 codes)")
+    if scale_block < 1 or kv_scales.numel() * scale_block != kv_cache.shape[0]:
+        raise ValueError("kv_scales must hold one float32 per scale_block rows of kv_cache")
+
+
+def write_kv_scaled(kv_new, slot_map, kv_cache, kv_scales, scale_block, stream=None):
+    """mla_write_kv_scaled: kv_new [T, 576] bf16 quantised into kv_cache [N, 576] uint8 (e4m3
+    codes) at the rows slot_map [T] int32 names (-1: skipped), with a power-of-two float32 scale
+    per scale_block rows in kv_scales [N / scale_block].  Returns (kv_cache, kv_scales)."""
+    _here(kv_new, slot_map, kv_cache, kv_scales)
+    _check_scaled(kv_cache, kv_scales, scale_block)
+    T = int(kv_new.shape[0])
+    if kv_new.dim() != 2 or kv_new.shape[1] != D_QK or slot_map.numel() < T:
+        raise ValueError("kv_new must be [T, 576] and slot_map hold T entries")
+    _check(lib().mla_write_kv_scaled(T, _ptr(kv_new, torch.bfloat16, "kv_new"),
+                                     _ptr(slot_map, torch.int32, "slot_map"),
+                                     _ptr(kv_cache, torch.uint8, "kv_cache"),
+                                     _ptr(kv_scales, torch.float32, "kv_scales"), int(scale_block),
+                                     int(kv_cache.shape[0]), _stream(stream)), "mla_write_kv_scaled")
+    return kv_cache, kv_scales
+
+
+def decode_verify_scaled(q, kv_cache, kv_scales, scale_block, qo_indptr, row_len, subpage_table, page_size_,
+                         num_segments, max_qlen, sm_scale, out=None, lse=None, workspace=None,
+                         stream=None, num_views=1, wait_cycles=0):
+    """mla_decode_verify_scaled: decode_verify over e4m3 codes kv_cache [N, 576] uint8 with one
+    float32 scale per scale_block rows in kv_scales [N / scale_block].  The other arguments and
+    the result (out, lse, workspace) are decode_verify's."""
+    T, H, _ = q.shape
+    _here(q, kv_cache, kv_scales, qo_indptr, row_len, subpage_table, out, lse, workspace)
+    _check_scaled(kv_cache, kv_scales, scale_block)
+    V = max(1, int(num_views))
+    if row_len.numel() != V * T or subpage_table.numel() != V * (qo_indptr.shape[0] - 1) * subpage_table.shape[-1]:
+        raise ValueError("row_len must be [V, T] and subpage_table [V, B, width]")
+    lead = (V, T) if V > 1 else (T,)
+    if out is None:
+        out = torch.empty((*lead, H, D_V), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((*lead, H), dtype=torch.float32, device=q.device)
+    if out.numel() != V * T * H * D_V or lse.numel() != V * T * H:
+        raise ValueError("out must be [V, T, H, 512] and lse [V, T, H]")
+    a = make_decode_args(q, kv_cache, qo_indptr, row_len, subpage_table, page_size_, num_segments, max_qlen,
+                         sm_scale, 1.0, out, lse, num_views=V,
+                         wait_cycles=wait_cycles)
+    need = decode_verify_workspace_bytes(a)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib().mla_decode_verify_scaled(ctypes.byref(a), _ptr(kv_scales, torch.float32, "kv_scales"),
+                                          int(scale_block), _ptr(workspace, torch.uint8, "workspace"), need,
+                                          _stream(stream)), "mla_decode_verify_scaled")
+    return out, lse, workspace
 
 
 def get_device_error(stream=None) -> int:

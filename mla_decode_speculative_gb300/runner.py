@@ -8,7 +8,14 @@ mla_decode_verify (decode + segment merge).  Context-sharded step (W round-robin
 shards simulated on one device): mla_plan_rows (global windows) -> the W shard
 row views in one mla_shard_row_views launch -> one mla_decode_verify over the
 W row views (num_views = W)
-into a [W, T, H, .] state buffer -> mla_merge_segments (state mode).
+into a [W, T, H, .] state buffer -> mla_merge_segments (state mode).  With
+``scale_block`` the cache is e4m3 with a scale per block of rows and the decode
+is mla_decode_verify_scaled.
+
+``PagedLatentCache`` owns such a cache with its scales, block table and free
+blocks: ``append`` deals the blocks a step needs, makes its slot map and writes
+its new tokens, all on the device (mla_update_block_tables ->
+mla_write_kv_scaled).
 """
 from __future__ import annotations
 
@@ -24,7 +31,10 @@ class VerifyStep:
                  block_size: int, num_blocks: int, block_table_width: int, max_kv_len: int,
                  num_segments: int = 1, world_size: int = 1, kv_fp8: bool = False,
                  interleave: int = 1, uniform_segments: bool = False, fused_merge: bool = False,
-                 device="cuda"):
+                 scale_block: int = 0, device="cuda"):
+        if scale_block and (uniform_segments or fused_merge):
+            raise ValueError("a cache with block scales is decoded with the balanced split and the separate merge")
+        self.scale_block = scale_block   # rows per scale of an e4m3 cache (0: one scale, or bf16)
         self.B, self.T, self.H = num_reqs, num_rows, num_heads
         self.max_qlen = max_qlen
         self.block_size = block_size
@@ -66,16 +76,17 @@ class VerifyStep:
 
     def __call__(self, q: torch.Tensor, kv_cache: torch.Tensor, seq_lens: torch.Tensor,
                  qo_indptr: torch.Tensor, block_tables: torch.Tensor, sm_scale: float,
-                 kv_scale: float = 1.0, stream=None):
-        """block_tables: [W, B, width] int32 (W = 1 unsharded).  Returns (out, lse)."""
+                 kv_scale: float = 1.0, stream=None, kv_scales: Optional[torch.Tensor] = None):
+        """block_tables: [W, B, width] int32 (W = 1 unsharded); kv_scales: the cache's block
+        scales when the step was made with scale_block.  Returns (out, lse)."""
+        if (kv_scales is not None) != bool(self.scale_block):
+            raise ValueError("kv_scales goes with a step made with scale_block")
         if self.W == 1:
             mla.plan_rows(seq_lens, qo_indptr, self.T, block_tables[0], self.num_blocks,
                           self.block_size, self.sp_stride, row_len=self.row_len,
                           row_req=self.row_req, subpage_table=self.subpage[0], stream=stream)
-            mla.decode_verify(q, kv_cache, qo_indptr, self.row_len, self.subpage[0], self.P,
-                              self.S, self.max_qlen, sm_scale, kv_scale, out=self.out,
-                              lse=self.lse, workspace=self.workspace, stream=stream,
-                              uniform_segments=self.uniform, fused_merge=self.fused)
+            self._decode(q, kv_cache, kv_scales, qo_indptr, self.row_len, self.subpage[0], sm_scale, kv_scale,
+                         self.out, self.lse, stream)
             return self.out, self.lse
         mla.plan_rows(seq_lens, qo_indptr, self.T, row_len=self.row_len, row_req=self.row_req,
                       stream=stream)
@@ -85,12 +96,63 @@ class VerifyStep:
                             row_len_local=self.row_len_local, subpage_tables=self.subpage,
                             stream=stream)
         # all W shard views in one decode launch, straight into the shard states
-        mla.decode_verify(q, kv_cache, qo_indptr, self.row_len_local, self.subpage, self.P, self.S,
-                          self.max_qlen, sm_scale, kv_scale, out=self.part_out, lse=self.part_lse,
-                          workspace=self.workspace, stream=stream, num_views=self.W,
-                          uniform_segments=self.uniform, fused_merge=self.fused)
+        self._decode(q, kv_cache, kv_scales, qo_indptr, self.row_len_local, self.subpage, sm_scale, kv_scale,
+                     self.part_out, self.part_lse, stream)
         mla.merge_states(self.part_out, self.part_lse, out=self.out, lse=self.lse, stream=stream)
         return self.out, self.lse
+
+
+    def _decode(self, q, kv_cache, kv_scales, qo_indptr, row_len, subpage, sm_scale, kv_scale, out, lse, stream):
+        if self.scale_block:
+            mla.decode_verify_scaled(q, kv_cache, kv_scales, self.scale_block, qo_indptr, row_len, subpage, self.P,
+                                     self.S, self.max_qlen, sm_scale, out=out, lse=lse, workspace=self.workspace,
+                                     stream=stream, num_views=self.W)
+        else:
+            mla.decode_verify(q, kv_cache, qo_indptr, row_len, subpage, self.P, self.S, self.max_qlen, sm_scale,
+                              kv_scale, out=out, lse=lse, workspace=self.workspace, stream=stream,
+                              num_views=self.W, uniform_segments=self.uniform, fused_merge=self.fused)
+
+
+class PagedLatentCache:
+    """An e4m3 latent cache with one scale per ``scale_block`` rows, for up to ``num_reqs``
+    requests of up to ``max_kv_len`` tokens (on this shard) in ``num_blocks`` blocks.  Which
+    blocks a request holds, which are free and how many tokens each request has are device
+    state, so ``append`` can be captured in a CUDA graph and replayed with new lengths.
+    ``num_rows`` is the capacity of a step's new tokens."""
+
+    def __init__(self, *, num_reqs: int, num_rows: int, num_blocks: int, block_size: int, max_kv_len: int,
+                 scale_block: int = 16, world_size: int = 1, rank: int = 0, interleave: int = 1, device="cuda"):
+        if block_size % scale_block:
+            raise ValueError("scale_block must divide block_size")
+        dev = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.num_rows, self.block_size, self.scale_block = num_rows, block_size, scale_block
+        self.num_blocks = num_blocks
+        self.shard = dict(world_size=world_size, rank=rank, interleave=interleave)
+        self.codes = torch.zeros((num_blocks * block_size, mla.D_QK), dtype=torch.uint8, device=dev)
+        self.scales = torch.ones(num_blocks * block_size // scale_block, dtype=torch.float32, device=dev)
+        self.block_table = torch.full((num_reqs, max(1, -(-max_kv_len // block_size))), -1, **i32)
+        self.free_ring = torch.arange(num_blocks, **i32)
+        self.ring = torch.tensor([0, num_blocks], **i32)   # {head, count} of the free blocks
+        self.ring_next = torch.empty(2, **i32)
+        self.lens = torch.zeros(num_reqs, **i32)           # tokens whose blocks are held
+        self.slot_map = torch.empty(num_rows, **i32)
+
+    def append(self, kv_new: torch.Tensor, seq_lens: torch.Tensor, qo_indptr: torch.Tensor, stream=None):
+        """The step's new tokens: request b grows (or, drafts taken back, shrinks) to seq_lens[b]
+        tokens, the last qo_indptr[b + 1] - qo_indptr[b] of which are rows of kv_new [num_rows,
+        576] bf16; 0 tokens return all of its blocks.  Returns the slot map."""
+        if kv_new.shape[0] != self.num_rows:
+            raise ValueError("kv_new must have num_rows rows")
+        s = torch.cuda.current_stream() if stream is None else stream
+        mla.update_block_tables(self.lens, seq_lens, qo_indptr, self.block_table, self.free_ring, self.ring,
+                                self.block_size, self.num_rows, ring_out=self.ring_next, slot_map=self.slot_map,
+                                stream=s, **self.shard)
+        mla.write_kv_scaled(kv_new, self.slot_map, self.codes, self.scales, self.scale_block, stream=s)
+        with torch.cuda.stream(s):
+            self.ring.copy_(self.ring_next)
+            self.lens.copy_(seq_lens)
+        return self.slot_map
 
 
 class StepIO:
