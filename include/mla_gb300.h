@@ -418,7 +418,8 @@ mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, const int32_t *
  * rows, as mla_write_kv_scaled writes it: token j in cache row n has
  * k_j = kv_scales[n / scale_block] * code, v_j = its first 512 values.
  * a->kv_dtype must be MLA_KV_FP8_E4M3 and a->kv_scale is ignored; the scales
- * may be any positive finite values (below 2^-100 they count as 2^-100).
+ * may be any positive finite values, those of one request within 2^130 of each
+ * other (below 2^-100 they count as 2^-100, above 2^120 as 2^120).
  * scale_block is a power of two, 1 <= scale_block <= min(64, page_size);
  * num_cache_rows a multiple of it.  No flags are taken
  * (MLA_ERR_UNSUPPORTED).  A NaN code reaches the rows that see

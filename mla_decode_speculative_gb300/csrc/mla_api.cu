@@ -593,10 +593,34 @@ mla_status mla_decode_verify_scaled(const mla_decode_args *a, const float *kv_sc
   }
   int *err = device_error_word();
   if (err == nullptr) return MLA_ERR_CUDA;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  char *w = static_cast<char *>(workspace);
   DecodeLaunch d{};
   d.a = &s;
   d.err = err;
-  return launch_decode_scaled(d, kv_scales, scale_block, reinterpret_cast<cudaStream_t>(stream));
+  if (s.num_segments > 1) {
+    d.segm_out = reinterpret_cast<uint16_t *>(w + lay.segm_out);
+    d.segm_max = reinterpret_cast<float *>(w + lay.segm_max);
+    d.segm_sum = reinterpret_cast<float *>(w + lay.segm_sum);
+  }
+  st = launch_decode_scaled(d, kv_scales, scale_block, cs);
+  if (st != MLA_OK || s.num_segments == 1) return st;
+  MergeLaunch m{};
+  m.mode = MLA_MERGE_SEGMENTS;
+  m.num_rows = s.num_rows;
+  m.num_heads = s.num_heads;
+  m.num_parts = s.num_segments;
+  m.segm_out = d.segm_out;
+  m.segm_max = d.segm_max;
+  m.segm_sum = d.segm_sum;
+  m.qo_indptr = s.qo_indptr;
+  m.num_reqs = s.num_reqs;
+  m.num_views = s.num_views > 1 ? s.num_views : 1;
+  m.row_blocks = (s.max_qlen * s.num_heads + 63) / 64;
+  m.keep_nan = 1;
+  m.out = s.out;
+  m.lse = s.lse;
+  return launch_merge(m, cs);
 }
 
 mla_status mla_merge_segments(const mla_merge_args *a, mla_stream_t stream) {

@@ -6,149 +6,1019 @@
 // j < row_len[t], token j in cache row n with scale a_j = kv_scales[n / G]:
 //   s_j = sm_scale * a_j * <q[r], code_j>, out = sum softmax(s)_j a_j code_j[0:512],
 //   lse = ln sum e^{s_j}.
-// One warp per (view, row, head): lane l holds dims 18 l .. 18 l + 17 of q, an
-// online softmax runs over the tokens.
+//
+// Both products run on the 8-bit codes as they lie in the cache
+// (tcgen05 kind::f8f6f4), nothing is expanded to 16 bits:
+//  * q is split exactly: each row is scaled by a power of two so that its
+//    largest element lies in [128, 256); q1 = e4m3(q), and what is left, at
+//    most half a step of q1, has no more than four significant bits, so
+//    q2 = e4m3(32 (q - q1)) holds it (elements below 2^-14 of the row's
+//    largest keep an absolute 2^-22 of it).  s = (q1 + q2 / 32) . code.
+//  * a probability times its token's scale is written as two e5m2 terms, the
+//    second the rounded remainder of the first: at most 2^-7 of itself off,
+//    over a range of 2^28 below the row's largest (e4m3 terms would lose the
+//    many small weights beside one large one).  The sums of the weights before
+//    and after this rounding correct the row's mean, so one visible token, or
+//    equal ones, come out exact.
+//  * With a_j = f_j 2^k_j, f in [1, 2), the exponent joins the score,
+//      w_j = f_j 2^(s_j log2e + k_j - m),  l = sum w_j / a_j,  out = sum w_j code_j / l,
+//    so the running reference m bounds the weights whatever the scales are.
+//
+// Work: (row view, request, block of up to 64 query rows) units in 96-token
+// tiles.  The tiles of all units plus one overhead position per unit, end to
+// end, are cut into one equal chunk per CTA (one CTA per SM), never more than
+// S chunks per unit; a chunk's part of a unit is one of its split-K segments
+// (S = 1: whole units, by the chunk their first tile lies in).  Every CTA sums
+// up the positions for itself and its producer walks on from its chunk's first
+// unit, so nothing is tabulated and any number of units fits.
+//
+// Operands.  q1 and q2 of 16 rows share a quarter of the 128 TMEM lanes (lane
+// 32 w + i: q1 of row 16 w + i, lane 32 w + 16 + i: its q2), 144 columns, as
+// the A operand of S[128, 96 tok] = Q . K^T: with A in TMEM no query is held
+// in shared memory, which takes four whole tiles instead.  A tile is four
+// 128-dim chunks [96 tok x 128 B] (128-byte swizzle) and the rope chunk
+// [96 tok x 64 B] (64-byte swizzle): the B operand of S = Q K^T as it lies, and
+// of O^T[4 x 128 dims, 64 rows] += V^T P^T the A operand in the other major.
+// P^T, the B operand there, is 32-token blocks [64 rows x 32 B] (32-byte
+// swizzle): the first term's blocks replace the tile's rope chunk, which S has
+// used by then, the second term's have 6 KB of their own.
+// TMEM: Q 0-143, O^T 144-399, S 400-495.
+//
+// What bounds it: an instruction of 128 x N x 32 takes 53-63 cycles for N up to
+// 96 or so and 64 at N = 128 (measured), so a tile's 18 + 24 instructions take
+// about 2550 cycles = 1.3 us, against 1.24 us for its 55 KB at the HBM rate; 96
+// tokens is the widest S that the columns left by Q and O^T hold.  Tile g's
+// products are ordered QK(g + 1), PV(g): the softmax of a tile has the time of
+// one PV and one QK.  Two tiles are in use at any time and two in flight.
+//
+// Warps 0-7: queries into TMEM, softmax, epilogue (TMEM quarter w % 4, token
+// half w / 4); 8: work and TMA; 9: MMA; 10: the tiles' scales.  Every wait is
+// bounded; one that runs out records MLA_DEV_WAIT_TIMEOUT, all roles drain
+// without skipping a barrier, TMEM is freed and the kernel returns.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "mla_internal.h"
+#include "mla_ptx.cuh"
 
 namespace mla {
 namespace {
 
-struct ScaledParams {
+constexpr int kTile = 96;          // tokens of a tile
+constexpr int kStages = 4;         // tiles in shared memory
+constexpr int kRows = 64;          // query rows of a unit
+constexpr int kVChunk = kTile * 128;              // 128 dims of a tile
+constexpr int kRopeOff = 4 * kVChunk;             // rope chunk, then the first term of P^T
+constexpr int kStageBytes = kTile * 576;
+constexpr int kPBlock = kRows * 32;               // 32 tokens of one term of P^T
+constexpr int kOffP2 = kStages * kStageBytes;     // second term of P^T
+constexpr int kOffMisc = kOffP2 + 3 * kPBlock;
+constexpr int kSoftWarps = 8, kSoftThreads = 256;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10;
+constexpr int kThreads = 352;
+constexpr uint32_t kTmemQ = 0, kTmemO = 144, kTmemS = 400, kTmemCols = 512;
+constexpr int kWorkRing = 4;
+constexpr float kThreshold = 3.0f;   // the reference moves when a weight exceeds 2^3 of it
+constexpr float kTop = 11.0f;        // a weight at the reference is held as 2^11 .. 2^12: at most 2^15 < 57344
+constexpr float kInvTop = 4.8828125e-4f;  // 2^-kTop
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr uint32_t kBarSoft = 1;     // named barrier of the softmax warps
+
+// A part of a unit, as the producer publishes it.
+struct Part {
+  int stop;                 // 1: no more work
+  int b;                    // view * B + request
+  int rb, seg, fill_hi;     // slots seg + 1 .. fill_hi - 1 of the unit get no part: mark them empty
+  int q_row, row_base, n_rows;
+  int seg_lo, seg_hi, n_tiles;
+  int pad;
+  int lens[kRows];          // visible tokens of each row
+};
+
+struct Misc {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_full, s_free, p_full, o_done, q_full, sc_full, sc_free, fin;
+  uint64_t work_full[kWorkRing], work_empty[kWorkRing];
+  uint32_t tmem_base;
+  int abort;
+  int stop[2];
+  int first_vb, first_pos;  // the chunk's first (view, request) and its first position
+  int pad[2];
+  float4 sc[kTile];         // per token: a * sm_scale * log2e, k, f, 2^(-k - kTop)
+  Part part[kWorkRing];
+  float red[2][kRows];      // row maxima or sums of the two token halves
+  float alpha[kRows], factor[kRows];
+};
+constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kStageBytes % 1024 == 0 && kVChunk % 1024 == 0 && kOffP2 % 1024 == 0, "swizzle-atom alignment");
+static_assert(3 * kPBlock <= kTile * 64, "a term of P^T fits the rope chunk");
+static_assert(2 * (kThreads / 32) <= 2 * kRows, "the setup's sums fit red");
+
+struct Params {
   const __nv_bfloat16 *q;
-  const uint8_t *cache;
   const float *scales;
   const int32_t *qo_indptr, *row_len, *subpage_table;
+  __nv_bfloat16 *segm_out;
+  float *segm_max, *segm_sum;
   __nv_bfloat16 *out;
   float *lse;
   int *err;
   int64_t num_cache_rows;
-  float scale_log2;
-  int log_g, page_size, subpage_stride, num_reqs, num_rows, num_heads, num_views, max_qlen;
+  long long wait_budget, drain_budget;
+  float score_scale;        // sm_scale * log2(e)
+  int subpage_stride, page_size, log_g, num_heads, num_segments, row_blocks, num_reqs, num_views, max_qlen, num_rows,
+      max_len;
 };
 
-__device__ __forceinline__ float code_value(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half *>(&h));
+__device__ __forceinline__ void note(int *err, int code) { atomicCAS(err, 0, code); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__global__ void __launch_bounds__(256) decode_scaled_rows(const ScaledParams p) {
+// D (+)= A . B^T, kind::f8f6f4; A in TMEM / in shared memory.
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Shared-memory matrix descriptor (fields as sdesc_sw128's); layout: 2 = 128-,
+// 4 = 64-, 6 = 32-byte swizzle; sbo: bytes from one 8-row group to the next.
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t sbo, uint64_t layout) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) |
+         (layout << 61);
+}
+// Instruction descriptor: D f32; A e4m3; B e4m3 (0) or e5m2 (1); A's major-ness.
+__host__ __device__ constexpr uint32_t idesc_f8(int n, int b_fmt, int a_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(b_fmt) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// 32 lanes x 16 columns (thread i: lane base + i), without the wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack4_e5m2(float a, float b, float c, float d) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2)) |
+         (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E5M2)) << 16);
+}
+// x to three significant bits, halves away from zero (what is left goes to the
+// second term, or to the row's correction).
+__device__ __forceinline__ float round3(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x100000u) & 0xffe00000u);
+}
+
+// ---- work
+
+// Longest visible length of a request's rows in a view; 0 when its qo_indptr
+// entries are inconsistent.
+__device__ __forceinline__ int request_len(const Params &p, int v, int b, int &qlen) {
+  const int q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
+  qlen = 0;
+  if (q0 < 0 || q1 < q0 || q1 > p.num_rows || q1 - q0 > p.max_qlen) return 0;
+  qlen = q1 - q0;
+  const int32_t *rl = p.row_len + static_cast<int64_t>(v) * p.num_rows;
+  int len = 0;
+  for (int t0 = q0; t0 < q1; t0 += 8) {
+    int l[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) l[k] = t0 + k < q1 ? rl[t0 + k] : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) len = max(len, min(max(l[k], 0), p.max_len));
+  }
+  return len;
+}
+// Positions of a (view, request): for each of its row blocks one overhead and
+// its tiles, nothing when no row sees a token.
+__device__ __forceinline__ int positions(const Params &p, int vb, int &tiles) {
+  int qlen;
+  const int len = request_len(p, vb / p.num_reqs, vb % p.num_reqs, qlen);
+  tiles = (len + kTile - 1) / kTile;
+  return tiles > 0 ? (qlen * p.num_heads + kRows - 1) / kRows * (tiles + 1) : 0;
+}
+
+struct Split {
+  int total, n_chunks, chunk, lo, hi;  // positions; this CTA's chunk [lo, hi)
+};
+__device__ __forceinline__ int chunk_of(const Split &s, int x) {
+  return static_cast<int>((static_cast<long long>(x + 1) * s.n_chunks - 1) / s.total);
+}
+
+// The whole CTA: total positions, the chunk of this CTA, and the (view,
+// request) in which it starts (misc.first_vb, misc.first_pos).
+__device__ Split make_split(const Params &p, Misc &misc) {
+  const int n_vb = p.num_views * p.num_reqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  int *warp_sum = reinterpret_cast<int *>(misc.red), *warp_max = warp_sum + kWarps;
+  int mine = 0, pos = 0, t_max = 0;
+  for (int vb = tid; vb < n_vb; vb += kThreads) {
+    int t;
+    pos = positions(p, vb, t);
+    mine += pos;
+    t_max = max(t_max, t);
+  }
+  const int sum = __reduce_add_sync(0xffffffffu, mine);
+  t_max = __reduce_max_sync(0xffffffffu, t_max);
+  if (lane == 0) {
+    warp_sum[warp] = sum;
+    warp_max[warp] = t_max;
+  }
+  __syncthreads();
+  Split s;
+  s.total = 0;
+  t_max = 0;
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    s.total += warp_sum[w];
+    t_max = max(t_max, warp_max[w]);
+  }
+  // chunks of at least `need` tiles meet a unit at most S times
+  const int S = p.num_segments, need = S > 1 ? max((t_max + S - 2) / (S - 1), 1) : 1;
+  s.n_chunks = s.total > 0 ? min(static_cast<int>(gridDim.x), max(s.total / need, 1)) : 1;
+  s.chunk = blockIdx.x;
+  s.lo = static_cast<int>(static_cast<long long>(s.chunk) * s.total / s.n_chunks);
+  s.hi = static_cast<int>(static_cast<long long>(s.chunk + 1) * s.total / s.n_chunks);
+  if (s.chunk == s.n_chunks - 1) s.hi = s.total + 1;  // units without tiles at the very end
+  // the one with first position < lo <= end, or the very first: by one scan when
+  // every thread has one (view, request), else by scans of 352
+  int carry = 0;
+  for (int v0 = 0; v0 < n_vb && s.chunk < s.n_chunks; v0 += kThreads) {
+    const int vb = v0 + tid;
+    if (n_vb > kThreads) {
+      int t;
+      pos = vb < n_vb ? positions(p, vb, t) : 0;
+      const int part = __reduce_add_sync(0xffffffffu, pos);
+      __syncthreads();
+      if (lane == 0) warp_sum[warp] = part;
+      __syncthreads();
+      before = carry;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        carry += warp_sum[w];
+      }
+    }
+    int x = vb < n_vb ? pos : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int end = before + x, start = end - (vb < n_vb ? pos : 0);
+    if (vb < n_vb && end >= s.lo && (vb == 0 || start < s.lo)) {
+      misc.first_vb = vb;
+      misc.first_pos = start;
+    }
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_decode_scaled_kernel(const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r,
+                             const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Misc &misc = *reinterpret_cast<Misc *>(smem + kOffMisc);
+  const uint32_t s_base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.num_segments, P = p.page_size;
+
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&misc.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&misc.full[i]), 1);
+      mbar_init(smem_u32(&misc.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&misc.s_full), 1);
+    mbar_init(smem_u32(&misc.s_free), kSoftWarps);
+    mbar_init(smem_u32(&misc.p_full), kSoftWarps);
+    mbar_init(smem_u32(&misc.o_done), 1);
+    mbar_init(smem_u32(&misc.q_full), kSoftWarps);
+    mbar_init(smem_u32(&misc.sc_full), 1);
+    mbar_init(smem_u32(&misc.sc_free), kSoftWarps);
+    mbar_init(smem_u32(&misc.fin), 1);
+    for (int i = 0; i < kWorkRing; ++i) {
+      mbar_init(smem_u32(&misc.work_full[i]), 1);
+      mbar_init(smem_u32(&misc.work_empty[i]), kSoftWarps + 2);
+    }
+    misc.abort = 0;
+    misc.first_vb = misc.first_pos = 0;
+    fence_mbar_init();
+  }
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t items = static_cast<int64_t>(p.num_views) * p.num_rows * p.num_heads;
-  const int total = p.qo_indptr[p.num_reqs];
-  if (p.qo_indptr[0] != 0 || total < 0 || total > p.num_rows) {
-    if (threadIdx.x == 0) atomicCAS(p.err, 0, MLA_DEV_BAD_INDPTR);
-    return;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Split split = make_split(p, misc);
+  __syncthreads();
+  const uint32_t tmem = misc.tmem_base;
+  volatile int *abort_flag = &misc.abort;
+  const long long budget = p.wait_budget;
+  bool ok = true;
+  auto wait = [&](const uint64_t &bar, uint32_t parity) {
+    if (ok && !mbar_wait(smem_u32(&bar), parity & 1u, abort_flag, budget)) {
+      *abort_flag = 1;
+      note(p.err, MLA_DEV_WAIT_TIMEOUT);
+      ok = false;
+    }
+    return ok;
+  };
+
+  if (warp == kTmaWarp) {
+    // ================================================ work and tile copies
+    const uint64_t policy = l2_policy_evict_first();
+    const int run = min(P, 32);       // rows of a copy: one page, or 32 rows of one
+    const int run_v = run * 128, run_r = run * 64;
+    uint32_t armed = 0, armed_par = 0;  // stages with a copy possibly in flight (for the exit path)
+    uint32_t g = 0;
+    int vb = misc.first_vb, rb = 0, pos = misc.first_pos, u_pos = pos;
+    int tiles = 0, len = 0, q0 = 0, qlen = 0, my_len = 0, loaded = -1;
+    bool clipped = false, bad = false;
+    const int n_vb = p.num_views * p.num_reqs;
+    for (uint32_t k = 0;; ++k) {
+      Part &e = misc.part[k % kWorkRing];
+      if (lane == 0) wait(misc.work_empty[k % kWorkRing], (k / kWorkRing) ^ 1u);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      bool found = false;
+      int t_lo = 0, t_hi = 0, seg = 0, fill_hi = S;
+      while (ok && split.chunk < split.n_chunks && vb < n_vb) {
+        const int v = vb / p.num_reqs, b = vb - v * p.num_reqs;
+        if (loaded != vb) {  // the request's rows: lane t holds the length of row t (t < 32)
+          q0 = p.qo_indptr[b];
+          const int q1 = p.qo_indptr[b + 1];
+          bad = q0 < 0 || q1 < q0 || q1 > p.num_rows || q1 - q0 > p.max_qlen;
+          qlen = bad ? 0 : q1 - q0;
+          const int32_t *rl = p.row_len + static_cast<int64_t>(v) * p.num_rows + q0;
+          my_len = lane < qlen ? rl[lane] : 0;
+          len = 0;
+          clipped = false;
+          for (int t = lane; t < qlen; t += 32) {
+            const int l = t == lane ? my_len : rl[t];
+            clipped |= l > p.max_len;
+            len = max(len, min(max(l, 0), p.max_len));
+          }
+          len = __reduce_max_sync(0xffffffffu, len);
+          clipped = __any_sync(0xffffffffu, clipped);
+          tiles = (len + kTile - 1) / kTile;
+          loaded = vb;
+          if (lane == 0 && bad) note(p.err, MLA_DEV_BAD_INDPTR);
+          if (lane == 0 && clipped) note(p.err, MLA_DEV_LEN_BOUND);
+          // row blocks that end before the chunk
+          if (tiles > 0 && u_pos < split.lo) {
+            rb = (split.lo - u_pos) / (tiles + 1);
+            u_pos += rb * (tiles + 1);
+          }
+        }
+        const int blocks = (qlen * p.num_heads + kRows - 1) / kRows;
+        if (rb >= blocks) {
+          ++vb;
+          rb = 0;
+          continue;
+        }
+        if (u_pos >= split.hi) break;
+        const int here = u_pos, start = here + (tiles > 0 ? 1 : 0), end = start + tiles;
+        if (start >= split.hi) break;
+        u_pos = end;
+        const int this_rb = rb++;
+        if (tiles == 0) {
+          if (here < split.lo) continue;
+        } else if (S == 1) {
+          if (start < split.lo) continue;
+          t_hi = tiles;
+        } else {
+          const int lo = max(split.lo, start), hi = min(split.hi, end);
+          if (lo >= hi) continue;
+          t_lo = lo - start;
+          t_hi = hi - start;
+          seg = split.chunk - chunk_of(split, start);
+          fill_hi = end <= split.hi ? S : seg + 1;
+        }
+        found = true;
+        const int row_begin = this_rb * kRows;
+        const int n_rows = min(kRows, qlen * p.num_heads - row_begin);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = lane + 32 * h, t = (row_begin + c) / p.num_heads;
+          int l = __shfl_sync(0xffffffffu, my_len, t < 32 ? t : 0);
+          if (t >= 32 && c < n_rows) l = p.row_len[static_cast<int64_t>(v) * p.num_rows + q0 + t];
+          e.lens[c] = c < n_rows ? min(max(l, 0), p.max_len) : 0;
+        }
+        if (lane == 0) {
+          e.stop = 0;
+          e.b = vb;
+          e.rb = this_rb;
+          e.seg = seg;
+          e.fill_hi = fill_hi;
+          e.q_row = q0 * p.num_heads + row_begin;
+          e.row_base = (v * p.num_rows + q0) * p.num_heads + row_begin;
+          e.n_rows = n_rows;
+          e.seg_lo = t_lo * kTile;
+          e.seg_hi = min(t_hi * kTile, len);
+          e.n_tiles = t_hi - t_lo;
+        }
+        break;
+      }
+      __syncwarp();
+      if (!found) {
+        if (lane == 0) {
+          e.stop = 1;
+          mbar_arrive(smem_u32(&misc.work_full[k % kWorkRing]));
+        }
+        break;
+      }
+      if (lane == 0) mbar_arrive(smem_u32(&misc.work_full[k % kWorkRing]));
+      if (t_hi == t_lo) continue;
+      const int seg_lo = t_lo * kTile, seg_hi = min(t_hi * kTile, len);
+      const int32_t *pages = p.subpage_table + static_cast<int64_t>(vb) * p.subpage_stride;
+      const int last_page = (seg_hi - 1) / P;
+      int win = seg_lo / P;             // lane l holds the id of page win + l
+      int32_t win_id = win + lane <= last_page ? pages[win + lane] : -1;
+      for (int tok0 = seg_lo; tok0 < seg_hi; tok0 += kTile, ++g) {
+        const int n_valid = min(kTile, seg_hi - tok0);
+        const int boxes = (n_valid + run - 1) / run, ops = boxes * 5;
+        const uint32_t st = g % kStages;
+        if ((tok0 + n_valid - 1) / P >= win + 32) {
+          win = tok0 / P;
+          win_id = win + lane <= last_page ? pages[win + lane] : -1;
+        }
+        if (lane == 0) wait(misc.empty[st], (g / kStages) ^ 1u);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&misc.full[st]), dst = s_base + st * kStageBytes;
+        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * run * 576);
+        __syncwarp();
+        for (int o0 = 0; o0 < ops; o0 += 32) {  // copy o: box o / 5, chunk o % 5 (4: rope)
+          const int o = o0 + lane, box = o / 5, c = o - 5 * box, t = tok0 + box * run;
+          const int32_t id = __shfl_sync(0xffffffffu, win_id, o < ops ? t / P - win : 0);
+          if (o < ops) {
+            int32_t row = static_cast<int32_t>(p.num_cache_rows);  // past the last row: zeros
+            if (id < 0 || (static_cast<int64_t>(id) + 1) * P > p.num_cache_rows) note(p.err, MLA_DEV_BAD_SUBPAGE);
+            else row = id * P + t % P;
+            if (c < 4) tma_load_2d(dst + c * kVChunk + box * run_v, &tm_v, bar, c * 128, row, policy);
+            else tma_load_2d(dst + kRopeOff + box * run_r, &tm_r, bar, 512, row, policy);
+          }
+        }
+        armed |= 1u << st;
+        armed_par = (armed_par & ~(1u << st)) | (((g / kStages) & 1u) << st);
+      }
+    }
+    if (lane == 0 && (!ok || *abort_flag)) {  // let the copies land before the memory is released
+      const volatile int never = 0;
+      for (int st = 0; st < kStages; ++st)
+        if (armed & (1u << st)) mbar_wait(smem_u32(&misc.full[st]), (armed_par >> st) & 1u, &never, p.drain_budget);
+    }
+  } else if (warp == kMmaWarp) {
+    // ================================================ products
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_f8(kTile, 0, 0), id_pv = idesc_f8(kRows, 1, 1);
+      const uint64_t d_k = sdesc(s_base, 1024, 2), d_rope = sdesc(s_base + kRopeOff, 512, 4);
+      // V^T: a 128-byte row holds all of M, so only the step between 8-token groups counts
+      const uint64_t d_v = d_k | (static_cast<uint64_t>(kVChunk >> 4) << 16);
+      const uint64_t d_p1 = sdesc(s_base + kRopeOff, 256, 6), d_p2 = sdesc(s_base + kOffP2, 256, 6);
+      uint32_t gq = 0, gp = 0, kq = 0, k = 0;  // tiles of QK / PV issued, queries, parts
+      uint32_t first_bits = 0, steps = 0;      // per stage: first tile of its part, 32-token steps (4 bits)
+      int left = 0, at = 0, lo = 0, hi = 0;
+      bool q_ready = false, no_more = false;
+      long long idle = clock64();
+      while (true) {
+        bool progress = true;
+        if (gp < gq && mbar_test(smem_u32(&misc.p_full), gp & 1u)) {
+          tc_fence_after();
+          const uint32_t st = gp % kStages;
+          const uint64_t off = static_cast<uint64_t>(st) * (kStageBytes >> 4);
+          const bool first = (first_bits >> st) & 1u;
+          const int n32 = static_cast<int>((steps >> (4 * st)) & 15u);
+          for (int kk = 0; kk < n32; ++kk) {
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+              const uint64_t dv = d_v + off + static_cast<uint64_t>(blk) * (kVChunk >> 4) + kk * (4096 >> 4);
+              mma8_ss(tmem + kTmemO + blk * kRows, dv, d_p1 + off + kk * (kPBlock >> 4), id_pv, kk > 0 || !first);
+              mma8_ss(tmem + kTmemO + blk * kRows, dv, d_p2 + kk * (kPBlock >> 4), id_pv, 1u);
+            }
+          }
+          umma_commit(smem_u32(&misc.o_done));
+          umma_commit(smem_u32(&misc.empty[st]));
+          ++gp;
+        } else if (left == 0 && !no_more) {
+          const uint32_t ws = k % kWorkRing;
+          if (mbar_test(smem_u32(&misc.work_full[ws]), (k / kWorkRing) & 1u)) {
+            const Part &e = misc.part[ws];
+            no_more = e.stop != 0;
+            left = no_more ? 0 : e.n_tiles;
+            lo = e.seg_lo;
+            hi = e.seg_hi;
+            at = 0;
+            q_ready = false;
+            if (!no_more) mbar_arrive(smem_u32(&misc.work_empty[ws]));
+            ++k;
+          } else {
+            progress = false;
+          }
+        } else if (left > 0 && !q_ready) {
+          if (mbar_test(smem_u32(&misc.q_full), kq & 1u)) {
+            ++kq;
+            q_ready = true;
+          } else {
+            progress = false;
+          }
+        } else if (left > 0 && gq - gp < kStages && (gq == 0 || mbar_test(smem_u32(&misc.s_free), (gq - 1) & 1u)) &&
+                   mbar_test(smem_u32(&misc.full[gq % kStages]), (gq / kStages) & 1u)) {
+          tc_fence_after();
+          const uint32_t st = gq % kStages;
+          const uint64_t off = static_cast<uint64_t>(st) * (kStageBytes >> 4);
+#pragma unroll
+          for (int i = 0; i < 18; ++i) {
+            const uint64_t db = off + (i < 16 ? d_k + (i / 4) * (kVChunk >> 4) + (i % 4) * 2 : d_rope + (i - 16) * 2);
+            mma8_ts(tmem + kTmemS, tmem + kTmemQ + 8 * i, db, id_qk, i > 0);
+          }
+          umma_commit(smem_u32(&misc.s_full));
+          const int n_valid = min(kTile, hi - (lo + at * kTile));
+          first_bits = (first_bits & ~(1u << st)) | (static_cast<uint32_t>(at == 0) << st);
+          steps = (steps & ~(15u << (4 * st))) | (static_cast<uint32_t>((n_valid + 31) / 32) << (4 * st));
+          ++gq;
+          ++at;
+          --left;
+        } else {
+          progress = false;
+        }
+        if (no_more && left == 0 && gp == gq) break;
+        if (progress) {
+          idle = clock64();
+        } else if (*abort_flag || clock64() - idle > budget) {
+          *abort_flag = 1;
+          note(p.err, MLA_DEV_WAIT_TIMEOUT);
+          break;
+        }
+      }
+      umma_commit(smem_u32(&misc.fin));  // every product issued so far has retired
+      const volatile int never = 0;
+      mbar_wait(smem_u32(&misc.fin), 0, &never, p.drain_budget);
+    }
+  } else if (warp == kScaleWarp) {
+    // ================================================ the tiles' scales
+    uint32_t g = 0;
+    for (uint32_t k = 0;; ++k) {
+      const uint32_t ws = k % kWorkRing;
+      wait(misc.work_full[ws], k / kWorkRing);
+      if (!__all_sync(0xffffffffu, ok) || misc.part[ws].stop) break;
+      const Part &e = misc.part[ws];
+      const int seg_lo = e.seg_lo, seg_hi = e.seg_hi, n_tiles = e.n_tiles;
+      const int32_t *pages = p.subpage_table + static_cast<int64_t>(e.b) * p.subpage_stride;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&misc.work_empty[ws]));
+      // scale of token t, one tile ahead of its use; a page outside the cache is zeros
+      auto load = [&](int t) {
+        if (t >= seg_hi) return 1.0f;
+        const int id = pages[t / P];
+        if (id < 0 || (static_cast<int64_t>(id) + 1) * P > p.num_cache_rows) return 1.0f;
+        return p.scales[(static_cast<int64_t>(id) * P + t % P) >> p.log_g];
+      };
+      float a[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) a[i] = n_tiles > 0 ? load(seg_lo + lane + 32 * i) : 1.0f;
+      for (int i = 0; i < n_tiles; ++i, ++g) {
+        float next[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) next[j] = load(seg_lo + (i + 1) * kTile + lane + 32 * j);
+        wait(misc.sc_free, g ^ 1u);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const float s = fminf(fmaxf(a[j], 7.888609052210118e-31f), 1.329227995784916e36f);  // [2^-100, 2^120]
+          const uint32_t u = __float_as_uint(s), ex = u >> 23;
+          misc.sc[lane + 32 * j] = make_float4(s * p.score_scale, static_cast<float>(static_cast<int>(ex) - 127),
+                                               __uint_as_float((u & 0x7fffffu) | 0x3f800000u),
+                                               __uint_as_float((254u - ex) << 23) * kInvTop);
+          a[j] = next[j];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&misc.sc_full));
+      }
+    }
+  } else {
+    // ================================================ queries, softmax, epilogue
+    const int wq = warp & 3, h = warp >> 2, term = lane >> 4;
+    const int row = 16 * wq + (lane & 15);       // this thread's query row
+    const int c0 = 48 * h + 24 * term;           // its 24 tokens of a tile
+    const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
+    const bool owner = h == 0 && term == 0;      // of the row's statistics
+    const float w_mine = term ? 0.03125f : 1.0f, w_other = term ? 1.0f : 0.03125f;
+    uint32_t g = 0;
+    float q_scale = 1.0f;                        // q = q_scale * (q1 + q2 / 32); NaN for a row that is not finite
+
+    // A part's queries into TMEM.  Thread: 144 dims of its row, from
+    // 288 h + 144 term; both terms of them, one of which goes to the partner lane.
+    auto load_queries = [&](const Part &e) {
+      uint4 v[18];
+      const bool live = row < e.n_rows;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(e.q_row) + row) * 576) + 36 * h +
+                         18 * term;
+#pragma unroll
+      for (int i = 0; i < 18; ++i) v[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 18; ++i) {
+        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      if (term == 0) misc.red[h][row] = __uint_as_float(top);
+      named_bar_sync(kBarSoft, kSoftThreads);
+      top = max(__float_as_uint(misc.red[0][row]), __float_as_uint(misc.red[1][row]));
+      const bool finite = top < 0x7f80u;
+      const int ex = finite ? max(static_cast<int>(top >> 7), 27) : 127;  // exponent + 127, at least 2^-100
+      const float mult = finite ? __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - ex) << 23) : 0.0f;
+      q_scale = finite ? __uint_as_float(static_cast<uint32_t>(ex - 7) << 23) : NAN;
+      if (!live) q_scale = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 9; ++c) {  // 16 dims: four words of each term
+        uint32_t t1[4], t2[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 &u = v[2 * c + (j >> 1)];
+          const uint32_t a = (j & 1) ? u.z : u.x, b = (j & 1) ? u.w : u.y;
+          float x[4] = {__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
+                        __uint_as_float(b & 0xffff0000u)};
+          uint32_t w1 = 0, w2 = 0;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const float y0 = finite ? x[2 * s] * mult : 0.0f, y1 = finite ? x[2 * s + 1] * mult : 0.0f;
+            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+            const __nv_fp8x2_storage_t lo =
+                __nv_cvt_float2_to_fp8x2(make_float2((y0 - f.x) * 32.0f, (y1 - f.y) * 32.0f), __NV_SATFINITE, __NV_E4M3);
+            w1 |= static_cast<uint32_t>(hi) << (16 * s);
+            w2 |= static_cast<uint32_t>(lo) << (16 * s);
+          }
+          t1[j] = w1;
+          t2[j] = w2;
+        }
+        uint32_t got[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) got[j] = __shfl_xor_sync(0xffffffffu, term ? t1[j] : t2[j], 16);
+        const uint32_t col = tmem + kTmemQ + lanes + 72 * h + 4 * c;
+        tmem_st4(col, term ? got[0] : t1[0], term ? got[1] : t1[1], term ? got[2] : t1[2], term ? got[3] : t1[3]);
+        tmem_st4(col + 36, term ? t2[0] : got[0], term ? t2[1] : got[1], term ? t2[2] : got[2], term ? t2[3] : got[3]);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&misc.q_full));
+    };
+    // The softmax warps' shared decision whether part k is to be done.
+    auto next_part = [&](uint32_t k) {
+      wait(misc.work_full[k % kWorkRing], k / kWorkRing);
+      named_bar_sync(kBarSoft, kSoftThreads);
+      if (threadIdx.x == 0) misc.stop[k & 1u] = *abort_flag != 0 || misc.part[k % kWorkRing].stop;
+      named_bar_sync(kBarSoft, kSoftThreads);
+      return misc.stop[k & 1u] == 0;
+    };
+
+    bool more = next_part(0);
+    if (more && misc.part[0].n_tiles > 0) load_queries(misc.part[0]);
+    for (uint32_t k = 0; more; ++k) {
+      const Part &e = misc.part[k % kWorkRing];
+      const int n_rows = e.n_rows, n_tiles = e.n_tiles, seg_lo = e.seg_lo, seg_hi = e.seg_hi, len = e.lens[row];
+      const bool active = 16 * wq < n_rows;  // rows of the unit in this warp's quarter
+      float m_ref = -INFINITY, l = 0.0f, w_sum = 0.0f, w_lost = 0.0f;
+
+      for (int i = 0; i < n_tiles; ++i, ++g) {
+        const int tok0 = seg_lo + i * kTile, n_valid = min(kTile, seg_hi - tok0);
+        const uint32_t stage = s_base + (g % kStages) * kStageBytes;
+        wait(misc.s_full, g);
+        tc_fence_after();
+        float x[24];
+        uint32_t nan_tokens = 0;
+        if (active) {
+          uint32_t v[48];
+          const uint32_t col = tmem + kTmemS + lanes + 48 * h;
+          tmem_ld16(col, v);
+          tmem_ld16(col + 16, v + 16);
+          tmem_ld16(col + 32, v + 32);
+          tmem_wait_ld();
+          // lane i has q1 . k of its warp's 48 tokens, lane i + 16 q2 . k: each adds up half of them
+#pragma unroll
+          for (int j = 0; j < 24; ++j) {
+            const float mine = __uint_as_float(term ? v[24 + j] : v[j]);
+            const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(term ? v[j] : v[24 + j]), 16);
+            x[j] = fmaf(mine, w_mine, other * w_other);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
+        wait(misc.sc_full, g);
+        const int seen = min(n_valid, len - tok0);  // tokens this row sees of the tile
+        bool exceed = false;
+        float top = -INFINITY;
+        if (active) {
+#pragma unroll
+          for (int j = 0; j < 24; ++j) {
+            const float4 s = misc.sc[c0 + j];
+            if (x[j] != x[j]) nan_tokens |= 1u << j;
+            x[j] = c0 + j < seen ? fmaf(x[j] * q_scale, s.x, s.y) : -INFINITY;
+            top = fmaxf(top, x[j]);
+          }
+          exceed = top > m_ref + kThreshold;
+        }
+        bool rescale = false;
+        if (named_bar_red_or(kBarSoft, kSoftThreads, exceed)) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          if (term == 0) misc.red[h][row] = top;
+          named_bar_sync(kBarSoft, kSoftThreads);
+          top = fmaxf(misc.red[0][row], misc.red[1][row]);
+          float alpha = 1.0f;
+          if (top > m_ref + kThreshold) {
+            alpha = ex2(m_ref - top);  // 0 when m_ref is -inf
+            m_ref = top;
+            l *= alpha;
+            w_sum *= alpha;
+            w_lost *= alpha;
+          }
+          if (owner) misc.alpha[row] = alpha;
+          rescale = named_bar_red_or(kBarSoft, kSoftThreads, alpha != 1.0f);
+        }
+        // weights: first term in place, second in y
+        uint32_t p1[6], p2[6];
+        if (active) {
+          const float ref = m_ref - kTop;
+          float l_t = 0.0f, w_t = 0.0f, lost_t = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 6; ++q) {
+            float a[4], b[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int j = 4 * q + u;
+              const float2 s = *reinterpret_cast<const float2 *>(&misc.sc[c0 + j].z);
+              const float ej = x[j] == -INFINITY ? 0.0f : ex2(x[j] - ref);
+              const float w = ej * s.x;
+              l_t = fmaf(ej, s.y, l_t);
+              w_t += w;
+              a[u] = round3(w);
+              const float rest = w - a[u];
+              b[u] = round3(rest);
+              lost_t += rest - b[u];
+            }
+            p1[q] = pack4_e5m2(a[0], a[1], a[2], a[3]);
+            p2[q] = pack4_e5m2(b[0], b[1], b[2], b[3]);
+          }
+          l += l_t;
+          w_sum += w_t;
+          w_lost += lost_t;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&misc.sc_free));
+        // the previous tile's PV has read the second term's buffer, and O^T is at rest
+        if (g > 0) wait(misc.o_done, g - 1);
+        if (rescale && i > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int blk = 0; blk < 4; ++blk) {
+            const uint32_t taddr = tmem + lanes + kTmemO + blk * kRows + 32 * h;
+            uint32_t ov[32];
+            tmem_ld32(taddr, ov);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * misc.alpha[32 * h + j]);
+            tmem_st32(taddr, ov);
+          }
+        }
+        if (active) {
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            const int c = c0 + 8 * q;
+            const uint32_t off = (c >> 5) * kPBlock + row * 32 + ((((c >> 4) ^ (row >> 2)) & 1) << 4) + (c & 8);
+            st_shared_v2(stage + kRopeOff + off, p1[2 * q], p1[2 * q + 1]);
+            st_shared_v2(s_base + kOffP2 + off, p2[2 * q], p2[2 * q + 1]);
+          }
+          // a token with a NaN code: the rows that see it are NaN by their sums, and its
+          // values must not meet the zero weights of the others
+          while (nan_tokens != 0) {
+            const int tok = c0 + __ffs(nan_tokens) - 1;
+            nan_tokens &= nan_tokens - 1;
+            for (int c = 0; c < 32; ++c)
+              st_shared_v4(stage + (c >> 3) * kVChunk + tok * 128 + (c & 7) * 16, 0, 0, 0, 0);
+          }
+        }
+        // rows of the last 32-token step past the part's end hold anything: zeros
+        for (int c = threadIdx.x; c < (((n_valid + 31) & ~31) - n_valid) * 32; c += kSoftThreads)
+          st_shared_v4(stage + ((c & 31) >> 3) * kVChunk + (n_valid + (c >> 5)) * 128 + (c & 7) * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&misc.p_full));
+      }
+
+      // ---- the rows' sums, then the next part's queries (its S overlaps this
+      // part's last PV and the epilogue), then O^T
+      const int seg = e.seg, fill_hi = e.fill_hi, e_b = e.b, e_rb = e.rb;
+      const int64_t row_base = e.row_base;
+      named_bar_sync(kBarSoft, kSoftThreads);  // alpha and red have been read
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      w_sum += __shfl_xor_sync(0xffffffffu, w_sum, 16);
+      w_lost += __shfl_xor_sync(0xffffffffu, w_lost, 16);
+      if (h == 1 && term == 0) {
+        misc.red[0][row] = l;
+        misc.red[1][row] = w_sum;
+        misc.alpha[row] = w_lost;
+      }
+      named_bar_sync(kBarSoft, kSoftThreads);
+      if (owner) {
+        l += misc.red[0][row];
+        w_sum += misc.red[1][row];
+        w_lost += misc.alpha[row];
+        const bool none = l == 0.0f;
+        const float fix = w_sum / (w_sum - w_lost);
+        misc.factor[row] = none ? 0.0f : (S == 1 ? fix * kInvTop / l : fix * kInvTop);
+        if (ok && row < n_rows) {
+          const int64_t r = row_base + row;
+          if (S == 1) {
+            p.lse[r] = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+          } else {
+            // a NaN row keeps a finite maximum, so that the merge looks at its sum
+            p.segm_max[r * S + seg] = none ? -INFINITY : (m_ref == -INFINITY ? 0.0f : m_ref);
+            p.segm_sum[r * S + seg] = l;
+            for (int s = seg + 1; s < fill_hi; ++s) {
+              p.segm_max[r * S + s] = -INFINITY;
+              p.segm_sum[r * S + s] = 0.0f;
+            }
+          }
+        }
+      }
+      more = next_part(k + 1);
+      const bool was_ok = ok;
+      if (more && misc.part[(k + 1) % kWorkRing].n_tiles > 0) load_queries(misc.part[(k + 1) % kWorkRing]);
+      else named_bar_sync(kBarSoft, kSoftThreads);
+      if (n_tiles > 0) {
+        wait(misc.o_done, g - 1);
+        tc_fence_after();
+        const int n_cols = n_rows - 32 * h;  // rows of the unit among this warp's 32 columns
+#pragma unroll 1
+        for (int blk = 0; blk < 4 && n_cols > 0; ++blk) {
+          uint32_t ov[32];
+          tmem_ld32(tmem + lanes + kTmemO + blk * kRows + 32 * h, ov);
+          if (!ok || !was_ok || *abort_flag != 0) continue;
+          const int dim = blk * 128 + 32 * wq + lane;
+          if (S == 1) {
+            __nv_bfloat16 *o = p.out + (row_base + 32 * h) * 512 + dim;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float f = misc.factor[32 * h + j];
+              if (j < n_cols)
+                o[static_cast<int64_t>(j) * 512] = __float2bfloat16_rn(f != 0.0f ? __uint_as_float(ov[j]) * f : 0.0f);
+            }
+          } else {
+            // partial block [8 row octets][512 dims][8 rows]: one 16-byte store per octet
+            const int64_t block = (static_cast<int64_t>(e_b) * p.row_blocks + e_rb) * S + seg;
+            uint4 *o = reinterpret_cast<uint4 *>(p.segm_out + block * (512 * kRows)) + 4 * h * 512 + dim;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (8 * q >= n_cols) break;
+              uint32_t w4[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int j = 8 * q + 2 * u;
+                const float fa = misc.factor[32 * h + j], fb = misc.factor[32 * h + j + 1];
+                w4[u] = pack_bf16(fa != 0.0f ? __uint_as_float(ov[j]) * fa : 0.0f,
+                                  fb != 0.0f ? __uint_as_float(ov[j + 1]) * fb : 0.0f);
+              }
+              o[q * 512] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            }
+          }
+        }
+        tc_fence_before();
+      } else if (S == 1 && ok) {  // no row sees a token
+        uint4 *o = reinterpret_cast<uint4 *>(p.out + row_base * 512);
+        for (int c = threadIdx.x; c < n_rows * 64; c += kSoftThreads) o[c] = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&misc.work_empty[k % kWorkRing]));
+    }
   }
-  for (int64_t item = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; item < items;
-       item += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
-    const int64_t vr = item / p.num_heads;
-    const int v = static_cast<int>(vr / p.num_rows), r = static_cast<int>(vr % p.num_rows);
-    if (r >= total) continue;
-    int lo = 0, hi = p.num_reqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.qo_indptr[mid] <= r) lo = mid;
-      else hi = mid;
-    }
-    if (p.qo_indptr[lo + 1] <= r || p.qo_indptr[lo + 1] - p.qo_indptr[lo] > p.max_qlen) {
-      if (lane == 0) atomicCAS(p.err, 0, MLA_DEV_BAD_INDPTR);
-      continue;
-    }
-    const int h = static_cast<int>(item % p.num_heads);
-    int n = p.row_len[vr];
-    const int64_t bound = static_cast<int64_t>(p.subpage_stride) * p.page_size;
-    if (n > bound) {
-      if (lane == 0) atomicCAS(p.err, 0, MLA_DEV_LEN_BOUND);
-      n = static_cast<int>(bound);
-    }
-    const int32_t *pages = p.subpage_table + (static_cast<int64_t>(v) * p.num_reqs + lo) * p.subpage_stride;
-    float q[18], acc[18];
-    const __nv_bfloat16 *qr = p.q + (static_cast<int64_t>(r) * p.num_heads + h) * 576;
-#pragma unroll
-    for (int i = 0; i < 18; ++i) {
-      q[i] = __bfloat162float(qr[lane + 32 * i]);
-      acc[i] = 0.0f;
-    }
-    float m = -INFINITY, l = 0.0f, lost = 0.0f;  // l + lost: many small weights under a large one
-    for (int j = 0; j < n; ++j) {
-      const int id = pages[j / p.page_size];
-      const int64_t row = static_cast<int64_t>(id) * p.page_size + j % p.page_size;
-      float k[18], a = 0.0f;
-      if (id < 0 || (static_cast<int64_t>(id) + 1) * p.page_size > p.num_cache_rows) {
-        if (lane == 0) atomicCAS(p.err, 0, MLA_DEV_BAD_SUBPAGE);
-#pragma unroll
-        for (int i = 0; i < 18; ++i) k[i] = 0.0f;
-      } else {
-        a = fmaxf(p.scales[row >> p.log_g], 7.888609052210118e-31f);  // 2^-100 at least
-#pragma unroll
-        for (int i = 0; i < 18; ++i) k[i] = code_value(p.cache[row * 576 + lane + 32 * i]);
-      }
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 18; ++i) s += q[i] * k[i];
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float x = s * a * p.scale_log2;
-      if (x > m) {
-        const float c = exp2f(m - x);
-        l *= c;
-        lost *= c;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] *= c;
-        m = x;
-      }
-      const float e = exp2f(x - m);
-      const float y = e + lost, sum = l + y;
-      lost = y - (sum - l);
-      l = sum;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] += e * a * k[i];
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (n > 0 ? l : 0.0f);
-    __nv_bfloat16 *o = p.out + (vr * p.num_heads + h) * 512;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
-    if (lane == 0) p.lse[vr * p.num_heads + h] = n > 0 ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
+
+std::atomic<bool> g_attr_set[64];
+std::atomic<int> g_num_sms[64];
 
 }  // namespace
 
 mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, int scale_block, cudaStream_t stream) {
   const mla_decode_args &a = *d.a;
-  ScaledParams p{};
+  const uint32_t run = a.page_size < 32 ? a.page_size : 32;
+  CUtensorMap tm_v, tm_r;
+  mla_status st = make_tmap_2d(&tm_v, a.kv_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 576,
+                               static_cast<uint64_t>(a.num_cache_rows), 128, run, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == MLA_OK)
+    st = make_tmap_2d(&tm_r, a.kv_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 576, static_cast<uint64_t>(a.num_cache_rows),
+                      64, run, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != MLA_OK) return st;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (!g_attr_set[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(mla_decode_scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_scaled smem)");
+    g_attr_set[dev].store(true, std::memory_order_relaxed);
+  }
+  int num_sms = g_num_sms[dev].load(std::memory_order_relaxed);
+  if (num_sms == 0) {
+    e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(SM count)");
+    g_num_sms[dev].store(num_sms, std::memory_order_relaxed);
+  }
+  Params p{};
   p.q = static_cast<const __nv_bfloat16 *>(a.q);
-  p.cache = static_cast<const uint8_t *>(a.kv_cache);
   p.scales = kv_scales;
   p.qo_indptr = a.qo_indptr;
   p.row_len = a.row_len;
   p.subpage_table = a.subpage_table;
+  p.segm_out = reinterpret_cast<__nv_bfloat16 *>(d.segm_out);
+  p.segm_max = d.segm_max;
+  p.segm_sum = d.segm_sum;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;
   p.err = d.err;
   p.num_cache_rows = a.num_cache_rows;
-  p.scale_log2 = static_cast<float>(static_cast<double>(a.sm_scale) * 1.4426950408889634);
-  p.log_g = __builtin_ctz(static_cast<unsigned>(scale_block));
-  p.page_size = a.page_size;
+  constexpr long long kDefaultBudget = 4000000000LL;  // ~2 s of SM clock
+  p.wait_budget = a.wait_cycles > 0 ? static_cast<long long>(a.wait_cycles) : kDefaultBudget;
+  p.drain_budget = kDefaultBudget;
+  p.score_scale = static_cast<float>(static_cast<double>(a.sm_scale) * 1.4426950408889634);
   p.subpage_stride = a.subpage_stride;
-  p.num_reqs = a.num_reqs;
-  p.num_rows = a.num_rows;
+  p.page_size = a.page_size;
+  p.log_g = __builtin_ctz(static_cast<unsigned>(scale_block));
   p.num_heads = a.num_heads;
+  p.num_segments = a.num_segments;
+  p.row_blocks = (a.max_qlen * a.num_heads + kRows - 1) / kRows;
+  p.num_reqs = a.num_reqs;
   p.num_views = a.num_views > 1 ? a.num_views : 1;
   p.max_qlen = a.max_qlen;
-  const int64_t items = static_cast<int64_t>(p.num_views) * a.num_rows * a.num_heads;
-  const int64_t ctas = (items + 7) / 8;
-  const cudaError_t e = launch_pdl(decode_scaled_rows, dim3(static_cast<unsigned>(ctas < 65536 ? ctas : 65536)), dim3(256),
-                                   0, stream, p);
+  p.num_rows = a.num_rows;
+  p.max_len = a.subpage_stride * a.page_size;
+  // positions (tiles and one per unit) are counted in int32, at the static bound
+  const int64_t units = static_cast<int64_t>(a.num_reqs) * p.num_views * p.row_blocks;
+  if (units * ((p.max_len + kTile - 1) / kTile + 1) > INT32_MAX) {
+    set_error("mla_decode_verify_scaled: %lld row blocks of up to %d tokens overflow int32 positions", (long long)units,
+              p.max_len);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  const int64_t items = units * a.num_segments;
+  const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
+  e = launch_pdl(mla_decode_scaled_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, tm_v, tm_r, p);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "decode_scaled launch");
 }
 

@@ -132,6 +132,7 @@ struct MergeLaunch {
   int num_reqs;              // segment mode
   int num_views;             // segment mode: V row views (>= 1)
   int row_blocks;            // segment mode: RB
+  int keep_nan;              // segment mode: a NaN sum gives a NaN row (0: an empty one)
   const void *part_out;
   const float *part_lse;
   void *out;

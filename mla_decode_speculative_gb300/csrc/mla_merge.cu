@@ -58,6 +58,7 @@ struct SegParams {
   int num_parts;
   int row_blocks;
   int num_reqs;
+  int keep_nan;
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -169,8 +170,9 @@ __global__ void __launch_bounds__(256, kOctCtas) merge_segment_octets(const SegP
     }
     if (lane == 0) {
       s_M[warp] = M;
-      s_inv[warp] = d > 0.0f ? 1.0f / d : 0.0f;
-      if (warp < n_rows) p.lse[grow0 + warp] = d > 0.0f ? (M + log2f(d)) * kLn2 : -INFINITY;
+      const bool spoilt = p.keep_nan != 0 && d != d;
+      s_inv[warp] = d > 0.0f ? 1.0f / d : (spoilt ? d : 0.0f);
+      if (warp < n_rows) p.lse[grow0 + warp] = d > 0.0f ? (M + log2f(d)) * kLn2 : (spoilt ? d : -INFINITY);
     }
   }
   __syncthreads();
@@ -425,6 +427,7 @@ mla_status launch_merge(const MergeLaunch &m, cudaStream_t stream) {
     p.num_parts = m.num_parts;
     p.row_blocks = m.row_blocks;
     p.num_reqs = m.num_reqs;
+    p.keep_nan = m.keep_nan;
     const int64_t ctas = static_cast<int64_t>(m.num_reqs) * m.num_views * m.row_blocks;
     if (ctas > INT32_MAX || m.row_blocks < 1) {
       set_error("mla_merge_segments: bad row-block count (%lld)", (long long)ctas);

@@ -86,10 +86,12 @@ def write_scaled(x, slots, codes, scales, G):
 
 
 def attention(q, codes, scales, G, ind, row_len, sub, P, sm):
-    """(out, lse, mass) in float64: mass[t, h, d] = sum_j softmax_j |v_jd|.  row_len [T], sub [B, width]."""
+    """(out, lse, mass, far) in float64: mass[t, h, d] = sum_j softmax_j |v_jd|; far[t, h, d] = the largest
+    softmax_j a_j of the row times sum_j |code_jd|.  row_len [T], sub [B, width]."""
     T, H, _ = q.shape
     out = np.zeros((T, H, 512))
     mass = np.zeros((T, H, 512))
+    far = np.zeros((T, H, 512))
     lse = np.full((T, H), -np.inf)
     for b in range(len(ind) - 1):
         for t in range(int(ind[b]), int(ind[b + 1])):
@@ -98,19 +100,23 @@ def attention(q, codes, scales, G, ind, row_len, sub, P, sm):
                 continue
             j = np.arange(n)
             at = sub[b, j // P].astype(np.int64) * P + j % P
-            k = CODE_VALUE[codes[at]] * np.maximum(scales[at // G].astype(np.float64), 2.0 ** -100)[:, None]
+            a = np.maximum(scales[at // G].astype(np.float64), 2.0 ** -100)
+            k = CODE_VALUE[codes[at]] * a[:, None]
             s = q[t] @ k.T * sm
             m = s.max(1, keepdims=True)
             p = np.exp(s - m)
             total = p.sum(1, keepdims=True)
             out[t] = p @ k[:, :512] / total
             mass[t] = p @ np.abs(k[:, :512]) / total
+            far[t] = (p * a / total).max(1)[:, None] * np.abs(CODE_VALUE[codes[at]][:, :512]).sum(0)[None]
             lse[t] = (m + np.log(total))[:, 0]
-    return out, lse, mass
+    return out, lse, mass, far
 
 
-def out_bound(out, mass):
+def out_bound(out, mass, far):
     """What an output may be off: each probability is held to 2^-7 of itself (two terms of three
     significant bits), a split part and the result are rounded to bf16 (2^-8 each, a part's size
-    being at most its mass), and 2^-12 of the mass covers the float32 scores and sums."""
-    return (2.0 ** -7 + 2.0 ** -8 + 2.0 ** -12) * mass + 2.0 ** -8 * np.abs(out) + 1e-37
+    being at most its mass), and 2^-12 of the mass covers the float32 scores and sums.  A weight
+    softmax_j a_j far below the row's largest is held to an absolute step instead: e5m2 ends at
+    2^-16, half of which is 2^-28 of the reference weight 2^11, and that is at most the largest one."""
+    return (2.0 ** -7 + 2.0 ** -8 + 2.0 ** -12) * mass + 2.0 ** -8 * np.abs(out) + 2.0 ** -28 * far + 1e-37
