@@ -81,8 +81,8 @@ constexpr int kPBlock = kRows * 32;               // 32 tokens of one term of P^
 constexpr int kOffP2 = kStages * kStageBytes;     // second term of P^T
 constexpr int kOffMisc = kOffP2 + 3 * kPBlock;
 constexpr int kSoftWarps = 8, kSoftThreads = 256;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kScaleWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10, kScaleWarp = 11;
+constexpr int kThreads = 384;
 constexpr uint32_t kTmemQ = 0, kTmemO = 144, kTmemS = 400, kTmemCols = 512;
 constexpr int kWorkRing = 4;
 constexpr float kThreshold = 3.0f;   // the reference moves when a weight exceeds 2^3 of it
@@ -104,17 +104,18 @@ struct Part {
 
 struct Misc {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_full, s_free, p_full, o_done, q_full, sc_full, sc_free, fin;
+  uint64_t s_full, s_free, p_full, o_done, q_full, sc_full, sc_free, fin_qk, fin_pv;
   uint64_t work_full[kWorkRing], work_empty[kWorkRing];
   uint32_t tmem_base;
   int abort;
   int stop[2];
   int first_vb, first_pos;  // the chunk's first (view, request) and its first position
   int pad[2];
-  float4 sc[kTile];         // per token: a * sm_scale * log2e, k, f, 2^(-k - kTop)
+  alignas(16) float4 sc[kTile];         // per token: a * sm_scale * log2e, k, f, 2^(-k - kTop)
   Part part[kWorkRing];
   float red[2][kRows];      // row maxima or sums of the two token halves
-  float alpha[kRows], factor[kRows];
+  float alpha[kRows];
+  alignas(16) float factor[kRows];
 };
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -161,6 +162,13 @@ __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// One lane of a converged warp.  The compiler knows that a branch on this has a
+// single thread, and keeps descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t y;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(y));
+  return y != 0;
+}
 // Shared-memory matrix descriptor (fields as sdesc_sw128's); layout: 2 = 128-,
 // 4 = 64-, 6 = 32-byte swizzle; sbo: bytes from one 8-row group to the next.
 __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t sbo, uint64_t layout) {
@@ -200,14 +208,65 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t pack4_e5m2(float a, float b, float c, float d) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2)) |
-         (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E5M2)) << 16);
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {  // NaN if one is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
-// x to three significant bits, halves away from zero (what is left goes to the
-// second term, or to the row's correction).
-__device__ __forceinline__ float round3(float x) {
-  return __uint_as_float((__float_as_uint(x) + 0x100000u) & 0xffe00000u);
+
+// A wait that did not pass at once, kept out of line: the kernel's loops have to
+// stay small enough for the instruction caches.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int *abort, long long budget, int *err) {
+  if (mbar_wait(bar, parity, abort, budget)) return true;
+  *const_cast<volatile int *>(abort) = 1;
+  note(err, MLA_DEV_WAIT_TIMEOUT);
+  return false;
+}
+
+// A thread's 24 scores to weights against the reference: the sums, and the
+// weights' two e5m2 terms.  A weight goes through f16 (2^-12 of itself): there
+// e5m2 is the upper byte, so a term's value is its codes moved up and the
+// remainder is exact.  sc: {., ., f, 2^(-k - kTop)} of the tokens; kWide: one
+// scale for each run of eight.
+template <bool kWide>
+__device__ __forceinline__ void weigh(const float (&x)[24], const float4 *sc, float ref, float &l, float &w_sum,
+                                      float &w_lost, uint32_t (&p1)[6], uint32_t (&p2)[6]) {
+  float l_t = 0.0f, w_t = 0.0f;
+  __half2 lost = __float2half2_rn(0.0f);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    float run = 0.0f;
+    float2 s0 = *reinterpret_cast<const float2 *>(&sc[8 * q].z), s1 = s0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = 8 * q + 2 * u;
+      const float e0 = ex2(x[j] - ref), e1 = ex2(x[j + 1] - ref);
+      if (kWide) {
+        run += e0 + e1;
+      } else {
+        s0 = *reinterpret_cast<const float2 *>(&sc[j].z);
+        s1 = *reinterpret_cast<const float2 *>(&sc[j + 1].z);
+        l_t = fmaf(e0, s0.y, fmaf(e1, s1.y, l_t));
+        w_t = fmaf(e0, s0.x, fmaf(e1, s1.x, w_t));
+      }
+      const __half2 w = __floats2half2_rn(e0 * s0.x, e1 * s1.x);
+      const uint32_t c1 = __nv_cvt_halfraw2_to_fp8x2(w, __NV_SATFINITE, __NV_E5M2);
+      const uint32_t v1 = __byte_perm(c1, 0, 0x1404);
+      const __half2 rest = __hsub2(w, *reinterpret_cast<const __half2 *>(&v1));
+      const uint32_t c2 = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E5M2);
+      const uint32_t v2 = __byte_perm(c2, 0, 0x1404);
+      lost = __hadd2(lost, __hsub2(rest, *reinterpret_cast<const __half2 *>(&v2)));
+      p1[2 * q + u / 2] = (u & 1) ? __byte_perm(p1[2 * q + u / 2], c1, 0x5410) : c1;
+      p2[2 * q + u / 2] = (u & 1) ? __byte_perm(p2[2 * q + u / 2], c2, 0x5410) : c2;
+    }
+    if (kWide) {
+      l_t = fmaf(run, s0.y, l_t);
+      w_t = fmaf(run, s0.x, w_t);
+    }
+  }
+  l += l_t;
+  w_sum += w_t;
+  w_lost += __low2float(lost) + __high2float(lost);
 }
 
 // ---- work
@@ -317,6 +376,7 @@ __device__ Split make_split(const Params &p, Misc &misc) {
   return s;
 }
 
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_decode_scaled_kernel(const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r,
                              const Params p) {
@@ -327,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = p.num_segments, P = p.page_size;
 
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tmem_alloc(smem_u32(&misc.tmem_base), kTmemCols);
     tmem_relinquish();
   }
@@ -343,10 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&misc.q_full), kSoftWarps);
     mbar_init(smem_u32(&misc.sc_full), 1);
     mbar_init(smem_u32(&misc.sc_free), kSoftWarps);
-    mbar_init(smem_u32(&misc.fin), 1);
+    mbar_init(smem_u32(&misc.fin_qk), 1);
+    mbar_init(smem_u32(&misc.fin_pv), 1);
     for (int i = 0; i < kWorkRing; ++i) {
       mbar_init(smem_u32(&misc.work_full[i]), 1);
-      mbar_init(smem_u32(&misc.work_empty[i]), kSoftWarps + 2);
+      mbar_init(smem_u32(&misc.work_empty[i]), kSoftWarps + 3);
     }
     misc.abort = 0;
     misc.first_vb = misc.first_pos = 0;
@@ -364,11 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long budget = p.wait_budget;
   bool ok = true;
   auto wait = [&](const uint64_t &bar, uint32_t parity) {
-    if (ok && !mbar_wait(smem_u32(&bar), parity & 1u, abort_flag, budget)) {
-      *abort_flag = 1;
-      note(p.err, MLA_DEV_WAIT_TIMEOUT);
-      ok = false;
-    }
+    if (ok && !mbar_try_wait(smem_u32(&bar), parity & 1u))
+      ok = wait_long(smem_u32(&bar), parity & 1u, &misc.abort, budget, p.err);
     return ok;
   };
 
@@ -515,92 +573,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int st = 0; st < kStages; ++st)
         if (armed & (1u << st)) mbar_wait(smem_u32(&misc.full[st]), (armed_par >> st) & 1u, &never, p.drain_budget);
     }
-  } else if (warp == kMmaWarp) {
-    // ================================================ products
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f8(kTile, 0, 0), id_pv = idesc_f8(kRows, 1, 1);
+  } else if (warp == kQkWarp) {
+    // ================================================ S = Q K^T
+    if (elect_one()) {
+      constexpr uint32_t id_qk = idesc_f8(kTile, 0, 0);
       const uint64_t d_k = sdesc(s_base, 1024, 2), d_rope = sdesc(s_base + kRopeOff, 512, 4);
-      // V^T: a 128-byte row holds all of M, so only the step between 8-token groups counts
-      const uint64_t d_v = d_k | (static_cast<uint64_t>(kVChunk >> 4) << 16);
-      const uint64_t d_p1 = sdesc(s_base + kRopeOff, 256, 6), d_p2 = sdesc(s_base + kOffP2, 256, 6);
-      uint32_t gq = 0, gp = 0, kq = 0, k = 0;  // tiles of QK / PV issued, queries, parts
-      uint32_t first_bits = 0, steps = 0;      // per stage: first tile of its part, 32-token steps (4 bits)
-      int left = 0, at = 0, lo = 0, hi = 0;
-      bool q_ready = false, no_more = false;
-      long long idle = clock64();
-      while (true) {
-        bool progress = true;
-        if (gp < gq && mbar_test(smem_u32(&misc.p_full), gp & 1u)) {
+      uint32_t g = 0, kq = 0;
+      for (uint32_t k = 0; wait(misc.work_full[k % kWorkRing], k / kWorkRing); ++k) {
+        const Part &e = misc.part[k % kWorkRing];
+        if (e.stop) break;
+        const int n_tiles = e.n_tiles;
+        mbar_arrive(smem_u32(&misc.work_empty[k % kWorkRing]));
+        if (n_tiles > 0 && !wait(misc.q_full, kq++)) break;
+        for (int i = 0; i < n_tiles && ok; ++i, ++g) {
+          const uint32_t st = g % kStages;
+          if (!wait(misc.full[st], g / kStages)) break;
+          if (g > 0 && !wait(misc.s_free, g - 1)) break;
           tc_fence_after();
-          const uint32_t st = gp % kStages;
           const uint64_t off = static_cast<uint64_t>(st) * (kStageBytes >> 4);
-          const bool first = (first_bits >> st) & 1u;
-          const int n32 = static_cast<int>((steps >> (4 * st)) & 15u);
-          for (int kk = 0; kk < n32; ++kk) {
+#pragma unroll
+          for (int c = 0; c < 18; ++c) {
+            const uint64_t db = off + (c < 16 ? d_k + (c / 4) * (kVChunk >> 4) + (c % 4) * 2 : d_rope + (c - 16) * 2);
+            mma8_ts(tmem + kTmemS, tmem + kTmemQ + 8 * c, db, id_qk, c > 0);
+          }
+          umma_commit(smem_u32(&misc.s_full));
+        }
+      }
+      umma_commit(smem_u32(&misc.fin_qk));  // every product issued so far has retired
+      const volatile int never = 0;
+      mbar_wait(smem_u32(&misc.fin_qk), 0, &never, p.drain_budget);
+    }
+  } else if (warp == kPvWarp) {
+    // ================================================ O^T += V^T P^T
+    if (elect_one()) {
+      constexpr uint32_t id_pv = idesc_f8(kRows, 1, 1);
+      // V^T: a 128-byte row holds all of M, so only the step between 8-token groups counts
+      const uint64_t d_v = sdesc(s_base, 1024, 2) | (static_cast<uint64_t>(kVChunk >> 4) << 16);
+      const uint64_t d_p1 = sdesc(s_base + kRopeOff, 256, 6), d_p2 = sdesc(s_base + kOffP2, 256, 6);
+      uint32_t g = 0;
+      for (uint32_t k = 0; wait(misc.work_full[k % kWorkRing], k / kWorkRing); ++k) {
+        const Part &e = misc.part[k % kWorkRing];
+        if (e.stop) break;
+        const int n_tiles = e.n_tiles, tokens = e.seg_hi - e.seg_lo;
+        mbar_arrive(smem_u32(&misc.work_empty[k % kWorkRing]));
+        for (int i = 0; i < n_tiles && ok; ++i, ++g) {
+          const uint32_t st = g % kStages;
+          const uint64_t off = static_cast<uint64_t>(st) * (kStageBytes >> 4);
+          const int n32 = (min(kTile, tokens - i * kTile) + 31) / 32;
+          if (!wait(misc.p_full, g)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 3; ++kk) {
+            if (kk >= n32) break;
+            const uint64_t dv = d_v + off + kk * (4096 >> 4);
 #pragma unroll
             for (int blk = 0; blk < 4; ++blk) {
-              const uint64_t dv = d_v + off + static_cast<uint64_t>(blk) * (kVChunk >> 4) + kk * (4096 >> 4);
-              mma8_ss(tmem + kTmemO + blk * kRows, dv, d_p1 + off + kk * (kPBlock >> 4), id_pv, kk > 0 || !first);
-              mma8_ss(tmem + kTmemO + blk * kRows, dv, d_p2 + kk * (kPBlock >> 4), id_pv, 1u);
+              mma8_ss(tmem + kTmemO + blk * kRows, dv + blk * (kVChunk >> 4), d_p1 + off + kk * (kPBlock >> 4), id_pv,
+                      kk > 0 || i > 0);
+              mma8_ss(tmem + kTmemO + blk * kRows, dv + blk * (kVChunk >> 4), d_p2 + kk * (kPBlock >> 4), id_pv, 1u);
             }
           }
           umma_commit(smem_u32(&misc.o_done));
           umma_commit(smem_u32(&misc.empty[st]));
-          ++gp;
-        } else if (left == 0 && !no_more) {
-          const uint32_t ws = k % kWorkRing;
-          if (mbar_test(smem_u32(&misc.work_full[ws]), (k / kWorkRing) & 1u)) {
-            const Part &e = misc.part[ws];
-            no_more = e.stop != 0;
-            left = no_more ? 0 : e.n_tiles;
-            lo = e.seg_lo;
-            hi = e.seg_hi;
-            at = 0;
-            q_ready = false;
-            if (!no_more) mbar_arrive(smem_u32(&misc.work_empty[ws]));
-            ++k;
-          } else {
-            progress = false;
-          }
-        } else if (left > 0 && !q_ready) {
-          if (mbar_test(smem_u32(&misc.q_full), kq & 1u)) {
-            ++kq;
-            q_ready = true;
-          } else {
-            progress = false;
-          }
-        } else if (left > 0 && gq - gp < kStages && (gq == 0 || mbar_test(smem_u32(&misc.s_free), (gq - 1) & 1u)) &&
-                   mbar_test(smem_u32(&misc.full[gq % kStages]), (gq / kStages) & 1u)) {
-          tc_fence_after();
-          const uint32_t st = gq % kStages;
-          const uint64_t off = static_cast<uint64_t>(st) * (kStageBytes >> 4);
-#pragma unroll
-          for (int i = 0; i < 18; ++i) {
-            const uint64_t db = off + (i < 16 ? d_k + (i / 4) * (kVChunk >> 4) + (i % 4) * 2 : d_rope + (i - 16) * 2);
-            mma8_ts(tmem + kTmemS, tmem + kTmemQ + 8 * i, db, id_qk, i > 0);
-          }
-          umma_commit(smem_u32(&misc.s_full));
-          const int n_valid = min(kTile, hi - (lo + at * kTile));
-          first_bits = (first_bits & ~(1u << st)) | (static_cast<uint32_t>(at == 0) << st);
-          steps = (steps & ~(15u << (4 * st))) | (static_cast<uint32_t>((n_valid + 31) / 32) << (4 * st));
-          ++gq;
-          ++at;
-          --left;
-        } else {
-          progress = false;
-        }
-        if (no_more && left == 0 && gp == gq) break;
-        if (progress) {
-          idle = clock64();
-        } else if (*abort_flag || clock64() - idle > budget) {
-          *abort_flag = 1;
-          note(p.err, MLA_DEV_WAIT_TIMEOUT);
-          break;
         }
       }
-      umma_commit(smem_u32(&misc.fin));  // every product issued so far has retired
+      umma_commit(smem_u32(&misc.fin_pv));
       const volatile int never = 0;
-      mbar_wait(smem_u32(&misc.fin), 0, &never, p.drain_budget);
+      mbar_wait(smem_u32(&misc.fin_pv), 0, &never, p.drain_budget);
     }
   } else if (warp == kScaleWarp) {
     // ================================================ the tiles' scales
@@ -651,23 +690,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool owner = h == 0 && term == 0;      // of the row's statistics
     const float w_mine = term ? 0.03125f : 1.0f, w_other = term ? 1.0f : 0.03125f;
     uint32_t g = 0;
-    float q_scale = 1.0f;                        // q = q_scale * (q1 + q2 / 32); NaN for a row that is not finite
+    float q_scale = 1.0f;                        // q = q_scale * (q1 + q2 / 32)
+    bool spoilt = false;                        // the query row is not finite
 
     // A part's queries into TMEM.  Thread: 144 dims of its row, from
     // 288 h + 144 term; both terms of them, one of which goes to the partner lane.
     auto load_queries = [&](const Part &e) {
-      uint4 v[18];
       const bool live = row < e.n_rows;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(e.q_row) + row) * 576) + 36 * h +
                          18 * term;
-#pragma unroll
-      for (int i = 0; i < 18; ++i) v[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < 18; ++i) {
-        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+        const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+        top = max(top, max(max(max(v.x & 0x7fffu, (v.x >> 16) & 0x7fffu), max(v.y & 0x7fffu, (v.y >> 16) & 0x7fffu)),
+                           max(max(v.z & 0x7fffu, (v.z >> 16) & 0x7fffu), max(v.w & 0x7fffu, (v.w >> 16) & 0x7fffu))));
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
       if (term == 0) misc.red[h][row] = __uint_as_float(top);
@@ -676,14 +713,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool finite = top < 0x7f80u;
       const int ex = finite ? max(static_cast<int>(top >> 7), 27) : 127;  // exponent + 127, at least 2^-100
       const float mult = finite ? __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - ex) << 23) : 0.0f;
-      q_scale = finite ? __uint_as_float(static_cast<uint32_t>(ex - 7) << 23) : NAN;
-      if (!live) q_scale = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 9; ++c) {  // 16 dims: four words of each term
+      q_scale = finite ? __uint_as_float(static_cast<uint32_t>(ex - 7) << 23) : 0.0f;
+      spoilt = !finite;
+#pragma unroll 3
+      for (int c = 0; c < 9; ++c) {  // 16 dims, read again from L1: four words of each term
         uint32_t t1[4], t2[4];
+        uint4 v[2];
+        v[0] = live ? src[2 * c] : make_uint4(0, 0, 0, 0);
+        v[1] = live ? src[2 * c + 1] : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint4 &u = v[2 * c + (j >> 1)];
+          const uint4 &u = v[j >> 1];
           const uint32_t a = (j & 1) ? u.z : u.x, b = (j & 1) ? u.w : u.y;
           float x[4] = {__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
                         __uint_as_float(b & 0xffff0000u)};
@@ -723,27 +763,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       return misc.stop[k & 1u] == 0;
     };
 
-    bool more = next_part(0);
-    if (more && misc.part[0].n_tiles > 0) load_queries(misc.part[0]);
-    for (uint32_t k = 0; more; ++k) {
+    // Part k's queries go into TMEM before part k - 1's O^T is written out, so
+    // that S of the next part overlaps that part's last PV and its epilogue.
+    struct Done {
+      int b, rb, seg, n_rows, n_tiles;
+      int64_t row_base;
+    } last{};
+    for (uint32_t k = 0;; ++k) {
+      const bool more = next_part(k);
       const Part &e = misc.part[k % kWorkRing];
+      const bool was_ok = ok;
+      if (more && e.n_tiles > 0) load_queries(e);
+      if (k > 0) {
+        if (last.n_tiles > 0) {
+          wait(misc.o_done, g - 1);
+          tc_fence_after();
+          const int n_cols = last.n_rows - 32 * h;  // rows of the unit among this warp's 32 columns
+#pragma unroll 1
+          for (int blk = 0; blk < 4 && n_cols > 0; ++blk) {
+            uint32_t ov[32];
+            tmem_ld32(tmem + lanes + kTmemO + blk * kRows + 32 * h, ov);
+            if (!ok || !was_ok || *abort_flag != 0) continue;
+            const int dim = blk * 128 + 32 * wq + lane;
+            const float4 *factor = reinterpret_cast<const float4 *>(&misc.factor[32 * h]);
+            // O^T scaled; a factor of 0 is a row without a token
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 f = factor[j];
+              ov[4 * j] = __float_as_uint(f.x != 0.0f ? __uint_as_float(ov[4 * j]) * f.x : 0.0f);
+              ov[4 * j + 1] = __float_as_uint(f.y != 0.0f ? __uint_as_float(ov[4 * j + 1]) * f.y : 0.0f);
+              ov[4 * j + 2] = __float_as_uint(f.z != 0.0f ? __uint_as_float(ov[4 * j + 2]) * f.z : 0.0f);
+              ov[4 * j + 3] = __float_as_uint(f.w != 0.0f ? __uint_as_float(ov[4 * j + 3]) * f.w : 0.0f);
+            }
+            if (S == 1) {
+              __nv_bfloat16 *o = p.out + (last.row_base + 32 * h) * 512 + dim;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j < n_cols) o[static_cast<int64_t>(j) * 512] = __float2bfloat16_rn(__uint_as_float(ov[j]));
+            } else {
+              // partial block [8 row octets][512 dims][8 rows]: one 16-byte store per octet
+              const int64_t block = (static_cast<int64_t>(last.b) * p.row_blocks + last.rb) * S + last.seg;
+              uint4 *o = reinterpret_cast<uint4 *>(p.segm_out + block * (512 * kRows)) + 4 * h * 512 + dim;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (8 * q >= n_cols) break;
+                uint32_t w4[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  w4[u] = pack_bf16(__uint_as_float(ov[8 * q + 2 * u]), __uint_as_float(ov[8 * q + 2 * u + 1]));
+                o[q * 512] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              }
+            }
+          }
+          tc_fence_before();
+        } else if (S == 1 && ok) {  // no row sees a token
+          uint4 *o = reinterpret_cast<uint4 *>(p.out + last.row_base * 512);
+          for (int c = threadIdx.x; c < last.n_rows * 64; c += kSoftThreads) o[c] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (!more) break;
+
       const int n_rows = e.n_rows, n_tiles = e.n_tiles, seg_lo = e.seg_lo, seg_hi = e.seg_hi, len = e.lens[row];
       const bool active = 16 * wq < n_rows;  // rows of the unit in this warp's quarter
       float m_ref = -INFINITY, l = 0.0f, w_sum = 0.0f, w_lost = 0.0f;
 
+#pragma unroll 1
       for (int i = 0; i < n_tiles; ++i, ++g) {
         const int tok0 = seg_lo + i * kTile, n_valid = min(kTile, seg_hi - tok0);
         const uint32_t stage = s_base + (g % kStages) * kStageBytes;
         wait(misc.s_full, g);
         tc_fence_after();
         float x[24];
-        uint32_t nan_tokens = 0;
         if (active) {
           uint32_t v[48];
           const uint32_t col = tmem + kTmemS + lanes + 48 * h;
           tmem_ld16(col, v);
           tmem_ld16(col + 16, v + 16);
           tmem_ld16(col + 32, v + 32);
+          wait(misc.sc_full, g);  // long there: tested while the loads run
           tmem_wait_ld();
           // lane i has q1 . k of its warp's 48 tokens, lane i + 16 q2 . k: each adds up half of them
 #pragma unroll
@@ -756,22 +853,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
-        wait(misc.sc_full, g);
-        const int seen = min(n_valid, len - tok0);  // tokens this row sees of the tile
-        bool exceed = false;
+        const float4 *sc = &misc.sc[c0];
+        const int seen = min(n_valid, len - tok0) - c0;  // of this thread's tokens, the first `seen` are visible
+        uint32_t nan_tokens = 0;
         float top = -INFINITY;
         if (active) {
+          // scores in log2 units plus the scale's exponent; masked ones -inf
 #pragma unroll
           for (int j = 0; j < 24; ++j) {
-            const float4 s = misc.sc[c0 + j];
-            if (x[j] != x[j]) nan_tokens |= 1u << j;
-            x[j] = c0 + j < seen ? fmaf(x[j] * q_scale, s.x, s.y) : -INFINITY;
-            top = fmaxf(top, x[j]);
+            const float2 s = *reinterpret_cast<const float2 *>(&sc[kWide ? j & ~7 : j].x);
+            x[j] = fmaf(x[j], s.x * q_scale, s.y);
           }
-          exceed = top > m_ref + kThreshold;
+          if (__any_sync(0xffffffffu, seen < 24)) {
+#pragma unroll
+            for (int j = 0; j < 24; ++j)
+              if (j >= seen) x[j] = -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < 24; j += 2) top = max3_nan(top, x[j], x[j + 1]);
+          if (top != top) {  // a NaN code among them: the row's sums will say so
+            top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 24; ++j) {
+              if (x[j] != x[j]) nan_tokens |= 1u << j;
+              top = fmaxf(top, x[j]);
+            }
+          }
         }
+        // the reference moves when a weight exceeds 2^3 of it
         bool rescale = false;
-        if (named_bar_red_or(kBarSoft, kSoftThreads, exceed)) {
+        if (named_bar_red_or(kBarSoft, kSoftThreads, top > m_ref + kThreshold)) {
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           if (term == 0) misc.red[h][row] = top;
           named_bar_sync(kBarSoft, kSoftThreads);
@@ -785,41 +896,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             w_lost *= alpha;
           }
           if (owner) misc.alpha[row] = alpha;
-          rescale = named_bar_red_or(kBarSoft, kSoftThreads, alpha != 1.0f);
+          rescale = named_bar_red_or(kBarSoft, kSoftThreads, alpha != 1.0f) && i > 0;
         }
-        // weights: first term in place, second in y
         uint32_t p1[6], p2[6];
-        if (active) {
-          const float ref = m_ref - kTop;
-          float l_t = 0.0f, w_t = 0.0f, lost_t = 0.0f;
-#pragma unroll
-          for (int q = 0; q < 6; ++q) {
-            float a[4], b[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int j = 4 * q + u;
-              const float2 s = *reinterpret_cast<const float2 *>(&misc.sc[c0 + j].z);
-              const float ej = x[j] == -INFINITY ? 0.0f : ex2(x[j] - ref);
-              const float w = ej * s.x;
-              l_t = fmaf(ej, s.y, l_t);
-              w_t += w;
-              a[u] = round3(w);
-              const float rest = w - a[u];
-              b[u] = round3(rest);
-              lost_t += rest - b[u];
-            }
-            p1[q] = pack4_e5m2(a[0], a[1], a[2], a[3]);
-            p2[q] = pack4_e5m2(b[0], b[1], b[2], b[3]);
-          }
-          l += l_t;
-          w_sum += w_t;
-          w_lost += lost_t;
-        }
+        if (active) weigh<kWide>(x, sc, m_ref == -INFINITY ? 0.0f : m_ref - kTop, l, w_sum, w_lost, p1, p2);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&misc.sc_free));
         // the previous tile's PV has read the second term's buffer, and O^T is at rest
         if (g > 0) wait(misc.o_done, g - 1);
-        if (rescale && i > 0) {
+        if (rescale) {
           tc_fence_after();
 #pragma unroll 1
           for (int blk = 0; blk < 4; ++blk) {
@@ -839,8 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v2(stage + kRopeOff + off, p1[2 * q], p1[2 * q + 1]);
             st_shared_v2(s_base + kOffP2 + off, p2[2 * q], p2[2 * q + 1]);
           }
-          // a token with a NaN code: the rows that see it are NaN by their sums, and its
-          // values must not meet the zero weights of the others
+          // a token with a NaN code: its values must not meet the zero weights of the rows that do
+          // not see it (those that do are NaN by their sums)
           while (nan_tokens != 0) {
             const int tok = c0 + __ffs(nan_tokens) - 1;
             nan_tokens &= nan_tokens - 1;
@@ -857,14 +942,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&misc.p_full));
       }
 
-      // ---- the rows' sums, then the next part's queries (its S overlaps this
-      // part's last PV and the epilogue), then O^T
-      const int seg = e.seg, fill_hi = e.fill_hi, e_b = e.b, e_rb = e.rb;
-      const int64_t row_base = e.row_base;
-      named_bar_sync(kBarSoft, kSoftThreads);  // alpha and red have been read
+      // the rows' sums over the four threads that share one
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       w_sum += __shfl_xor_sync(0xffffffffu, w_sum, 16);
       w_lost += __shfl_xor_sync(0xffffffffu, w_lost, 16);
+      named_bar_sync(kBarSoft, kSoftThreads);  // alpha and red have been read
       if (h == 1 && term == 0) {
         misc.red[0][row] = l;
         misc.red[1][row] = w_sum;
@@ -875,70 +957,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += misc.red[0][row];
         w_sum += misc.red[1][row];
         w_lost += misc.alpha[row];
+        if (spoilt && l > 0.0f) l = NAN;
         const bool none = l == 0.0f;
         const float fix = w_sum / (w_sum - w_lost);
         misc.factor[row] = none ? 0.0f : (S == 1 ? fix * kInvTop / l : fix * kInvTop);
         if (ok && row < n_rows) {
-          const int64_t r = row_base + row;
+          const int64_t r = static_cast<int64_t>(e.row_base) + row;
           if (S == 1) {
             p.lse[r] = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
           } else {
             // a NaN row keeps a finite maximum, so that the merge looks at its sum
-            p.segm_max[r * S + seg] = none ? -INFINITY : (m_ref == -INFINITY ? 0.0f : m_ref);
-            p.segm_sum[r * S + seg] = l;
-            for (int s = seg + 1; s < fill_hi; ++s) {
+            p.segm_max[r * S + e.seg] = none ? -INFINITY : (m_ref == -INFINITY ? 0.0f : m_ref);
+            p.segm_sum[r * S + e.seg] = l;
+            for (int s = e.seg + 1; s < e.fill_hi; ++s) {
               p.segm_max[r * S + s] = -INFINITY;
               p.segm_sum[r * S + s] = 0.0f;
             }
           }
         }
       }
-      more = next_part(k + 1);
-      const bool was_ok = ok;
-      if (more && misc.part[(k + 1) % kWorkRing].n_tiles > 0) load_queries(misc.part[(k + 1) % kWorkRing]);
-      else named_bar_sync(kBarSoft, kSoftThreads);
-      if (n_tiles > 0) {
-        wait(misc.o_done, g - 1);
-        tc_fence_after();
-        const int n_cols = n_rows - 32 * h;  // rows of the unit among this warp's 32 columns
-#pragma unroll 1
-        for (int blk = 0; blk < 4 && n_cols > 0; ++blk) {
-          uint32_t ov[32];
-          tmem_ld32(tmem + lanes + kTmemO + blk * kRows + 32 * h, ov);
-          if (!ok || !was_ok || *abort_flag != 0) continue;
-          const int dim = blk * 128 + 32 * wq + lane;
-          if (S == 1) {
-            __nv_bfloat16 *o = p.out + (row_base + 32 * h) * 512 + dim;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float f = misc.factor[32 * h + j];
-              if (j < n_cols)
-                o[static_cast<int64_t>(j) * 512] = __float2bfloat16_rn(f != 0.0f ? __uint_as_float(ov[j]) * f : 0.0f);
-            }
-          } else {
-            // partial block [8 row octets][512 dims][8 rows]: one 16-byte store per octet
-            const int64_t block = (static_cast<int64_t>(e_b) * p.row_blocks + e_rb) * S + seg;
-            uint4 *o = reinterpret_cast<uint4 *>(p.segm_out + block * (512 * kRows)) + 4 * h * 512 + dim;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (8 * q >= n_cols) break;
-              uint32_t w4[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int j = 8 * q + 2 * u;
-                const float fa = misc.factor[32 * h + j], fb = misc.factor[32 * h + j + 1];
-                w4[u] = pack_bf16(fa != 0.0f ? __uint_as_float(ov[j]) * fa : 0.0f,
-                                  fb != 0.0f ? __uint_as_float(ov[j + 1]) * fb : 0.0f);
-              }
-              o[q * 512] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-            }
-          }
-        }
-        tc_fence_before();
-      } else if (S == 1 && ok) {  // no row sees a token
-        uint4 *o = reinterpret_cast<uint4 *>(p.out + row_base * 512);
-        for (int c = threadIdx.x; c < n_rows * 64; c += kSoftThreads) o[c] = make_uint4(0, 0, 0, 0);
-      }
+      last = {e.b, e.rb, e.seg, n_rows, n_tiles, static_cast<int64_t>(e.row_base)};
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&misc.work_empty[k % kWorkRing]));
     }
@@ -946,13 +984,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-std::atomic<bool> g_attr_set[64];
+std::atomic<bool> g_attr_set[2][64];  // [kWide][device]
 std::atomic<int> g_num_sms[64];
 
 }  // namespace
@@ -970,10 +1008,13 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (!g_attr_set[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(mla_decode_scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  // scale blocks of eight rows or more: a thread's runs of eight tokens have one scale each
+  const bool wide = scale_block >= 8;
+  auto kern = wide ? mla_decode_scaled_kernel<true> : mla_decode_scaled_kernel<false>;
+  if (!g_attr_set[wide][dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_scaled smem)");
-    g_attr_set[dev].store(true, std::memory_order_relaxed);
+    g_attr_set[wide][dev].store(true, std::memory_order_relaxed);
   }
   int num_sms = g_num_sms[dev].load(std::memory_order_relaxed);
   if (num_sms == 0) {
@@ -1018,7 +1059,7 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   }
   const int64_t items = units * a.num_segments;
   const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
-  e = launch_pdl(mla_decode_scaled_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, tm_v, tm_r, p);
+  e = launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, stream, tm_v, tm_r, p);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "decode_scaled launch");
 }
 
