@@ -84,7 +84,7 @@ constexpr int kSoftWarps = 8, kSoftThreads = 256;
 constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10, kScaleWarp = 11;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemQ = 0, kTmemO = 144, kTmemS = 400, kTmemCols = 512;
-constexpr int kWorkRing = 4;
+constexpr int kWorkRing = 3;
 constexpr float kThreshold = 3.0f;   // the reference moves when a weight exceeds 2^3 of it
 constexpr float kTop = 11.0f;        // a weight at the reference is held as 2^11 .. 2^12: at most 2^15 < 57344
 constexpr float kInvTop = 4.8828125e-4f;  // 2^-kTop
@@ -110,11 +110,10 @@ struct Misc {
   int abort;
   int stop[2];
   int first_vb, first_pos;  // the chunk's first (view, request) and its first position
-  int pad[2];
-  alignas(16) float4 sc[kTile];         // per token: a * sm_scale * log2e, k, f, 2^(-k - kTop)
+  float sc[kTile];          // scales of the tile's tokens
   Part part[kWorkRing];
   float red[2][kRows];      // row maxima or sums of the two token halves
-  float alpha[kRows];
+  alignas(16) float alpha[kRows];
   alignas(16) float factor[kRows];
 };
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
@@ -208,9 +207,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {  // NaN if one is
+__device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two floats at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 y, a, b;\n\t"
+      "mov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 y, a, b;\n\t"
+      "mov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, c, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 y, a, b, c;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return y;
 }
 
@@ -223,33 +247,45 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int *abort
   return false;
 }
 
-// A thread's 24 scores to weights against the reference: the sums, and the
-// weights' two e5m2 terms.  A weight goes through f16 (2^-12 of itself): there
-// e5m2 is the upper byte, so a term's value is its codes moved up and the
-// remainder is exact.  sc: {., ., f, 2^(-k - kTop)} of the tokens; kWide: one
-// scale for each run of eight.
+// A scale a = f 2^k: k as a float, f in [1, 2), and 2^(-k - kTop).
+struct Scale {
+  float k, f, inv;
+};
+__device__ __forceinline__ Scale split_scale(float a) {
+  const uint32_t u = __float_as_uint(a), ex = u >> 23;
+  return {static_cast<float>(static_cast<int>(ex) - 127), __uint_as_float((u & 0x7fffffu) | 0x3f800000u),
+          __uint_as_float((254u - ex) << 23) * kInvTop};
+}
+
+// A thread's 24 scores (three runs of eight tokens, 16 apart) to weights against
+// the reference: the sums, and the weights' two e5m2 terms.  A weight goes
+// through f16 (2^-12 of itself): there e5m2 is the upper byte, so a term's value
+// is its codes moved up and the remainder is exact.  kWide: a run has one scale.
 template <bool kWide>
-__device__ __forceinline__ void weigh(const float (&x)[24], const float4 *sc, float ref, float &l, float &w_sum,
+__device__ __forceinline__ void weigh(const float2 (&x)[12], const float *sc, float ref, float &l_t, float &w_sum,
                                       float &w_lost, uint32_t (&p1)[6], uint32_t (&p2)[6]) {
-  float l_t = 0.0f, w_t = 0.0f;
+  float w_t = 0.0f;
   __half2 lost = __float2half2_rn(0.0f);
+  const float2 neg = make_float2(-ref, -ref);
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    float run = 0.0f;
-    float2 s0 = *reinterpret_cast<const float2 *>(&sc[8 * q].z), s1 = s0;
+    float2 run = make_float2(0.0f, 0.0f);
+    const Scale s = split_scale(sc[16 * q]);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int j = 8 * q + 2 * u;
-      const float e0 = ex2(x[j] - ref), e1 = ex2(x[j + 1] - ref);
+      const float2 d = add2(x[4 * q + u], neg);
+      const float2 e = make_float2(ex2(d.x), ex2(d.y));
+      float2 f = make_float2(s.f, s.f);
       if (kWide) {
-        run += e0 + e1;
+        run = add2(run, e);
       } else {
-        s0 = *reinterpret_cast<const float2 *>(&sc[j].z);
-        s1 = *reinterpret_cast<const float2 *>(&sc[j + 1].z);
-        l_t = fmaf(e0, s0.y, fmaf(e1, s1.y, l_t));
-        w_t = fmaf(e0, s0.x, fmaf(e1, s1.x, w_t));
+        const Scale s0 = split_scale(sc[16 * q + 2 * u]), s1 = split_scale(sc[16 * q + 2 * u + 1]);
+        f = make_float2(s0.f, s1.f);
+        l_t = fmaf(e.x, s0.inv, fmaf(e.y, s1.inv, l_t));
+        w_t = fmaf(e.x, s0.f, fmaf(e.y, s1.f, w_t));
       }
-      const __half2 w = __floats2half2_rn(e0 * s0.x, e1 * s1.x);
+      const float2 wf = mul2(e, f);
+      const __half2 w = __floats2half2_rn(wf.x, wf.y);
       const uint32_t c1 = __nv_cvt_halfraw2_to_fp8x2(w, __NV_SATFINITE, __NV_E5M2);
       const uint32_t v1 = __byte_perm(c1, 0, 0x1404);
       const __half2 rest = __hsub2(w, *reinterpret_cast<const __half2 *>(&v1));
@@ -260,11 +296,10 @@ __device__ __forceinline__ void weigh(const float (&x)[24], const float4 *sc, fl
       p2[2 * q + u / 2] = (u & 1) ? __byte_perm(p2[2 * q + u / 2], c2, 0x5410) : c2;
     }
     if (kWide) {
-      l_t = fmaf(run, s0.y, l_t);
-      w_t = fmaf(run, s0.x, w_t);
+      l_t = fmaf(run.x + run.y, s.inv, l_t);
+      w_t = fmaf(run.x + run.y, s.f, w_t);
     }
   }
-  l += l_t;
   w_sum += w_t;
   w_lost += __low2float(lost) + __high2float(lost);
 }
@@ -433,8 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kTmaWarp) {
     // ================================================ work and tile copies
     const uint64_t policy = l2_policy_evict_first();
-    const int run = min(P, 32);       // rows of a copy: one page, or 32 rows of one
-    const int run_v = run * 128, run_r = run * 64;
+    const int run = min(P, 32), lg_p = 31 - __clz(P);  // rows of a copy: one page, or 32 rows of one
+    // Copy o of a tile: box o / 5, chunk o % 5 (4: rope); a lane issues copies lane
+    // and, for pages of eight rows, lane + 32.
+    const int o_last = kTile / run * 5 > 32 ? 2 : 1;
+    int c_tok[2], c_x[2];
+    uint32_t c_dst[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int o = lane + 32 * j, c = o % 5;
+      c_tok[j] = o / 5 * run;
+      c_x[j] = c * 128;
+      c_dst[j] = s_base + (c < 4 ? c * kVChunk + c_tok[j] * 128 : kRopeOff + c_tok[j] * 64);
+    }
     uint32_t armed = 0, armed_par = 0;  // stages with a copy possibly in flight (for the exit path)
     uint32_t g = 0;
     int vb = misc.first_vb, rb = 0, pos = misc.first_pos, u_pos = pos;
@@ -536,37 +582,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t_hi == t_lo) continue;
       const int seg_lo = t_lo * kTile, seg_hi = min(t_hi * kTile, len);
       const int32_t *pages = p.subpage_table + static_cast<int64_t>(vb) * p.subpage_stride;
-      const int last_page = (seg_hi - 1) / P;
-      int win = seg_lo / P;             // lane l holds the id of page win + l
+      const int last_page = (seg_hi - 1) >> lg_p;
+      int win = seg_lo >> lg_p;         // lane l holds the id of page win + l
       int32_t win_id = win + lane <= last_page ? pages[win + lane] : -1;
+#pragma unroll 1
       for (int tok0 = seg_lo; tok0 < seg_hi; tok0 += kTile, ++g) {
         const int n_valid = min(kTile, seg_hi - tok0);
-        const int boxes = (n_valid + run - 1) / run, ops = boxes * 5;
         const uint32_t st = g % kStages;
-        if ((tok0 + n_valid - 1) / P >= win + 32) {
-          win = tok0 / P;
+        if ((tok0 + n_valid - 1) >> lg_p >= win + 32) {
+          win = tok0 >> lg_p;
           win_id = win + lane <= last_page ? pages[win + lane] : -1;
         }
-        if (lane == 0) wait(misc.empty[st], (g / kStages) ^ 1u);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&misc.full[st]), dst = s_base + st * kStageBytes;
-        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * run * 576);
+        if (!__all_sync(0xffffffffu, wait(misc.empty[st], (g / kStages) ^ 1u))) break;
+        const uint32_t bar = smem_u32(&misc.full[st]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, ((n_valid + run - 1) & -run) * 576);
         __syncwarp();
-        for (int o0 = 0; o0 < ops; o0 += 32) {  // copy o: box o / 5, chunk o % 5 (4: rope)
-          const int o = o0 + lane, box = o / 5, c = o - 5 * box, t = tok0 + box * run;
-          const int32_t id = __shfl_sync(0xffffffffu, win_id, o < ops ? t / P - win : 0);
-          if (o < ops) {
+#pragma unroll 1
+        for (int j = 0; j < o_last; ++j) {
+          const int off = j == 0 ? c_tok[0] : c_tok[1], x = j == 0 ? c_x[0] : c_x[1], t = tok0 + off;
+          const bool mine = off < n_valid;
+          const int32_t id = __shfl_sync(0xffffffffu, win_id, mine ? (t >> lg_p) - win : 0);
+          if (mine) {
             int32_t row = static_cast<int32_t>(p.num_cache_rows);  // past the last row: zeros
-            if (id < 0 || (static_cast<int64_t>(id) + 1) * P > p.num_cache_rows) note(p.err, MLA_DEV_BAD_SUBPAGE);
-            else row = id * P + t % P;
-            if (c < 4) tma_load_2d(dst + c * kVChunk + box * run_v, &tm_v, bar, c * 128, row, policy);
-            else tma_load_2d(dst + kRopeOff + box * run_r, &tm_r, bar, 512, row, policy);
+            if (id < 0 || (static_cast<int64_t>(id) + 1) << lg_p > p.num_cache_rows) note(p.err, MLA_DEV_BAD_SUBPAGE);
+            else row = (id << lg_p) + (t & (P - 1));
+            tma_load_2d((j == 0 ? c_dst[0] : c_dst[1]) + st * kStageBytes, x < 512 ? &tm_v : &tm_r, bar, x, row, policy);
           }
         }
         armed |= 1u << st;
         armed_par = (armed_par & ~(1u << st)) | (((g / kStages) & 1u) << st);
       }
+      ok = __all_sync(0xffffffffu, ok) != 0;
     }
     if (lane == 0 && (!ok || *abort_flag)) {  // let the copies land before the memory is released
       const volatile int never = 0;
@@ -591,11 +637,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (g > 0 && !wait(misc.s_free, g - 1)) break;
           tc_fence_after();
           const uint64_t off = static_cast<uint64_t>(st) * (kStageBytes >> 4);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int c = 0; c < 18; ++c) {
-            const uint64_t db = off + (c < 16 ? d_k + (c / 4) * (kVChunk >> 4) + (c % 4) * 2 : d_rope + (c - 16) * 2);
-            mma8_ts(tmem + kTmemS, tmem + kTmemQ + 8 * c, db, id_qk, c > 0);
-          }
+            for (int i = 0; i < 4; ++i)
+              mma8_ts(tmem + kTmemS, tmem + kTmemQ + 32 * c + 8 * i, d_k + off + c * (kVChunk >> 4) + 2 * i, id_qk,
+                      (c | i) > 0);
+          mma8_ts(tmem + kTmemS, tmem + kTmemQ + 128, d_rope + off, id_qk, 1u);
+          mma8_ts(tmem + kTmemS, tmem + kTmemQ + 136, d_rope + off + 2, id_qk, 1u);
           umma_commit(smem_u32(&misc.s_full));
         }
       }
@@ -622,9 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n32 = (min(kTile, tokens - i * kTile) + 31) / 32;
           if (!wait(misc.p_full, g)) break;
           tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 3; ++kk) {
-            if (kk >= n32) break;
+#pragma unroll 1
+          for (int kk = 0; kk < n32; ++kk) {
             const uint64_t dv = d_v + off + kk * (4096 >> 4);
 #pragma unroll
             for (int blk = 0; blk < 4; ++blk) {
@@ -654,15 +702,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&misc.work_empty[ws]));
       // scale of token t, one tile ahead of its use; a page outside the cache is zeros
+      const int lg_p = 31 - __clz(P);
       auto load = [&](int t) {
-        if (t >= seg_hi) return 1.0f;
-        const int id = pages[t / P];
-        if (id < 0 || (static_cast<int64_t>(id) + 1) * P > p.num_cache_rows) return 1.0f;
-        return p.scales[(static_cast<int64_t>(id) * P + t % P) >> p.log_g];
+        float a = 1.0f;
+        if (t < seg_hi) {
+          const int id = pages[t >> lg_p];
+          if (id >= 0 && (static_cast<int64_t>(id) + 1) << lg_p <= p.num_cache_rows)
+            a = p.scales[((id << lg_p) + (t & (P - 1))) >> p.log_g];
+        }
+        return fminf(fmaxf(a, 7.888609052210118e-31f), 1.329227995784916e36f);  // within [2^-100, 2^120]
       };
       float a[3];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) a[i] = n_tiles > 0 ? load(seg_lo + lane + 32 * i) : 1.0f;
+      for (int j = 0; j < 3; ++j) a[j] = load(seg_lo + lane + 32 * j);
+#pragma unroll 1
       for (int i = 0; i < n_tiles; ++i, ++g) {
         float next[3];
 #pragma unroll
@@ -670,11 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(misc.sc_free, g ^ 1u);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-          const float s = fminf(fmaxf(a[j], 7.888609052210118e-31f), 1.329227995784916e36f);  // [2^-100, 2^120]
-          const uint32_t u = __float_as_uint(s), ex = u >> 23;
-          misc.sc[lane + 32 * j] = make_float4(s * p.score_scale, static_cast<float>(static_cast<int>(ex) - 127),
-                                               __uint_as_float((u & 0x7fffffu) | 0x3f800000u),
-                                               __uint_as_float((254u - ex) << 23) * kInvTop);
+          misc.sc[lane + 32 * j] = a[j];
           a[j] = next[j];
         }
         __syncwarp();
@@ -685,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================ queries, softmax, epilogue
     const int wq = warp & 3, h = warp >> 2, term = lane >> 4;
     const int row = 16 * wq + (lane & 15);       // this thread's query row
-    const int c0 = 48 * h + 24 * term;           // its 24 tokens of a tile
+    const int c0 = 48 * h + 8 * term;            // its tokens of a tile: runs of eight from c0, c0 + 16, c0 + 32
     const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
     const bool owner = h == 0 && term == 0;      // of the row's statistics
     const float w_mine = term ? 0.03125f : 1.0f, w_other = term ? 1.0f : 0.03125f;
@@ -700,54 +749,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(e.q_row) + row) * 576) + 36 * h +
                          18 * term;
       uint32_t top = 0;
+      uint4 v[18];
+#pragma unroll
+      for (int i = 0; i < 18; ++i) v[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 18; ++i) {
-        const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
-        top = max(top, max(max(max(v.x & 0x7fffu, (v.x >> 16) & 0x7fffu), max(v.y & 0x7fffu, (v.y >> 16) & 0x7fffu)),
-                           max(max(v.z & 0x7fffu, (v.z >> 16) & 0x7fffu), max(v.w & 0x7fffu, (v.w >> 16) & 0x7fffu))));
+        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
       if (term == 0) misc.red[h][row] = __uint_as_float(top);
       named_bar_sync(kBarSoft, kSoftThreads);
       top = max(__float_as_uint(misc.red[0][row]), __float_as_uint(misc.red[1][row]));
-      const bool finite = top < 0x7f80u;
+      const bool finite = top < 0x7f80u;  // otherwise zeros, and the row is spoilt
       const int ex = finite ? max(static_cast<int>(top >> 7), 27) : 127;  // exponent + 127, at least 2^-100
-      const float mult = finite ? __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - ex) << 23) : 0.0f;
-      q_scale = finite ? __uint_as_float(static_cast<uint32_t>(ex - 7) << 23) : 0.0f;
+      const float mult = __uint_as_float(static_cast<uint32_t>(127 + 127 + 7 - ex) << 23);
+      const uint32_t keep = finite ? 0xffff0000u : 0u;
+      q_scale = __uint_as_float(static_cast<uint32_t>(ex - 7) << 23);
       spoilt = !finite;
-#pragma unroll 3
-      for (int c = 0; c < 9; ++c) {  // 16 dims, read again from L1: four words of each term
-        uint32_t t1[4], t2[4];
-        uint4 v[2];
-        v[0] = live ? src[2 * c] : make_uint4(0, 0, 0, 0);
-        v[1] = live ? src[2 * c + 1] : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+      for (int c0 = 0; c0 < 9; c0 += 3) {  // 48 dims; the code of 144 at once would crowd out the tiles'
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 &u = v[j >> 1];
-          const uint32_t a = (j & 1) ? u.z : u.x, b = (j & 1) ? u.w : u.y;
-          float x[4] = {__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
-                        __uint_as_float(b & 0xffff0000u)};
-          uint32_t w1 = 0, w2 = 0;
+        for (int c = 0; c < 3; ++c) {  // 16 dims: four words of each term
+          uint32_t t1[4], t2[4];
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const float y0 = finite ? x[2 * s] * mult : 0.0f, y1 = finite ? x[2 * s + 1] * mult : 0.0f;
-            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-            const __nv_fp8x2_storage_t lo =
-                __nv_cvt_float2_to_fp8x2(make_float2((y0 - f.x) * 32.0f, (y1 - f.y) * 32.0f), __NV_SATFINITE, __NV_E4M3);
-            w1 |= static_cast<uint32_t>(hi) << (16 * s);
-            w2 |= static_cast<uint32_t>(lo) << (16 * s);
+          for (int j = 0; j < 4; ++j) {
+            const uint4 &u = v[2 * c + (j >> 1)];
+            const uint32_t w[2] = {(j & 1) ? u.z : u.x, (j & 1) ? u.w : u.y};
+            uint32_t code[2][2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const float2 y = mul2(make_float2(__uint_as_float((w[s] << 16) & keep), __uint_as_float(w[s] & keep)),
+                                    make_float2(mult, mult));
+              code[0][s] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(code[0][s], __NV_E4M3);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
+              const float2 rest = mul2(add2(y, make_float2(-f.x, -f.y)), make_float2(32.0f, 32.0f));
+              code[1][s] = __nv_cvt_float2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+            }
+            t1[j] = __byte_perm(code[0][0], code[0][1], 0x5410);
+            t2[j] = __byte_perm(code[1][0], code[1][1], 0x5410);
           }
-          t1[j] = w1;
-          t2[j] = w2;
-        }
-        uint32_t got[4];
+          uint32_t got[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) got[j] = __shfl_xor_sync(0xffffffffu, term ? t1[j] : t2[j], 16);
-        const uint32_t col = tmem + kTmemQ + lanes + 72 * h + 4 * c;
-        tmem_st4(col, term ? got[0] : t1[0], term ? got[1] : t1[1], term ? got[2] : t1[2], term ? got[3] : t1[3]);
-        tmem_st4(col + 36, term ? t2[0] : got[0], term ? t2[1] : got[1], term ? t2[2] : got[2], term ? t2[3] : got[3]);
+          for (int j = 0; j < 4; ++j) got[j] = __shfl_xor_sync(0xffffffffu, term ? t1[j] : t2[j], 16);
+          const uint32_t col = tmem + kTmemQ + lanes + 72 * h + 4 * (c0 + c);
+          tmem_st4(col, term ? got[0] : t1[0], term ? got[1] : t1[1], term ? got[2] : t1[2], term ? got[3] : t1[3]);
+          tmem_st4(col + 36, term ? t2[0] : got[0], term ? t2[1] : got[1], term ? t2[2] : got[2],
+                   term ? t2[3] : got[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 12; ++i) v[i] = v[i + 6];
       }
       tmem_wait_st();
       tc_fence_before();
@@ -825,60 +878,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       const int n_rows = e.n_rows, n_tiles = e.n_tiles, seg_lo = e.seg_lo, seg_hi = e.seg_hi, len = e.lens[row];
       const bool active = 16 * wq < n_rows;  // rows of the unit in this warp's quarter
-      float m_ref = -INFINITY, l = 0.0f, w_sum = 0.0f, w_lost = 0.0f;
+      const float mult = q_scale * p.score_scale;
+      float m_ref = -INFINITY, l = 0.0f, w_sum = 0.0f, w_lost = 0.0f;  // sums in units of 2^m_ref
 
 #pragma unroll 1
       for (int i = 0; i < n_tiles; ++i, ++g) {
         const int tok0 = seg_lo + i * kTile, n_valid = min(kTile, seg_hi - tok0);
         const uint32_t stage = s_base + (g % kStages) * kStageBytes;
+        const float *sc = misc.sc + c0;
+        float2 x[12];
+        float top = -INFINITY;
         wait(misc.s_full, g);
         tc_fence_after();
-        float x[24];
         if (active) {
           uint32_t v[48];
-          const uint32_t col = tmem + kTmemS + lanes + 48 * h;
-          tmem_ld16(col, v);
-          tmem_ld16(col + 16, v + 16);
-          tmem_ld16(col + 32, v + 32);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) tmem_ld16(tmem + kTmemS + lanes + 48 * h + 16 * c, v + 16 * c);
           wait(misc.sc_full, g);  // long there: tested while the loads run
           tmem_wait_ld();
-          // lane i has q1 . k of its warp's 48 tokens, lane i + 16 q2 . k: each adds up half of them
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
+          // lane i has q1 . k of 48 tokens, lane i + 16 q2 . k: each adds up half of them, to scores in
+          // log2 units plus the scale's exponent
+          const float2 w_a = make_float2(w_mine, w_mine), w_b = make_float2(w_other, w_other);
 #pragma unroll
-          for (int j = 0; j < 24; ++j) {
-            const float mine = __uint_as_float(term ? v[24 + j] : v[j]);
-            const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(term ? v[j] : v[24 + j]), 16);
-            x[j] = fmaf(mine, w_mine, other * w_other);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
-        const float4 *sc = &misc.sc[c0];
-        const int seen = min(n_valid, len - tok0) - c0;  // of this thread's tokens, the first `seen` are visible
-        uint32_t nan_tokens = 0;
-        float top = -INFINITY;
-        if (active) {
-          // scores in log2 units plus the scale's exponent; masked ones -inf
+          for (int q = 0; q < 3; ++q) {
 #pragma unroll
-          for (int j = 0; j < 24; ++j) {
-            const float2 s = *reinterpret_cast<const float2 *>(&sc[kWide ? j & ~7 : j].x);
-            x[j] = fmaf(x[j], s.x * q_scale, s.y);
-          }
-          if (__any_sync(0xffffffffu, seen < 24)) {
-#pragma unroll
-            for (int j = 0; j < 24; ++j)
-              if (j >= seen) x[j] = -INFINITY;
-          }
-#pragma unroll
-          for (int j = 0; j < 24; j += 2) top = max3_nan(top, x[j], x[j + 1]);
-          if (top != top) {  // a NaN code among them: the row's sums will say so
-            top = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 24; ++j) {
-              if (x[j] != x[j]) nan_tokens |= 1u << j;
-              top = fmaxf(top, x[j]);
+            for (int u = 0; u < 4; ++u) {
+              const int a = 16 * q + 2 * u, b = a + 8;
+              const float2 mine = make_float2(__uint_as_float(term ? v[b] : v[a]), __uint_as_float(term ? v[b + 1] : v[a + 1]));
+              const float2 other = make_float2(__shfl_xor_sync(0xffffffffu, __uint_as_float(term ? v[a] : v[b]), 16),
+                                               __shfl_xor_sync(0xffffffffu, __uint_as_float(term ? v[a + 1] : v[b + 1]), 16));
+              const float2 dot = fma2(mine, w_a, mul2(other, w_b));
+              const float s0 = sc[16 * q + (kWide ? 0 : 2 * u)], s1 = sc[16 * q + (kWide ? 0 : 2 * u + 1)];
+              x[4 * q + u] = fma2(dot, make_float2(s0 * mult, s1 * mult), make_float2(split_scale(s0).k, split_scale(s1).k));
             }
           }
+          const int seen = min(n_valid, len - tok0) - c0;  // tokens this row sees, counted from c0
+          if (__any_sync(0xffffffffu, seen < 40)) {
+#pragma unroll
+            for (int j = 0; j < 12; ++j) {
+              const int tok = 16 * (j / 4) + 2 * (j % 4);
+              if (tok >= seen) x[j].x = -INFINITY;
+              if (tok + 1 >= seen) x[j].y = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 12; ++j) top = max3(top, x[j].x, x[j].y);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
         }
         // the reference moves when a weight exceeds 2^3 of it
         bool rescale = false;
@@ -899,38 +950,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           rescale = named_bar_red_or(kBarSoft, kSoftThreads, alpha != 1.0f) && i > 0;
         }
         uint32_t p1[6], p2[6];
-        if (active) weigh<kWide>(x, sc, m_ref == -INFINITY ? 0.0f : m_ref - kTop, l, w_sum, w_lost, p1, p2);
+        float l_tile = 0.0f;
+        if (active) weigh<kWide>(x, sc, m_ref == -INFINITY ? 0.0f : m_ref - kTop, l_tile, w_sum, w_lost, p1, p2);
+        l += l_tile;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&misc.sc_free));
         // the previous tile's PV has read the second term's buffer, and O^T is at rest
         if (g > 0) wait(misc.o_done, g - 1);
         if (rescale) {
           tc_fence_after();
+          const float4 *alpha = reinterpret_cast<const float4 *>(&misc.alpha[32 * h]);
 #pragma unroll 1
           for (int blk = 0; blk < 4; ++blk) {
             const uint32_t taddr = tmem + lanes + kTmemO + blk * kRows + 32 * h;
             uint32_t ov[32];
             tmem_ld32(taddr, ov);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * misc.alpha[32 * h + j]);
+            for (int j = 0; j < 8; ++j) {
+              const float4 a = alpha[j];
+              ov[4 * j] = __float_as_uint(__uint_as_float(ov[4 * j]) * a.x);
+              ov[4 * j + 1] = __float_as_uint(__uint_as_float(ov[4 * j + 1]) * a.y);
+              ov[4 * j + 2] = __float_as_uint(__uint_as_float(ov[4 * j + 2]) * a.z);
+              ov[4 * j + 3] = __float_as_uint(__uint_as_float(ov[4 * j + 3]) * a.w);
+            }
             tmem_st32(taddr, ov);
           }
         }
         if (active) {
+          // 32-token blocks [64 rows x 32 B], the 16-byte halves swapped in every other four rows
+          const uint32_t at = row * 32 + ((row >> 2) & 1) * 16 + 8 * term;
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
-            const int c = c0 + 8 * q;
-            const uint32_t off = (c >> 5) * kPBlock + row * 32 + ((((c >> 4) ^ (row >> 2)) & 1) << 4) + (c & 8);
+            const uint32_t off = ((3 * h + q) >> 1) * kPBlock + (at ^ (((3 * h + q) & 1) * 16));
             st_shared_v2(stage + kRopeOff + off, p1[2 * q], p1[2 * q + 1]);
             st_shared_v2(s_base + kOffP2 + off, p2[2 * q], p2[2 * q + 1]);
           }
-          // a token with a NaN code: its values must not meet the zero weights of the rows that do
-          // not see it (those that do are NaN by their sums)
-          while (nan_tokens != 0) {
-            const int tok = c0 + __ffs(nan_tokens) - 1;
-            nan_tokens &= nan_tokens - 1;
-            for (int c = 0; c < 32; ++c)
-              st_shared_v4(stage + (c >> 3) * kVChunk + tok * 128 + (c & 7) * 16, 0, 0, 0, 0);
+          if (l_tile != l_tile) {
+            // A NaN code: the rows that see its token are NaN by their sums, and its values must not
+            // meet the zero weights of the others.
+#pragma unroll 1
+            for (int t = 0; t < 24; ++t) {
+              const int b = 3 * h + (t >> 3);  // 16-token block
+              uint32_t code;
+              asm volatile("ld.shared.u8 %0, [%1];"
+                           : "=r"(code)
+                           : "r"(stage + kRopeOff + (b >> 1) * kPBlock + (at ^ ((b & 1) * 16)) + (t & 7))
+                           : "memory");
+              if ((code & 0x7fu) > 0x7cu)
+                for (int c = 0; c < 32; ++c)
+                  st_shared_v4(stage + (c >> 3) * kVChunk + (16 * b + 8 * term + (t & 7)) * 128 + (c & 7) * 16, 0, 0, 0, 0);
+            }
           }
         }
         // rows of the last 32-token step past the part's end hold anything: zeros
