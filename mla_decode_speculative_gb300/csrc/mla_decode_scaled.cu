@@ -85,6 +85,7 @@ constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10, kScaleWarp = 11;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemQ = 0, kTmemO = 144, kTmemS = 400, kTmemCols = 512;
 constexpr int kWorkRing = 3;
+constexpr int kPartCost = 6;         // what a part costs besides its tiles (queries, sums, epilogue), in tiles
 constexpr float kThreshold = 3.0f;   // the reference moves when a weight exceeds 2^3 of it
 constexpr float kTop = 11.0f;        // a weight at the reference is held as 2^11 .. 2^12: at most 2^15 < 57344
 constexpr float kInvTop = 4.8828125e-4f;  // 2^-kTop
@@ -104,7 +105,7 @@ struct Part {
 
 struct Misc {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_full, s_free, p_full, o_done, q_full, sc_full, sc_free, fin_qk, fin_pv;
+  uint64_t s_full, s_free, p1_full, p2_full, o_done, q_full, sc_full, sc_free, fin_qk, fin_pv;
   uint64_t work_full[kWorkRing], work_empty[kWorkRing];
   uint32_t tmem_base;
   int abort;
@@ -135,7 +136,7 @@ struct Params {
   long long wait_budget, drain_budget;
   float score_scale;        // sm_scale * log2(e)
   int subpage_stride, page_size, log_g, num_heads, num_segments, row_blocks, num_reqs, num_views, max_qlen, num_rows,
-      max_len;
+      max_len, q_aligned;
 };
 
 __device__ __forceinline__ void note(int *err, int code) { atomicCAS(err, 0, code); }
@@ -304,6 +305,16 @@ __device__ __forceinline__ void weigh(const float2 (&x)[12], const float *sc, fl
   w_lost += __low2float(lost) + __high2float(lost);
 }
 
+__device__ __forceinline__ void ld_global_32(const uint4 *ptr, uint4 &a, uint4 &b) {  // 32-byte aligned
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(ptr)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *ptr, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
+}
+
 // ---- work
 
 // Longest visible length of a request's rows in a view; 0 when its qo_indptr
@@ -324,13 +335,13 @@ __device__ __forceinline__ int request_len(const Params &p, int v, int b, int &q
   }
   return len;
 }
-// Positions of a (view, request): for each of its row blocks one overhead and
+// Positions of a (view, request): for each of its row blocks a part's cost and
 // its tiles, nothing when no row sees a token.
 __device__ __forceinline__ int positions(const Params &p, int vb, int &tiles) {
   int qlen;
   const int len = request_len(p, vb / p.num_reqs, vb % p.num_reqs, qlen);
   tiles = (len + kTile - 1) / kTile;
-  return tiles > 0 ? (qlen * p.num_heads + kRows - 1) / kRows * (tiles + 1) : 0;
+  return tiles > 0 ? (qlen * p.num_heads + kRows - 1) / kRows * (tiles + kPartCost) : 0;
 }
 
 struct Split {
@@ -433,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&misc.s_full), 1);
     mbar_init(smem_u32(&misc.s_free), kSoftWarps);
-    mbar_init(smem_u32(&misc.p_full), kSoftWarps);
+    mbar_init(smem_u32(&misc.p1_full), kSoftWarps);
+    mbar_init(smem_u32(&misc.p2_full), kSoftWarps);
     mbar_init(smem_u32(&misc.o_done), 1);
     mbar_init(smem_u32(&misc.q_full), kSoftWarps);
     mbar_init(smem_u32(&misc.sc_full), 1);
@@ -447,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc.abort = 0;
     misc.first_vb = misc.first_pos = 0;
     fence_mbar_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_r);
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -517,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0 && clipped) note(p.err, MLA_DEV_LEN_BOUND);
           // row blocks that end before the chunk
           if (tiles > 0 && u_pos < split.lo) {
-            rb = (split.lo - u_pos) / (tiles + 1);
-            u_pos += rb * (tiles + 1);
+            rb = (split.lo - u_pos) / (tiles + kPartCost);
+            u_pos += rb * (tiles + kPartCost);
           }
         }
         const int blocks = (qlen * p.num_heads + kRows - 1) / kRows;
@@ -528,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if (u_pos >= split.hi) break;
-        const int here = u_pos, start = here + (tiles > 0 ? 1 : 0), end = start + tiles;
+        const int here = u_pos, start = here + (tiles > 0 ? kPartCost : 0), end = start + tiles;
         if (start >= split.hi) break;
         u_pos = end;
         const int this_rb = rb++;
@@ -567,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           e.seg_lo = t_lo * kTile;
           e.seg_hi = min(t_hi * kTile, len);
           e.n_tiles = t_hi - t_lo;
+          if (t_hi > t_lo) prefetch_l2(p.q + static_cast<int64_t>(q0 * p.num_heads + row_begin) * 576, n_rows * 1152);
         }
         break;
       }
@@ -593,6 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           win = tok0 >> lg_p;
           win_id = win + lane <= last_page ? pages[win + lane] : -1;
         }
+        // The first part's queries come before its third tile: all CTAs ask for everything at once.
+        if (k == 0 && g == 2 && !__all_sync(0xffffffffu, wait(misc.q_full, 0))) break;
         if (!__all_sync(0xffffffffu, wait(misc.empty[st], (g / kStages) ^ 1u))) break;
         const uint32_t bar = smem_u32(&misc.full[st]);
         if (lane == 0) mbar_arrive_expect_tx(bar, ((n_valid + run - 1) & -run) * 576);
@@ -669,18 +688,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t st = g % kStages;
           const uint64_t off = static_cast<uint64_t>(st) * (kStageBytes >> 4);
           const int n32 = (min(kTile, tokens - i * kTile) + 31) / 32;
-          if (!wait(misc.p_full, g)) break;
-          tc_fence_after();
+          // The first term's products need not wait for the second term, whose buffer the tile
+          // before has until its own are done.
 #pragma unroll 1
-          for (int kk = 0; kk < n32; ++kk) {
-            const uint64_t dv = d_v + off + kk * (4096 >> 4);
+          for (int term = 0; term < 2; ++term) {
+            if (!wait(term == 0 ? misc.p1_full : misc.p2_full, g)) break;
+            tc_fence_after();
+            uint64_t dv = d_v + off, dp = term == 0 ? d_p1 + off : d_p2;
+#pragma unroll 1
+            for (int kk = 0; kk < n32; ++kk, dv += 4096 >> 4, dp += kPBlock >> 4) {
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) {
-              mma8_ss(tmem + kTmemO + blk * kRows, dv + blk * (kVChunk >> 4), d_p1 + off + kk * (kPBlock >> 4), id_pv,
-                      kk > 0 || i > 0);
-              mma8_ss(tmem + kTmemO + blk * kRows, dv + blk * (kVChunk >> 4), d_p2 + kk * (kPBlock >> 4), id_pv, 1u);
+              for (int blk = 0; blk < 4; ++blk)
+                mma8_ss(tmem + kTmemO + blk * kRows, dv + blk * (kVChunk >> 4), dp, id_pv, (term | kk | i) > 0);
             }
           }
+          if (!ok) break;
           umma_commit(smem_u32(&misc.o_done));
           umma_commit(smem_u32(&misc.empty[st]));
         }
@@ -751,7 +773,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t top = 0;
       uint4 v[18];
 #pragma unroll
-      for (int i = 0; i < 18; ++i) v[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 18; i += 2) {
+        v[i] = v[i + 1] = make_uint4(0, 0, 0, 0);
+        if (live) {
+          if (p.q_aligned) {
+            ld_global_32(src + i, v[i], v[i + 1]);
+          } else {
+            v[i] = src[i];
+            v[i + 1] = src[i + 1];
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 18; ++i) {
         const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -780,13 +812,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t code[2][2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
+              // in f16, exact but for elements below 2^-21 of the row's largest
               const float2 y = mul2(make_float2(__uint_as_float((w[s] << 16) & keep), __uint_as_float(w[s] & keep)),
                                     make_float2(mult, mult));
-              code[0][s] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(code[0][s], __NV_E4M3);
-              const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
-              const float2 rest = mul2(add2(y, make_float2(-f.x, -f.y)), make_float2(32.0f, 32.0f));
-              code[1][s] = __nv_cvt_float2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
+              const __half2 yh = __floats2half2_rn(y.x, y.y);
+              code[0][s] = __nv_cvt_halfraw2_to_fp8x2(yh, __NV_SATFINITE, __NV_E4M3);
+              const __half2 first = __half2(__nv_cvt_fp8x2_to_halfraw2(code[0][s], __NV_E4M3));
+              const __half2 rest = __hmul2(__hsub2(yh, first), __float2half2_rn(32.0f));
+              code[1][s] = __nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3);
             }
             t1[j] = __byte_perm(code[0][0], code[0][1], 0x5410);
             t2[j] = __byte_perm(code[1][0], code[1][1], 0x5410);
@@ -955,36 +988,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += l_tile;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&misc.sc_free));
-        // the previous tile's PV has read the second term's buffer, and O^T is at rest
-        if (g > 0) wait(misc.o_done, g - 1);
-        if (rescale) {
-          tc_fence_after();
-          const float4 *alpha = reinterpret_cast<const float4 *>(&misc.alpha[32 * h]);
-#pragma unroll 1
-          for (int blk = 0; blk < 4; ++blk) {
-            const uint32_t taddr = tmem + lanes + kTmemO + blk * kRows + 32 * h;
-            uint32_t ov[32];
-            tmem_ld32(taddr, ov);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 a = alpha[j];
-              ov[4 * j] = __float_as_uint(__uint_as_float(ov[4 * j]) * a.x);
-              ov[4 * j + 1] = __float_as_uint(__uint_as_float(ov[4 * j + 1]) * a.y);
-              ov[4 * j + 2] = __float_as_uint(__uint_as_float(ov[4 * j + 2]) * a.z);
-              ov[4 * j + 3] = __float_as_uint(__uint_as_float(ov[4 * j + 3]) * a.w);
-            }
-            tmem_st32(taddr, ov);
-          }
-        }
+        // 32-token blocks [64 rows x 32 B] of each term, the 16-byte halves swapped in every other four rows
+        const uint32_t at = row * 32 + ((row >> 2) & 1) * 16 + 8 * term;
         if (active) {
-          // 32-token blocks [64 rows x 32 B], the 16-byte halves swapped in every other four rows
-          const uint32_t at = row * 32 + ((row >> 2) & 1) * 16 + 8 * term;
 #pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            const uint32_t off = ((3 * h + q) >> 1) * kPBlock + (at ^ (((3 * h + q) & 1) * 16));
-            st_shared_v2(stage + kRopeOff + off, p1[2 * q], p1[2 * q + 1]);
-            st_shared_v2(s_base + kOffP2 + off, p2[2 * q], p2[2 * q + 1]);
-          }
+          for (int q = 0; q < 3; ++q)
+            st_shared_v2(stage + kRopeOff + ((3 * h + q) >> 1) * kPBlock + (at ^ (((3 * h + q) & 1) * 16)), p1[2 * q],
+                         p1[2 * q + 1]);
           if (l_tile != l_tile) {
             // A NaN code: the rows that see its token are NaN by their sums, and its values must not
             // meet the zero weights of the others.
@@ -1006,9 +1016,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = threadIdx.x; c < (((n_valid + 31) & ~31) - n_valid) * 32; c += kSoftThreads)
           st_shared_v4(stage + ((c & 31) >> 3) * kVChunk + (n_valid + (c >> 5)) * 128 + (c & 7) * 16, 0, 0, 0, 0);
         fence_proxy_async_smem();
+        if (rescale) {  // O^T at rest
+          wait(misc.o_done, g - 1);
+          tc_fence_after();
+          const float4 *alpha = reinterpret_cast<const float4 *>(&misc.alpha[32 * h]);
+#pragma unroll 1
+          for (int blk = 0; blk < 4; ++blk) {
+            const uint32_t taddr = tmem + lanes + kTmemO + blk * kRows + 32 * h;
+            uint32_t ov[32];
+            tmem_ld32(taddr, ov);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 a = alpha[j];
+              ov[4 * j] = __float_as_uint(__uint_as_float(ov[4 * j]) * a.x);
+              ov[4 * j + 1] = __float_as_uint(__uint_as_float(ov[4 * j + 1]) * a.y);
+              ov[4 * j + 2] = __float_as_uint(__uint_as_float(ov[4 * j + 2]) * a.z);
+              ov[4 * j + 3] = __float_as_uint(__uint_as_float(ov[4 * j + 3]) * a.w);
+            }
+            tmem_st32(taddr, ov);
+          }
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&misc.p_full));
+        if (lane == 0) mbar_arrive(smem_u32(&misc.p1_full));
+        if (g > 0) wait(misc.o_done, g - 1);  // the tile before has left the second term's buffer
+        if (active) {
+#pragma unroll
+          for (int q = 0; q < 3; ++q)
+            st_shared_v2(s_base + kOffP2 + ((3 * h + q) >> 1) * kPBlock + (at ^ (((3 * h + q) & 1) * 16)), p2[2 * q],
+                         p2[2 * q + 1]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&misc.p2_full));
       }
 
       // the rows' sums over the four threads that share one
@@ -1094,6 +1134,7 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   Params p{};
   p.q = static_cast<const __nv_bfloat16 *>(a.q);
   p.scales = kv_scales;
+  p.q_aligned = reinterpret_cast<uintptr_t>(a.q) % 32 == 0;
   p.qo_indptr = a.qo_indptr;
   p.row_len = a.row_len;
   p.subpage_table = a.subpage_table;
@@ -1121,7 +1162,7 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   p.max_len = a.subpage_stride * a.page_size;
   // positions (tiles and one per unit) are counted in int32, at the static bound
   const int64_t units = static_cast<int64_t>(a.num_reqs) * p.num_views * p.row_blocks;
-  if (units * ((p.max_len + kTile - 1) / kTile + 1) > INT32_MAX) {
+  if (units * ((p.max_len + kTile - 1) / kTile + kPartCost) > INT32_MAX) {
     set_error("mla_decode_verify_scaled: %lld row blocks of up to %d tokens overflow int32 positions", (long long)units,
               p.max_len);
     return MLA_ERR_UNSUPPORTED;
