@@ -81,6 +81,7 @@ constexpr int kPBlock = kRows * 32;               // 32 tokens of one term of P^
 constexpr int kOffP2 = kStages * kStageBytes;     // second term of P^T
 constexpr int kOffMisc = kOffP2 + 3 * kPBlock;
 constexpr int kSoftWarps = 8, kSoftThreads = 256;
+constexpr int kGroupWarps = 4, kGroupThreads = 128;  // two groups take turns with the tiles
 constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10, kScaleWarp = 11;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemQ = 0, kTmemO = 144, kTmemS = 400, kTmemCols = 512;
@@ -90,7 +91,7 @@ constexpr float kThreshold = 3.0f;   // the reference moves when a weight exceed
 constexpr float kTop = 11.0f;        // a weight at the reference is held as 2^11 .. 2^12: at most 2^15 < 57344
 constexpr float kInvTop = 4.8828125e-4f;  // 2^-kTop
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr uint32_t kBarSoft = 1;     // named barrier of the softmax warps
+constexpr uint32_t kBarSoft = 1;     // named barriers: the softmax warps, and 2, 3 their groups
 
 // A part of a unit, as the producer publishes it.
 struct Part {
@@ -105,16 +106,20 @@ struct Part {
 
 struct Misc {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_full, s_free, p1_full, p2_full, o_done, q_full, sc_full, sc_free, fin_qk, fin_pv;
+  uint64_t s_free, p2_full, q_full, fin_qk, fin_pv;
+  // by the tile's parity, so by softmax group: a group looks at every other tile,
+  // and one barrier's phases look alike two tiles apart
+  uint64_t s_full[2], p1_full[2], o_done[2], turn[2], sc_full[2], sc_free[2];
   uint64_t work_full[kWorkRing], work_empty[kWorkRing];
   uint32_t tmem_base;
   int abort;
   int stop[2];
   int first_vb, first_pos;  // the chunk's first (view, request) and its first position
-  float sc[kTile];          // scales of the tile's tokens
+  float sc[2][kTile];       // scales of a tile's tokens
   Part part[kWorkRing];
-  float red[2][kRows];      // row maxima or sums of the two token halves
-  alignas(16) float alpha[kRows];
+  float ref[kRows];         // running reference of each row (log2 units)
+  float red[2][kRows];      // sums of the setup, the queries' maxima, the rows' sums
+  alignas(16) float alpha[2][kRows];  // what a group's new references scale O^T by
   alignas(16) float factor[kRows];
 };
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
@@ -258,18 +263,18 @@ __device__ __forceinline__ Scale split_scale(float a) {
           __uint_as_float((254u - ex) << 23) * kInvTop};
 }
 
-// A thread's 24 scores (three runs of eight tokens, 16 apart) to weights against
+// A thread's 48 scores (six runs of eight tokens, 16 apart) to weights against
 // the reference: the sums, and the weights' two e5m2 terms.  A weight goes
 // through f16 (2^-12 of itself): there e5m2 is the upper byte, so a term's value
 // is its codes moved up and the remainder is exact.  kWide: a run has one scale.
 template <bool kWide>
-__device__ __forceinline__ void weigh(const float2 (&x)[12], const float *sc, float ref, float &l_t, float &w_sum,
-                                      float &w_lost, uint32_t (&p1)[6], uint32_t (&p2)[6]) {
+__device__ __forceinline__ void weigh(const float2 (&x)[24], const float *sc, float ref, float &l_t, float &w_sum,
+                                      float &w_lost, uint32_t (&p1)[12], uint32_t (&p2)[12]) {
   float w_t = 0.0f;
   __half2 lost = __float2half2_rn(0.0f);
   const float2 neg = make_float2(-ref, -ref);
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
+  for (int q = 0; q < 6; ++q) {
     float2 run = make_float2(0.0f, 0.0f);
     const Scale s = split_scale(sc[16 * q]);
 #pragma unroll
@@ -442,16 +447,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&misc.full[i]), 1);
       mbar_init(smem_u32(&misc.empty[i]), 1);
     }
-    mbar_init(smem_u32(&misc.s_full), 1);
-    mbar_init(smem_u32(&misc.s_free), kSoftWarps);
-    mbar_init(smem_u32(&misc.p1_full), kSoftWarps);
-    mbar_init(smem_u32(&misc.p2_full), kSoftWarps);
-    mbar_init(smem_u32(&misc.o_done), 1);
+    mbar_init(smem_u32(&misc.s_free), kGroupWarps);
+    mbar_init(smem_u32(&misc.p2_full), kGroupWarps);
     mbar_init(smem_u32(&misc.q_full), kSoftWarps);
-    mbar_init(smem_u32(&misc.sc_full), 1);
-    mbar_init(smem_u32(&misc.sc_free), kSoftWarps);
     mbar_init(smem_u32(&misc.fin_qk), 1);
     mbar_init(smem_u32(&misc.fin_pv), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&misc.s_full[i]), 1);
+      mbar_init(smem_u32(&misc.p1_full[i]), kGroupWarps);
+      mbar_init(smem_u32(&misc.o_done[i]), 1);
+      mbar_init(smem_u32(&misc.turn[i]), kGroupWarps);
+      mbar_init(smem_u32(&misc.sc_full[i]), 1);
+      mbar_init(smem_u32(&misc.sc_free[i]), kGroupWarps);
+    }
     for (int i = 0; i < kWorkRing; ++i) {
       mbar_init(smem_u32(&misc.work_full[i]), 1);
       mbar_init(smem_u32(&misc.work_empty[i]), kSoftWarps + 3);
@@ -664,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       (c | i) > 0);
           mma8_ts(tmem + kTmemS, tmem + kTmemQ + 128, d_rope + off, id_qk, 1u);
           mma8_ts(tmem + kTmemS, tmem + kTmemQ + 136, d_rope + off + 2, id_qk, 1u);
-          umma_commit(smem_u32(&misc.s_full));
+          umma_commit(smem_u32(&misc.s_full[g & 1u]));
         }
       }
       umma_commit(smem_u32(&misc.fin_qk));  // every product issued so far has retired
@@ -692,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // before has until its own are done.
 #pragma unroll 1
           for (int term = 0; term < 2; ++term) {
-            if (!wait(term == 0 ? misc.p1_full : misc.p2_full, g)) break;
+            if (!wait(term == 0 ? misc.p1_full[g & 1u] : misc.p2_full, term == 0 ? g >> 1 : g)) break;
             tc_fence_after();
             uint64_t dv = d_v + off, dp = term == 0 ? d_p1 + off : d_p2;
 #pragma unroll 1
@@ -703,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!ok) break;
-          umma_commit(smem_u32(&misc.o_done));
+          umma_commit(smem_u32(&misc.o_done[g & 1u]));
           umma_commit(smem_u32(&misc.empty[st]));
         }
       }
@@ -742,25 +750,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         float next[3];
 #pragma unroll
         for (int j = 0; j < 3; ++j) next[j] = load(seg_lo + (i + 1) * kTile + lane + 32 * j);
-        wait(misc.sc_free, g ^ 1u);
+        wait(misc.sc_free[g & 1u], (g >> 1) ^ 1u);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
-          misc.sc[lane + 32 * j] = a[j];
+          misc.sc[g & 1u][lane + 32 * j] = a[j];
           a[j] = next[j];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&misc.sc_full));
+        if (lane == 0) mbar_arrive(smem_u32(&misc.sc_full[g & 1u]));
       }
     }
   } else {
     // ================================================ queries, softmax, epilogue
     const int wq = warp & 3, h = warp >> 2, term = lane >> 4;
     const int row = 16 * wq + (lane & 15);       // this thread's query row
-    const int c0 = 48 * h + 8 * term;            // its tokens of a tile: runs of eight from c0, c0 + 16, c0 + 32
+    const uint32_t bar_group = kBarSoft + 1 + h;
     const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
     const bool owner = h == 0 && term == 0;      // of the row's statistics
     const float w_mine = term ? 0.03125f : 1.0f, w_other = term ? 1.0f : 0.03125f;
-    uint32_t g = 0;
+    uint32_t g0 = 0;                             // tiles of the parts before
     float q_scale = 1.0f;                        // q = q_scale * (q1 + q2 / 32)
     bool spoilt = false;                        // the query row is not finite
 
@@ -862,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more && e.n_tiles > 0) load_queries(e);
       if (k > 0) {
         if (last.n_tiles > 0) {
-          wait(misc.o_done, g - 1);
+          wait(misc.o_done[(g0 - 1) & 1u], (g0 - 1) >> 1);
           tc_fence_after();
           const int n_cols = last.n_rows - 32 * h;  // rows of the unit among this warp's 32 columns
 #pragma unroll 1
@@ -914,29 +922,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mult = q_scale * p.score_scale;
       float m_ref = -INFINITY, l = 0.0f, w_sum = 0.0f, w_lost = 0.0f;  // sums in units of 2^m_ref
 
+      // group h takes every other tile; a thread: runs of eight tokens, from 8 term on, 16 apart
 #pragma unroll 1
-      for (int i = 0; i < n_tiles; ++i, ++g) {
+      for (int i = static_cast<int>((g0 ^ h) & 1u); i < n_tiles; i += 2) {
+        const uint32_t g = g0 + i;
         const int tok0 = seg_lo + i * kTile, n_valid = min(kTile, seg_hi - tok0);
         const uint32_t stage = s_base + (g % kStages) * kStageBytes;
-        const float *sc = misc.sc + c0;
-        float2 x[12];
+        const float *sc = misc.sc[h] + 8 * term;
+        float2 x[24];
         float top = -INFINITY;
-        wait(misc.s_full, g);
+        wait(misc.s_full[h], g >> 1);
         tc_fence_after();
         if (active) {
-          uint32_t v[48];
+          uint32_t v[96];
 #pragma unroll
-          for (int c = 0; c < 3; ++c) tmem_ld16(tmem + kTmemS + lanes + 48 * h + 16 * c, v + 16 * c);
-          wait(misc.sc_full, g);  // long there: tested while the loads run
+          for (int c = 0; c < 6; ++c) tmem_ld16(tmem + kTmemS + lanes + 16 * c, v + 16 * c);
+          wait(misc.sc_full[h], g >> 1);  // long there: tested while the loads run
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
-          // lane i has q1 . k of 48 tokens, lane i + 16 q2 . k: each adds up half of them, to scores in
+          // lane i has q1 . k of the tile, lane i + 16 q2 . k: each adds up half of them, to scores in
           // log2 units plus the scale's exponent
           const float2 w_a = make_float2(w_mine, w_mine), w_b = make_float2(w_other, w_other);
 #pragma unroll
-          for (int q = 0; q < 3; ++q) {
+          for (int q = 0; q < 6; ++q) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int a = 16 * q + 2 * u, b = a + 8;
@@ -948,59 +958,57 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[4 * q + u] = fma2(dot, make_float2(s0 * mult, s1 * mult), make_float2(split_scale(s0).k, split_scale(s1).k));
             }
           }
-          const int seen = min(n_valid, len - tok0) - c0;  // tokens this row sees, counted from c0
-          if (__any_sync(0xffffffffu, seen < 40)) {
+          const int seen = min(n_valid, len - tok0) - 8 * term;  // tokens this row sees, counted from 8 term
+          if (__any_sync(0xffffffffu, seen < 88)) {
 #pragma unroll
-            for (int j = 0; j < 12; ++j) {
+            for (int j = 0; j < 24; ++j) {
               const int tok = 16 * (j / 4) + 2 * (j % 4);
               if (tok >= seen) x[j].x = -INFINITY;
               if (tok + 1 >= seen) x[j].y = -INFINITY;
             }
           }
 #pragma unroll
-          for (int j = 0; j < 12; ++j) top = max3(top, x[j].x, x[j].y);
+          for (int j = 0; j < 24; ++j) top = max3(top, x[j].x, x[j].y);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
         } else {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
         }
-        // the reference moves when a weight exceeds 2^3 of it
-        bool rescale = false;
-        if (named_bar_red_or(kBarSoft, kSoftThreads, top > m_ref + kThreshold)) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          if (term == 0) misc.red[h][row] = top;
-          named_bar_sync(kBarSoft, kSoftThreads);
-          top = fmaxf(misc.red[0][row], misc.red[1][row]);
-          float alpha = 1.0f;
-          if (top > m_ref + kThreshold) {
-            alpha = ex2(m_ref - top);  // 0 when m_ref is -inf
-            m_ref = top;
-            l *= alpha;
-            w_sum *= alpha;
-            w_lost *= alpha;
-          }
-          if (owner) misc.alpha[row] = alpha;
-          rescale = named_bar_red_or(kBarSoft, kSoftThreads, alpha != 1.0f) && i > 0;
+        // The reference as the tile before left it; it moves when a weight exceeds 2^3 of it.
+        if (i > 0) wait(misc.turn[(g - 1) & 1u], (g - 1) >> 1);
+        const float ref = i > 0 ? misc.ref[row] : -INFINITY;
+        const bool move = top > ref + kThreshold;
+        const float m_new = move ? top : ref;
+        if (term == 0) misc.ref[row] = m_new;
+        const bool rescale = named_bar_red_or(bar_group, kGroupThreads, move) && i > 0;
+        if (lane == 0) mbar_arrive(smem_u32(&misc.turn[h]));
+        if (rescale && term == 0) misc.alpha[h][row] = move ? ex2(ref - top) : 1.0f;  // 0 when ref is -inf
+        if (m_ref != m_new) {
+          const float c = m_ref == -INFINITY ? 0.0f : ex2(m_ref - m_new);
+          l *= c;
+          w_sum *= c;
+          w_lost *= c;
+          m_ref = m_new;
         }
-        uint32_t p1[6], p2[6];
+        uint32_t p1[12], p2[12];
         float l_tile = 0.0f;
         if (active) weigh<kWide>(x, sc, m_ref == -INFINITY ? 0.0f : m_ref - kTop, l_tile, w_sum, w_lost, p1, p2);
         l += l_tile;
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&misc.sc_free));
+        if (lane == 0) mbar_arrive(smem_u32(&misc.sc_free[h]));
         // 32-token blocks [64 rows x 32 B] of each term, the 16-byte halves swapped in every other four rows
         const uint32_t at = row * 32 + ((row >> 2) & 1) * 16 + 8 * term;
         if (active) {
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
-            st_shared_v2(stage + kRopeOff + ((3 * h + q) >> 1) * kPBlock + (at ^ (((3 * h + q) & 1) * 16)), p1[2 * q],
-                         p1[2 * q + 1]);
+          for (int q = 0; q < 6; ++q)
+            st_shared_v2(stage + kRopeOff + (q >> 1) * kPBlock + (at ^ ((q & 1) * 16)), p1[2 * q], p1[2 * q + 1]);
           if (l_tile != l_tile) {
             // A NaN code: the rows that see its token are NaN by their sums, and its values must not
             // meet the zero weights of the others.
 #pragma unroll 1
-            for (int t = 0; t < 24; ++t) {
-              const int b = 3 * h + (t >> 3);  // 16-token block
+            for (int t = 0; t < 48; ++t) {
+              const int b = t >> 3;  // 16-token block
               uint32_t code;
               asm volatile("ld.shared.u8 %0, [%1];"
                            : "=r"(code)
@@ -1013,16 +1021,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // rows of the last 32-token step past the part's end hold anything: zeros
-        for (int c = threadIdx.x; c < (((n_valid + 31) & ~31) - n_valid) * 32; c += kSoftThreads)
+        for (int c = threadIdx.x & (kGroupThreads - 1); c < (((n_valid + 31) & ~31) - n_valid) * 32; c += kGroupThreads)
           st_shared_v4(stage + ((c & 31) >> 3) * kVChunk + (n_valid + (c >> 5)) * 128 + (c & 7) * 16, 0, 0, 0, 0);
         fence_proxy_async_smem();
-        if (rescale) {  // O^T at rest
-          wait(misc.o_done, g - 1);
+        if (rescale) {
+          wait(misc.o_done[(g - 1) & 1u], (g - 1) >> 1);  // O^T at rest
+          named_bar_sync(bar_group, kGroupThreads);        // every row's alpha is there
           tc_fence_after();
-          const float4 *alpha = reinterpret_cast<const float4 *>(&misc.alpha[32 * h]);
 #pragma unroll 1
-          for (int blk = 0; blk < 4; ++blk) {
-            const uint32_t taddr = tmem + lanes + kTmemO + blk * kRows + 32 * h;
+          for (int blk = 0; blk < 8; ++blk) {
+            const uint32_t taddr = tmem + lanes + kTmemO + 32 * blk;
+            const float4 *alpha = reinterpret_cast<const float4 *>(&misc.alpha[h][32 * (blk & 1)]);
             uint32_t ov[32];
             tmem_ld32(taddr, ov);
 #pragma unroll
@@ -1038,34 +1047,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&misc.p1_full));
-        if (g > 0) wait(misc.o_done, g - 1);  // the tile before has left the second term's buffer
+        if (lane == 0) mbar_arrive(smem_u32(&misc.p1_full[h]));
+        if (g > 0) wait(misc.o_done[(g - 1) & 1u], (g - 1) >> 1);  // the tile before has left the second term's buffer
         if (active) {
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
-            st_shared_v2(s_base + kOffP2 + ((3 * h + q) >> 1) * kPBlock + (at ^ (((3 * h + q) & 1) * 16)), p2[2 * q],
-                         p2[2 * q + 1]);
+          for (int q = 0; q < 6; ++q)
+            st_shared_v2(s_base + kOffP2 + (q >> 1) * kPBlock + (at ^ ((q & 1) * 16)), p2[2 * q], p2[2 * q + 1]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&misc.p2_full));
       }
+      g0 += n_tiles;
 
       // the rows' sums over the four threads that share one
+      named_bar_sync(kBarSoft, kSoftThreads);  // both groups' last references are there
+      const float m_row = n_tiles > 0 ? misc.ref[row] : -INFINITY;
+      const float c_row = m_ref == -INFINITY ? 0.0f : ex2(m_ref - m_row);
+      l *= c_row;
+      w_sum *= c_row;
+      w_lost *= c_row;
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       w_sum += __shfl_xor_sync(0xffffffffu, w_sum, 16);
       w_lost += __shfl_xor_sync(0xffffffffu, w_lost, 16);
-      named_bar_sync(kBarSoft, kSoftThreads);  // alpha and red have been read
       if (h == 1 && term == 0) {
         misc.red[0][row] = l;
         misc.red[1][row] = w_sum;
-        misc.alpha[row] = w_lost;
+        misc.alpha[0][row] = w_lost;
       }
       named_bar_sync(kBarSoft, kSoftThreads);
       if (owner) {
         l += misc.red[0][row];
         w_sum += misc.red[1][row];
-        w_lost += misc.alpha[row];
+        w_lost += misc.alpha[0][row];
         if (spoilt && l > 0.0f) l = NAN;
         const bool none = l == 0.0f;
         const float fix = w_sum / (w_sum - w_lost);
@@ -1073,10 +1087,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && row < n_rows) {
           const int64_t r = static_cast<int64_t>(e.row_base) + row;
           if (S == 1) {
-            p.lse[r] = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+            p.lse[r] = none ? -INFINITY : (m_row + log2f(l)) * kLn2;
           } else {
             // a NaN row keeps a finite maximum, so that the merge looks at its sum
-            p.segm_max[r * S + e.seg] = none ? -INFINITY : (m_ref == -INFINITY ? 0.0f : m_ref);
+            p.segm_max[r * S + e.seg] = none ? -INFINITY : (m_row == -INFINITY ? 0.0f : m_row);
             p.segm_sum[r * S + e.seg] = l;
             for (int s = e.seg + 1; s < e.fill_hi; ++s) {
               p.segm_max[r * S + s] = -INFINITY;
