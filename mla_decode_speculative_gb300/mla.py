@@ -433,12 +433,21 @@ def write_kv(seq_lens, qo_indptr, kv_new, kv_cache, block_table, num_blocks, blo
     return kv_cache
 
 
-def _here(*tensors):
-    """The tensors' one device must be the current one: the library launches there."""
+def _current(stream):
+    """(library, current device, raw stream) of a call.  The handle of the current stream is read
+    without making a Stream object, which takes as long as the launch."""
     dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    return _lib or lib(), dev, raw
+
+
+def _dev_ptr(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of this dtype on the current device (the library launches
+    there), or a refusal."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _ptr(t, dtype, name)
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
 def update_block_tables(prev_lens, seq_lens, qo_indptr, block_table, free_ring, ring_in, block_size,
@@ -449,49 +458,52 @@ def update_block_tables(prev_lens, seq_lens, qo_indptr, block_table, free_ring, 
     prev_lens, seq_lens [B], qo_indptr [B + 1], block_table [B, width] (updated), free_ring
     [num_blocks] (updated), ring_in [2] = (head, count).  Returns (slot_map [num_rows],
     ring_out [2])."""
-    B = int(seq_lens.shape[0])
-    _here(prev_lens, seq_lens, qo_indptr, block_table, free_ring, ring_in, ring_out, slot_map)
-    if block_table.dim() != 2 or block_table.shape[0] != B or prev_lens.shape[0] != B or \
-            qo_indptr.shape[0] != B + 1 or ring_in.numel() != 2:
-        raise ValueError("prev_lens, seq_lens [B], qo_indptr [B + 1], block_table [B, width], ring_in [2]")
+    L, dev, raw = _current(stream)
     if ring_out is None:
         ring_out = torch.empty_like(ring_in)
     if slot_map is None:
         slot_map = torch.empty(num_rows, dtype=torch.int32, device=seq_lens.device)
-    if slot_map.numel() < num_rows or ring_out.numel() != 2:
-        raise ValueError("slot_map holds fewer than num_rows entries, or ring_out is not [2]")
+    B, width = block_table.shape
+    if prev_lens.numel() != B or seq_lens.numel() != B or qo_indptr.numel() != B + 1 or \
+            ring_in.numel() != 2 or ring_out.numel() != 2 or slot_map.numel() < num_rows:
+        raise ValueError("prev_lens, seq_lens [B], qo_indptr [B + 1], block_table [B, width], ring_in and "
+                         "ring_out [2], slot_map [num_rows]")
     i32 = torch.int32
-    a = TableArgs(B, int(num_rows), _ptr(prev_lens, i32, "prev_lens"), _ptr(seq_lens, i32, "seq_lens"),
-                  _ptr(qo_indptr, i32, "qo_indptr"), int(world_size), int(rank), int(interleave),
-                  int(block_size), int(free_ring.numel()), _ptr(block_table, i32, "block_table"),
-                  int(block_table.shape[1]), _ptr(free_ring, i32, "free_ring"),
-                  _ptr(ring_in, i32, "ring_in"), _ptr(ring_out, i32, "ring_out"),
-                  _ptr(slot_map, i32, "slot_map"))
-    _check(lib().mla_update_block_tables(ctypes.byref(a), _stream(stream)), "mla_update_block_tables")
+    a = TableArgs(B, num_rows, _dev_ptr(prev_lens, i32, dev, "prev_lens"), _dev_ptr(seq_lens, i32, dev, "seq_lens"),
+                  _dev_ptr(qo_indptr, i32, dev, "qo_indptr"), world_size, rank, interleave, block_size,
+                  free_ring.numel(), _dev_ptr(block_table, i32, dev, "block_table"), width,
+                  _dev_ptr(free_ring, i32, dev, "free_ring"), _dev_ptr(ring_in, i32, dev, "ring_in"),
+                  _dev_ptr(ring_out, i32, dev, "ring_out"), _dev_ptr(slot_map, i32, dev, "slot_map"))
+    st = L.mla_update_block_tables(ctypes.byref(a), raw)
+    if st:
+        _check(st, "mla_update_block_tables")
     return slot_map, ring_out
 
 
 def _check_scaled(kv_cache, kv_scales, scale_block):
-    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 2 or kv_cache.shape[1] != D_QK:
+    shape = kv_cache.shape
+    if kv_cache.dtype is not torch.uint8 or len(shape) != 2 or shape[1] != D_QK:
         raise ValueError("kv_cache must be [N, 576] uint8 (e4m3 codes)")
-    if scale_block < 1 or kv_scales.numel() * scale_block != kv_cache.shape[0]:
+    if scale_block < 1 or kv_scales.numel() * scale_block != shape[0]:
         raise ValueError("kv_scales must hold one float32 per scale_block rows of kv_cache")
+    return shape[0]
 
 
 def write_kv_scaled(kv_new, slot_map, kv_cache, kv_scales, scale_block, stream=None):
     """mla_write_kv_scaled: kv_new [T, 576] bf16 quantised into kv_cache [N, 576] uint8 (e4m3
     codes) at the rows slot_map [T] int32 names (-1: skipped), with a power-of-two float32 scale
     per scale_block rows in kv_scales [N / scale_block].  Returns (kv_cache, kv_scales)."""
-    _here(kv_new, slot_map, kv_cache, kv_scales)
-    _check_scaled(kv_cache, kv_scales, scale_block)
-    T = int(kv_new.shape[0])
-    if kv_new.dim() != 2 or kv_new.shape[1] != D_QK or slot_map.numel() < T:
+    L, dev, raw = _current(stream)
+    rows = _check_scaled(kv_cache, kv_scales, scale_block)
+    shape = kv_new.shape
+    if len(shape) != 2 or shape[1] != D_QK or slot_map.numel() < shape[0]:
         raise ValueError("kv_new must be [T, 576] and slot_map hold T entries")
-    _check(lib().mla_write_kv_scaled(T, _ptr(kv_new, torch.bfloat16, "kv_new"),
-                                     _ptr(slot_map, torch.int32, "slot_map"),
-                                     _ptr(kv_cache, torch.uint8, "kv_cache"),
-                                     _ptr(kv_scales, torch.float32, "kv_scales"), int(scale_block),
-                                     int(kv_cache.shape[0]), _stream(stream)), "mla_write_kv_scaled")
+    st = L.mla_write_kv_scaled(shape[0], _dev_ptr(kv_new, torch.bfloat16, dev, "kv_new"),
+                               _dev_ptr(slot_map, torch.int32, dev, "slot_map"),
+                               _dev_ptr(kv_cache, torch.uint8, dev, "kv_cache"),
+                               _dev_ptr(kv_scales, torch.float32, dev, "kv_scales"), scale_block, rows, raw)
+    if st:
+        _check(st, "mla_write_kv_scaled")
     return kv_cache, kv_scales
 
 
@@ -501,28 +513,34 @@ def decode_verify_scaled(q, kv_cache, kv_scales, scale_block, qo_indptr, row_len
     """mla_decode_verify_scaled: decode_verify over e4m3 codes kv_cache [N, 576] uint8 with one
     float32 scale per scale_block rows in kv_scales [N / scale_block].  The other arguments and
     the result (out, lse, workspace) are decode_verify's."""
-    T, H, _ = q.shape
-    _here(q, kv_cache, kv_scales, qo_indptr, row_len, subpage_table, out, lse, workspace)
-    _check_scaled(kv_cache, kv_scales, scale_block)
+    L, dev, raw = _current(stream)
+    T, H, dk = q.shape
+    rows = _check_scaled(kv_cache, kv_scales, scale_block)
     V = max(1, int(num_views))
-    if row_len.numel() != V * T or subpage_table.numel() != V * (qo_indptr.shape[0] - 1) * subpage_table.shape[-1]:
-        raise ValueError("row_len must be [V, T] and subpage_table [V, B, width]")
-    lead = (V, T) if V > 1 else (T,)
+    B, width = qo_indptr.numel() - 1, subpage_table.shape[-1]
+    if dk != D_QK or row_len.numel() != V * T or subpage_table.numel() != V * B * width:
+        raise ValueError("q must be [T, H, 576], row_len [V, T] and subpage_table [V, B, width]")
     if out is None:
-        out = torch.empty((*lead, H, D_V), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((V, T, H, D_V) if V > 1 else (T, H, D_V), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((*lead, H), dtype=torch.float32, device=q.device)
+        lse = torch.empty((V, T, H) if V > 1 else (T, H), dtype=torch.float32, device=q.device)
     if out.numel() != V * T * H * D_V or lse.numel() != V * T * H:
         raise ValueError("out must be [V, T, H, 512] and lse [V, T, H]")
-    a = make_decode_args(q, kv_cache, qo_indptr, row_len, subpage_table, page_size_, num_segments, max_qlen,
-                         sm_scale, 1.0, out, lse, num_views=V,
-                         wait_cycles=wait_cycles)
-    need = decode_verify_workspace_bytes(a)
+    i32 = torch.int32
+    a = DecodeArgs(B, T, H, max_qlen, MLA_KV_FP8_E4M3, sm_scale, 1.0, _dev_ptr(q, torch.bfloat16, dev, "q"),
+                   _dev_ptr(kv_cache, torch.uint8, dev, "kv_cache"), rows,
+                   _dev_ptr(qo_indptr, i32, dev, "qo_indptr"), _dev_ptr(row_len, i32, dev, "row_len"),
+                   _dev_ptr(subpage_table, i32, dev, "subpage_table"), width, page_size_, num_segments,
+                   _dev_ptr(out, torch.bfloat16, dev, "out"), _dev_ptr(lse, torch.float32, dev, "lse"), 0, V,
+                   wait_cycles)
+    ref = ctypes.byref(a)
+    need = L.mla_decode_verify_workspace(ref)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(lib().mla_decode_verify_scaled(ctypes.byref(a), _ptr(kv_scales, torch.float32, "kv_scales"),
-                                          int(scale_block), _ptr(workspace, torch.uint8, "workspace"), need,
-                                          _stream(stream)), "mla_decode_verify_scaled")
+    st = L.mla_decode_verify_scaled(ref, _dev_ptr(kv_scales, torch.float32, dev, "kv_scales"), scale_block,
+                                    _dev_ptr(workspace, torch.uint8, dev, "workspace"), need, raw)
+    if st:
+        _check(st, "mla_decode_verify_scaled")
     return out, lse, workspace
 
 
