@@ -4,11 +4,16 @@
 // A unit is one scale block that receives rows: its first new row (offset f in
 // the block) leads it, the rows that follow it in the block belong to it, and
 // the f rows before it were written by earlier calls.  The unit's threads load
-// all of its new rows at once (at most 64 rows of 72 16-byte pieces, 18 pieces
-// a thread), reduce max |x|, choose the scale, and write the codes from the
-// registers that still hold the rows: each value is read once and each code
-// written once, which is the whole traffic unless a scale grows (the earlier
-// rows' codes are then read and rewritten).
+// all of its new rows at once, reduce max |x|, choose the scale, and write the
+// codes from the registers that still hold the rows: each value is read once and
+// each code written once, which is the whole traffic unless a scale grows (the
+// earlier rows' codes are then read and rewritten).
+//
+// Bound by memory, so by the loads in flight: the pieces a thread holds follow
+// from G (a warp per unit up to G = 4, then a CTA of 128 to 512 threads), which
+// keeps the registers low enough for 32 warps per SM.  One kernel with 18
+// pieces for every G ran at one CTA of 8 warps per SM: 109 us for 131,000 rows
+// at G = 64 and 53 us for 20,600 rows at G = 1.
 //
 // Scale: 2^k, the smallest with max |x| <= 448 * 2^k.  With max |x| = m 2^e,
 // m in [1, 2), and 448 = 1.75 * 2^8, that is k = e - 8, plus one when m > 1.75;
@@ -28,9 +33,8 @@ namespace {
 
 constexpr int kRowPieces = 72;   // 16-byte pieces (8 values) of a new row
 constexpr int kMaxGroup = 64;    // rows of a scale block at most
-constexpr int kHeld = 18;        // pieces a thread holds: 64 rows over 256 threads, 8 rows over 32
 constexpr int kMinExp = -100;
-constexpr int kThreads = 256;
+constexpr int kWarpCta = 256;    // threads of a CTA whose warps take a unit each
 
 struct WriteScaledParams {
   const uint4 *x;
@@ -88,11 +92,12 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
 }
 
 // One unit by `kTeam` threads (a warp, or the whole CTA): rows[0 .. n) are its
-// new rows, ascending; first_slot is rows[0]'s cache row.
-template <int kTeam>
+// new rows, ascending, n <= kG; first_slot is rows[0]'s cache row.
+template <int kTeam, int kG>
 __device__ __forceinline__ void write_unit(const WriteScaledParams &p, const int *rows, int n, int first_slot, int t,
                                            uint32_t *team_max) {
   constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int kHeld = (kG * kRowPieces + kTeam - 1) / kTeam;  // pieces a thread holds
   const int pieces = n * kRowPieces;
   uint4 v[kHeld];
 #pragma unroll
@@ -203,8 +208,9 @@ __device__ __forceinline__ int members(const WriteScaledParams &p, int r0, int f
   return n;
 }
 
-// A CTA per unit: scale blocks of more than 8 rows.
-__global__ void __launch_bounds__(kThreads) write_scaled_cta(const WriteScaledParams p) {
+// A CTA per unit: scale blocks of 8 rows or more.
+template <int kThreads, int kG>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(const WriteScaledParams p) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int s_lead[kMaxGroup], s_slot[kMaxGroup], s_rows[kMaxGroup], s_n, s_units;
@@ -233,18 +239,19 @@ __global__ void __launch_bounds__(kThreads) write_scaled_cta(const WriteScaledPa
       if (lane == 0) s_n = n;
     }
     __syncthreads();
-    write_unit<kThreads>(p, s_rows, s_n, s_slot[u], tid, s_max);
+    write_unit<kThreads, kG>(p, s_rows, s_n, s_slot[u], tid, s_max);
     __syncthreads();
   }
 }
 
-// A warp per unit: scale blocks of up to 8 rows.
-__global__ void __launch_bounds__(kThreads) write_scaled_warp(const WriteScaledParams p) {
+// A warp per unit: scale blocks of up to 4 rows.
+template <int kG>
+__global__ void __launch_bounds__(kWarpCta, 4) write_scaled_warp(const WriteScaledParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  __shared__ int s_rows[kThreads / 32][8];
+  __shared__ int s_rows[kWarpCta / 32][kG];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp) * p.window;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kWarpCta / 32) + warp) * p.window;
   if (r0 >= p.num_rows) return;
   const int r_end = static_cast<int>(min(static_cast<int64_t>(p.num_rows), r0 + p.window));
   int slot;
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) write_scaled_warp(const WriteScaledP
     lead &= lead - 1;
     const int first_slot = __shfl_sync(0xffffffffu, slot, l);
     const int n = members(p, static_cast<int>(r0) + l, first_slot, lane, s_rows[warp]);
-    write_unit<32>(p, s_rows[warp], n, first_slot, lane, nullptr);
+    write_unit<32, kG>(p, s_rows[warp], n, first_slot, lane, nullptr);
     __syncwarp();
   }
 }
@@ -309,18 +316,26 @@ extern "C" mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, cons
   p.num_rows = num_rows;
   p.log_g = __builtin_ctz(static_cast<unsigned>(scale_block));
   p.num_cache_rows = static_cast<int>(num_cache_rows);
-  const bool by_cta = scale_block > 8;
-  // rows per team: one while the GPU holds a team for every row, then as many
-  // as keep it at two full waves, within the list of leaders (64) or a warp
-  const int teams = sms * (by_cta ? 8 : 64);
-  const int most = by_cta ? kMaxGroup : 32;
+  const bool by_cta = scale_block >= 8;
+  // Rows per team: one while the GPU holds a team for every row (so that a
+  // step's few tokens spread out), then as many as keep it at two full waves,
+  // within the list of leaders (64) or a warp.
+  const int team_warps = scale_block == kMaxGroup ? 16 : scale_block >= 16 ? 8 : by_cta ? 4 : 1;
+  const int teams = sms * 64 / team_warps, most = by_cta ? kMaxGroup : 32;
   int window = num_rows / teams;
   window = window < 1 ? 1 : (window > most ? most : window);
   p.window = window;
-  const int per_cta = by_cta ? window : window * (kThreads / 32);
+  const int per_cta = by_cta ? window : window * (kWarpCta / 32);
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_rows) + per_cta - 1) / per_cta));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  e = by_cta ? launch_pdl(write_scaled_cta, grid, dim3(kThreads), 0, s, p)
-             : launch_pdl(write_scaled_warp, grid, dim3(kThreads), 0, s, p);
+  switch (scale_block) {
+    case 1: e = launch_pdl(write_scaled_warp<1>, grid, dim3(kWarpCta), 0, s, p); break;
+    case 2: e = launch_pdl(write_scaled_warp<2>, grid, dim3(kWarpCta), 0, s, p); break;
+    case 4: e = launch_pdl(write_scaled_warp<4>, grid, dim3(kWarpCta), 0, s, p); break;
+    case 8: e = launch_pdl(write_scaled_cta<128, 8>, grid, dim3(128), 0, s, p); break;
+    case 16: e = launch_pdl(write_scaled_cta<256, 16>, grid, dim3(256), 0, s, p); break;
+    case 32: e = launch_pdl(write_scaled_cta<256, 32>, grid, dim3(256), 0, s, p); break;
+    default: e = launch_pdl(write_scaled_cta<512, 64>, grid, dim3(512), 0, s, p); break;
+  }
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "write_kv_scaled launch");
 }
