@@ -65,18 +65,21 @@ __device__ __forceinline__ int scale_exp(uint32_t bits) {
 
 __device__ __forceinline__ float pow2f(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
-__device__ __forceinline__ uint32_t quantise4(uint32_t a, uint32_t b, float inv, float scale, bool exact) {
-  float2 lo = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
-  float2 hi = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
-  if (exact) {
-    lo = make_float2(lo.x * inv, lo.y * inv);
-    hi = make_float2(hi.x * inv, hi.y * inv);
-  } else {  // a scale that another writer chose: divide
-    lo = make_float2(lo.x / scale, lo.y / scale);
-    hi = make_float2(hi.x / scale, hi.y / scale);
-  }
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3)) |
-         (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16);
+// Two bf16 values by a factor, as floats.
+__device__ __forceinline__ float2 scaled(uint32_t v, float f) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, y;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmul.rn.f32x2 y, a, b;\n\t"
+      "mov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "r"(v << 16), "r"(v & 0xffff0000u), "f"(f));
+  return y;
+}
+__device__ __forceinline__ uint32_t codes4(float2 lo, float2 hi) {
+  return __byte_perm(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3),
+                     __nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3), 0x5410);
+}
+__device__ __forceinline__ float2 divided(uint32_t v, float d) {
+  return make_float2(__uint_as_float(v << 16) / d, __uint_as_float(v & 0xffff0000u) / d);
 }
 
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
@@ -92,70 +95,79 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
 }
 
 // One unit by `kTeam` threads (a warp, or the whole CTA): rows[0 .. n) are its
-// new rows, ascending, n <= kG; first_slot is rows[0]'s cache row.
+// new rows, ascending, n <= kG; first_slot is rows[0]'s cache row.  A CTA meets
+// at one barrier: team[0 .. kTeam / 32) takes the warps' maxima and team[kTeam /
+// 32] the old scale, in the other of two copies every unit.
 template <int kTeam, int kG>
 __device__ __forceinline__ void write_unit(const WriteScaledParams &p, const int *rows, int n, int first_slot, int t,
-                                           uint32_t *team_max) {
+                                           uint32_t *team) {
   constexpr uint32_t kAll = 0xffffffffu;
   constexpr int kHeld = (kG * kRowPieces + kTeam - 1) / kTeam;  // pieces a thread holds
   const int pieces = n * kRowPieces;
+  const int f = first_slot & ((1 << p.log_g) - 1), block = first_slot >> p.log_g;
   uint4 v[kHeld];
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int c = t + i * kTeam;
+    v[i] = make_uint4(0, 0, 0, 0);
     if (c < pieces) v[i] = p.x[static_cast<int64_t>(rows[c / kRowPieces]) * kRowPieces + c % kRowPieces];
   }
-  const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
-  __nv_bfloat162 m = zero;
+  float old = 0.0f;
+  if (f > 0 && (kTeam == 32 || t == 0)) old = p.scales[block];
+  __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (t + i * kTeam < pieces) m = pair_max(pair_max(pair_max(pair_max(m, v[i].x), v[i].y), v[i].z), v[i].w);
+  for (int i = 0; i < kHeld; ++i) m = pair_max(pair_max(pair_max(pair_max(m, v[i].x), v[i].y), v[i].z), v[i].w);
   uint32_t top = max_bits(m);
   if (top >= 0x7f80) {  // an infinity among them: only finite values count
     top = 0;
+#pragma unroll 1
+    for (int c = t; c < pieces; c += kTeam) {
+      const uint4 u = p.x[static_cast<int64_t>(rows[c / kRowPieces]) * kRowPieces + c % kRowPieces];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (t + i * kTeam < pieces) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-        }
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
       }
+    }
   }
   top = __reduce_max_sync(kAll, top);
   if (kTeam > 32) {
-    if ((t & 31) == 0) team_max[t >> 5] = top;
+    if ((t & 31) == 0) team[t >> 5] = top;
+    if (t == 0) team[kTeam / 32] = __float_as_uint(old);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kTeam / 32; ++w) top = max(top, team_max[w]);
+    top = __reduce_max_sync(kAll, (t & 31) < kTeam / 32 ? team[t & 31] : 0u);
+    old = __uint_as_float(team[kTeam / 32]);
   }
-  const int f = first_slot & ((1 << p.log_g) - 1), block = first_slot >> p.log_g;
   const float want = pow2f(scale_exp(top));
-  const float old = f > 0 ? p.scales[block] : want;
   const float scale = f > 0 ? fmaxf(old, want) : want;
-  const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
-  const float inv = 1.0f / scale;
+  uint2 *dst = p.cache + static_cast<int64_t>(first_slot) * kRowPieces;  // the unit's slots follow one another
+  if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
+    const float inv = 1.0f / scale;
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int c = t + i * kTeam;
-    if (c < pieces) {
-      const int row = c / kRowPieces;  // the unit's slots follow one another
-      p.cache[static_cast<int64_t>(first_slot + row) * kRowPieces + c % kRowPieces] =
-          make_uint2(quantise4(v[i].x, v[i].y, inv, scale, exact), quantise4(v[i].z, v[i].w, inv, scale, exact));
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = t + i * kTeam;
+      if (c < pieces)
+        dst[c] = make_uint2(codes4(scaled(v[i].x, inv), scaled(v[i].y, inv)),
+                            codes4(scaled(v[i].z, inv), scaled(v[i].w, inv)));
+    }
+  } else {  // a scale that another writer chose: divide
+#pragma unroll 1
+    for (int c = t; c < pieces; c += kTeam) {
+      const uint4 u = p.x[static_cast<int64_t>(rows[c / kRowPieces]) * kRowPieces + c % kRowPieces];
+      dst[c] = make_uint2(codes4(divided(u.x, scale), divided(u.y, scale)),
+                          codes4(divided(u.z, scale), divided(u.w, scale)));
     }
   }
   if (f > 0 && scale > old) {
     const float ratio = old / scale;
-    uint2 *prior = p.cache + static_cast<int64_t>(first_slot - f) * kRowPieces;
+    uint2 *prior = dst - f * kRowPieces;
+#pragma unroll 2
     for (int c = t; c < f * kRowPieces; c += kTeam) {
       const uint2 u = prior[c];
       prior[c] = make_uint2(rescale4(u.x, ratio), rescale4(u.y, ratio));
     }
   }
-  if (kTeam > 32) __syncthreads();  // every thread has read the old scale
-  else __syncwarp();
   if (t == 0) p.scales[block] = scale;
 }
 
@@ -213,8 +225,9 @@ template <int kThreads, int kG>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(const WriteScaledParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  __shared__ int s_lead[kMaxGroup], s_slot[kMaxGroup], s_rows[kMaxGroup], s_n, s_units;
-  __shared__ uint32_t s_max[kThreads / 32];
+  __shared__ int s_lead[kMaxGroup], s_slot[kMaxGroup], s_units;
+  __shared__ int s_rows[kThreads / 32][kG];
+  __shared__ uint32_t s_team[2][kThreads / 32 + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.x * p.window, r_end = min(p.num_rows, r0 + p.window);
   if (warp == 0) {
@@ -233,14 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(co
   }
   __syncthreads();
   const int units = s_units;
-  for (int u = 0; u < units; ++u) {
-    if (warp == 0) {
-      const int n = members(p, s_lead[u], s_slot[u], lane, s_rows);
-      if (lane == 0) s_n = n;
-    }
-    __syncthreads();
-    write_unit<kThreads, kG>(p, s_rows, s_n, s_slot[u], tid, s_max);
-    __syncthreads();
+  for (int u = 0; u < units; ++u) {  // every warp finds the unit's rows itself: a barrier less
+    const int n = members(p, s_lead[u], s_slot[u], lane, s_rows[warp]);
+    write_unit<kThreads, kG>(p, s_rows[warp], n, s_slot[u], tid, s_team[u & 1]);
+    __syncwarp();
   }
 }
 
