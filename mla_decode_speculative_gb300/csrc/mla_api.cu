@@ -585,6 +585,10 @@ mla_status mla_decode_verify_scaled(const mla_decode_args *a, const float *kv_sc
               (long long)s.num_cache_rows, scale_block);
     return MLA_ERR_INVALID_ARG;
   }
+  if (static_cast<int64_t>(s.subpage_stride) * s.page_size > INT32_MAX - 512) {  // a tile past it is still an int
+    set_error("mla_decode_verify_scaled: %d pages of %d tokens overflow int32 positions", s.subpage_stride, s.page_size);
+    return MLA_ERR_UNSUPPORTED;
+  }
   const WorkspaceLayout lay = decode_workspace_layout(s);
   if (workspace == nullptr || workspace_bytes < lay.total || !is_aligned(workspace, 256)) {
     set_error("mla_decode_verify_scaled: workspace of %zu bytes (256-byte aligned) needed, got %zu at %p",

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) wait(misc.work_empty[k % kWorkRing], (k / kWorkRing) ^ 1u);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       bool found = false;
-      int t_lo = 0, t_hi = 0, seg = 0, fill_hi = S;
+      int t_lo = 0, t_hi = 0, seg = 0, fill_hi = S, unit_len = 0;
       while (ok && split.chunk < split.n_chunks && vb < n_vb) {
         const int v = vb / p.num_reqs, b = vb - v * p.num_reqs;
         if (loaded != vb) {  // the request's rows: lane t holds the length of row t (t < 32)
@@ -572,13 +572,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         found = true;
         const int row_begin = this_rb * kRows;
         const int n_rows = min(kRows, qlen * p.num_heads - row_begin);
+        unit_len = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int c = lane + 32 * h, t = (row_begin + c) / p.num_heads;
           int l = __shfl_sync(0xffffffffu, my_len, t < 32 ? t : 0);
           if (t >= 32 && c < n_rows) l = p.row_len[static_cast<int64_t>(v) * p.num_rows + q0 + t];
-          e.lens[c] = c < n_rows ? min(max(l, 0), p.max_len) : 0;
+          l = c < n_rows ? min(max(l, 0), p.max_len) : 0;
+          e.lens[c] = l;
+          unit_len = max(unit_len, l);
         }
+        // a token that only other units' rows see is not in this unit's tiles: its code may be a NaN
+        unit_len = __reduce_max_sync(0xffffffffu, unit_len);
+        t_hi = min(t_hi, (unit_len + kTile - 1) / kTile);
+        t_lo = min(t_lo, t_hi);
         if (lane == 0) {
           e.stop = 0;
           e.b = vb;
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           e.row_base = (v * p.num_rows + q0) * p.num_heads + row_begin;
           e.n_rows = n_rows;
           e.seg_lo = t_lo * kTile;
-          e.seg_hi = min(t_hi * kTile, len);
+          e.seg_hi = min(t_hi * kTile, unit_len);
           e.n_tiles = t_hi - t_lo;
           if (t_hi > t_lo) prefetch_l2(p.q + static_cast<int64_t>(q0 * p.num_heads + row_begin) * 576, n_rows * 1152);
         }
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) mbar_arrive(smem_u32(&misc.work_full[k % kWorkRing]));
       if (t_hi == t_lo) continue;
-      const int seg_lo = t_lo * kTile, seg_hi = min(t_hi * kTile, len);
+      const int seg_lo = t_lo * kTile, seg_hi = min(t_hi * kTile, unit_len);
       const int32_t *pages = p.subpage_table + static_cast<int64_t>(vb) * p.subpage_stride;
       const int last_page = (seg_hi - 1) >> lg_p;
       int win = seg_lo >> lg_p;         // lane l holds the id of page win + l
@@ -1004,8 +1011,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 6; ++q)
             st_shared_v2(stage + kRopeOff + (q >> 1) * kPBlock + (at ^ ((q & 1) * 16)), p1[2 * q], p1[2 * q + 1]);
           if (l_tile != l_tile) {
-            // A NaN code: the rows that see its token are NaN by their sums, and its values must not
-            // meet the zero weights of the others.
+            // A NaN code: the rows that see its token are NaN by their sums, and it must not meet the
+            // zero weights of the others.  (Or a score beyond float32, which spoils its own row only.)
+            wait(misc.full[g % kStages], g / kStages);  // long there: what the copies wrote, to this thread
 #pragma unroll 1
             for (int t = 0; t < 48; ++t) {
               const int b = t >> 3;  // 16-token block
@@ -1015,8 +1023,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                            : "r"(stage + kRopeOff + (b >> 1) * kPBlock + (at ^ ((b & 1) * 16)) + (t & 7))
                            : "memory");
               if ((code & 0x7fu) > 0x7cu)
-                for (int c = 0; c < 32; ++c)
-                  st_shared_v4(stage + (c >> 3) * kVChunk + (16 * b + 8 * term + (t & 7)) * 128 + (c & 7) * 16, 0, 0, 0, 0);
+                for (int c = 0; c < 128; ++c) {
+                  const uint32_t word =
+                      stage + (c >> 5) * kVChunk + (16 * b + 8 * term + (t & 7)) * 128 + (c & 31) * 4;
+                  uint32_t v;
+                  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(word) : "memory");
+                  const uint32_t nan = __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  if (nan) asm volatile("st.shared.u32 [%0], %1;" ::"r"(word), "r"(v & ~nan) : "memory");
+                }
             }
           }
         }
@@ -1174,7 +1188,7 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   p.max_qlen = a.max_qlen;
   p.num_rows = a.num_rows;
   p.max_len = a.subpage_stride * a.page_size;
-  // positions (tiles and one per unit) are counted in int32, at the static bound
+  // positions (a unit's tiles and its cost) are counted in int32, at the static bound
   const int64_t units = static_cast<int64_t>(a.num_reqs) * p.num_views * p.row_blocks;
   if (units * ((p.max_len + kTile - 1) / kTile + kPartCost) > INT32_MAX) {
     set_error("mla_decode_verify_scaled: %lld row blocks of up to %d tokens overflow int32 positions", (long long)units,

@@ -89,6 +89,30 @@ def test_tables_of_many_requests_and_many_rows():
     assert mla.get_device_error() == 0
 
 
+@pytest.mark.parametrize("W,rank,I,at", [(1, 0, 1, 0), (1, 0, 1, 1), (2, 1, 3, 0), (5, 0, 16, 1)])
+def test_tables_of_many_rows(W, rank, I, at):
+    """More rows than a thread each: several requests, some short, shards, rows behind the last one, and a
+    slot map that starts off a 16-byte boundary."""
+    ql = np.array([30001, 3, 0, 1, 40000, 2, 5])
+    prev = np.array([5, 90, 33, 0, 0, 17, 1000])
+    seq = prev + ql - np.array([2, 40, 30, 0, 0, 0, 1])
+    bs, width = 24, 2000
+    pool = sum(-(-ref.local_len(int(n), W, rank, I) // bs) for n in np.maximum(prev, seq)) + 3
+    table, ring, state = table_state(prev, pool, width, bs, W, rank, I, head=pool - 2, seed=4)
+    T = int(ql.sum()) + 7
+    assert T > 65536
+    want = ref.update_tables(prev, seq, indptr(ql), table, ring, state, bs, T, W, rank, I)
+    room = torch.full((T + 8,), 77, dtype=torch.int32, device="cuda")
+    d_table, d_ring = i32(table), i32(ring)
+    slots, out = mla.update_block_tables(i32(prev), i32(seq), i32(indptr(ql)), d_table, d_ring, i32(state), bs, T,
+                                         slot_map=room[at:at + T], world_size=W, rank=rank, interleave=I)
+    assert mla.get_device_error() == 0
+    got = d_table.cpu().numpy(), d_ring.cpu().numpy(), tuple(out.tolist()), slots.cpu().numpy()
+    for g, w in zip(got, want):
+        assert np.array_equal(g, w)
+    assert (room[:at] == 77).all() and (room[at + T:] == 77).all()
+
+
 def test_tables_are_the_same_when_called_again():
     prev, seq, ql = [20, 40, 0, 9], [24, 10, 33, 0], [4, 2, 33, 0]
     table, ring, state = table_state(prev, 24, 6, 8, head=20)
@@ -428,6 +452,85 @@ def test_attention_nan_stays_with_its_rows(S):
     check_rows(out, lse, args, 16, nan_rows)
 
 
+@pytest.mark.parametrize("H,S", [(64, 1), (64, 4), (128, 1), (128, 3), (24, 2)])
+def test_attention_nan_of_a_later_draft(H, S):
+    """A NaN code in the last drafts' tokens, with row blocks whose rows all end before them."""
+    L, ql = np.array([300, 97, 193]), np.array([6, 3, 4])
+    args = list(attention_inputs(L, ql, H, 32, 32, 17 + H))
+    codes, sub, P = args[1], args[5][0], args[6]
+    at = lambda b, j: int(sub[b, j // P]) * P + j % P
+    codes[at(0, 298), 3] = 0x7F
+    codes[at(1, 96), 511] = 0xFF       # the only token of a tile
+    codes[at(2, 191), 575] = 0x7F      # rope, the last token of a tile
+    nan_rows = np.zeros((13, H), bool)
+    nan_rows[[4, 5, 8, 11, 12]] = True
+    out, lse, _ = run_attention(*args[:3], 32, *args[3:], S, 6)
+    assert mla.get_device_error() == 0
+    check_rows(out, lse, args, 32, nan_rows)
+
+
+@pytest.mark.parametrize("S", [1, 4])
+def test_attention_scores_beyond_float32_spoil_their_row_only(S):
+    """A query of +-3e38, whose scores have no float32 value, beside ordinary ones in its row block."""
+    L, ql = np.array([400, 130]), np.array([3, 1])
+    args = list(attention_inputs(L, ql, 16, 16, 16, 18))
+    args[2] = torch.ones_like(args[2])
+    sign = torch.where(torch.randn(576, generator=torch.Generator().manual_seed(3)) < 0, -1.0, 1.0)
+    args[0][1, 5] = (3e38 * sign).to(torch.bfloat16)
+    args[0][:, :5] *= 0.02
+    args[0][:, 6:] *= 0.02
+    nan_rows = np.zeros((4, 16), bool)
+    nan_rows[1, 5] = True
+    out, lse, _ = run_attention(*args[:3], 16, *args[3:], S, 3)
+    assert mla.get_device_error() == 0
+    check_rows(out, lse, args, 16, nan_rows)
+
+
+def test_attention_queries_off_a_32_byte_boundary():
+    L, ql = np.array([260, 500]), np.array([3, 5])
+    args = attention_inputs(L, ql, 20, 32, 16, 19)
+    first = run_attention(*args[:3], 16, *args[3:], 3, 5)
+    room = torch.empty(args[0].numel() + 8, dtype=torch.bfloat16, device="cuda")
+    q = room[8:].view(args[0].shape)
+    q.copy_(args[0])
+    assert q.data_ptr() % 32 == 16
+    out, lse, _ = mla.decode_verify_scaled(q, args[1].cuda(), args[2].cuda(), 16, i32(args[3]), i32(args[4][0]),
+                                           i32(args[5][0]), args[6], 3, 5, SM)
+    assert mla.get_device_error() == 0
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    check_rows(out, lse, args, 16)
+
+
+@pytest.mark.parametrize("G", [4, 64])
+def test_cache_past_32_bit_offsets(G):
+    """Rows on both sides of byte 2^32 of the codes: written through the slot map, then read."""
+    bs, L, H = 64, 900, 16
+    edge = (1 << 32) // 576 // bs      # the block that byte 2^32 lies in
+    blocks = edge + 10
+    codes = torch.zeros((blocks * bs, 576), dtype=torch.uint8, device="cuda")
+    scales = torch.ones(blocks * bs // G, device="cuda")
+    mine = np.array([edge - 3, blocks - 1, edge, 0, edge + 1, 5, edge - 1, edge + 3, edge + 7, 1, edge + 2, 9, edge + 5,
+                     2, edge + 4])
+    j = np.arange(L)
+    slots = mine[j // bs] * bs + j % bs
+    x = new_rows(L, G)
+    mla.write_kv_scaled(x.cuda(), i32(slots), codes, scales, G)
+    small_c, small_s = ref.write_scaled(x.double().numpy(), j, np.zeros((15 * bs, 576), np.uint8),
+                                        np.ones(15 * bs // G), G)
+    pick = torch.as_tensor(mine).cuda()
+    assert np.array_equal(codes.view(blocks, bs, 576)[pick].view(-1, 576).cpu().numpy(), small_c)
+    assert np.array_equal(scales.view(blocks, bs // G)[pick].view(-1).cpu().numpy(), small_s)
+    g = torch.Generator().manual_seed(4)
+    q = (torch.randn((2, H, 576), generator=g) * 0.05).to(torch.bfloat16)
+    ind, row_len = np.array([0, 2]), np.array([[L - 1, L]], np.int32)
+    out, lse, _ = mla.decode_verify_scaled(q.cuda(), codes, scales, G, i32(ind), i32(row_len[0]),
+                                           i32(mine[None]), bs, 4, 2, SM)
+    assert mla.get_device_error() == 0
+    args = (q, torch.tensor(small_c), torch.tensor(small_s, dtype=torch.float32), ind, row_len,
+            np.arange(15, dtype=np.int32)[None, None], bs)
+    check_rows(out, lse, args, G)
+
+
 def test_attention_outliers():
     """Peaked rows (one token holds almost everything), flat rows, and a row of a hundred far tokens
     under one large one: probabilities keep their relative precision."""
@@ -585,6 +688,40 @@ def test_serving_steps(W, graph):
         # one more rounding of each shard's state to bf16 when states are merged
         assert (err <= ref.out_bound(o, mass, far) + (W > 1) * 2.0 ** -8 * mass).all()
         assert np.abs(lse.cpu().numpy()[:n_rows] - l).max() <= LSE_TOL
+
+
+def test_append_that_ran_out_of_blocks_is_undone():
+    """Too few free blocks: the error, blocks and lengths back as before, then a smaller step, and every
+    block returned in the end.  A refused call changes nothing either."""
+    c = runner.PagedLatentCache(num_reqs=2, num_rows=64, num_blocks=6, block_size=16, max_kv_len=96, scale_block=16)
+    x = new_rows(64, 1).cuda()
+    c.append(x, i32([40, 10]), i32([0, 40, 50]))
+    held = c.block_table.clone(), c.ring.clone(), c.lens.clone()
+    codes = c.codes.clone()
+    assert mla.get_device_error() == 0 and held[1].tolist() == [4, 2]
+    c.append(x, i32([70, 40]), i32([0, 30, 60]))
+    assert mla.get_device_error() == 7
+    c.undo()
+    assert torch.equal(c.ring, held[1]) and torch.equal(c.lens, held[2])
+    for bad in (lambda: c.append(x.float(), i32([41, 10]), i32([0, 1, 1])),
+                lambda: c.append(x, i32([41, 10]).float(), i32([0, 1, 1])),
+                lambda: c.append(x, i32([41]), i32([0, 1]))):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+        assert torch.equal(c.ring, held[1]) and torch.equal(c.lens, held[2])
+    slots = c.append(x, i32([41, 40]), i32([0, 1, 31])).cpu().numpy()
+    assert mla.get_device_error() == 0 and c.ring.tolist() == [0, 0]
+    table = c.block_table.cpu().numpy()
+    assert slots[0] == table[0, 2] * 16 + 8 and (slots[31:] == -1).all()
+    assert list(slots[1:31]) == [table[1, n // 16] * 16 + n % 16 for n in range(10, 40)]
+    for b, n in ((0, 40), (1, 10)):   # the tokens before are where they were
+        at = held[0][b].cpu().numpy()[np.arange(n) // 16] * 16 + np.arange(n) % 16
+        assert np.array_equal(table[b, :-(-n // 16)], held[0][b, :-(-n // 16)].cpu().numpy())
+        whole = torch.as_tensor(at[:n // 16 * 16]).cuda()
+        assert torch.equal(c.codes[whole], codes[whole])
+    c.append(x, i32([0, 0]), i32([0, 0, 0]))
+    assert mla.get_device_error() == 0 and c.ring[1].item() == 6
+    assert sorted(c.free_ring.tolist()) == list(range(6))
 
 
 def test_two_streams_and_two_graphs_at_once():
