@@ -250,9 +250,9 @@ extern "C" mla_status mla_update_block_tables(const mla_table_args *a, mla_strea
     return MLA_ERR_INVALID_ARG;
   }
   if (a->qo_indptr == nullptr || a->free_ring == nullptr || a->ring_in == nullptr || a->ring_out == nullptr ||
-      a->ring_in == a->ring_out || (a->num_rows > 0 && a->slot_map == nullptr) ||
+      (a->ring_out < a->ring_in + 2 && a->ring_in < a->ring_out + 2) || (a->num_rows > 0 && a->slot_map == nullptr) ||
       (a->num_reqs > 0 && (a->prev_lens == nullptr || a->seq_lens == nullptr || a->block_table == nullptr))) {
-    set_error("mla_update_block_tables: null pointer, or ring_out is ring_in");
+    set_error("mla_update_block_tables: null pointer, or ring_out overlaps ring_in");
     return MLA_ERR_INVALID_ARG;
   }
   if (a->num_reqs > kMaxTableReqs) {

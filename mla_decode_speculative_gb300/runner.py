@@ -122,8 +122,8 @@ class PagedLatentCache:
 
     def __init__(self, *, num_reqs: int, num_rows: int, num_blocks: int, block_size: int, max_kv_len: int,
                  scale_block: int = 16, world_size: int = 1, rank: int = 0, interleave: int = 1, device="cuda"):
-        if block_size % scale_block:
-            raise ValueError("scale_block must divide block_size")
+        if scale_block not in (1, 2, 4, 8, 16, 32, 64) or block_size % scale_block:
+            raise ValueError("scale_block must be a power of two up to 64 that divides block_size")
         dev = torch.device(device)
         i32 = dict(dtype=torch.int32, device=dev)
         self.num_rows, self.block_size, self.scale_block = num_rows, block_size, scale_block
@@ -133,9 +133,11 @@ class PagedLatentCache:
         self.scales = torch.ones(num_blocks * block_size // scale_block, dtype=torch.float32, device=dev)
         self.block_table = torch.full((num_reqs, max(1, -(-max_kv_len // block_size))), -1, **i32)
         self.free_ring = torch.arange(num_blocks, **i32)
-        self.ring = torch.tensor([0, num_blocks], **i32)   # {head, count} of the free blocks
-        self.ring_next = torch.empty(2, **i32)
-        self.lens = torch.zeros(num_reqs, **i32)           # tokens whose blocks are held
+        # {head, count} of the free blocks and the tokens whose blocks each request holds; before the last append
+        self._now = torch.zeros(2 + num_reqs, **i32)
+        self._now[1] = num_blocks
+        self._before = self._now.clone()
+        self.ring, self.lens = self._now[:2], self._now[2:]
         self.slot_map = torch.empty(num_rows, **i32)
 
     def append(self, kv_new: torch.Tensor, seq_lens: torch.Tensor, qo_indptr: torch.Tensor, stream=None):
@@ -145,14 +147,29 @@ class PagedLatentCache:
         if kv_new.shape[0] != self.num_rows:
             raise ValueError("kv_new must have num_rows rows")
         s = torch.cuda.current_stream() if stream is None else stream
-        mla.update_block_tables(self.lens, seq_lens, qo_indptr, self.block_table, self.free_ring, self.ring,
-                                self.block_size, self.num_rows, ring_out=self.ring_next, slot_map=self.slot_map,
-                                stream=s, **self.shard)
-        mla.write_kv_scaled(kv_new, self.slot_map, self.codes, self.scales, self.scale_block, stream=s)
+        if seq_lens.shape != self.lens.shape:
+            raise ValueError("seq_lens must have num_reqs entries")
         with torch.cuda.stream(s):
-            self.ring.copy_(self.ring_next)
+            self._before.copy_(self._now)
+        try:
+            mla.update_block_tables(self._before[2:], seq_lens, qo_indptr, self.block_table, self.free_ring,
+                                    self._before[:2], self.block_size, self.num_rows, ring_out=self.ring,
+                                    slot_map=self.slot_map, stream=s, **self.shard)
+            mla.write_kv_scaled(kv_new, self.slot_map, self.codes, self.scales, self.scale_block, stream=s)
+        except Exception:
+            self.undo(s)
+            raise
+        with torch.cuda.stream(s):
             self.lens.copy_(seq_lens)
         return self.slot_map
+
+    def undo(self, stream=None):
+        """Blocks and lengths as before the last append: after one that the free blocks did not
+        suffice for (MLA_DEV_NO_FREE_BLOCK), before appending less.  The rows that it wrote stay
+        written, so a request's next new tokens start no later than they did in it."""
+        s = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(s):
+            self._now.copy_(self._before)
 
 
 class StepIO:

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import scaled_reference as ref
-from mla_decode_speculative_gb300 import build, mla
+from mla_decode_speculative_gb300 import build, mla, runner
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mla_gb300.h")
 VP = ctypes.c_void_p
@@ -39,7 +39,8 @@ def _tables(**kw):
     (dict(block_table_stride=0), INVALID), (dict(num_reqs=1 << 14, block_table_stride=1 << 18), INVALID),
     (dict(prev_lens=None), INVALID), (dict(seq_lens=None), INVALID), (dict(qo_indptr=None), INVALID),
     (dict(block_table=None), INVALID), (dict(free_ring=None), INVALID), (dict(ring_in=None), INVALID),
-    (dict(ring_out=None), INVALID), (dict(ring_out=256), INVALID), (dict(slot_map=None), INVALID),
+    (dict(ring_out=None), INVALID), (dict(ring_out=256), INVALID), (dict(ring_out=252), INVALID),
+    (dict(ring_out=260), INVALID), (dict(slot_map=None), INVALID),
     (dict(num_reqs=16385), UNSUPPORTED)])
 def test_table_refusals(L, change, status):
     assert L.mla_update_block_tables(ctypes.byref(_tables(**change)), None) == status
@@ -84,6 +85,7 @@ def _decode(**kw):
     (dict(), 0, UNSUPPORTED), (dict(), 12, UNSUPPORTED), (dict(), 32, UNSUPPORTED),
     (dict(page_size=128, num_cache_rows=128), 128, UNSUPPORTED), (dict(num_cache_rows=72), 16, INVALID),
     (dict(page_size=4), 4, UNSUPPORTED), (dict(num_segments=1025), 16, UNSUPPORTED), (dict(q=264), 16, INVALID),
+    (dict(subpage_stride=(1 << 28) - 1, page_size=8), 8, UNSUPPORTED),
     (dict(wait_cycles=-1), 16, INVALID), (dict(sm_scale=0.0), 16, INVALID), (dict(), 16, WORKSPACE)])
 def test_decode_refusals(L, change, G, status):
     a = _decode(**change)
@@ -111,6 +113,13 @@ def test_wrapper_refusals_on_the_host():
         with pytest.raises(ValueError):
             mla._check_scaled(*bad)
     mla._check_scaled(cache, scales, 16)
+
+
+@pytest.mark.parametrize("scale_block,block_size", [(0, 16), (3, 48), (128, 128), (16, 24), (32, 16)])
+def test_cache_refuses_scale_blocks(scale_block, block_size):
+    with pytest.raises(ValueError, match="scale_block"):
+        runner.PagedLatentCache(num_reqs=1, num_rows=1, num_blocks=1, block_size=block_size, max_kv_len=48,
+                                scale_block=scale_block, device="cpu")
 
 
 def test_reference_encoder_is_the_oracles():
