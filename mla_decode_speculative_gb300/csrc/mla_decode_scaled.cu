@@ -25,12 +25,12 @@
 //    so the running reference m bounds the weights whatever the scales are.
 //
 // Work: (row view, request, block of up to 64 query rows) units in 96-token
-// tiles.  The tiles of all units plus one overhead position per unit, end to
-// end, are cut into one equal chunk per CTA (one CTA per SM), never more than
-// S chunks per unit; a chunk's part of a unit is one of its split-K segments
-// (S = 1: whole units, by the chunk their first tile lies in).  Every CTA sums
-// up the positions for itself and its producer walks on from its chunk's first
-// unit, so nothing is tabulated and any number of units fits.
+// tiles.  The tiles of all units plus a few overhead positions per unit
+// (part_cost), end to end, are cut into one equal chunk per CTA (one CTA per
+// SM), never more than S chunks per unit; a chunk's part of a unit is one of its
+// split-K segments (S = 1: whole units, by the chunk their first tile lies in).
+// Every CTA sums up the positions for itself and its producer walks on from its
+// chunk's first unit, so nothing is tabulated and any number of units fits.
 //
 // Operands.  q1 and q2 of 16 rows share a quarter of the 128 TMEM lanes (lane
 // 32 w + i: q1 of row 16 w + i, lane 32 w + 16 + i: its q2), 144 columns, as
@@ -42,19 +42,30 @@
 // P^T, the B operand there, is 32-token blocks [64 rows x 32 B] (32-byte
 // swizzle): the first term's blocks replace the tile's rope chunk, which S has
 // used by then, the second term's have 6 KB of their own.
-// TMEM: Q 0-143, O^T 144-399, S 400-495.
+// TMEM: Q 0-143, O^T 144-399, S 400-495; 96 tokens is the widest S that the
+// columns left by Q and O^T hold.
 //
-// What bounds it: an instruction of 128 x N x 32 takes 53-63 cycles for N up to
-// 96 or so and 64 at N = 128 (measured), so a tile's 18 + 24 instructions take
-// about 2550 cycles = 1.3 us, against 1.24 us for its 55 KB at the HBM rate; 96
-// tokens is the widest S that the columns left by Q and O^T hold.  Tile g's
-// products are ordered QK(g + 1), PV(g): the softmax of a tile has the time of
-// one PV and one QK.  Two tiles are in use at any time and two in flight.
+// Warps.  0-7: queries into TMEM, softmax, epilogue; two groups of four take
+// turns with the tiles, so one group's loads and exponentials run beside the
+// other's (all eight on each tile: 2665 cycles a tile, in turns 2390).  8: work
+// and TMA.  9: S = Q K^T, 10: O^T += V^T P^T, an elected thread each, so that
+// neither waits for the other's barriers.  11: the tiles' scales.  S and the
+// second term of P^T have one buffer each: tile g + 1's S is issued when tile
+// g's has been read, its second term is written when tile g's products are done.
 //
-// Warps 0-7: queries into TMEM, softmax, epilogue (TMEM quarter w % 4, token
-// half w / 4); 8: work and TMA; 9: MMA; 10: the tiles' scales.  Every wait is
-// bounded; one that runs out records MLA_DEV_WAIT_TIMEOUT, all roles drain
-// without skipping a barrier, TMEM is freed and the kernel returns.
+// What bounds it.  An instruction of 128 x N x 32 takes 53-63 cycles for N up to
+// 96 and 64 at N = 128 (measured), a tile's 18 + 24 about 2500 if nothing
+// overlapped; the steady state is 2390 cycles a tile, 1.25 us, against 1.24 us for
+// the SM's share of the HBM rate (55 KB at 6.76 TB/s / 152).  16 requests of
+// 131,072 tokens take 248 us (4.9 TB/s) and run at the power limit.  Short calls
+// are latency: about 12 us from the call's start to the first S (lengths, split,
+// queries and the first tiles through L2 at once), 5 us from the last tile to the
+// partial output, and the merge kernel; 32 requests of 1,024 to 8,192 tokens take
+// 43 us, 13 of them at the HBM rate.  The loops are kept small: the instruction
+// cache holds about 32 KB for four loops that run at once.
+//
+// Every wait is bounded; one that runs out records MLA_DEV_WAIT_TIMEOUT, all
+// roles drain without skipping a barrier, TMEM is freed and the kernel returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -86,7 +97,6 @@ constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10, kScaleWarp = 11;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemQ = 0, kTmemO = 144, kTmemS = 400, kTmemCols = 512;
 constexpr int kWorkRing = 3;
-constexpr int kPartCost = 6;         // what a part costs besides its tiles (queries, sums, epilogue), in tiles
 constexpr float kThreshold = 3.0f;   // the reference moves when a weight exceeds 2^3 of it
 constexpr float kTop = 11.0f;        // a weight at the reference is held as 2^11 .. 2^12: at most 2^15 < 57344
 constexpr float kInvTop = 4.8828125e-4f;  // 2^-kTop
@@ -100,7 +110,6 @@ struct Part {
   int rb, seg, fill_hi;     // slots seg + 1 .. fill_hi - 1 of the unit get no part: mark them empty
   int q_row, row_base, n_rows;
   int seg_lo, seg_hi, n_tiles;
-  int pad;
   int lens[kRows];          // visible tokens of each row
 };
 
@@ -340,13 +349,19 @@ __device__ __forceinline__ int request_len(const Params &p, int v, int b, int &q
   }
   return len;
 }
+// What a part costs besides its tiles (queries, sums, epilogue), in tiles, by the
+// request's query rows: the second part of a CTA takes 11.7 us at 64 rows and 7.6
+// at 12 to 36, a tile 1.3 to 1.6.  With one for all, 8 against 6 is 42.2 against
+// 43.4 us for 32 requests of 64 rows, but 85.2 against 83.6 for 64 of 12 to 36.
+__host__ __device__ __forceinline__ int part_cost(int rows) { return 4 + (rows < kRows ? rows : kRows) / 16; }
 // Positions of a (view, request): for each of its row blocks a part's cost and
 // its tiles, nothing when no row sees a token.
 __device__ __forceinline__ int positions(const Params &p, int vb, int &tiles) {
   int qlen;
   const int len = request_len(p, vb / p.num_reqs, vb % p.num_reqs, qlen);
   tiles = (len + kTile - 1) / kTile;
-  return tiles > 0 ? (qlen * p.num_heads + kRows - 1) / kRows * (tiles + kPartCost) : 0;
+  const int rows = qlen * p.num_heads;
+  return tiles > 0 ? (rows + kRows - 1) / kRows * (tiles + part_cost(rows)) : 0;
 }
 
 struct Split {
@@ -394,7 +409,7 @@ __device__ Split make_split(const Params &p, Misc &misc) {
   s.hi = static_cast<int>(static_cast<long long>(s.chunk + 1) * s.total / s.n_chunks);
   if (s.chunk == s.n_chunks - 1) s.hi = s.total + 1;  // units without tiles at the very end
   // the one with first position < lo <= end, or the very first: by one scan when
-  // every thread has one (view, request), else by scans of 352
+  // every thread has one (view, request), else by scans of kThreads
   int carry = 0;
   for (int v0 = 0; v0 < n_vb && s.chunk < s.n_chunks; v0 += kThreads) {
     const int vb = v0 + tid;
@@ -541,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0 && clipped) note(p.err, MLA_DEV_LEN_BOUND);
           // row blocks that end before the chunk
           if (tiles > 0 && u_pos < split.lo) {
-            rb = (split.lo - u_pos) / (tiles + kPartCost);
-            u_pos += rb * (tiles + kPartCost);
+            rb = (split.lo - u_pos) / (tiles + part_cost(qlen * p.num_heads));
+            u_pos += rb * (tiles + part_cost(qlen * p.num_heads));
           }
         }
         const int blocks = (qlen * p.num_heads + kRows - 1) / kRows;
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if (u_pos >= split.hi) break;
-        const int here = u_pos, start = here + (tiles > 0 ? kPartCost : 0), end = start + tiles;
+        const int here = u_pos, start = here + (tiles > 0 ? part_cost(qlen * p.num_heads) : 0), end = start + tiles;
         if (start >= split.hi) break;
         u_pos = end;
         const int this_rb = rb++;
@@ -640,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int32_t row = static_cast<int32_t>(p.num_cache_rows);  // past the last row: zeros
             if (id < 0 || (static_cast<int64_t>(id) + 1) << lg_p > p.num_cache_rows) note(p.err, MLA_DEV_BAD_SUBPAGE);
             else row = (id << lg_p) + (t & (P - 1));
-            tma_load_2d((j == 0 ? c_dst[0] : c_dst[1]) + st * kStageBytes, x < 512 ? &tm_v : &tm_r, bar, x, row, policy);
+            const uint32_t dst = (j == 0 ? c_dst[0] : c_dst[1]) + st * kStageBytes;
+            tma_load_2d(dst, x < 512 ? &tm_v : &tm_r, bar, x, row, policy);
           }
         }
         armed |= 1u << st;
@@ -957,12 +973,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int a = 16 * q + 2 * u, b = a + 8;
-              const float2 mine = make_float2(__uint_as_float(term ? v[b] : v[a]), __uint_as_float(term ? v[b + 1] : v[a + 1]));
-              const float2 other = make_float2(__shfl_xor_sync(0xffffffffu, __uint_as_float(term ? v[a] : v[b]), 16),
-                                               __shfl_xor_sync(0xffffffffu, __uint_as_float(term ? v[a + 1] : v[b + 1]), 16));
+              const float2 mine = make_float2(__uint_as_float(term ? v[b] : v[a]),
+                                              __uint_as_float(term ? v[b + 1] : v[a + 1]));
+              const uint32_t give0 = term ? v[a] : v[b], give1 = term ? v[a + 1] : v[b + 1];
+              const float2 other = make_float2(__shfl_xor_sync(0xffffffffu, __uint_as_float(give0), 16),
+                                               __shfl_xor_sync(0xffffffffu, __uint_as_float(give1), 16));
               const float2 dot = fma2(mine, w_a, mul2(other, w_b));
               const float s0 = sc[16 * q + (kWide ? 0 : 2 * u)], s1 = sc[16 * q + (kWide ? 0 : 2 * u + 1)];
-              x[4 * q + u] = fma2(dot, make_float2(s0 * mult, s1 * mult), make_float2(split_scale(s0).k, split_scale(s1).k));
+              x[4 * q + u] = fma2(dot, make_float2(s0 * mult, s1 * mult),
+                                  make_float2(split_scale(s0).k, split_scale(s1).k));
             }
           }
           const int seen = min(n_valid, len - tok0) - 8 * term;  // tokens this row sees, counted from 8 term
@@ -1145,7 +1164,9 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  // scale blocks of eight rows or more: a thread's runs of eight tokens have one scale each
+  // Scale blocks of eight rows or more: a thread's runs of eight tokens have one scale each, which saves
+  // a split and a multiplication per score (64 requests at G = 8: 84 us against 103 by token, 16 x 131,072
+  // tokens at G = 32: 258 against 284).
   const bool wide = scale_block >= 8;
   auto kern = wide ? mla_decode_scaled_kernel<true> : mla_decode_scaled_kernel<false>;
   if (!g_attr_set[wide][dev].load(std::memory_order_relaxed)) {
@@ -1190,7 +1211,7 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   p.max_len = a.subpage_stride * a.page_size;
   // positions (a unit's tiles and its cost) are counted in int32, at the static bound
   const int64_t units = static_cast<int64_t>(a.num_reqs) * p.num_views * p.row_blocks;
-  if (units * ((p.max_len + kTile - 1) / kTile + kPartCost) > INT32_MAX) {
+  if (units * ((p.max_len + kTile - 1) / kTile + part_cost(kRows)) > INT32_MAX) {
     set_error("mla_decode_verify_scaled: %lld row blocks of up to %d tokens overflow int32 positions", (long long)units,
               p.max_len);
     return MLA_ERR_UNSUPPORTED;

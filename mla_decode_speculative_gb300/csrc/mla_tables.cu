@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kTabThreads) update_tables_kernel(const TabPar
       next = true;  // a shard's tokens follow one another in its own index space
     }
     if (whole && r0 + kPer <= T) {
-      *reinterpret_cast<int4 *>(a.slot_map + r0) = make_int4(slot[0], slot[kPer > 1], slot[kPer > 2 ? 2 : 0], slot[kPer - 1]);
+      *reinterpret_cast<int4 *>(a.slot_map + r0) =
+          make_int4(slot[0], slot[kPer > 1 ? 1 : 0], slot[kPer > 2 ? 2 : 0], slot[kPer - 1]);
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
