@@ -88,6 +88,7 @@ constexpr int kRows = 64;          // query rows of a unit
 constexpr int kVChunk = kTile * 128;              // 128 dims of a tile
 constexpr int kRopeOff = 4 * kVChunk;             // rope chunk, then the first term of P^T
 constexpr int kStageBytes = kTile * 576;
+constexpr int kQPitch = 1152 + 16;  // a query row there: rows a quarter of the banks apart
 constexpr int kPBlock = kRows * 32;               // 32 tokens of one term of P^T
 constexpr int kOffP2 = kStages * kStageBytes;     // second term of P^T
 constexpr int kOffMisc = kOffP2 + 3 * kPBlock;
@@ -115,7 +116,7 @@ struct Part {
 
 struct Misc {
   uint64_t full[kStages], empty[kStages];
-  uint64_t s_free, p2_full, q_full, fin_qk, fin_pv;
+  uint64_t s_free, p2_full, q_here, q_read, q_full, fin_qk, fin_pv;
   // by the tile's parity, so by softmax group: a group looks at every other tile,
   // and one barrier's phases look alike two tiles apart
   uint64_t s_full[2], p1_full[2], o_done[2], turn[2], sc_full[2], sc_free[2];
@@ -134,6 +135,7 @@ struct Misc {
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kStageBytes % 1024 == 0 && kVChunk % 1024 == 0 && kOffP2 % 1024 == 0, "swizzle-atom alignment");
+static_assert(kRows * kQPitch <= 2 * kStageBytes, "the first part's queries fit two stages");
 static_assert(3 * kPBlock <= kTile * 64, "a term of P^T fits the rope chunk");
 static_assert(2 * (kThreads / 32) <= 2 * kRows, "the setup's sums fit red");
 
@@ -325,6 +327,19 @@ __device__ __forceinline__ void ld_global_32(const uint4 *ptr, uint4 &a, uint4 &
                : "l"(ptr)
                : "memory");
 }
+__device__ __forceinline__ void copy_to_smem(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void prefetch_l2(const void *ptr, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
 }
@@ -464,6 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&misc.s_free), kGroupWarps);
     mbar_init(smem_u32(&misc.p2_full), kGroupWarps);
+    mbar_init(smem_u32(&misc.q_here), 1);
+    mbar_init(smem_u32(&misc.q_read), 1);
     mbar_init(smem_u32(&misc.q_full), kSoftWarps);
     mbar_init(smem_u32(&misc.fin_qk), 1);
     mbar_init(smem_u32(&misc.fin_pv), 1);
@@ -520,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       c_x[j] = c * 128;
       c_dst[j] = s_base + (c < 4 ? c * kVChunk + c_tok[j] * 128 : kRopeOff + c_tok[j] * 64);
     }
+    bool q_armed = false;
     uint32_t armed = 0, armed_par = 0;  // stages with a copy possibly in flight (for the exit path)
     uint32_t g = 0;
     int vb = misc.first_vb, rb = 0, pos = misc.first_pos, u_pos = pos;
@@ -613,7 +631,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           e.seg_lo = t_lo * kTile;
           e.seg_hi = min(t_hi * kTile, unit_len);
           e.n_tiles = t_hi - t_lo;
-          if (t_hi > t_lo) prefetch_l2(p.q + static_cast<int64_t>(q0 * p.num_heads + row_begin) * 576, n_rows * 1152);
+          const __nv_bfloat16 *q = p.q + static_cast<int64_t>(e.q_row) * 576;
+          if (t_hi > t_lo && k > 0) prefetch_l2(q, n_rows * 1152);
+        }
+        if (t_hi > t_lo && k == 0) {  // the first part's queries, into the third and fourth stage
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&misc.q_here), n_rows * 1152);
+          __syncwarp();
+          const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(q0) * p.num_heads + row_begin) * 576;
+          for (int r = lane; r < n_rows; r += 32)
+            copy_to_smem(s_base + 2 * kStageBytes + r * kQPitch, q + r * 576, 1152, smem_u32(&misc.q_here));
+          q_armed = true;
         }
         break;
       }
@@ -640,8 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           win = tok0 >> lg_p;
           win_id = win + lane <= last_page ? pages[win + lane] : -1;
         }
-        // The first part's queries come before its third tile: all CTAs ask for everything at once.
-        if (k == 0 && g == 2 && !__all_sync(0xffffffffu, wait(misc.q_full, 0))) break;
+        if (q_armed && g == 2 && !__all_sync(0xffffffffu, wait(misc.q_read, 0))) break;  // queries are in its stage
         if (!__all_sync(0xffffffffu, wait(misc.empty[st], (g / kStages) ^ 1u))) break;
         const uint32_t bar = smem_u32(&misc.full[st]);
         if (lane == 0) mbar_arrive_expect_tx(bar, ((n_valid + run - 1) & -run) * 576);
@@ -666,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0 && (!ok || *abort_flag)) {  // let the copies land before the memory is released
       const volatile int never = 0;
+      if (q_armed) mbar_wait(smem_u32(&misc.q_here), 0, &never, p.drain_budget);
       for (int st = 0; st < kStages; ++st)
         if (armed & (1u << st)) mbar_wait(smem_u32(&misc.full[st]), (armed_par >> st) & 1u, &never, p.drain_budget);
     }
@@ -797,33 +824,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // A part's queries into TMEM.  Thread: 144 dims of its row, from
     // 288 h + 144 term; both terms of them, one of which goes to the partner lane.
-    auto load_queries = [&](const Part &e) {
+    auto load_queries = [&](const Part &e, bool first) {
       const bool live = row < e.n_rows;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(e.q_row) + row) * 576) + 36 * h +
                          18 * term;
-      uint32_t top = 0;
       uint4 v[18];
 #pragma unroll
-      for (int i = 0; i < 18; i += 2) {
-        v[i] = v[i + 1] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 18; ++i) v[i] = make_uint4(0, 0, 0, 0);
+      if (first) {
+        wait(misc.q_here, 0);
+        const uint32_t at = s_base + 2 * kStageBytes + row * kQPitch + 576 * h + 288 * term;
         if (live) {
-          if (p.q_aligned) {
-            ld_global_32(src + i, v[i], v[i + 1]);
-          } else {
-            v[i] = src[i];
-            v[i + 1] = src[i + 1];
-          }
+#pragma unroll
+          for (int i = 0; i < 18; ++i) v[i] = ld_shared_v4(at + 16 * i);
         }
+      } else if (live && p.q_aligned) {
+#pragma unroll
+        for (int i = 0; i < 18; i += 2) ld_global_32(src + i, v[i], v[i + 1]);
+      } else if (live) {
+#pragma unroll
+        for (int i = 0; i < 18; ++i) v[i] = src[i];
       }
+      uint32_t most = 0;  // two elements at a time: magnitudes compare as their bits, NaN on top
 #pragma unroll
       for (int i = 0; i < 18; ++i) {
         const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+        for (int j = 0; j < 4; j += 2) most = __vimax3_u16x2(most, u[j] & 0x7fff7fffu, u[j + 1] & 0x7fff7fffu);
       }
+      uint32_t top = max(most & 0xffffu, most >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
       if (term == 0) misc.red[h][row] = __uint_as_float(top);
       named_bar_sync(kBarSoft, kSoftThreads);
+      if (first && threadIdx.x == 0) mbar_arrive(smem_u32(&misc.q_read));
       top = max(__float_as_uint(misc.red[0][row]), __float_as_uint(misc.red[1][row]));
       const bool finite = top < 0x7f80u;  // otherwise zeros, and the row is spoilt
       const int ex = finite ? max(static_cast<int>(top >> 7), 27) : 127;  // exponent + 127, at least 2^-100
@@ -890,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool more = next_part(k);
       const Part &e = misc.part[k % kWorkRing];
       const bool was_ok = ok;
-      if (more && e.n_tiles > 0) load_queries(e);
+      if (more && e.n_tiles > 0) load_queries(e, k == 0);
       if (k > 0) {
         if (last.n_tiles > 0) {
           wait(misc.o_done[(g0 - 1) & 1u], (g0 - 1) >> 1);
