@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       c_x[j] = c * 128;
       c_dst[j] = s_base + (c < 4 ? c * kVChunk + c_tok[j] * 128 : kRopeOff + c_tok[j] * 64);
     }
-    bool q_armed = false;
+    bool q_staged = false;  // the first part's queries are in the third and fourth stage
     uint32_t armed = 0, armed_par = 0;  // stages with a copy possibly in flight (for the exit path)
     uint32_t g = 0;
     int vb = misc.first_vb, rb = 0, pos = misc.first_pos, u_pos = pos;
@@ -632,16 +632,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           e.seg_hi = min(t_hi * kTile, unit_len);
           e.n_tiles = t_hi - t_lo;
           const __nv_bfloat16 *q = p.q + static_cast<int64_t>(e.q_row) * 576;
-          if (t_hi > t_lo && k > 0) prefetch_l2(q, n_rows * 1152);
+          if (t_hi > t_lo) prefetch_l2(q, n_rows * 1152);
         }
-        if (t_hi > t_lo && k == 0) {  // the first part's queries, into the third and fourth stage
-          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&misc.q_here), n_rows * 1152);
-          __syncwarp();
-          const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(q0) * p.num_heads + row_begin) * 576;
-          for (int r = lane; r < n_rows; r += 32)
-            copy_to_smem(s_base + 2 * kStageBytes + r * kQPitch, q + r * 576, 1152, smem_u32(&misc.q_here));
-          q_armed = true;
-        }
+        if (k == 0) q_staged = t_hi > t_lo;
         break;
       }
       __syncwarp();
@@ -667,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           win = tok0 >> lg_p;
           win_id = win + lane <= last_page ? pages[win + lane] : -1;
         }
-        if (q_armed && g == 2 && !__all_sync(0xffffffffu, wait(misc.q_read, 0))) break;  // queries are in its stage
+        if (q_staged && g == 2 && !__all_sync(0xffffffffu, wait(misc.q_read, 0))) break;
         if (!__all_sync(0xffffffffu, wait(misc.empty[st], (g / kStages) ^ 1u))) break;
         const uint32_t bar = smem_u32(&misc.full[st]);
         if (lane == 0) mbar_arrive_expect_tx(bar, ((n_valid + run - 1) & -run) * 576);
@@ -692,7 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0 && (!ok || *abort_flag)) {  // let the copies land before the memory is released
       const volatile int never = 0;
-      if (q_armed) mbar_wait(smem_u32(&misc.q_here), 0, &never, p.drain_budget);
       for (int st = 0; st < kStages; ++st)
         if (armed & (1u << st)) mbar_wait(smem_u32(&misc.full[st]), (armed_par >> st) & 1u, &never, p.drain_budget);
     }
@@ -832,7 +824,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 18; ++i) v[i] = make_uint4(0, 0, 0, 0);
       if (first) {
-        wait(misc.q_here, 0);
+        // a bulk copy per row: eight from each warp, since one warp takes 50 cycles for each
+        const uint32_t bar = smem_u32(&misc.q_here);
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, e.n_rows * 1152);
+        const int r = 8 * warp + lane;
+        if (lane < 8 && r < e.n_rows)
+          copy_to_smem(s_base + 2 * kStageBytes + r * kQPitch, p.q + (static_cast<int64_t>(e.q_row) + r) * 576, 1152, bar);
+        __syncwarp();
+        if (!wait(misc.q_here, 0) && threadIdx.x == 0) {  // the copies land before the memory is released
+          const volatile int never = 0;
+          mbar_wait(bar, 0, &never, p.drain_budget);
+        }
         const uint32_t at = s_base + 2 * kStageBytes + row * kQPitch + 576 * h + 288 * term;
         if (live) {
 #pragma unroll
