@@ -58,11 +58,12 @@
 // overlapped; the steady state is 2390 cycles a tile, 1.25 us, against 1.24 us for
 // the SM's share of the HBM rate (55 KB at 6.76 TB/s / 152).  16 requests of
 // 131,072 tokens take 248 us (4.9 TB/s) and run at the power limit.  Short calls
-// are latency: about 12 us from the call's start to the first S (lengths, split,
-// queries and the first tiles through L2 at once), 5 us from the last tile to the
-// partial output, and the merge kernel; 32 requests of 1,024 to 8,192 tokens take
-// 43 us, 13 of them at the HBM rate.  The loops are kept small: the instruction
-// cache holds about 32 KB for four loops that run at once.
+// are latency: about 10 us from the call's start to the first S (lengths and
+// split 1.8, finding the part 1.9, its queries 1.4 and their two terms 2.3), 3 us
+// from the last tile to the partial output, then the merge kernel; 32 requests of
+// 1,024 to 8,192 tokens take 39 us, 13 of them at the HBM rate.  The loops are
+// kept small: the instruction cache holds about 32 KB for four loops that run at
+// once.
 //
 // Every wait is bounded; one that runs out records MLA_DEV_WAIT_TIMEOUT, all
 // roles drain without skipping a barrier, TMEM is freed and the kernel returns.
@@ -816,6 +817,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // A part's queries into TMEM.  Thread: 144 dims of its row, from
     // 288 h + 144 term; both terms of them, one of which goes to the partner lane.
+    // A CTA's first queries are copied to the stages that its tiles reach last:
+    // read from global memory, 32 sectors an instruction and behind the first
+    // tiles' copies, they took 3 us more (32 requests of 64 rows: 42.9 -> 39.3 us).
+    // Those of a later part, in L2 by then, are read directly: its tiles are
+    // on their way into all stages.
     auto load_queries = [&](const Part &e, bool first) {
       const bool live = row < e.n_rows;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (static_cast<int64_t>(e.q_row) + row) * 576) + 36 * h +
@@ -829,7 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, e.n_rows * 1152);
         const int r = 8 * warp + lane;
         if (lane < 8 && r < e.n_rows)
-          copy_to_smem(s_base + 2 * kStageBytes + r * kQPitch, p.q + (static_cast<int64_t>(e.q_row) + r) * 576, 1152, bar);
+          copy_to_smem(s_base + 2 * kStageBytes + r * kQPitch, p.q + (static_cast<int64_t>(e.q_row) + r) * 576, 1152,
+                       bar);
         __syncwarp();
         if (!wait(misc.q_here, 0) && threadIdx.x == 0) {  // the copies land before the memory is released
           const volatile int never = 0;
