@@ -230,17 +230,17 @@ mla_status make_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType 
 
 mla_status make_tmap_tile3d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype,
                             int elem_bytes, uint64_t rows, uint32_t box_rows,
-                            CUtensorMapSwizzle swizzle) {
-  // A latent row of 576 values seen as 9 chunks of 64: dims (64 values, row,
-  // chunk) with strides (row = 576 values, chunk = 64 values), so one box of
-  // (64, box_rows, 9) lands chunk-major in shared memory: chunk c at
-  // c * box_rows * 64 * elem_bytes, rows inside a chunk contiguous.
+                            CUtensorMapSwizzle swizzle, uint32_t chunk, uint32_t chunks) {
+  // A latent row of 576 values seen as chunks (9 of 64): dims (values, row,
+  // chunk) with strides (row = 576 values, chunk = its values), so one box of
+  // (chunk, box_rows, chunks) lands chunk-major in shared memory: chunk c at
+  // c * box_rows * chunk * elem_bytes, rows inside a chunk contiguous.
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return MLA_ERR_CUDA;
   const uint64_t eb = static_cast<uint64_t>(elem_bytes);
-  const cuuint64_t dims[3] = {64, rows, 9};
-  const cuuint64_t strides[2] = {576 * eb, 64 * eb};
-  const cuuint32_t box[3] = {64, box_rows, 9};
+  const cuuint64_t dims[3] = {chunk, rows, chunks};
+  const cuuint64_t strides[2] = {576 * eb, chunk * eb};
+  const cuuint32_t box[3] = {chunk, box_rows, chunks};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = encode(map, dtype, 3, const_cast<void *>(base), dims, strides, box, estr,
                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,

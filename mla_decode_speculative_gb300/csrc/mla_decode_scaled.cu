@@ -86,8 +86,9 @@ namespace {
 constexpr int kTile = 96;          // tokens of a tile
 constexpr int kStages = 4;         // tiles in shared memory
 constexpr int kRows = 64;          // query rows of a unit
-constexpr int kVChunk = kTile * 128;              // 128 dims of a tile
-constexpr int kRopeOff = 4 * kVChunk;             // rope chunk, then the first term of P^T
+constexpr int kAtom = 1024;                       // 128 dims of eight tokens
+constexpr int kGroup = 4 * kAtom;                 // 512 dims of eight tokens
+constexpr int kRopeOff = kTile / 8 * kGroup;      // rope chunk, then the first term of P^T
 constexpr int kStageBytes = kTile * 576;
 constexpr int kQPitch = 1152 + 16;  // a query row there: rows a quarter of the banks apart
 constexpr int kPBlock = kRows * 32;               // 32 tokens of one term of P^T
@@ -135,7 +136,7 @@ struct Misc {
 };
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kStageBytes % 1024 == 0 && kVChunk % 1024 == 0 && kOffP2 % 1024 == 0, "swizzle-atom alignment");
+static_assert(kStageBytes % 1024 == 0 && kRopeOff % 1024 == 0 && kOffP2 % 1024 == 0, "swizzle-atom alignment");
 static_assert(kRows * kQPitch <= 2 * kStageBytes, "the first part's queries fit two stages");
 static_assert(3 * kPBlock <= kTile * 64, "a term of P^T fits the rope chunk");
 static_assert(2 * (kThreads / 32) <= 2 * kRows, "the setup's sums fit red");
@@ -525,19 +526,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kTmaWarp) {
     // ================================================ work and tile copies
     const uint64_t policy = l2_policy_evict_first();
-    const int run = min(P, 32), lg_p = 31 - __clz(P);  // rows of a copy: one page, or 32 rows of one
-    // Copy o of a tile: box o / 5, chunk o % 5 (4: rope); a lane issues copies lane
-    // and, for pages of eight rows, lane + 32.
-    const int o_last = kTile / run * 5 > 32 ? 2 : 1;
-    int c_tok[2], c_x[2];
-    uint32_t c_dst[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int o = lane + 32 * j, c = o % 5;
-      c_tok[j] = o / 5 * run;
-      c_x[j] = c * 128;
-      c_dst[j] = s_base + (c < 4 ? c * kVChunk + c_tok[j] * 128 : kRopeOff + c_tok[j] * 64);
-    }
+    const int run = min(P, 32), lg_p = 31 - __clz(P);  // rope rows of a copy: one page, or 32 of one
+    // A lane's copy of a tile: 512 dims of eight tokens, or the rope dims of `run` tokens.
+    const bool is_v = lane < kTile / 8;
+    const int c_tok = is_v ? 8 * lane : (lane - kTile / 8) * run;
+    const uint32_t c_dst = s_base + (is_v ? lane * kGroup : kRopeOff + c_tok * 64);
     bool q_staged = false;  // the first part's queries are in the third and fourth stage
     uint32_t armed = 0, armed_par = 0;  // stages with a copy possibly in flight (for the exit path)
     uint32_t g = 0;
@@ -664,20 +657,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q_staged && g == 2 && !__all_sync(0xffffffffu, wait(misc.q_read, 0))) break;
         if (!__all_sync(0xffffffffu, wait(misc.empty[st], (g / kStages) ^ 1u))) break;
         const uint32_t bar = smem_u32(&misc.full[st]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, ((n_valid + run - 1) & -run) * 576);
+        if (lane == 0) mbar_arrive_expect_tx(bar, ((n_valid + 7) & -8) * 512 + ((n_valid + run - 1) & -run) * 64);
         __syncwarp();
-#pragma unroll 1
-        for (int j = 0; j < o_last; ++j) {
-          const int off = j == 0 ? c_tok[0] : c_tok[1], x = j == 0 ? c_x[0] : c_x[1], t = tok0 + off;
-          const bool mine = off < n_valid;
-          const int32_t id = __shfl_sync(0xffffffffu, win_id, mine ? (t >> lg_p) - win : 0);
-          if (mine) {
-            int32_t row = static_cast<int32_t>(p.num_cache_rows);  // past the last row: zeros
-            if (id < 0 || (static_cast<int64_t>(id) + 1) << lg_p > p.num_cache_rows) note(p.err, MLA_DEV_BAD_SUBPAGE);
-            else row = (id << lg_p) + (t & (P - 1));
-            const uint32_t dst = (j == 0 ? c_dst[0] : c_dst[1]) + st * kStageBytes;
-            tma_load_2d(dst, x < 512 ? &tm_v : &tm_r, bar, x, row, policy);
-          }
+        const bool mine = c_tok < n_valid;
+        const int t = tok0 + c_tok;
+        const int32_t id = __shfl_sync(0xffffffffu, win_id, mine ? (t >> lg_p) - win : 0);
+        if (mine) {
+          int32_t row = static_cast<int32_t>(p.num_cache_rows);  // past the last row: zeros
+          if (id < 0 || (static_cast<int64_t>(id) + 1) << lg_p > p.num_cache_rows) note(p.err, MLA_DEV_BAD_SUBPAGE);
+          else row = (id << lg_p) + (t & (P - 1));
+          if (is_v) tma_load_3d(c_dst + st * kStageBytes, &tm_v, bar, 0, row, 0, policy);
+          else tma_load_2d(c_dst + st * kStageBytes, &tm_r, bar, 512, row, policy);
         }
         armed |= 1u << st;
         armed_par = (armed_par & ~(1u << st)) | (((g / kStages) & 1u) << st);
@@ -693,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================================ S = Q K^T
     if (elect_one()) {
       constexpr uint32_t id_qk = idesc_f8(kTile, 0, 0);
-      const uint64_t d_k = sdesc(s_base, 1024, 2), d_rope = sdesc(s_base + kRopeOff, 512, 4);
+      const uint64_t d_k = sdesc(s_base, kGroup, 2), d_rope = sdesc(s_base + kRopeOff, 512, 4);
       uint32_t g = 0, kq = 0;
       for (uint32_t k = 0; wait(misc.work_full[k % kWorkRing], k / kWorkRing); ++k) {
         const Part &e = misc.part[k % kWorkRing];
@@ -711,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma8_ts(tmem + kTmemS, tmem + kTmemQ + 32 * c + 8 * i, d_k + off + c * (kVChunk >> 4) + 2 * i, id_qk,
+              mma8_ts(tmem + kTmemS, tmem + kTmemQ + 32 * c + 8 * i, d_k + off + c * (kAtom >> 4) + 2 * i, id_qk,
                       (c | i) > 0);
           mma8_ts(tmem + kTmemS, tmem + kTmemQ + 128, d_rope + off, id_qk, 1u);
           mma8_ts(tmem + kTmemS, tmem + kTmemQ + 136, d_rope + off + 2, id_qk, 1u);
@@ -727,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       constexpr uint32_t id_pv = idesc_f8(kRows, 1, 1);
       // V^T: a 128-byte row holds all of M, so only the step between 8-token groups counts
-      const uint64_t d_v = sdesc(s_base, 1024, 2) | (static_cast<uint64_t>(kVChunk >> 4) << 16);
+      const uint64_t d_v = sdesc(s_base, kGroup, 2) | (static_cast<uint64_t>(kAtom >> 4) << 16);
       const uint64_t d_p1 = sdesc(s_base + kRopeOff, 256, 6), d_p2 = sdesc(s_base + kOffP2, 256, 6);
       uint32_t g = 0;
       for (uint32_t k = 0; wait(misc.work_full[k % kWorkRing], k / kWorkRing); ++k) {
@@ -747,10 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             uint64_t dv = d_v + off, dp = term == 0 ? d_p1 + off : d_p2;
 #pragma unroll 1
-            for (int kk = 0; kk < n32; ++kk, dv += 4096 >> 4, dp += kPBlock >> 4) {
+            for (int kk = 0; kk < n32; ++kk, dv += 4 * kGroup >> 4, dp += kPBlock >> 4) {
 #pragma unroll
               for (int blk = 0; blk < 4; ++blk)
-                mma8_ss(tmem + kTmemO + blk * kRows, dv + blk * (kVChunk >> 4), dp, id_pv, (term | kk | i) > 0);
+                mma8_ss(tmem + kTmemO + blk * kRows, dv + blk * (kAtom >> 4), dp, id_pv, (term | kk | i) > 0);
             }
           }
           if (!ok) break;
@@ -1085,8 +1075,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            : "memory");
               if ((code & 0x7fu) > 0x7cu)
                 for (int c = 0; c < 128; ++c) {
-                  const uint32_t word =
-                      stage + (c >> 5) * kVChunk + (16 * b + 8 * term + (t & 7)) * 128 + (c & 31) * 4;
+                  const int tok = 16 * b + 8 * term + (t & 7);
+                  const uint32_t word = stage + (tok >> 3) * kGroup + (c >> 5) * kAtom + (tok & 7) * 128 + (c & 31) * 4;
                   uint32_t v;
                   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(word) : "memory");
                   const uint32_t nan = __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -1096,8 +1086,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // rows of the last 32-token step past the part's end hold anything: zeros
-        for (int c = threadIdx.x & (kGroupThreads - 1); c < (((n_valid + 31) & ~31) - n_valid) * 32; c += kGroupThreads)
-          st_shared_v4(stage + ((c & 31) >> 3) * kVChunk + (n_valid + (c >> 5)) * 128 + (c & 7) * 16, 0, 0, 0, 0);
+        const int behind = ((n_valid + 31) & ~31) - n_valid;
+        for (int c = threadIdx.x & (kGroupThreads - 1); c < behind * 32; c += kGroupThreads) {
+          const int tok = n_valid + (c >> 5), chunk = (c & 31) >> 3;
+          st_shared_v4(stage + (tok >> 3) * kGroup + chunk * kAtom + (tok & 7) * 128 + (c & 7) * 16, 0, 0, 0, 0);
+        }
         fence_proxy_async_smem();
         if (rescale) {
           wait(misc.o_done[(g - 1) & 1u], (g - 1) >> 1);  // O^T at rest
@@ -1197,8 +1190,8 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   const mla_decode_args &a = *d.a;
   const uint32_t run = a.page_size < 32 ? a.page_size : 32;
   CUtensorMap tm_v, tm_r;
-  mla_status st = make_tmap_2d(&tm_v, a.kv_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 576,
-                               static_cast<uint64_t>(a.num_cache_rows), 128, run, CU_TENSOR_MAP_SWIZZLE_128B);
+  mla_status st = make_tmap_tile3d(&tm_v, a.kv_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
+                                   static_cast<uint64_t>(a.num_cache_rows), 8, CU_TENSOR_MAP_SWIZZLE_128B, 128, 4);
   if (st == MLA_OK)
     st = make_tmap_2d(&tm_r, a.kv_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 576, static_cast<uint64_t>(a.num_cache_rows),
                       64, run, CU_TENSOR_MAP_SWIZZLE_64B);
