@@ -111,6 +111,7 @@ struct Part {
   int stop;                 // 1: no more work
   int b;                    // view * B + request
   int rb, seg, fill_hi;     // slots seg + 1 .. fill_hi - 1 of the unit get no part: mark them empty
+                            // seg -1: the unit's only part, which writes the outputs itself
   int q_row, row_base, n_rows;
   int seg_lo, seg_hi, n_tiles;
   int lens[kRows];          // visible tokens of each row
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) wait(misc.work_empty[k % kWorkRing], (k / kWorkRing) ^ 1u);
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       bool found = false;
-      int t_lo = 0, t_hi = 0, seg = 0, fill_hi = S, unit_len = 0;
+      int t_lo = 0, t_hi = 0, seg = -1, fill_hi = S, unit_len = 0;
       while (ok && split.chunk < split.n_chunks && vb < n_vb) {
         const int v = vb / p.num_reqs, b = vb - v * p.num_reqs;
         if (loaded != vb) {  // the request's rows: lane t holds the length of row t (t < 32)
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lo >= hi) continue;
           t_lo = lo - start;
           t_hi = hi - start;
-          seg = split.chunk - chunk_of(split, start);
+          if (t_lo > 0 || t_hi < tiles) seg = split.chunk - chunk_of(split, start);
           fill_hi = end <= split.hi ? S : seg + 1;
         }
         found = true;
@@ -944,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ov[4 * j + 2] = __float_as_uint(f.z != 0.0f ? __uint_as_float(ov[4 * j + 2]) * f.z : 0.0f);
               ov[4 * j + 3] = __float_as_uint(f.w != 0.0f ? __uint_as_float(ov[4 * j + 3]) * f.w : 0.0f);
             }
-            if (S == 1) {
+            if (last.seg < 0) {
               __nv_bfloat16 *o = p.out + (last.row_base + 32 * h) * 512 + dim;
 #pragma unroll
               for (int j = 0; j < 32; ++j)
@@ -965,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_fence_before();
-        } else if (S == 1 && ok) {  // no row sees a token
+        } else if (last.seg < 0 && ok) {  // no row sees a token
           uint4 *o = reinterpret_cast<uint4 *>(p.out + last.row_base * 512);
           for (int c = threadIdx.x; c < last.n_rows * 64; c += kSoftThreads) o[c] = make_uint4(0, 0, 0, 0);
         }
@@ -1151,11 +1152,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (spoilt && l > 0.0f) l = NAN;
         const bool none = l == 0.0f;
         const float fix = w_sum / (w_sum - w_lost);
-        misc.factor[row] = none ? 0.0f : (S == 1 ? fix * kInvTop / l : fix * kInvTop);
+        misc.factor[row] = none ? 0.0f : (e.seg < 0 ? fix * kInvTop / l : fix * kInvTop);
         if (ok && row < n_rows) {
           const int64_t r = static_cast<int64_t>(e.row_base) + row;
-          if (S == 1) {
+          if (e.seg < 0) {
             p.lse[r] = none ? -INFINITY : (m_row + log2f(l)) * kLn2;
+            if (S > 1) p.segm_sum[r * S] = -1.0f;  // for the merge: written
           } else {
             // a NaN row keeps a finite maximum, so that the merge looks at its sum
             p.segm_max[r * S + e.seg] = none ? -INFINITY : (m_row == -INFINITY ? 0.0f : m_row);

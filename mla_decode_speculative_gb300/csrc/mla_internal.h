@@ -132,7 +132,8 @@ struct MergeLaunch {
   int num_reqs;              // segment mode
   int num_views;             // segment mode: V row views (>= 1)
   int row_blocks;            // segment mode: RB
-  int keep_nan;              // segment mode: a NaN sum gives a NaN row (0: an empty one)
+  int keep_nan;              // segment mode, scaled decode: a NaN sum gives a NaN row (0: an empty one),
+                             // a negative first sum marks a row block that is written already
   const void *part_out;
   const float *part_lse;
   void *out;
