@@ -10,10 +10,11 @@
 // earlier rows' codes are then read and rewritten).
 //
 // Bound by memory, so by the loads in flight: the pieces a thread holds follow
-// from G (a warp per unit up to G = 4, then a CTA of 128 to 512 threads), which
-// keeps the registers low enough for 32 warps per SM.  One kernel with 18
-// pieces for every G ran at one CTA of 8 warps per SM: 109 us for 131,000 rows
-// at G = 64 and 53 us for 20,600 rows at G = 1.
+// from G (four rows a warp at G = 1, a warp per unit up to G = 4, then a CTA of
+// 128 to 512 threads), which keeps the registers low enough for 32 warps per SM.
+// One kernel with 18 pieces for every G ran at one CTA of 8 warps per SM: 109 us
+// for 131,000 rows at G = 64; and a warp that took one row at a time 65 us for as
+// many at G = 1, against 43 with four.
 //
 // Scale: 2^k, the smallest with max |x| <= 448 * 2^k.  With max |x| = m 2^e,
 // m in [1, 2), and 448 = 1.75 * 2^8, that is k = e - 8, plus one when m > 1.75;
@@ -55,6 +56,12 @@ __device__ __forceinline__ __nv_bfloat162 pair_max(__nv_bfloat162 m, uint32_t v)
 __device__ __forceinline__ uint32_t max_bits(__nv_bfloat162 m) {
   const uint32_t u = *reinterpret_cast<const uint32_t *>(&m);
   return max(u & 0xffffu, u >> 16);
+}
+
+// bits of the larger finite one of two bf16 magnitudes
+__device__ __forceinline__ uint32_t finite_bits(uint32_t v) {
+  const uint32_t lo = v & 0x7fffu, hi = (v >> 16) & 0x7fffu;
+  return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
 }
 
 // The exponent k of the scale for a largest magnitude given as bf16 bits.
@@ -123,12 +130,7 @@ __device__ __forceinline__ void write_unit(const WriteScaledParams &p, const int
 #pragma unroll 1
     for (int c = t; c < pieces; c += kTeam) {
       const uint4 u = p.x[static_cast<int64_t>(rows[c / kRowPieces]) * kRowPieces + c % kRowPieces];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-      }
+      top = max(max(top, max(finite_bits(u.x), finite_bits(u.y))), max(finite_bits(u.z), finite_bits(u.w)));
     }
   }
   top = __reduce_max_sync(kAll, top);
@@ -253,7 +255,63 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(co
   }
 }
 
-// A warp per unit: scale blocks of up to 4 rows.
+// G = 1: every row has a scale of its own and no row before it, so a row needs
+// nothing but itself.  A warp takes up to kRowsHeld rows at once, so that its
+// loads do not wait for the row before.
+constexpr int kRowsHeld = 4;
+__global__ void __launch_bounds__(kWarpCta, 4) write_scaled_rows(const WriteScaledParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kWarpCta / 32) + (threadIdx.x >> 5)) * p.window;
+  int slot = lane < p.window && r0 + lane < p.num_rows ? p.slots[r0 + lane] : -1;
+  if (slot >= p.num_cache_rows || slot < -1) {
+    atomicCAS(p.err, 0, MLA_DEV_BAD_BLOCK_ID);
+    slot = -1;
+  }
+  if (__ballot_sync(0xffffffffu, slot >= 0) == 0) return;
+  constexpr int kHeld = (kRowPieces + 31) / 32;
+  uint4 v[kRowsHeld][kHeld];
+#pragma unroll
+  for (int u = 0; u < kRowsHeld; ++u) {
+    const bool live = __shfl_sync(0xffffffffu, slot, u) >= 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = lane + 32 * i;
+      v[u][i] = make_uint4(0, 0, 0, 0);
+      if (live && c < kRowPieces) v[u][i] = p.x[(r0 + u) * kRowPieces + c];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsHeld; ++u) {
+    const int at = __shfl_sync(0xffffffffu, slot, u);
+    if (at < 0) continue;
+    __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      m = pair_max(pair_max(pair_max(pair_max(m, v[u][i].x), v[u][i].y), v[u][i].z), v[u][i].w);
+    uint32_t top = max_bits(m);
+    if (top >= 0x7f80) {  // an infinity among them: only finite values count
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        top = max(max(top, max(finite_bits(v[u][i].x), finite_bits(v[u][i].y))),
+                  max(finite_bits(v[u][i].z), finite_bits(v[u][i].w)));
+    }
+    const float scale = pow2f(scale_exp(__reduce_max_sync(0xffffffffu, top))), inv = 1.0f / scale;
+    uint2 *dst = p.cache + static_cast<int64_t>(at) * kRowPieces;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int c = lane + 32 * i;
+      if (c < kRowPieces)
+        dst[c] = make_uint2(codes4(scaled(v[u][i].x, inv), scaled(v[u][i].y, inv)),
+                            codes4(scaled(v[u][i].z, inv), scaled(v[u][i].w, inv)));
+    }
+    if (lane == 0) p.scales[at] = scale;
+  }
+}
+
+// A warp per unit: scale blocks of 2 or 4 rows.
 template <int kG>
 __global__ void __launch_bounds__(kWarpCta, 4) write_scaled_warp(const WriteScaledParams p) {
   grid_dep_wait();
@@ -330,7 +388,7 @@ extern "C" mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, cons
   // step's few tokens spread out), then as many as keep it at two full waves,
   // within the list of leaders (64) or a warp.
   const int team_warps = scale_block == kMaxGroup ? 16 : scale_block >= 16 ? 8 : by_cta ? 4 : 1;
-  const int teams = sms * 64 / team_warps, most = by_cta ? kMaxGroup : 32;
+  const int teams = sms * 64 / team_warps, most = by_cta ? kMaxGroup : scale_block == 1 ? kRowsHeld : 32;
   int window = num_rows / teams;
   window = window < 1 ? 1 : (window > most ? most : window);
   p.window = window;
@@ -338,7 +396,7 @@ extern "C" mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, cons
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(num_rows) + per_cta - 1) / per_cta));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (scale_block) {
-    case 1: e = launch_pdl(write_scaled_warp<1>, grid, dim3(kWarpCta), 0, s, p); break;
+    case 1: e = launch_pdl(write_scaled_rows, grid, dim3(kWarpCta), 0, s, p); break;
     case 2: e = launch_pdl(write_scaled_warp<2>, grid, dim3(kWarpCta), 0, s, p); break;
     case 4: e = launch_pdl(write_scaled_warp<4>, grid, dim3(kWarpCta), 0, s, p); break;
     case 8: e = launch_pdl(write_scaled_cta<128, 8>, grid, dim3(128), 0, s, p); break;
