@@ -20,9 +20,10 @@
 //    many small weights beside one large one).  The sums of the weights before
 //    and after this rounding correct the row's mean, so one visible token, or
 //    equal ones, come out exact.
-//  * With a_j = f_j 2^k_j, f in [1, 2), the exponent joins the score,
-//      w_j = f_j 2^(s_j log2e + k_j - m),  l = sum w_j / a_j,  out = sum w_j code_j / l,
+//  * The scale joins the score,
+//      w_j = 2^(s_j log2e + log2 a_j - m),  l = sum w_j / a_j,  out = sum w_j code_j / l,
 //    so the running reference m bounds the weights whatever the scales are.
+//    log2 a_j and 1 / a_j come from a warp of their own, once per token.
 //
 // Work: (row view, request, block of up to 64 query rows) units in 96-token
 // tiles.  The tiles of all units plus a few overhead positions per unit
@@ -101,7 +102,7 @@ constexpr int kThreads = 384;
 constexpr uint32_t kTmemQ = 0, kTmemO = 144, kTmemS = 400, kTmemCols = 512;
 constexpr int kWorkRing = 3;
 constexpr float kThreshold = 3.0f;   // the reference moves when a weight exceeds 2^3 of it
-constexpr float kTop = 11.0f;        // a weight at the reference is held as 2^11 .. 2^12: at most 2^15 < 57344
+constexpr float kTop = 11.0f;        // a weight at the reference is held as 2^11: at most 2^14 < 57344
 constexpr float kInvTop = 4.8828125e-4f;  // 2^-kTop
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint32_t kBarSoft = 1;     // named barriers: the softmax warps, and 2, 3 their groups
@@ -114,7 +115,6 @@ struct Part {
                             // seg -1: the unit's only part, which writes the outputs itself
   int q_row, row_base, n_rows;
   int seg_lo, seg_hi, n_tiles;
-  int lens[kRows];          // visible tokens of each row
 };
 
 struct Misc {
@@ -128,12 +128,13 @@ struct Misc {
   int abort;
   int stop[2];
   int first_vb, first_pos;  // the chunk's first (view, request) and its first position
-  float sc[2][kTile];       // scales of a tile's tokens
+  alignas(16) float sc[2][kTile], lg[2][kTile], rc[2][kTile];  // a tile's scales, their logarithms and reciprocals
   Part part[kWorkRing];
   float ref[kRows];         // running reference of each row (log2 units)
   float red[2][kRows];      // sums of the setup, the queries' maxima, the rows' sums
-  alignas(16) float alpha[2][kRows];  // what a group's new references scale O^T by
-  alignas(16) float factor[kRows];
+  // What a group's new references scale O^T by.  Between the parts' tiles: [0] the rows' lost weights,
+  // [1] what the epilogue scales O^T by (group 1 writes it again only after group 0's first tile).
+  alignas(16) float alpha[2][kRows];
 };
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -160,6 +161,18 @@ struct Params {
 
 __device__ __forceinline__ void note(int *err, int code) { atomicCAS(err, 0, code); }
 
+// A scale's logarithm (within 2^-22 of it, so a weight within 2^-15) and reciprocal (within an ulp): with
+// log2f and a division the loop of the warp that makes them costs the others 2% in the instruction cache.
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -267,45 +280,37 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int *abort
   return false;
 }
 
-// A scale a = f 2^k: k as a float, f in [1, 2), and 2^(-k - kTop).
-struct Scale {
-  float k, f, inv;
-};
-__device__ __forceinline__ Scale split_scale(float a) {
-  const uint32_t u = __float_as_uint(a), ex = u >> 23;
-  return {static_cast<float>(static_cast<int>(ex) - 127), __uint_as_float((u & 0x7fffffu) | 0x3f800000u),
-          __uint_as_float((254u - ex) << 23) * kInvTop};
+__device__ __forceinline__ void load8(const float *ptr, float (&v)[8]) {  // 16-byte aligned
+  const float4 lo = reinterpret_cast<const float4 *>(ptr)[0], hi = reinterpret_cast<const float4 *>(ptr)[1];
+  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+  v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
 }
 
 // A thread's 48 scores (six runs of eight tokens, 16 apart) to weights against
-// the reference: the sums, and the weights' two e5m2 terms.  A weight goes
-// through f16 (2^-12 of itself): there e5m2 is the upper byte, so a term's value
-// is its codes moved up and the remainder is exact.  kWide: a run has one scale.
+// the reference: the sums (rc: the tokens' 1 / scale), and the weights' two e5m2
+// terms.  A weight goes through f16 (2^-12 of itself): there e5m2 is the upper
+// byte, so a term's value is its codes moved up and the remainder is exact.
+// kWide: a run has one scale.
 template <bool kWide>
-__device__ __forceinline__ void weigh(const float2 (&x)[24], const float *sc, float ref, float &l_t, float &w_sum,
+__device__ __forceinline__ void weigh(const float2 (&x)[24], const float *rc, float ref, float &l_t, float &w_sum,
                                       float &w_lost, uint32_t (&p1)[12], uint32_t (&p2)[12]) {
-  float w_t = 0.0f;
+  float w_t = 0.0f, l_w = 0.0f;
+  float2 l_2 = make_float2(0.0f, 0.0f);
   __half2 lost = __float2half2_rn(0.0f);
   const float2 neg = make_float2(-ref, -ref);
 #pragma unroll
   for (int q = 0; q < 6; ++q) {
     float2 run = make_float2(0.0f, 0.0f);
-    const Scale s = split_scale(sc[16 * q]);
+    float r[8];
+    if (kWide) r[0] = rc[16 * q];
+    else load8(rc + 16 * q, r);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float2 d = add2(x[4 * q + u], neg);
       const float2 e = make_float2(ex2(d.x), ex2(d.y));
-      float2 f = make_float2(s.f, s.f);
-      if (kWide) {
-        run = add2(run, e);
-      } else {
-        const Scale s0 = split_scale(sc[16 * q + 2 * u]), s1 = split_scale(sc[16 * q + 2 * u + 1]);
-        f = make_float2(s0.f, s1.f);
-        l_t = fmaf(e.x, s0.inv, fmaf(e.y, s1.inv, l_t));
-        w_t = fmaf(e.x, s0.f, fmaf(e.y, s1.f, w_t));
-      }
-      const float2 wf = mul2(e, f);
-      const __half2 w = __floats2half2_rn(wf.x, wf.y);
+      run = add2(run, e);
+      if (!kWide) l_2 = fma2(e, make_float2(r[2 * u], r[2 * u + 1]), l_2);
+      const __half2 w = __floats2half2_rn(e.x, e.y);
       const uint32_t c1 = __nv_cvt_halfraw2_to_fp8x2(w, __NV_SATFINITE, __NV_E5M2);
       const uint32_t v1 = __byte_perm(c1, 0, 0x1404);
       const __half2 rest = __hsub2(w, *reinterpret_cast<const __half2 *>(&v1));
@@ -315,11 +320,11 @@ __device__ __forceinline__ void weigh(const float2 (&x)[24], const float *sc, fl
       p1[2 * q + u / 2] = (u & 1) ? __byte_perm(p1[2 * q + u / 2], c1, 0x5410) : c1;
       p2[2 * q + u / 2] = (u & 1) ? __byte_perm(p2[2 * q + u / 2], c2, 0x5410) : c2;
     }
-    if (kWide) {
-      l_t = fmaf(run.x + run.y, s.inv, l_t);
-      w_t = fmaf(run.x + run.y, s.f, w_t);
-    }
+    const float both = run.x + run.y;
+    if (kWide) l_w = fmaf(both, r[0], l_w);
+    w_t += both;
   }
+  l_t = (kWide ? l_w : l_2.x + l_2.y) * kInvTop;
   w_sum += w_t;
   w_lost += __low2float(lost) + __high2float(lost);
 }
@@ -606,9 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c = lane + 32 * h, t = (row_begin + c) / p.num_heads;
           int l = __shfl_sync(0xffffffffu, my_len, t < 32 ? t : 0);
           if (t >= 32 && c < n_rows) l = p.row_len[static_cast<int64_t>(v) * p.num_rows + q0 + t];
-          l = c < n_rows ? min(max(l, 0), p.max_len) : 0;
-          e.lens[c] = l;
-          unit_len = max(unit_len, l);
+          if (c < n_rows) unit_len = max(unit_len, min(max(l, 0), p.max_len));
         }
         // a token that only other units' rows see is not in this unit's tiles: its code may be a NaN
         unit_len = __reduce_max_sync(0xffffffffu, unit_len);
@@ -788,6 +791,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           misc.sc[g & 1u][lane + 32 * j] = a[j];
+          misc.lg[g & 1u][lane + 32 * j] = lg2(a[j]);
+          misc.rc[g & 1u][lane + 32 * j] = rcp(a[j]);
           a[j] = next[j];
         }
         __syncwarp();
@@ -935,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tmem + lanes + kTmemO + blk * kRows + 32 * h, ov);
             if (!ok || !was_ok || *abort_flag != 0) continue;
             const int dim = blk * 128 + 32 * wq + lane;
-            const float4 *factor = reinterpret_cast<const float4 *>(&misc.factor[32 * h]);
+            const float4 *factor = reinterpret_cast<const float4 *>(&misc.alpha[1][32 * h]);
             // O^T scaled; a factor of 0 is a row without a token
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -973,7 +978,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!more) break;
 
-      const int n_rows = e.n_rows, n_tiles = e.n_tiles, seg_lo = e.seg_lo, seg_hi = e.seg_hi, len = e.lens[row];
+      const int n_rows = e.n_rows, n_tiles = e.n_tiles, seg_lo = e.seg_lo, seg_hi = e.seg_hi;
+      const int len = row < n_rows ? min(max(p.row_len[(e.row_base + row) / p.num_heads], 0), p.max_len) : 0;
       const bool active = 16 * wq < n_rows;  // rows of the unit in this warp's quarter
       const float mult = q_scale * p.score_scale;
       float m_ref = -INFINITY, l = 0.0f, w_sum = 0.0f, w_lost = 0.0f;  // sums in units of 2^m_ref
@@ -984,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t g = g0 + i;
         const int tok0 = seg_lo + i * kTile, n_valid = min(kTile, seg_hi - tok0);
         const uint32_t stage = s_base + (g % kStages) * kStageBytes;
-        const float *sc = misc.sc[h] + 8 * term;
+        const float *sc = misc.sc[h] + 8 * term, *lg = misc.lg[h] + 8 * term, *rc = misc.rc[h] + 8 * term;
         float2 x[24];
         float top = -INFINITY;
         wait(misc.s_full[h], g >> 1);
@@ -999,10 +1005,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&misc.s_free));
           // lane i has q1 . k of the tile, lane i + 16 q2 . k: each adds up half of them, to scores in
-          // log2 units plus the scale's exponent
+          // log2 units plus the scale's logarithm
           const float2 w_a = make_float2(w_mine, w_mine), w_b = make_float2(w_other, w_other);
 #pragma unroll
           for (int q = 0; q < 6; ++q) {
+            float s8[8], g8[8];
+            if (kWide) {
+              s8[0] = sc[16 * q];
+              g8[0] = lg[16 * q];
+            } else {
+              load8(sc + 16 * q, s8);
+              load8(lg + 16 * q, g8);
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int a = 16 * q + 2 * u, b = a + 8;
@@ -1012,9 +1026,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 other = make_float2(__shfl_xor_sync(0xffffffffu, __uint_as_float(give0), 16),
                                                __shfl_xor_sync(0xffffffffu, __uint_as_float(give1), 16));
               const float2 dot = fma2(mine, w_a, mul2(other, w_b));
-              const float s0 = sc[16 * q + (kWide ? 0 : 2 * u)], s1 = sc[16 * q + (kWide ? 0 : 2 * u + 1)];
-              x[4 * q + u] = fma2(dot, make_float2(s0 * mult, s1 * mult),
-                                  make_float2(split_scale(s0).k, split_scale(s1).k));
+              const int i0 = kWide ? 0 : 2 * u, i1 = kWide ? 0 : 2 * u + 1;
+              x[4 * q + u] =
+                  fma2(dot, mul2(make_float2(s8[i0], s8[i1]), make_float2(mult, mult)), make_float2(g8[i0], g8[i1]));
             }
           }
           const int seen = min(n_valid, len - tok0) - 8 * term;  // tokens this row sees, counted from 8 term
@@ -1052,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t p1[12], p2[12];
         float l_tile = 0.0f;
-        if (active) weigh<kWide>(x, sc, m_ref == -INFINITY ? 0.0f : m_ref - kTop, l_tile, w_sum, w_lost, p1, p2);
+        if (active) weigh<kWide>(x, rc, m_ref == -INFINITY ? 0.0f : m_ref - kTop, l_tile, w_sum, w_lost, p1, p2);
         l += l_tile;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&misc.sc_free[h]));
@@ -1152,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (spoilt && l > 0.0f) l = NAN;
         const bool none = l == 0.0f;
         const float fix = w_sum / (w_sum - w_lost);
-        misc.factor[row] = none ? 0.0f : (e.seg < 0 ? fix * kInvTop / l : fix * kInvTop);
+        misc.alpha[1][row] = none ? 0.0f : (e.seg < 0 ? fix * kInvTop / l : fix * kInvTop);
         if (ok && row < n_rows) {
           const int64_t r = static_cast<int64_t>(e.row_base) + row;
           if (e.seg < 0) {
@@ -1202,8 +1216,8 @@ mla_status launch_decode_scaled(const DecodeLaunch &d, const float *kv_scales, i
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   // Scale blocks of eight rows or more: a thread's runs of eight tokens have one scale each, which saves
-  // a split and a multiplication per score (64 requests at G = 8: 84 us against 103 by token, 16 x 131,072
-  // tokens at G = 32: 258 against 284).
+  // three loads from shared memory a token (64 requests at G = 8: 79.4 us against 82.9 by token, 32 of 64
+  // rows at G = 64: 39.0 against 40.9, 16 x 131,072 tokens at G = 32: 258 against 264).
   const bool wide = scale_block >= 8;
   auto kern = wide ? mla_decode_scaled_kernel<true> : mla_decode_scaled_kernel<false>;
   if (!g_attr_set[wide][dev].load(std::memory_order_relaxed)) {
