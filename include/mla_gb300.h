@@ -422,9 +422,12 @@ mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, const int32_t *
  * other (below 2^-100 they count as 2^-100, above 2^120 as 2^120).
  * scale_block is a power of two, 1 <= scale_block <= min(64, page_size);
  * num_cache_rows a multiple of it.  No flags are taken
- * (MLA_ERR_UNSUPPORTED).  A NaN code reaches the rows that see
- * its token and no other row.  Workspace, partial layout, outputs, errors and
- * device checks are those of mla_decode_verify. */
+ * (MLA_ERR_UNSUPPORTED).  A probability is held to 2^-7 of itself, or to 2^-28
+ * of the row's largest.  A NaN code reaches the rows that see its token and no
+ * other row; a query that is not finite, or one whose scores pass float32's
+ * range, spoils its own row only.  Workspace size, outputs, errors and device
+ * checks are those of mla_decode_verify; what the workspace holds afterwards is
+ * not defined. */
 mla_status mla_decode_verify_scaled(const mla_decode_args *a, const float *kv_scales,
                                     int scale_block, void *workspace, size_t workspace_bytes,
                                     mla_stream_t stream);
