@@ -13,8 +13,8 @@
 // from G (four rows a warp at G = 1, a warp per unit up to G = 4, then a CTA of
 // 128 to 512 threads), which keeps the registers low enough for 32 warps per SM.
 // One kernel with 18 pieces for every G ran at one CTA of 8 warps per SM: 109 us
-// for 131,000 rows at G = 64; and a warp that took one row at a time 65 us for as
-// many at G = 1, against 43 with four.
+// for 136,000 rows at G = 64; and a warp that took one row at a time 65 us for
+// 131,072 at G = 1, against 43 with four.
 //
 // Scale: 2^k, the smallest with max |x| <= 448 * 2^k.  With max |x| = m 2^e,
 // m in [1, 2), and 448 = 1.75 * 2^8, that is k = e - 8, plus one when m > 1.75;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(co
   __shared__ int s_rows[kThreads / 32][kG];
   __shared__ uint32_t s_team[2][kThreads / 32 + 1];
   // The slots that the window and its last unit touch, and 32 before, in one load: leaders and members
-  // read from the map are three loads, one after another, before the first row's (131,000 rows at
+  // read from the map are three loads, one after another, before the first row's (136,000 rows at
   // G = 64: 51.4 -> 48.4 us).
   constexpr int kNear = 32 + kMaxGroup + kG;
   static_assert(kNear <= kThreads, "a thread per slot");

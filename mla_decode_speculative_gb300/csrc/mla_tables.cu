@@ -35,7 +35,7 @@ struct TabParams {
 // With l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, (n + floor(m n / 2^32)) >> l is n / d for
 // every n < 2^32 (Granlund and Montgomery, division by invariant integers); n < 2^31 keeps the sum in 32
 // bits.  A division by a variable is 20 instructions or more, and a prompt's look-ups are bound by the ALU
-// (994,000 tokens: 10.3 -> 8.2 us).
+// (884,000 tokens: 10.3 -> 8.2 us).
 __device__ __forceinline__ int div_bs(const TabParams &p, int n) {
   return static_cast<int>((static_cast<uint32_t>(n) + __umulhi(static_cast<uint32_t>(n), p.bs_mul)) >> p.bs_shift);
 }
@@ -282,8 +282,8 @@ extern "C" mla_status mla_update_block_tables(const mla_table_args *a, mla_strea
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   // A step's few tokens one per thread, so that their look-ups run side by side
-  // (1,150 tokens of a shard: 5.1 us against 9.4 with four); a prompt's many four per
-  // thread (994,000 tokens: 10.9 -> 8.2 us).
+  // (27,600 tokens on a shard: 5.1 us against 9.4 with four); a prompt's many four per
+  // thread (884,000 tokens: 10.9 -> 8.2 us).
   const bool many = a->num_rows > 65536;
   auto kern = many ? update_tables_kernel<4> : update_tables_kernel<1>;
   if (!g_tab_attr[many][dev].load(std::memory_order_relaxed)) {
