@@ -410,7 +410,7 @@ extern "C" mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, cons
   const bool by_cta = scale_block >= 8;
   // Rows per team: one while the GPU holds a team for every row (so that a
   // step's few tokens spread out), then as many as keep it at two full waves,
-  // within the list of leaders (64) or a warp.
+  // within the list of leaders (64), a warp's lanes or the rows that it holds.
   const int team_warps = scale_block == kMaxGroup ? 16 : scale_block >= 16 ? 8 : by_cta ? 4 : 1;
   const int teams = sms * 64 / team_warps, most = by_cta ? kMaxGroup : scale_block == 1 ? kRowsHeld : 32;
   int window = num_rows / teams;
