@@ -690,6 +690,40 @@ def test_serving_steps(W, graph):
         assert np.abs(lse.cpu().numpy()[:n_rows] - l).max() <= LSE_TOL
 
 
+@pytest.mark.parametrize("W,I,S", [(3, 1, 4), (2, 4, 1), (8, 1, 16)])
+def test_verify_step_over_shard_views(W, I, S):
+    """VerifyStep with every shard's view in one launch of the block-scaled decode, requests too short for
+    some shards among them: the merged states against the whole sequences."""
+    bs, G, H, L, ql = 32, 16, 8, np.array([700, 5, 131, 1]), np.array([4, 3, 2, 1])
+    B, T, width = len(L), int(ql.sum()) + 2, 24
+    g = torch.Generator().manual_seed(W)
+    table = np.random.default_rng(W).permutation(W * B * width).astype(np.int32).reshape(W, B, width)
+    pool = table.size
+    codes = (torch.randn((pool * bs, 576), generator=g) * 100).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    codes = codes.view(torch.uint8)
+    scales = torch.exp2(torch.round(torch.randn(pool * bs // G, generator=g)) - 6) * 1.25
+    q = torch.randn((T, H, 576), generator=g).to(torch.bfloat16)
+    ind = indptr(ql)
+    step = runner.VerifyStep(num_reqs=B, num_rows=T, num_heads=H, max_qlen=4, block_size=bs, num_blocks=pool,
+                             block_table_width=width, max_kv_len=700, num_segments=S, world_size=W, interleave=I,
+                             scale_block=G)
+    dev = q.cuda(), codes.cuda(), i32(L), i32(ind), i32(table), scales.cuda()
+    out, lse = step(*dev[:5], SM, kv_scales=dev[5])
+    assert mla.get_device_error() == 0
+    n, flat = int(ql.sum()), np.full((B, int(L.max())), -1, np.int64)
+    for b in range(B):
+        for pos in range(L[b]):
+            r, j = ref.local_index(pos, W, I)
+            flat[b, pos] = table[r, b, j // bs] * bs + j % bs
+    row_len = np.concatenate([np.arange(L[b] - ql[b] + 1, L[b] + 1) for b in range(B)])
+    row_scale = scales.numpy().repeat(G)
+    o, l, mass, far = ref.attention(q[:n].double().numpy(), codes.numpy(), row_scale, 1, ind, row_len, flat, 1, SM)
+    err = np.abs(out[:n].float().cpu().numpy() - o)
+    # one more rounding of each shard's state to bf16 when states are merged
+    assert (err <= ref.out_bound(o, mass, far) + 2.0 ** -8 * mass).all()
+    assert np.abs(lse[:n].cpu().numpy() - l).max() <= LSE_TOL
+
+
 def test_append_that_ran_out_of_blocks_is_undone():
     """Too few free blocks: the error, blocks and lengths back as before, then a smaller step, and every
     block returned in the end.  A refused call changes nothing either."""
