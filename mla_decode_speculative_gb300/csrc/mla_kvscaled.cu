@@ -248,12 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(co
   // read from the map are three loads, one after another, before the first row's (136,000 rows at
   // G = 64: 51.4 -> 48.4 us).
   constexpr int kNear = 32 + kMaxGroup + kG;
-  static_assert(kNear <= kThreads, "a thread per slot");
   __shared__ int s_near[kNear];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.x * p.window, r_end = min(p.num_rows, r0 + p.window);
   const Slots slots{p.slots, s_near, r0 - 32, kNear};
-  if (tid < kNear) s_near[tid] = r0 - 32 + tid >= 0 && r0 - 32 + tid < p.num_rows ? p.slots[r0 - 32 + tid] : -1;
+#pragma unroll
+  for (int i = tid; i < kNear; i += kThreads) {
+    const int r = r0 - 32 + i;
+    s_near[i] = r >= 0 && r < p.num_rows ? p.slots[r] : -1;
+  }
   __syncthreads();
   if (warp == 0) {
     int units = 0;
@@ -408,12 +411,14 @@ extern "C" mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, cons
   p.log_g = __builtin_ctz(static_cast<unsigned>(scale_block));
   p.num_cache_rows = static_cast<int>(num_cache_rows);
   const bool by_cta = scale_block >= 8;
-  // Rows per team: one while the GPU holds a team for every row (so that a
-  // step's few tokens spread out), then as many as keep it at two full waves,
-  // within the list of leaders (64), a warp's lanes or the rows that it holds.
-  const int team_warps = scale_block == kMaxGroup ? 16 : scale_block >= 16 ? 8 : by_cta ? 4 : 1;
+  // Rows per team: one while the GPU holds a team for every row (so that a step's few tokens spread out),
+  // then as many as give one wave of teams (rounded down, a second wave of a few: 131,072 rows at G = 8 44.4
+  // us against 40.4), within the list of leaders (64), a warp's lanes or the rows that it holds.  Teams of
+  // CTAs have nine pieces a thread (G = 16 with 256 threads: 43.4 us against 39.4), but at G = 8, whose 64
+  // threads would be slow for a step's few rows (1,152 rows: 4.0 us against 3.2).
+  const int team_warps = !by_cta ? 1 : scale_block == 8 ? 4 : scale_block / 4;
   const int teams = sms * 64 / team_warps, most = by_cta ? kMaxGroup : scale_block == 1 ? kRowsHeld : 32;
-  int window = num_rows / teams;
+  int window = (num_rows + teams - 1) / teams;
   window = window < 1 ? 1 : (window > most ? most : window);
   p.window = window;
   const int per_cta = by_cta ? window : window * (kWarpCta / 32);
@@ -424,7 +429,7 @@ extern "C" mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, cons
     case 2: e = launch_pdl(write_scaled_warp<2>, grid, dim3(kWarpCta), 0, s, p); break;
     case 4: e = launch_pdl(write_scaled_warp<4>, grid, dim3(kWarpCta), 0, s, p); break;
     case 8: e = launch_pdl(write_scaled_cta<128, 8>, grid, dim3(128), 0, s, p); break;
-    case 16: e = launch_pdl(write_scaled_cta<256, 16>, grid, dim3(256), 0, s, p); break;
+    case 16: e = launch_pdl(write_scaled_cta<128, 16>, grid, dim3(128), 0, s, p); break;
     case 32: e = launch_pdl(write_scaled_cta<256, 32>, grid, dim3(256), 0, s, p); break;
     default: e = launch_pdl(write_scaled_cta<512, 64>, grid, dim3(512), 0, s, p); break;
   }
