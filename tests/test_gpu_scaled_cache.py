@@ -486,8 +486,11 @@ def test_attention_scores_beyond_float32_spoil_their_row_only(S):
     check_rows(out, lse, args, 16, nan_rows)
 
 
-def test_attention_queries_off_a_32_byte_boundary():
-    L, ql = np.array([260, 500]), np.array([3, 5])
+@pytest.mark.parametrize("B", [2, 500])
+def test_attention_queries_off_a_32_byte_boundary(B):
+    """Few row blocks (the first of a CTA each) and many (several per CTA, read another way)."""
+    r = np.random.default_rng(B)
+    L, ql = (np.array([260, 500]), np.array([3, 5])) if B == 2 else (r.integers(5, 110, B), r.integers(1, 6, B))
     args = attention_inputs(L, ql, 20, 32, 16, 19)
     first = run_attention(*args[:3], 16, *args[3:], 3, 5)
     room = torch.empty(args[0].numel() + 8, dtype=torch.bfloat16, device="cuda")
