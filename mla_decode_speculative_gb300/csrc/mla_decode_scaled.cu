@@ -977,6 +977,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!more) break;
+      // All eight warps have read their columns of O^T.  The first product of this part overwrites them
+      // all, and waits only for the group that has the part's first tile.
+      if (k > 0) named_bar_sync(kBarSoft, kSoftThreads);
 
       const int n_rows = e.n_rows, n_tiles = e.n_tiles, seg_lo = e.seg_lo, seg_hi = e.seg_hi;
       const int len = row < n_rows ? min(max(p.row_len[(e.row_base + row) / p.num_heads], 0), p.max_len) : 0;
