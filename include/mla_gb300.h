@@ -390,6 +390,13 @@ typedef struct mla_table_args {
  * MLA_DEV_BAD_BLOCK_ID (an id outside the pool in the ring or table: -1). */
 mla_status mla_update_block_tables(const mla_table_args *a, mla_stream_t stream);
 
+/* The same, and lens_out [B] gets the lengths whose blocks the requests hold
+ * after the call, the next call's prev_lens: max(seq_lens, 0), or prev_lens
+ * where the device checks refused the step (MLA_DEV_BAD_INDPTR,
+ * MLA_DEV_BAD_FREE_RING), so that a caller who keeps this state on the device
+ * need not know which.  lens_out must not overlap prev_lens or seq_lens. */
+mla_status mla_update_block_tables_lens(const mla_table_args *a, int32_t *lens_out, mla_stream_t stream);
+
 /* Quantising write of new latent rows into an e4m3 cache with one float32
  * scale per block of scale_block consecutive cache rows (kv_scales
  * [num_cache_rows / scale_block]; a row's values are scale * code).  Row r of

@@ -27,6 +27,7 @@ constexpr int kMaxTableReqs = 16384;  // two prefix sums and the row offsets in 
 
 struct TabParams {
   mla_table_args a;
+  int32_t *lens_out;  // or null
   int *err;
   uint32_t bs_mul;  // n / block_size = (n + umulhi(n, bs_mul)) >> bs_shift, 0 <= n < 2^31
   int bs_shift;
@@ -148,6 +149,8 @@ __global__ void __launch_bounds__(kTabThreads) update_tables_kernel(const TabPar
     a.ring_out[1] = good ? count - dealt + n_rel : count;
   }
   const int first = blockIdx.x * kTabThreads + tid, step = gridDim.x * kTabThreads;
+  if (p.lens_out != nullptr)
+    for (int b = first; b < B; b += step) p.lens_out[b] = good ? max(a.seq_lens[b], 0) : a.prev_lens[b];
   if (!good) {
     for (int r = first; r < T; r += step) a.slot_map[r] = -1;
     return;
@@ -244,12 +247,7 @@ __global__ void __launch_bounds__(kTabThreads) update_tables_kernel(const TabPar
 
 std::atomic<bool> g_tab_attr[2][64];
 
-}  // namespace
-}  // namespace mla
-
-using namespace mla;
-
-extern "C" mla_status mla_update_block_tables(const mla_table_args *a, mla_stream_t stream) {
+mla_status update_block_tables(const mla_table_args *a, int32_t *lens_out, mla_stream_t stream) {
   if (a == nullptr || a->num_reqs < 0 || a->num_rows < 0 || a->world_size < 1 || a->rank < 0 ||
       a->rank >= a->world_size || a->interleave < 1 ||
       static_cast<int64_t>(a->interleave) * a->world_size > INT32_MAX) {
@@ -270,6 +268,11 @@ extern "C" mla_status mla_update_block_tables(const mla_table_args *a, mla_strea
       (a->ring_out < a->ring_in + 2 && a->ring_in < a->ring_out + 2) || (a->num_rows > 0 && a->slot_map == nullptr) ||
       (a->num_reqs > 0 && (a->prev_lens == nullptr || a->seq_lens == nullptr || a->block_table == nullptr))) {
     set_error("mla_update_block_tables: null pointer, or ring_out overlaps ring_in");
+    return MLA_ERR_INVALID_ARG;
+  }
+  const auto overlaps = [&](const int32_t *lens) { return lens_out < lens + a->num_reqs && lens < lens_out + a->num_reqs; };
+  if (lens_out != nullptr && a->num_reqs > 0 && (overlaps(a->prev_lens) || overlaps(a->seq_lens))) {
+    set_error("mla_update_block_tables_lens: lens_out overlaps prev_lens or seq_lens");
     return MLA_ERR_INVALID_ARG;
   }
   if (a->num_reqs > kMaxTableReqs) {
@@ -295,7 +298,7 @@ extern "C" mla_status mla_update_block_tables(const mla_table_args *a, mla_strea
   int shift = 0;
   while ((1LL << shift) < a->block_size) ++shift;
   const uint64_t rest = (1ULL << shift) - static_cast<uint64_t>(a->block_size);
-  const TabParams p{*a, err, static_cast<uint32_t>((rest << 32) / static_cast<uint64_t>(a->block_size) + 1), shift};
+  const TabParams p{*a, lens_out, err, static_cast<uint32_t>((rest << 32) / static_cast<uint64_t>(a->block_size) + 1), shift};
   // up to 8 CTAs per SM's worth; tables without tokens still get a thread per request
   const int rows = many ? a->num_rows / 4 + 1 : a->num_rows;
   const int items = rows > a->num_reqs ? rows : a->num_reqs;
@@ -304,4 +307,21 @@ extern "C" mla_status mla_update_block_tables(const mla_table_args *a, mla_strea
   e = launch_pdl(kern, dim3(grid), dim3(kTabThreads), 3 * (static_cast<size_t>(a->num_reqs) + 1) * sizeof(int),
                  reinterpret_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "update_block_tables launch");
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" mla_status mla_update_block_tables(const mla_table_args *a, mla_stream_t stream) {
+  return update_block_tables(a, nullptr, stream);
+}
+
+extern "C" mla_status mla_update_block_tables_lens(const mla_table_args *a, int32_t *lens_out, mla_stream_t stream) {
+  if (lens_out == nullptr && (a == nullptr || a->num_reqs != 0)) {
+    set_error("mla_update_block_tables_lens: null lens_out");
+    return MLA_ERR_INVALID_ARG;
+  }
+  return update_block_tables(a, lens_out, stream);
 }

@@ -85,7 +85,8 @@ _lock = threading.Lock()
 EXPORTS = ("mla_page_size", "mla_plan_rows", "mla_shard_row_view", "mla_shard_row_views",
            "mla_decode_verify_workspace",
            "mla_decode_verify", "mla_decode_verify_noalloc", "mla_write_kv", "mla_merge_segments",
-           "mla_update_block_tables", "mla_write_kv_scaled", "mla_decode_verify_scaled", "mla_get_device_error",
+           "mla_update_block_tables", "mla_update_block_tables_lens", "mla_write_kv_scaled", "mla_decode_verify_scaled",
+           "mla_get_device_error",
            "mla_last_error_string", "mla_status_string", "mla_abi_version")
 
 
@@ -127,6 +128,8 @@ def lib():
         L.mla_write_kv.restype = c_int
         L.mla_update_block_tables.argtypes = [ctypes.POINTER(TableArgs), vp]
         L.mla_update_block_tables.restype = c_int
+        L.mla_update_block_tables_lens.argtypes = [ctypes.POINTER(TableArgs), vp, vp]
+        L.mla_update_block_tables_lens.restype = c_int
         L.mla_write_kv_scaled.argtypes = [c_int, vp, i32p, vp, vp, c_int, ctypes.c_int64, vp]
         L.mla_write_kv_scaled.restype = c_int
         L.mla_decode_verify_scaled.argtypes = [ctypes.POINTER(DecodeArgs), vp, c_int, vp, ctypes.c_size_t, vp]
@@ -452,12 +455,13 @@ def _dev_ptr(t: torch.Tensor, dtype, dev: int, name: str) -> int:
 
 def update_block_tables(prev_lens, seq_lens, qo_indptr, block_table, free_ring, ring_in, block_size,
                         num_rows, ring_out=None, slot_map=None, world_size=1, rank=0, interleave=1,
-                        stream=None):
+                        stream=None, lens_out=None):
     """mla_update_block_tables: blocks for the requests that grow from prev_lens to seq_lens
     tokens, blocks back from those that shrink, and the new tokens' cache rows.  All int32:
     prev_lens, seq_lens [B], qo_indptr [B + 1], block_table [B, width] (updated), free_ring
-    [num_blocks] (updated), ring_in [2] = (head, count).  Returns (slot_map [num_rows],
-    ring_out [2])."""
+    [num_blocks] (updated), ring_in [2] = (head, count).  lens_out [B], if given, gets the lengths
+    that the requests hold blocks for after the call (mla_update_block_tables_lens).  Returns
+    (slot_map [num_rows], ring_out [2])."""
     L, dev, raw = _current(stream)
     if ring_out is None:
         ring_out = torch.empty_like(ring_in)
@@ -465,16 +469,20 @@ def update_block_tables(prev_lens, seq_lens, qo_indptr, block_table, free_ring, 
         slot_map = torch.empty(num_rows, dtype=torch.int32, device=seq_lens.device)
     B, width = block_table.shape
     if prev_lens.numel() != B or seq_lens.numel() != B or qo_indptr.numel() != B + 1 or \
-            ring_in.numel() != 2 or ring_out.numel() != 2 or slot_map.numel() < num_rows:
-        raise ValueError("prev_lens, seq_lens [B], qo_indptr [B + 1], block_table [B, width], ring_in and "
-                         "ring_out [2], slot_map [num_rows]")
+            ring_in.numel() != 2 or ring_out.numel() != 2 or slot_map.numel() < num_rows or \
+            (lens_out is not None and lens_out.numel() != B):
+        raise ValueError("prev_lens, seq_lens, lens_out [B], qo_indptr [B + 1], block_table [B, width], ring_in "
+                         "and ring_out [2], slot_map [num_rows]")
     i32 = torch.int32
     a = TableArgs(B, num_rows, _dev_ptr(prev_lens, i32, dev, "prev_lens"), _dev_ptr(seq_lens, i32, dev, "seq_lens"),
                   _dev_ptr(qo_indptr, i32, dev, "qo_indptr"), world_size, rank, interleave, block_size,
                   free_ring.numel(), _dev_ptr(block_table, i32, dev, "block_table"), width,
                   _dev_ptr(free_ring, i32, dev, "free_ring"), _dev_ptr(ring_in, i32, dev, "ring_in"),
                   _dev_ptr(ring_out, i32, dev, "ring_out"), _dev_ptr(slot_map, i32, dev, "slot_map"))
-    st = L.mla_update_block_tables(ctypes.byref(a), raw)
+    if lens_out is None:
+        st = L.mla_update_block_tables(ctypes.byref(a), raw)
+    else:
+        st = L.mla_update_block_tables_lens(ctypes.byref(a), _dev_ptr(lens_out, i32, dev, "lens_out"), raw)
     if st:
         _check(st, "mla_update_block_tables")
     return slot_map, ring_out

@@ -143,7 +143,8 @@ class PagedLatentCache:
     def append(self, kv_new: torch.Tensor, seq_lens: torch.Tensor, qo_indptr: torch.Tensor, stream=None):
         """The step's new tokens: request b grows (or, drafts taken back, shrinks) to seq_lens[b]
         tokens, the last qo_indptr[b + 1] - qo_indptr[b] of which are rows of kv_new [num_rows,
-        576] bf16; 0 tokens return all of its blocks.  Returns the slot map."""
+        576] bf16; 0 tokens return all of its blocks.  A step that the device checks refuse
+        (MLA_DEV_BAD_INDPTR, MLA_DEV_BAD_FREE_RING) changes nothing.  Returns the slot map."""
         if kv_new.shape[0] != self.num_rows:
             raise ValueError("kv_new must have num_rows rows")
         s = torch.cuda.current_stream() if stream is None else stream
@@ -151,16 +152,16 @@ class PagedLatentCache:
             raise ValueError("seq_lens must have num_reqs entries")
         with torch.cuda.stream(s):
             self._before.copy_(self._now)
+        if seq_lens.data_ptr() == self.lens.data_ptr():   # lengths as they are: the table call writes them
+            seq_lens = self._before[2:]
         try:
             mla.update_block_tables(self._before[2:], seq_lens, qo_indptr, self.block_table, self.free_ring,
                                     self._before[:2], self.block_size, self.num_rows, ring_out=self.ring,
-                                    slot_map=self.slot_map, stream=s, **self.shard)
+                                    slot_map=self.slot_map, stream=s, lens_out=self.lens, **self.shard)
             mla.write_kv_scaled(kv_new, self.slot_map, self.codes, self.scales, self.scale_block, stream=s)
         except Exception:
             self.undo(s)
             raise
-        with torch.cuda.stream(s):
-            self.lens.copy_(seq_lens)
         return self.slot_map
 
     def undo(self, stream=None):

@@ -783,6 +783,59 @@ def test_append_that_ran_out_of_blocks_is_undone():
     assert sorted(c.free_ring.tolist()) == list(range(6))
 
 
+@pytest.mark.parametrize("graph", [False, True])
+def test_append_that_the_tables_refuse_changes_nothing(graph):
+    """An inconsistent qo_indptr, then a ring state outside the pool: lengths, blocks and codes as before,
+    and the next step is dealt as if the refused one had not been."""
+    c = runner.PagedLatentCache(num_reqs=3, num_rows=64, num_blocks=12, block_size=16, max_kv_len=96, scale_block=16)
+    x, seq, ind = new_rows(64, 1).cuda(), i32([40, 10, 14]), i32([0, 40, 50, 64])
+    g = None
+
+    def step(L, rows):
+        nonlocal g
+        seq.copy_(i32(L)), ind.copy_(i32(rows))
+        if graph and g is None:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                c.append(x, seq, ind)
+        g.replay() if graph else c.append(x, seq, ind)
+        return mla.get_device_error()
+
+    assert step([40, 10, 14], [0, 40, 50, 64]) == 0
+    keep = lambda: [t.clone() for t in (c.ring, c.lens, c.block_table, c.free_ring, c.codes, c.scales)]
+    same = lambda a: all(torch.equal(u, v) for u, v in zip(a, keep()))
+    before = keep()
+    assert before[1].tolist() == [40, 10, 14]
+    for bad in ([0, 30, 20, 44], [1, 30, 40, 44], [0, 30, 40, 65]):
+        assert step([70, 40, 30], bad) == 1 and same(before) and (c.slot_map == -1).all()
+    count = int(c.ring[1])
+    c.ring[1] = 13
+    assert step([70, 40, 30], [0, 30, 40, 44]) == 8 and c.lens.tolist() == [40, 10, 14]
+    c.ring[1] = count
+    assert same(before)
+    m = ref.update_tables([40, 10, 14], [42, 0, 33], [0, 2, 2, 21], before[2].cpu().numpy(), before[3].cpu().numpy(),
+                          tuple(before[0].tolist()), 16, 64)
+    assert step([42, 0, 33], [0, 2, 2, 21]) == 0
+    assert np.array_equal(c.block_table.cpu().numpy(), m[0]) and np.array_equal(c.free_ring.cpu().numpy(), m[1])
+    assert tuple(c.ring.tolist()) == m[2] and np.array_equal(c.slot_map.cpu().numpy(), m[3])
+    assert c.lens.tolist() == [42, 0, 33]
+
+
+def test_append_with_the_caches_own_lengths_and_a_negative_one():
+    """The cache's own lens as the new lengths (nothing changes); a negative length counts as 0, flagged."""
+    c = runner.PagedLatentCache(num_reqs=2, num_rows=32, num_blocks=6, block_size=16, max_kv_len=48, scale_block=16)
+    x = new_rows(32, 1).cuda()
+    c.append(x, i32([20, 10]), i32([0, 20, 30]))
+    state = c.ring.tolist(), c.block_table.clone()
+    c.append(x, c.lens, i32([0, 0, 0]))
+    assert mla.get_device_error() == 0
+    assert c.lens.tolist() == [20, 10] and c.ring.tolist() == state[0] and torch.equal(c.block_table, state[1])
+    c.append(x, i32([-5, 10]), i32([0, 0, 0]))
+    assert mla.get_device_error() == 2 and c.lens.tolist() == [0, 10] and c.ring[1].item() == 5
+    c.append(x, i32([0, 10]), i32([0, 0, 0]))
+    assert mla.get_device_error() == 0 and c.ring[1].item() == 5
+
+
 def test_two_streams_and_two_graphs_at_once():
     """Two captured graphs with a workspace each, replayed on two streams together, and an eager call
     on a third: the same outputs as alone."""

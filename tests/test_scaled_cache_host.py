@@ -47,6 +47,16 @@ def test_table_refusals(L, change, status):
     assert b"mla_update_block_tables" in L.mla_last_error_string()
 
 
+@pytest.mark.parametrize("lens_out", [None, 256, 260, 252, 1024, 1028])
+def test_table_lens_out_refusals(L, lens_out):
+    """Null, or overlapping prev_lens (at 256) or seq_lens (at 1024), two requests each."""
+    a = _tables(seq_lens=1024)
+    assert L.mla_update_block_tables_lens(ctypes.byref(a), VP(lens_out) if lens_out else None, None) == INVALID
+    assert b"lens_out" in L.mla_last_error_string()
+    assert L.mla_update_block_tables_lens(None, VP(4096), None) == INVALID
+    assert L.mla_update_block_tables_lens(ctypes.byref(_tables(seq_lens=1024, rank=1)), VP(4096), None) == INVALID
+
+
 def test_null_structs(L):
     assert L.mla_update_block_tables(None, None) == INVALID
     assert L.mla_decode_verify_scaled(None, VP(256), 16, VP(256), 1 << 20, None) == INVALID
