@@ -387,7 +387,10 @@ typedef struct mla_table_args {
  * length, read as 0: that request's slots are -1), MLA_DEV_LEN_BOUND (need
  * clipped to the table's width, slots past it -1), MLA_DEV_NO_FREE_BLOCK
  * (entries the ring could not serve are -1, and so are their tokens' slots),
- * MLA_DEV_BAD_BLOCK_ID (an id outside the pool in the ring or table: -1). */
+ * MLA_DEV_BAD_BLOCK_ID (an id outside the pool in the ring or table counts as
+ * -1; a returned one takes its place in the ring as -1, so a step that ended
+ * with MLA_DEV_NO_FREE_BLOCK is best taken back: prev_lens and ring state as
+ * before it). */
 mla_status mla_update_block_tables(const mla_table_args *a, mla_stream_t stream);
 
 /* The same, and lens_out [B] gets the lengths whose blocks the requests hold

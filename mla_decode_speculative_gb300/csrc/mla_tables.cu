@@ -9,9 +9,10 @@
 // and those being returned) and what is written (ring places from head +
 // count on, table entries from held_b on) never overlap, so one launch
 // without a grid barrier does it all: every CTA makes the prefix sums of all
-// requests for itself in shared memory (two passes over 8 B bytes, from L2)
-// and then takes its share of the dealt blocks, the returned blocks and the
-// new tokens.
+// requests for itself in shared memory (one pass over the lengths and
+// qo_indptr, 12 B bytes from L2) and then takes its share of the dealt blocks,
+// the returned blocks and the new tokens, reading the lengths of their
+// requests once more.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -172,8 +173,11 @@ __global__ void __launch_bounds__(kTabThreads) update_tables_kernel(const TabPar
   for (int k = first; k < n_rel; k += step) {
     const int b = owner_of(roff, B, k);
     const int e = blocks_of(p, a.seq_lens[b], over) + k - roff[b];
-    const int id = a.block_table[static_cast<int64_t>(b) * a.block_table_stride + e];
-    if (id < 0 || id >= C) tab_error(p, MLA_DEV_BAD_BLOCK_ID);
+    int id = a.block_table[static_cast<int64_t>(b) * a.block_table_stride + e];
+    if (id < 0 || id >= C) {
+      tab_error(p, MLA_DEV_BAD_BLOCK_ID);
+      id = -1;
+    }
     a.free_ring[ring_place(head, count + k, C)] = id;
   }
   // A thread's rows: one search for their request and one look-up per block

@@ -166,6 +166,26 @@ def test_tables_device_checks():
     assert t[0, 2] == -1 and (slots[:2] >= 0).sum() == 0
 
 
+def test_tables_return_bad_entries_as_minus_one():
+    """Table entries outside the pool go back to the ring as -1, flagged, and are dealt as -1; the good
+    ones among them keep their places."""
+    prev, seq = [40, 24], [10, 0]
+    table, ring, state = table_state(prev, 12, 6, 8, head=9)
+    table[0, 3], table[1, 1], table[1, 2] = 12, -1, 1 << 30
+    d_table, d_ring = i32(table), i32(ring)
+    slots, out = mla.update_block_tables(i32(prev), i32(seq), i32([0, 0, 0]), d_table, d_ring, i32(state), 8, 0)
+    assert mla.get_device_error() == 3 and out.tolist() == [9, 10]
+    want = ring.copy()
+    want[(9 + 4 + np.arange(6)) % 12] = [table[0, 2], -1, table[0, 4], table[1, 0], -1, -1]
+    assert np.array_equal(d_ring.cpu().numpy(), want) and np.array_equal(d_table.cpu().numpy(), table)
+    slots, out = mla.update_block_tables(i32(seq), i32([10, 48]), i32([0, 0, 48]), d_table, d_ring, out, 8, 48)
+    assert mla.get_device_error() == 3 and out.tolist() == [3, 4]
+    got = d_table.cpu().numpy()
+    assert np.array_equal(got[1], [*ring[(9 + np.arange(4)) % 12], table[0, 2], -1])
+    assert np.array_equal(slots.cpu().numpy(), np.where(got[1] < 0, -1, got[1] * 8).repeat(8)
+                          + np.where(got[1] < 0, 0, 1).repeat(8) * np.tile(np.arange(8), 6))
+
+
 # ------------------------------------------------------------------ quantising write
 
 def slots_of(L, ql, bs, W, rank, I, seed):
