@@ -185,6 +185,28 @@ struct Slots {
   }
 };
 
+__device__ __forceinline__ bool has_slot(const WriteScaledParams &p, int s) { return s >= 0 && s < p.num_cache_rows; }
+
+// Nearest slot before row `end` (a warp; -1: none).  Rows without one may be many: another shard's, or those
+// before the first request's own.
+__device__ __forceinline__ int slot_before(const WriteScaledParams &p, int end, int lane) {
+  constexpr int kLook = 16;  // loads in flight
+  for (; end > 0; end -= 32 * kLook) {
+    int s[kLook];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      const int r = end - 32 * (i + 1) + lane;
+      s[i] = r >= 0 ? p.slots[r] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      const uint32_t got = __ballot_sync(0xffffffffu, has_slot(p, s[i]));
+      if (got) return __shfl_sync(0xffffffffu, s[i], 31 - __clz(got));
+    }
+  }
+  return -1;
+}
+
 // Leaders among rows r0 .. r0 + 31 (a warp): the row of lane l opens a unit.
 // A row whose nearest earlier row with a slot lies in the same scale block
 // follows a leader; rows without a slot (another shard's) are passed over.
@@ -203,35 +225,113 @@ __device__ __forceinline__ uint32_t leaders(const WriteScaledParams &p, const Sl
   int prev = __shfl_sync(0xffffffffu, slot, below ? 31 - __clz(below) : 0);
   const int head_slot = __shfl_sync(0xffffffffu, slot, __ffs(have) - 1);
   int before = -1;
-  if ((head_slot & ((1 << p.log_g) - 1)) != 0)
-    for (int b0 = r0 - 32; b0 > -32 && before < 0; b0 -= 32) {
-      const int s = b0 + lane >= 0 ? slots[b0 + lane] : -1;
-      const uint32_t got = __ballot_sync(0xffffffffu, s >= 0 && s < p.num_cache_rows);
-      if (got) before = __shfl_sync(0xffffffffu, s, 31 - __clz(got));
-    }
+  if ((head_slot & ((1 << p.log_g) - 1)) != 0) {
+    const int s = r0 - 32 + lane >= 0 ? slots[r0 - 32 + lane] : -1;
+    const uint32_t got = __ballot_sync(0xffffffffu, has_slot(p, s));
+    before = got ? __shfl_sync(0xffffffffu, s, 31 - __clz(got)) : slot_before(p, r0 - 32, lane);
+  }
   if (below == 0) prev = before;
   const bool lead = slot >= 0 && (prev < 0 || (prev >> p.log_g) != (slot >> p.log_g));
   return __ballot_sync(0xffffffffu, lead);
 }
 
-// The rows of the unit that row r0 leads (a warp), into rows[]; returns how many.
-__device__ __forceinline__ int members(const WriteScaledParams &p, const Slots &slots, int r0, int first_slot, int lane,
-                                       int *rows) {
+// 32 slots, row r's for lane 0 first (a warp): the rows of the unit among them go to rows[n ..), at most
+// `room` in all.  False when the unit ends here.
+__device__ __forceinline__ bool take_rows(const WriteScaledParams &p, int r, int s, int block, int room, int lane,
+                                          int *rows, int &n, bool &blank) {
+  const bool valid = has_slot(p, s);
+  const uint32_t other = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) != block);
+  const uint32_t upto = other ? (1u << (__ffs(other) - 1)) - 1u : 0xffffffffu;
+  const uint32_t mine = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) == block) & upto;
+  const int at = n + __popc(mine & ((1u << lane) - 1u));
+  if ((mine >> lane & 1u) && at < room) rows[at] = r + lane;
+  n = min(n + __popc(mine), room);
+  blank = mine == 0;
+  return other == 0 && n < room;
+}
+
+// The rows of the unit that row r0 leads, among rows r0 .. end - 1 (a warp), into rows[]; returns how many,
+// and whether later rows may belong to it.
+__device__ __forceinline__ int members(const WriteScaledParams &p, const Slots &slots, int r0, int end, int first_slot,
+                                       int lane, int *rows, bool &open) {
   const int block = first_slot >> p.log_g;
   const int room = (1 << p.log_g) - (first_slot & ((1 << p.log_g) - 1));
   int n = 0;
-  for (int b0 = r0; b0 < p.num_rows && n < room; b0 += 32) {
-    const int r = b0 + lane;
-    const int s = r < p.num_rows ? slots[r] : -1;
-    const bool valid = s >= 0 && s < p.num_cache_rows;
-    const uint32_t other = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) != block);
-    const uint32_t upto = other ? (1u << (__ffs(other) - 1)) - 1u : 0xffffffffu;
-    const uint32_t mine = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) == block) & upto;
-    const int at = n + __popc(mine & ((1u << lane) - 1u));
-    if ((mine >> lane & 1u) && at < room) rows[at] = r;
-    n = min(n + __popc(mine), room);
-    if (other) break;
+  bool blank;
+  open = true;
+  for (int b0 = r0; b0 < end && open; b0 += 32)
+    open = take_rows(p, b0, b0 + lane < end ? slots[b0 + lane] : -1, block, room, lane, rows, n, blank);
+  open = open && end < p.num_rows;
+  __syncwarp();
+  return n;
+}
+
+// What a team shares while it looks for a unit's far rows.
+template <int kG>
+struct Far {
+  int next, at, n;
+  int rows[kG];
+};
+
+// The unit's rows from row `at` on, n of them being known (the whole team, kTeam threads: a warp or the CTA);
+// copied behind the others into rows[] of every warp, returns how many there are now.  Between a unit's rows,
+// and behind the last one in a step that is smaller than its capacity, any number of rows may have no slot.
+// The first warp takes rows while they are near each other, then the team looks for the next one together,
+// 16 slots a thread in flight: nine new rows in a capacity of 8,192 or 131,072 take 4.5-4.9 and 13-24 us at
+// G >= 8 in a graph (each warp for itself, 32 slots at a time: 76-91 and 1,200-1,420), 32 slots a thread
+// the same but slower steps without empty rows (22,200 rows at G = 2: 7.7 us against 7.5), 8 slots 5.0-5.6
+// and 16-36.
+template <int kTeam, int kG>
+__device__ __forceinline__ int far_members(const WriteScaledParams &p, int first_slot, int at, int n, int t, int *rows,
+                                        Far<kG> &far) {
+  constexpr int kWarps = kTeam / 32, kLook = 16;
+  const int lane = t & 31, warp = t >> 5, n0 = n;
+  const int block = first_slot >> p.log_g;
+  const int room = (1 << p.log_g) - (first_slot & ((1 << p.log_g) - 1));
+  auto sync = [] {
+    if (kTeam == 32) __syncwarp();
+    else __syncthreads();
+  };
+  for (;;) {
+    if (warp == 0) {  // up to 32 rows without a slot
+      bool more = true, blank = false;
+      int b0 = at;
+      for (; b0 < p.num_rows && more && !blank; b0 += 32)
+        more = take_rows(p, b0, b0 + lane < p.num_rows ? p.slots[b0 + lane] : -1, block, room, lane, far.rows, n, blank);
+      if (lane == 0) {
+        far.at = b0;
+        far.n = n;
+        far.next = more ? p.num_rows : 0;
+      }
+    }
+    sync();
+    n = far.n;
+    if (far.next == 0) break;
+    // the next row with a slot: the warps take stretches of 32 kLook rows in turn
+    sync();
+    for (int64_t c0 = far.at + 32 * kLook * warp;; c0 += 32 * kLook * kWarps) {
+      if (c0 >= __shfl_sync(0xffffffffu, *const_cast<volatile int *>(&far.next), 0)) break;
+      int s[kLook], found = INT32_MAX;
+#pragma unroll
+      for (int i = 0; i < kLook; ++i) {
+        const int64_t r = c0 + 32 * i + lane;
+        s[i] = r < p.num_rows ? p.slots[r] : -1;
+      }
+#pragma unroll
+      for (int i = kLook - 1; i >= 0; --i)
+        if (has_slot(p, s[i])) found = 32 * i + lane;
+      found = __reduce_min_sync(0xffffffffu, found);
+      if (found != INT32_MAX) {
+        if (lane == 0) atomicMin(&far.next, static_cast<int>(c0) + found);
+        break;
+      }
+    }
+    sync();
+    at = far.next;
+    if (at >= p.num_rows) break;
+    sync();  // (next is written anew)
   }
+  for (int i = n0 + lane; i < n; i += 32) rows[i] = far.rows[i];
   __syncwarp();
   return n;
 }
@@ -244,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(co
   __shared__ int s_lead[kMaxGroup], s_slot[kMaxGroup], s_units;
   __shared__ int s_rows[kThreads / 32][kG];
   __shared__ uint32_t s_team[2][kThreads / 32 + 1];
+  __shared__ Far<kG> s_far;
   // The slots that the window and its last unit touch, and 32 before, in one load: leaders and members
   // read from the map are three loads, one after another, before the first row's (136,000 rows at
   // G = 64: 51.4 -> 48.4 us).
@@ -274,8 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) write_scaled_cta(co
   }
   __syncthreads();
   const int units = s_units;
+  const int near_end = min(p.num_rows, r0 - 32 + kNear);
   for (int u = 0; u < units; ++u) {  // every warp finds the unit's rows itself: a barrier less
-    const int n = members(p, slots, s_lead[u], s_slot[u], lane, s_rows[warp]);
+    bool open;  // (the same in all warps, which read the same slots in shared memory)
+    int n = members(p, slots, s_lead[u], near_end, s_slot[u], lane, s_rows[warp], open);
+    if (open) n = far_members<kThreads, kG>(p, s_slot[u], near_end, n, tid, s_rows[warp], s_far);
     write_unit<kThreads, kG>(p, s_rows[warp], n, s_slot[u], tid, s_team[u & 1]);
     __syncwarp();
   }
@@ -343,6 +447,7 @@ __global__ void __launch_bounds__(kWarpCta, 4) write_scaled_warp(const WriteScal
   grid_dep_wait();
   grid_dep_launch();
   __shared__ int s_rows[kWarpCta / 32][kG];
+  __shared__ Far<kG> s_far[kWarpCta / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kWarpCta / 32) + warp) * p.window;
   if (r0 >= p.num_rows) return;
@@ -354,7 +459,10 @@ __global__ void __launch_bounds__(kWarpCta, 4) write_scaled_warp(const WriteScal
     const int l = __ffs(lead) - 1;
     lead &= lead - 1;
     const int first_slot = __shfl_sync(0xffffffffu, slot, l);
-    const int n = members(p, slots, static_cast<int>(r0) + l, first_slot, lane, s_rows[warp]);
+    const int r = static_cast<int>(r0) + l, end = min(p.num_rows, r + 32);
+    bool open;
+    int n = members(p, slots, r, end, first_slot, lane, s_rows[warp], open);
+    if (open) n = far_members<32, kG>(p, first_slot, end, n, lane, s_rows[warp], s_far[warp]);
     write_unit<32, kG>(p, s_rows[warp], n, first_slot, lane, nullptr);
     __syncwarp();
   }

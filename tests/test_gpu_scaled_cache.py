@@ -242,6 +242,48 @@ def test_write_sizes(G, T):
     check_write(new_rows(T, 3), slots, rows, G, 3)
 
 
+@pytest.mark.parametrize("G", [1, 2, 4, 8, 16, 32, 64])
+@pytest.mark.parametrize("T", [700, 9000, 40003])
+def test_write_of_rows_far_apart(G, T):
+    """Rows of one scale block with any number of rows without a slot before, between and behind them: a few
+    next to each other, some hundreds or thousands apart, the blocks entered at any offset."""
+    r = np.random.default_rng(G + T)
+    slots, row, block = np.full(T, -1, np.int32), int(r.integers(0, 300)), 0
+    while row < T - 200:
+        f = int(r.integers(0, G))
+        for i in range(int(r.integers(1, G - f + 1))):
+            if row >= T - 200:
+                break
+            slots[row] = block * G + f + i
+            row += 1 + int(r.choice([0, 0, 0, 0, 1, 7, 31, 32, 40, 200, 1500, 5000], p=[.2, .2, .2, .1, .08, .08] + 4 * [.03] + 2 * [.01]))
+        block += int(r.integers(1, 3))
+    assert (slots >= 0).any()
+    check_write(new_rows(T, G), slots, (block + 2) * G, G, G)
+
+
+@pytest.mark.parametrize("G", [2, 16, 64])
+def test_write_of_a_few_rows_in_a_large_capacity(G):
+    """A step's few rows in front of a capacity sized for prompts: the call does not look over the rest slot
+    by slot (131,072 slots are 512 KB; read 32 at a time, one after another, they take 1.2 ms or more)."""
+    T = 131072
+    slots = np.full(T, -1, np.int32)
+    slots[:9] = [5, 6, 70, 71, 72, 73, 130, 131, 132]
+    x = new_rows(1, 1).expand(T, 576).contiguous()
+    codes, scales = check_write(x, slots, 192, G, G)
+    x, s = x.cuda(), i32(slots)
+    best = 1e9
+    for _ in range(10):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(10):
+            mla.write_kv_scaled(x, s, codes, scales, G)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 100)
+    print(f"G = {G}: {best:.1f} us")
+    assert best < 300
+
+
 def test_write_of_a_foreign_scale_divides():
     """Scales that are no powers of two (another writer's) stay where they are larger."""
     slots = np.concatenate([np.arange(3, 9), np.arange(40, 48)]).astype(np.int32)
