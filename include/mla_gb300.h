@@ -419,7 +419,8 @@ mla_status mla_update_block_tables_lens(const mla_table_args *a, int32_t *lens_o
  * slot_map comes from mla_update_block_tables or is made alike: slots
  * distinct, and the rows of one scale block ascending by one with only -1 rows
  * between them.  Device check: MLA_DEV_BAD_BLOCK_ID (a slot >= num_cache_rows
- * or < -1: the row is not written). */
+ * or < -1: the row is not written; a row that is not the next one of its scale
+ * block: neither it nor the block's rows after it are written). */
 mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, const int32_t *slot_map,
                                void *kv_cache, float *kv_scales, int scale_block,
                                int64_t num_cache_rows, mla_stream_t stream);

@@ -209,10 +209,12 @@ __device__ __forceinline__ int slot_before(const WriteScaledParams &p, int end, 
 
 // Leaders among rows r0 .. r0 + 31 (a warp): the row of lane l opens a unit.
 // A row whose nearest earlier row with a slot lies in the same scale block
-// follows a leader; rows without a slot (another shard's) are passed over.
+// follows a leader; rows without a slot (another shard's) are passed over.  A
+// follower has the next cache row, or is recorded as out of order.
 __device__ __forceinline__ uint32_t leaders(const WriteScaledParams &p, const Slots &slots, int r0, int r_end, int lane,
                                             int &slot) {
   const int r = r0 + lane;
+  const int prior = r0 - 32 + lane >= 0 ? slots[r0 - 32 + lane] : -1;
   slot = r < r_end ? slots[r] : -1;
   if (slot >= p.num_cache_rows || slot < -1) {
     atomicCAS(p.err, 0, MLA_DEV_BAD_BLOCK_ID);
@@ -223,44 +225,42 @@ __device__ __forceinline__ uint32_t leaders(const WriteScaledParams &p, const Sl
   // the nearest earlier slot: in these 32 rows, or before them
   const uint32_t below = have & ((1u << lane) - 1u);
   int prev = __shfl_sync(0xffffffffu, slot, below ? 31 - __clz(below) : 0);
-  const int head_slot = __shfl_sync(0xffffffffu, slot, __ffs(have) - 1);
-  int before = -1;
-  if ((head_slot & ((1 << p.log_g) - 1)) != 0) {
-    const int s = r0 - 32 + lane >= 0 ? slots[r0 - 32 + lane] : -1;
-    const uint32_t got = __ballot_sync(0xffffffffu, has_slot(p, s));
-    before = got ? __shfl_sync(0xffffffffu, s, 31 - __clz(got)) : slot_before(p, r0 - 32, lane);
-  }
+  const uint32_t got = __ballot_sync(0xffffffffu, has_slot(p, prior));
+  const int before = got ? __shfl_sync(0xffffffffu, prior, 31 - __clz(got)) : slot_before(p, r0 - 32, lane);
   if (below == 0) prev = before;
-  const bool lead = slot >= 0 && (prev < 0 || (prev >> p.log_g) != (slot >> p.log_g));
-  return __ballot_sync(0xffffffffu, lead);
+  const bool follows = slot >= 0 && prev >= 0 && (prev >> p.log_g) == (slot >> p.log_g);
+  if (follows && slot != prev + 1) atomicCAS(p.err, 0, MLA_DEV_BAD_BLOCK_ID);
+  return __ballot_sync(0xffffffffu, slot >= 0 && !follows);
 }
 
-// 32 slots, row r's for lane 0 first (a warp): the rows of the unit among them go to rows[n ..), at most
-// `room` in all.  False when the unit ends here.
-__device__ __forceinline__ bool take_rows(const WriteScaledParams &p, int r, int s, int block, int room, int lane,
-                                          int *rows, int &n, bool &blank) {
+// 32 slots, row r's for lane 0 first (a warp): the rows of the unit among them go to rows[n ..).  False when
+// the unit ends here: with another block's row, the block's last row, or before a row that is not the next one
+// of its block (the unit's codes go to one run of cache rows).
+__device__ __forceinline__ bool take_rows(const WriteScaledParams &p, int r, int s, int first_slot, int lane, int *rows,
+                                          int &n, bool &blank) {
   const bool valid = has_slot(p, s);
-  const uint32_t other = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) != block);
+  const uint32_t other = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) != (first_slot >> p.log_g));
   const uint32_t upto = other ? (1u << (__ffs(other) - 1)) - 1u : 0xffffffffu;
-  const uint32_t mine = __ballot_sync(0xffffffffu, valid && (s >> p.log_g) == block) & upto;
+  const uint32_t mine = __ballot_sync(0xffffffffu, valid) & upto;
   const int at = n + __popc(mine & ((1u << lane) - 1u));
-  if ((mine >> lane & 1u) && at < room) rows[at] = r + lane;
-  n = min(n + __popc(mine), room);
+  const bool here = mine >> lane & 1u, next = s == first_slot + at;
+  const uint32_t odd = __ballot_sync(0xffffffffu, here && !next);
+  const uint32_t good = odd ? mine & ((1u << (__ffs(odd) - 1)) - 1u) : mine;
+  if (good >> lane & 1u) rows[at] = r + lane;
+  n += __popc(good);
   blank = mine == 0;
-  return other == 0 && n < room;
+  return (other | odd) == 0 && ((first_slot + n) & ((1 << p.log_g) - 1)) != 0;
 }
 
 // The rows of the unit that row r0 leads, among rows r0 .. end - 1 (a warp), into rows[]; returns how many,
 // and whether later rows may belong to it.
 __device__ __forceinline__ int members(const WriteScaledParams &p, const Slots &slots, int r0, int end, int first_slot,
                                        int lane, int *rows, bool &open) {
-  const int block = first_slot >> p.log_g;
-  const int room = (1 << p.log_g) - (first_slot & ((1 << p.log_g) - 1));
   int n = 0;
   bool blank;
   open = true;
   for (int b0 = r0; b0 < end && open; b0 += 32)
-    open = take_rows(p, b0, b0 + lane < end ? slots[b0 + lane] : -1, block, room, lane, rows, n, blank);
+    open = take_rows(p, b0, b0 + lane < end ? slots[b0 + lane] : -1, first_slot, lane, rows, n, blank);
   open = open && end < p.num_rows;
   __syncwarp();
   return n;
@@ -286,8 +286,6 @@ __device__ __forceinline__ int far_members(const WriteScaledParams &p, int first
                                         Far<kG> &far) {
   constexpr int kWarps = kTeam / 32, kLook = 16;
   const int lane = t & 31, warp = t >> 5, n0 = n;
-  const int block = first_slot >> p.log_g;
-  const int room = (1 << p.log_g) - (first_slot & ((1 << p.log_g) - 1));
   auto sync = [] {
     if (kTeam == 32) __syncwarp();
     else __syncthreads();
@@ -297,7 +295,7 @@ __device__ __forceinline__ int far_members(const WriteScaledParams &p, int first
       bool more = true, blank = false;
       int b0 = at;
       for (; b0 < p.num_rows && more && !blank; b0 += 32)
-        more = take_rows(p, b0, b0 + lane < p.num_rows ? p.slots[b0 + lane] : -1, block, room, lane, far.rows, n, blank);
+        more = take_rows(p, b0, b0 + lane < p.num_rows ? p.slots[b0 + lane] : -1, first_slot, lane, far.rows, n, blank);
       if (lane == 0) {
         far.at = b0;
         far.n = n;

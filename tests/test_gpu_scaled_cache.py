@@ -331,6 +331,25 @@ def test_write_bad_slots_are_skipped():
     assert (codes.cpu().numpy().any(1) == np.isin(np.arange(32), [3, 4])).all()
 
 
+@pytest.mark.parametrize("G,slots,good", [
+    (16, [3, 5, 6, 40], 1), (16, [3, 4, 4, 5, 40], 2), (16, [7, 6, 40], 1), (16, [3, -1, 4, -1, 6, 7, 40], 3),
+    (2, [4, 4, 40], 1), (4, [5, 7, 40], 1), (64, [3, 4, 5, 7, 8, 70], 3), (8, [1, 2, 3, 0, 40], 3),
+    (64, [9] + 300 * [-1] + [10, 12, 70], 302), (4, [4] + 50 * [-1] + [5, 7, 40], 52)])
+def test_write_of_rows_out_of_order_is_refused(G, slots, good):
+    """A row that is not the next one of its scale block: the block's rows before it are written, it and the
+    rest are not, and the next block is; nothing goes to a row that the map does not name."""
+    x = new_rows(len(slots), G)
+    codes = np.full((128, 576), 3, np.uint8)
+    scales = np.ones(128 // G, np.float32)
+    d = torch.tensor(codes).cuda(), torch.tensor(scales).cuda()
+    mla.write_kv_scaled(x.cuda(), i32(slots), *d, G)
+    assert mla.get_device_error() == 3
+    kept = np.array(slots)
+    kept[good:-1] = -1
+    want_c, want_s = ref.write_scaled(x.float().numpy().astype(np.float64), kept, codes, scales, G)
+    assert np.array_equal(d[0].cpu().numpy(), want_c) and np.array_equal(d[1].cpu().numpy().astype(np.float64), want_s)
+
+
 # ------------------------------------------------------------------ attention
 
 def attention_inputs(L, ql, H, bs, G, seed, mag=0.7, views=1):
