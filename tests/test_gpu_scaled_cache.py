@@ -796,6 +796,31 @@ def test_serving_steps(W, graph):
         assert np.abs(lse.cpu().numpy()[:n_rows] - l).max() <= LSE_TOL
 
 
+@pytest.mark.parametrize("S", [1, 4])
+def test_verify_step_with_a_finished_request(S):
+    """A request that was finished keeps its place in the batch without tokens or rows: the plan records it
+    (MLA_DEV_BAD_QLEN), and the others' rows are what they are without it.  On a stream that is not the
+    current one."""
+    cfg = dict(num_rows=24, block_size=16, num_blocks=40, max_kv_len=320)
+    s = torch.cuda.Stream()
+    x, q = new_rows(24, 5).cuda(), torch.randn((24, 8, 576), generator=torch.Generator().manual_seed(1)).cuda()
+    q = q.to(torch.bfloat16)
+    outs = []
+    for L, ql in ((([9, 12, 0, 3]), [9, 12, 0, 3]), ([9, 12, 3], [9, 12, 3])):
+        B = len(L)
+        c = runner.PagedLatentCache(num_reqs=B, scale_block=8, **cfg)
+        step = runner.VerifyStep(num_reqs=B, num_heads=8, max_qlen=12, block_table_width=20, num_segments=S,
+                                 scale_block=8, **cfg)
+        seq, ind = i32(L), i32(indptr(ql))
+        s.wait_stream(torch.cuda.current_stream())
+        c.append(x, seq, ind, stream=s)
+        out, lse = step(q, c.codes, seq, ind, c.block_table[None], SM, kv_scales=c.scales, stream=s)
+        s.synchronize()
+        assert mla.get_device_error() == (2 if 0 in L else 0)
+        outs.append((out.clone(), lse.clone()))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 @pytest.mark.parametrize("W,I,S", [(3, 1, 4), (2, 4, 1), (8, 1, 16)])
 def test_verify_step_over_shard_views(W, I, S):
     """VerifyStep with every shard's view in one launch of the block-scaled decode, requests too short for
