@@ -433,8 +433,12 @@ mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, const int32_t *
  * other (below 2^-100 they count as 2^-100, above 2^120 as 2^120).
  * scale_block is a power of two, 1 <= scale_block <= min(64, page_size);
  * num_cache_rows a multiple of it.  No flags are taken
- * (MLA_ERR_UNSUPPORTED).  A probability is held to 2^-7 of itself, or to 2^-28
- * of the row's largest.  A NaN code reaches the rows that see its token and no
+ * (MLA_ERR_UNSUPPORTED).  A probability times its token's scale is held to
+ * 2^-7 of itself, or to 2^-28 of the row's largest such product: a token of a
+ * small scale beside one of a far larger scale adds what it should up to
+ * 2^-28 max_j(p_j scale_j) |code|.  Every SM reads a request's row lengths by
+ * one thread, about 30 ns a row: made for drafts, not for thousands of rows in
+ * one request.  A NaN code reaches the rows that see its token and no
  * other row; a query that is not finite, or one whose scores pass float32's
  * range, spoils its own row only.  Workspace size, outputs, errors and device
  * checks are those of mla_decode_verify; what the workspace holds afterwards is

@@ -58,7 +58,7 @@
 // 96 and 64 at N = 128 (measured), a tile's 18 + 24 about 2500 if nothing
 // overlapped; the steady state is 2390 cycles a tile, 1.25 us, against 1.24 us for
 // the SM's share of the HBM rate (55 KB at 6.76 TB/s / 152).  16 requests of
-// 131,072 tokens take 248 us (4.9 TB/s) and run at the power limit.  Short calls
+// 131,072 tokens take 255 us (4.7 TB/s) and run at the power limit.  Short calls
 // are latency: about 10 us from the call's start to the first S (lengths and
 // split 1.8, finding the part 1.9, its queries 1.4 and their two terms 2.3), 3 us
 // from the last tile to the partial output, then the merge kernel; 32 requests of

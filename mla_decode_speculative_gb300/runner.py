@@ -27,6 +27,10 @@ from . import mla
 
 
 class VerifyStep:
+    """num_segments bounds the split of a (request, 64 query rows) over the SMs: 1 leaves each whole to
+    one SM, which only batches with at least as many of them as SMs want; 16 suits long requests in
+    small batches (eight of 32,768 tokens on an 8-bit cache: 441 us with 1, 64 us with 16)."""
+
     def __init__(self, *, num_reqs: int, num_rows: int, num_heads: int, max_qlen: int,
                  block_size: int, num_blocks: int, block_table_width: int, max_kv_len: int,
                  num_segments: int = 1, world_size: int = 1, kv_fp8: bool = False,
@@ -118,7 +122,10 @@ class PagedLatentCache:
     requests of up to ``max_kv_len`` tokens (on this shard) in ``num_blocks`` blocks.  Which
     blocks a request holds, which are free and how many tokens each request has are device
     state, so ``append`` can be captured in a CUDA graph and replayed with new lengths.
-    ``num_rows`` is the capacity of a step's new tokens."""
+    ``num_rows`` is the capacity of a step's new tokens.  ``block_table``, ``ring``, ``lens``
+    and ``free_ring`` are that state: to be read, not written.  A request that was finished (0
+    tokens, no rows) keeps its place; VerifyStep's plan records MLA_DEV_BAD_QLEN for it, the
+    other rows are not affected."""
 
     def __init__(self, *, num_reqs: int, num_rows: int, num_blocks: int, block_size: int, max_kv_len: int,
                  scale_block: int = 16, world_size: int = 1, rank: int = 0, interleave: int = 1, device="cuda"):
@@ -166,7 +173,8 @@ class PagedLatentCache:
 
     def undo(self, stream=None):
         """Blocks and lengths as before the last append: after one that the free blocks did not
-        suffice for (MLA_DEV_NO_FREE_BLOCK), before appending less.  The rows that it wrote stay
+        suffice for (MLA_DEV_NO_FREE_BLOCK; without it the blocks that were not there count as
+        held, and go back to the free ones as -1), before appending less.  The rows that it wrote stay
         written, so a request's next new tokens start no later than they did in it."""
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
