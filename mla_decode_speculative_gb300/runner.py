@@ -27,9 +27,9 @@ from . import mla
 
 
 class VerifyStep:
-    """num_segments bounds the split of a (request, 64 query rows) over the SMs: 1 leaves each whole to
-    one SM, which only batches with at least as many of them as SMs want; 16 suits long requests in
-    small batches (eight of 32,768 tokens on an 8-bit cache: 441 us with 1, 64 us with 16)."""
+    """num_segments bounds how many SMs share a (request, 64 query rows): 1 leaves each whole to one SM,
+    which is enough only where there are as many of them as SMs; 16 suits long requests in small
+    batches (eight of 32,768 tokens on an 8-bit cache: 441 us with 1, 64 us with 16)."""
 
     def __init__(self, *, num_reqs: int, num_rows: int, num_heads: int, max_qlen: int,
                  block_size: int, num_blocks: int, block_table_width: int, max_kv_len: int,
@@ -173,9 +173,10 @@ class PagedLatentCache:
 
     def undo(self, stream=None):
         """Blocks and lengths as before the last append: after one that the free blocks did not
-        suffice for (MLA_DEV_NO_FREE_BLOCK; without it the blocks that were not there count as
-        held, and go back to the free ones as -1), before appending less.  The rows that it wrote stay
-        written, so a request's next new tokens start no later than they did in it."""
+        suffice for (MLA_DEV_NO_FREE_BLOCK), before appending less.  An append that is left so
+        counts the blocks that were not there as held, and they go back to the free ones as -1.
+        The rows that an undone append wrote stay written, so a request's next new tokens start
+        no later than they did in it."""
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
             self._now.copy_(self._before)
