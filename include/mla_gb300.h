@@ -78,7 +78,8 @@ typedef enum mla_device_error {
   MLA_DEV_BAD_SUBPAGE = 5,   /* the decode met a sub-page id outside the cache */
   MLA_DEV_WAIT_TIMEOUT = 6,  /* an in-kernel wait gave up; the CTA returned without its result */
   MLA_DEV_NO_FREE_BLOCK = 7, /* the free ring held fewer blocks than the requests needed */
-  MLA_DEV_BAD_FREE_RING = 8  /* ring state outside [0, num_blocks], or more blocks returned than the pool has */
+  MLA_DEV_BAD_FREE_RING = 8, /* ring state outside [0, num_blocks], or more blocks returned than the pool has */
+  MLA_DEV_BAD_AXIS = 9       /* a rotary pair's axis outside [0, num_axes) */
 } mla_device_error;
 
 /* Sub-page size P for a physical block size: the largest power of two dividing
@@ -446,6 +447,132 @@ mla_status mla_write_kv_scaled(int num_rows, const void *kv_new, const int32_t *
 mla_status mla_decode_verify_scaled(const mla_decode_args *a, const float *kv_scales,
                                     int scale_block, void *workspace, size_t workspace_bytes,
                                     mla_stream_t stream);
+
+/* Rotary positions.  One tensor of mla_rotary_args: row r, head h, value d of
+ * the source at src[r * src_row + h * src_head + d] (strides in elements, the
+ * values of a head contiguous), likewise the destination. */
+typedef struct mla_heads {
+  int heads;             /* >= 1 (0: this tensor is absent) */
+  int dim;               /* values per head; the first rot_dim are rotated, the others copied */
+  const void *src;       /* bf16 */
+  int64_t src_row, src_head;
+  void *dst;             /* bf16; may be src with the same strides (in place), must not overlap it otherwise */
+  int64_t dst_row, dst_head;
+} mla_heads;
+
+typedef struct mla_rotary_args {
+  int num_rows;              /* T */
+  int num_axes;              /* A: 1 for text; 3 for (time, height, width) */
+  int rot_dim;               /* R: even, 2 <= R <= 512 */
+  int neighbours;            /* pair i is values (i, i + R/2) if 0, values (2i, 2i + 1) if not */
+  const int32_t *positions;  /* [A, T] */
+  int64_t axis_stride;       /* elements from one axis's positions to the next's */
+  const int64_t *turns;      /* [R/2] turns per position of pair i, in units of 2^-64, modulo 1 (bit patterns) */
+  const int32_t *axes;       /* [R/2] the axis whose position turns pair i; NULL: axis 0 */
+  mla_heads q, k, v;         /* v: mla_rotary_write only, and never rotated (R does not bound its dim) */
+  const int32_t *slot_map;   /* mla_rotary_write: [T] cache row of row r's keys and values, -1: none here */
+  int64_t num_cache_rows;    /* mla_rotary_write */
+} mla_rotary_args;
+
+/* Rotates queries and keys (either may be absent) by their rows' positions,
+ * the step before mla_write_kv and the decode [sglang #34432, 实现拆解 4:
+ * positions are applied to q_pe and k_pe before attention].  With x, y the
+ * two values of pair i of a head and a = 2 pi * positions[axes[i]][r] *
+ * turns[i] / 2^64,
+ *     x' = x cos a - y sin a,   y' = y cos a + x sin a,
+ * computed in float32 and rounded to bf16 once.  The product of position and
+ * turns is taken modulo 2^64, exactly, so the angle of a far position is as
+ * good as that of a near one: what turns[i] is off by (2^-65), times the
+ * position.  Positions may be any int32.  The pages rotate by one position per
+ * token; several axes are this library's.
+ * The latent form is two tensors of 64 values, which go to the ends of wider
+ * rows: dst = q + 512 with dst_head = 576.
+ * Device check: MLA_DEV_BAD_AXIS (the pair is turned by axis 0). */
+mla_status mla_rotary(const mla_rotary_args *a, mla_stream_t stream);
+
+/* mla_rotary, and the keys and values go to a paged K/V cache: row r of k
+ * (rotated) and of v (as it is) to cache row slot_map[r] of k.dst and v.dst
+ * [num_cache_rows, heads, dim], row r of q to row r of q.dst.  slot_map comes
+ * from mla_update_block_tables or is made alike: distinct rows, -1 for a token
+ * that is not this shard's.  The caches' strides are free (one pool of
+ * [num_cache_rows, 2, heads, dim], for instance).
+ * Device checks: MLA_DEV_BAD_AXIS, MLA_DEV_BAD_BLOCK_ID (a slot >=
+ * num_cache_rows or < -1: that row's keys and values are not written). */
+mla_status mla_rotary_write(const mla_rotary_args *a, mla_stream_t stream);
+
+/* Arguments of mla_decode_grouped and mla_decode_differential (host struct,
+ * read during the call). */
+typedef struct mla_grouped_args {
+  int num_reqs;          /* B >= 1 */
+  int num_rows;          /* T: row capacity of q / out / lse; qo_indptr[B] <= T */
+  int num_heads;         /* H query heads (differential: pairs of them) */
+  int num_kv_heads;      /* Hkv >= 1, divides H: heads h of group g = h / (H / Hkv) read its keys and values */
+  int max_qlen;          /* static bound on qlen_b */
+  int head_dim;          /* D: 64, 128 or 256 (differential: 64 or 128) */
+  int window;            /* row r sees its last `window` tokens only; 0: all of them */
+  float sm_scale;
+  const void *q;         /* [T, H, D] bf16, rows q_row elements apart (differential: [T, H, 2, D]) */
+  int64_t q_row;
+  const void *k_cache;   /* [num_cache_rows, Hkv, D] bf16, rows k_row elements apart ([.., Hkv, 2, D]) */
+  int64_t k_row;
+  const void *v_cache;   /* [num_cache_rows, Hkv, D] bf16, rows v_row elements apart ([.., Hkv, 2 D]) */
+  int64_t v_row;
+  int64_t num_cache_rows;
+  const int32_t *qo_indptr;      /* [B+1] */
+  const int32_t *row_len;        /* [T] tokens up to and with row r's own (mla_plan_rows) */
+  const int32_t *subpage_table;  /* [B, subpage_stride] sub-page ids (mla_plan_rows) */
+  int subpage_stride;
+  int page_size;         /* P = mla_page_size(block_size); 8 <= P <= 128 */
+  void *out;             /* [T, H, D] bf16 (differential: [T, H, 2 D]) */
+  float *lse;            /* [T, H] natural log, -inf for a row that sees nothing (differential: [T, H, 2]) */
+  int64_t wait_cycles;   /* as in mla_decode_args */
+} mla_grouped_args;
+
+/* Workspace bytes of mla_decode_grouped (differential: of
+ * mla_decode_differential) for `a`; reads num_heads, num_kv_heads, max_qlen
+ * and head_dim only.  0 for sizes that the calls refuse.  Host only.  Calls
+ * that may overlap on the GPU, two captured graphs among them, need a
+ * workspace each; its contents need not be kept from one call to the next. */
+size_t mla_decode_grouped_workspace(const mla_grouped_args *a, int differential);
+
+/* Grouped-query decode / causal verify over a paged K/V cache: the attention
+ * of the model that drafts, over the block tables, row plans and slot maps of
+ * the latent cache beside it (the pages group the draft's and the target's
+ * caches [sglang #34432, 实现拆解 5]).  For row r of request b and head h of
+ * group g, with n = row_len[r] and tokens j = max(0, n - window) .. n - 1
+ * (0 .. n - 1 without a window), token j in cache row
+ * subpage_table[b][j / P] * P + j % P:
+ *   s_j = sm_scale * <q[r,h,:], k[j,g,:]>,
+ *   out[r,h,:] = sum_j softmax(s)_j v[j,g,:],  lse[r,h] = ln sum_j e^{s_j}.
+ * A row that sees nothing gives out = 0 and lse = -inf.  Rows from
+ * qo_indptr[B] on are left as they were.  Scores, softmax sums and outputs are
+ * held in float32; probabilities are rounded to bf16 for the product with the
+ * values (2^-9 relative each, 2^-8 at most), and so is the result.
+ * q, k_cache and v_cache are 16-byte aligned with rows a multiple of 8
+ * elements apart; num_cache_rows is a multiple of 8.
+ * Keys and values that no row of a request sees are never used as numbers.  A
+ * key that is not finite reaches the rows that see its token only; so does a
+ * value, but where some rows of the request see its token and others do not,
+ * those that see it become NaN in all of their dims.
+ * Device checks: MLA_DEV_BAD_INDPTR (the request's rows are left as they were),
+ * MLA_DEV_LEN_BOUND (row_len > subpage_stride * P: clipped),
+ * MLA_DEV_BAD_SUBPAGE (the page is read as zeros), MLA_DEV_WAIT_TIMEOUT. */
+mla_status mla_decode_grouped(const mla_grouped_args *a, void *workspace, size_t workspace_bytes,
+                              mla_stream_t stream);
+
+/* Differential attention over the same cache: every head has two queries, and
+ * every group two keys, of D values each, and one value of 2 D.  With
+ * o_m = sum_j softmax(sm_scale <q[r,h,m], k[j,g,m]>)_j v[j,g,:], m = 0, 1,
+ *   y = o_0 - lambda[h] o_1,
+ *   out[r,h,:] = y                                              (gain == NULL)
+ *              = y / sqrt(mean_d y_d^2 + eps) * gain[d]          (otherwise)
+ * and lse[r,h,m] is the natural log of map m's sum.  lambda [H] is what the
+ * learned vectors come to, float32; a constant that the model multiplies the
+ * norm by belongs into gain [2 D] float32.  Other arguments, rows and checks
+ * as mla_decode_grouped. */
+mla_status mla_decode_differential(const mla_grouped_args *a, const float *lambda, const float *gain,
+                                   float eps, void *workspace, size_t workspace_bytes,
+                                   mla_stream_t stream);
 
 /* The same decode / verify as mla_decode_verify, for callers that cannot
  * allocate device memory where they make the call -- serving runtimes that

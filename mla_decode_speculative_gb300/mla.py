@@ -38,7 +38,8 @@ MLA_DECODE_FUSED_MERGE = 4
 
 DEVICE_ERRORS = {0: "MLA_DEV_OK", 1: "MLA_DEV_BAD_INDPTR", 2: "MLA_DEV_BAD_QLEN",
                  3: "MLA_DEV_BAD_BLOCK_ID", 4: "MLA_DEV_LEN_BOUND", 5: "MLA_DEV_BAD_SUBPAGE",
-                 6: "MLA_DEV_WAIT_TIMEOUT", 7: "MLA_DEV_NO_FREE_BLOCK", 8: "MLA_DEV_BAD_FREE_RING"}
+                 6: "MLA_DEV_WAIT_TIMEOUT", 7: "MLA_DEV_NO_FREE_BLOCK", 8: "MLA_DEV_BAD_FREE_RING",
+                 9: "MLA_DEV_BAD_AXIS"}
 
 
 class MLAError(RuntimeError):
@@ -80,13 +81,39 @@ class TableArgs(ctypes.Structure):
                 ("ring_out", ctypes.c_void_p), ("slot_map", ctypes.c_void_p)]
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int), ("dim", ctypes.c_int), ("src", ctypes.c_void_p),
+                ("src_row", ctypes.c_int64), ("src_head", ctypes.c_int64), ("dst", ctypes.c_void_p),
+                ("dst_row", ctypes.c_int64), ("dst_head", ctypes.c_int64)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int), ("num_axes", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("neighbours", ctypes.c_int), ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+                ("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("q", Heads), ("k", Heads), ("v", Heads),
+                ("slot_map", ctypes.c_void_p), ("num_cache_rows", ctypes.c_int64)]
+
+
+class GroupedArgs(ctypes.Structure):
+    _fields_ = [("num_reqs", ctypes.c_int), ("num_rows", ctypes.c_int), ("num_heads", ctypes.c_int),
+                ("num_kv_heads", ctypes.c_int), ("max_qlen", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("window", ctypes.c_int), ("sm_scale", ctypes.c_float), ("q", ctypes.c_void_p),
+                ("q_row", ctypes.c_int64), ("k_cache", ctypes.c_void_p), ("k_row", ctypes.c_int64),
+                ("v_cache", ctypes.c_void_p), ("v_row", ctypes.c_int64), ("num_cache_rows", ctypes.c_int64),
+                ("qo_indptr", ctypes.c_void_p), ("row_len", ctypes.c_void_p),
+                ("subpage_table", ctypes.c_void_p), ("subpage_stride", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("wait_cycles", ctypes.c_int64)]
+
+
 _lib = None
 _lock = threading.Lock()
 EXPORTS = ("mla_page_size", "mla_plan_rows", "mla_shard_row_view", "mla_shard_row_views",
            "mla_decode_verify_workspace",
            "mla_decode_verify", "mla_decode_verify_noalloc", "mla_write_kv", "mla_merge_segments",
            "mla_update_block_tables", "mla_update_block_tables_lens", "mla_write_kv_scaled", "mla_decode_verify_scaled",
-           "mla_get_device_error",
+           "mla_rotary", "mla_rotary_write", "mla_decode_grouped_workspace", "mla_decode_grouped",
+           "mla_decode_differential", "mla_get_device_error",
            "mla_last_error_string", "mla_status_string", "mla_abi_version")
 
 
@@ -134,6 +161,15 @@ def lib():
         L.mla_write_kv_scaled.restype = c_int
         L.mla_decode_verify_scaled.argtypes = [ctypes.POINTER(DecodeArgs), vp, c_int, vp, ctypes.c_size_t, vp]
         L.mla_decode_verify_scaled.restype = c_int
+        L.mla_rotary.argtypes = L.mla_rotary_write.argtypes = [ctypes.POINTER(RotaryArgs), vp]
+        L.mla_rotary.restype = L.mla_rotary_write.restype = c_int
+        L.mla_decode_grouped_workspace.argtypes = [ctypes.POINTER(GroupedArgs), c_int]
+        L.mla_decode_grouped_workspace.restype = ctypes.c_size_t
+        L.mla_decode_grouped.argtypes = [ctypes.POINTER(GroupedArgs), vp, ctypes.c_size_t, vp]
+        L.mla_decode_grouped.restype = c_int
+        L.mla_decode_differential.argtypes = [ctypes.POINTER(GroupedArgs), vp, vp, ctypes.c_float, vp,
+                                              ctypes.c_size_t, vp]
+        L.mla_decode_differential.restype = c_int
         L.mla_merge_segments.argtypes = [ctypes.POINTER(MergeArgs), vp]
         L.mla_merge_segments.restype = c_int
         L.mla_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
@@ -549,6 +585,178 @@ def decode_verify_scaled(q, kv_cache, kv_scales, scale_block, qo_indptr, row_len
                                     _dev_ptr(workspace, torch.uint8, dev, "workspace"), need, raw)
     if st:
         _check(st, "mla_decode_verify_scaled")
+    return out, lse, workspace
+
+
+def _view_ptr(t: torch.Tensor, dev: int, name: str) -> int:
+    """Address of a bf16 tensor on the current device whose last dimension is contiguous."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    return t.data_ptr()
+
+
+def rotary_turns(freq, device="cuda") -> torch.Tensor:
+    """The table mla_rotary takes for pairs of `freq` radians per position (float64 [R / 2]): the
+    turns per position in units of 2^-64, modulo 1, as int64 [R / 2] on `device`."""
+    f = torch.as_tensor(freq, dtype=torch.float64).cpu()
+    if f.dim() != 1 or not torch.isfinite(f).all():
+        raise ValueError("freq must be [R / 2] finite radians per position")
+    pi = 3141592653589793238462643383279502884197  # pi * 10^39: the quotient in whole numbers, rounded once
+    units = []
+    for x in f.tolist():
+        n, d = x.as_integer_ratio()
+        n, d = n * 2 ** 64 * 10 ** 39, 2 * d * pi
+        units.append(((2 * n + d) // (2 * d) + 2 ** 63) % 2 ** 64 - 2 ** 63)
+    return torch.tensor(units, dtype=torch.int64, device=device)
+
+
+def _heads(x, out, rows, dev, name) -> Heads:
+    """x [T, heads, dim] to out [.., heads, dim]."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != rows or out.dim() != 3 or out.shape[1:] != shape[1:]:
+        raise ValueError(f"{name} must be [{rows}, heads, dim] and its output hold as many heads and dims")
+    xs, os_ = x.stride(), out.stride()
+    return Heads(shape[1], shape[2], _view_ptr(x, dev, name), xs[0], xs[1], _view_ptr(out, dev, f"{name}'s output"),
+                 os_[0], os_[1])
+
+
+def _rotary_args(positions, turns, axes, neighbours, dev):
+    i64, i32 = torch.int64, torch.int32
+    A, T = positions.shape if positions.dim() == 2 else (1, positions.shape[0])
+    if positions.dtype is not i32 or positions.get_device() != dev or (T > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions must be [T] or [axes, T] int32 on cuda:{dev}, an axis's contiguous")
+    if axes is not None and axes.numel() != turns.numel():
+        raise ValueError("axes must name one axis per entry of turns")
+    return RotaryArgs(T, A, 2 * turns.numel(), int(neighbours), positions.data_ptr(),
+                      positions.stride(0) if positions.dim() == 2 else 0, _dev_ptr(turns, i64, dev, "turns"),
+                      None if axes is None else _dev_ptr(axes, i32, dev, "axes"))
+
+
+def rotary(q, k, positions, turns, axes=None, neighbours=False, q_out=None, k_out=None, stream=None):
+    """mla_rotary: rotary positions on q [T, H, dim] and k [T, Hk, dim] bf16 (either may be None),
+    whose first R = 2 * turns.numel() values of a head are rotated.  positions [T] or [axes, T]
+    int32; turns from rotary_turns; axes [R / 2] int32: which axis turns a pair (None: the first).
+    neighbours: pairs are (2i, 2i + 1) instead of (i, i + R / 2).  In place without q_out / k_out;
+    any strides, the values of a head contiguous.  Returns (q_out, k_out)."""
+    L, dev, raw = _current(stream)
+    a = _rotary_args(positions, turns, axes, neighbours, dev)
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        a.q = _heads(q, q_out, a.num_rows, dev, "q")
+        if q_out.shape[0] != a.num_rows:
+            raise ValueError("q_out must have q's rows")
+    if k is not None:
+        k_out = k if k_out is None else k_out
+        a.k = _heads(k, k_out, a.num_rows, dev, "k")
+        if k_out.shape[0] != a.num_rows:
+            raise ValueError("k_out must have k's rows")
+    st = L.mla_rotary(ctypes.byref(a), raw)
+    if st:
+        _check(st, "mla_rotary")
+    return q_out, k_out
+
+
+def rotary_write(q, k, v, positions, turns, slot_map, k_cache, v_cache, axes=None, neighbours=False, q_out=None,
+                 stream=None):
+    """mla_rotary_write: rotary on q [T, H, dim] (may be None) and k [T, Hk, dim], and row r of k
+    (rotated) and of v [T, Hv, dim_v] written to row slot_map[r] (int32, -1: nowhere) of k_cache
+    [N, Hk, dim] and v_cache [N, Hv, dim_v].  The other arguments are rotary's.  Returns q_out."""
+    L, dev, raw = _current(stream)
+    a = _rotary_args(positions, turns, axes, neighbours, dev)
+    T = a.num_rows
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        a.q = _heads(q, q_out, T, dev, "q")
+        if q_out.shape[0] != T:
+            raise ValueError("q_out must have q's rows")
+    a.k, a.v = _heads(k, k_cache, T, dev, "k"), _heads(v, v_cache, T, dev, "v")
+    if slot_map.numel() < T or k_cache.shape[0] != v_cache.shape[0]:
+        raise ValueError("slot_map must hold T entries, and k_cache and v_cache as many rows as each other")
+    a.slot_map = _dev_ptr(slot_map, torch.int32, dev, "slot_map")
+    a.num_cache_rows = k_cache.shape[0]
+    st = L.mla_rotary_write(ctypes.byref(a), raw)
+    if st:
+        _check(st, "mla_rotary_write")
+    return q_out
+
+
+def decode_grouped_workspace_bytes(num_heads, num_kv_heads, max_qlen, head_dim, differential=False) -> int:
+    """mla_decode_grouped_workspace."""
+    a = GroupedArgs(num_heads=num_heads, num_kv_heads=num_kv_heads, max_qlen=max_qlen, head_dim=head_dim)
+    return int(lib().mla_decode_grouped_workspace(ctypes.byref(a), int(differential)))
+
+
+def _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale, window, out, lse,
+             workspace, wait_cycles, dev, maps):
+    """(arguments, out, lse, workspace, its size needed) of a grouped call of 1 or 2 maps."""
+    T, H, D = q.shape[0], q.shape[1], q.shape[-1]
+    N, Hkv = k_cache.shape[:2]
+    pair = (2,) if maps == 2 else ()
+    if q.shape != (T, H, *pair, D) or k_cache.shape != (N, Hkv, *pair, D) or v_cache.shape != (N, Hkv, maps * D):
+        raise ValueError("q must be [T, H, D], k_cache and v_cache [N, Hkv, D]" if maps == 1 else
+                         "q must be [T, H, 2, D], k_cache [N, Hkv, 2, D] and v_cache [N, Hkv, 2 D]")
+    B, width = qo_indptr.numel() - 1, subpage_table.shape[-1]
+    if row_len.numel() != T or subpage_table.numel() != B * width:
+        raise ValueError("row_len must be [T] and subpage_table [B, width]")
+    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        step = D if name != "v_cache" else maps * D
+        if t.stride(1) != maps * D and t.shape[1] > 1 or maps == 2 and t.dim() == 4 and t.stride(2) != step:
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if out is None:
+        out = torch.empty((T, H, maps * D), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, H, *pair), dtype=torch.float32, device=q.device)
+    if out.numel() != T * H * maps * D or lse.numel() != T * H * maps:
+        raise ValueError("out must hold a value vector and lse a number per row and head (and map)")
+    i32 = torch.int32
+    a = GroupedArgs(B, T, H, Hkv, max_qlen, D, window, sm_scale, _view_ptr(q, dev, "q"), q.stride(0),
+                    _view_ptr(k_cache, dev, "k_cache"), k_cache.stride(0), _view_ptr(v_cache, dev, "v_cache"),
+                    v_cache.stride(0), N, _dev_ptr(qo_indptr, i32, dev, "qo_indptr"),
+                    _dev_ptr(row_len, i32, dev, "row_len"), _dev_ptr(subpage_table, i32, dev, "subpage_table"), width,
+                    page_size_, _dev_ptr(out, torch.bfloat16, dev, "out"), _dev_ptr(lse, torch.float32, dev, "lse"),
+                    wait_cycles)
+    need = lib().mla_decode_grouped_workspace(ctypes.byref(a), maps - 1)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    return a, out, lse, workspace, need
+
+
+def decode_grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale, window=0,
+                   out=None, lse=None, workspace=None, stream=None, wait_cycles=0):
+    """mla_decode_grouped: q [T, H, D] bf16 over k_cache, v_cache [N, Hkv, D] bf16 (D 64, 128 or
+    256), each of any row stride; qo_indptr, row_len, subpage_table, page_size_ as decode_verify's.
+    window: a row sees its last `window` tokens only (0: all).  Returns (out [T, H, D] bf16,
+    lse [T, H] f32, workspace)."""
+    L, dev, raw = _current(stream)
+    a, out, lse, workspace, need = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen,
+                                            sm_scale, window, out, lse, workspace, wait_cycles, dev, 1)
+    st = L.mla_decode_grouped(ctypes.byref(a), _dev_ptr(workspace, torch.uint8, dev, "workspace"), need, raw)
+    if st:
+        _check(st, "mla_decode_grouped")
+    return out, lse, workspace
+
+
+def decode_differential(q, k_cache, v_cache, lam, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale,
+                        gain=None, eps=1e-5, window=0, out=None, lse=None, workspace=None, stream=None, wait_cycles=0):
+    """mla_decode_differential: q [T, H, 2, D] over k_cache [N, Hkv, 2, D] and v_cache [N, Hkv, 2 D]
+    bf16 (D 64 or 128): map 0 minus lam[h] (float32 [H]) times map 1, then, with gain (float32
+    [2 D]), the norm over the head's 2 D values.  Returns (out [T, H, 2 D] bf16, lse [T, H, 2]
+    f32, workspace)."""
+    L, dev, raw = _current(stream)
+    a, out, lse, workspace, need = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen,
+                                            sm_scale, window, out, lse, workspace, wait_cycles, dev, 2)
+    f32 = torch.float32
+    if lam.numel() != a.num_heads or (gain is not None and gain.numel() != 2 * a.head_dim):
+        raise ValueError("lam must be [H] and gain [2 D]")
+    st = L.mla_decode_differential(ctypes.byref(a), _dev_ptr(lam, f32, dev, "lam"),
+                                   None if gain is None else _dev_ptr(gain, f32, dev, "gain"), eps,
+                                   _dev_ptr(workspace, torch.uint8, dev, "workspace"), need, raw)
+    if st:
+        _check(st, "mla_decode_differential")
     return out, lse, workspace
 
 

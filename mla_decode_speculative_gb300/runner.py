@@ -117,7 +117,54 @@ class VerifyStep:
                               num_views=self.W, uniform_segments=self.uniform, fused_merge=self.fused)
 
 
-class PagedLatentCache:
+class _PagedBlocks:
+    """Which blocks of a pool each request holds, which are free and how many tokens each request
+    has, as device state (``block_table``, ``free_ring``, ``ring``, ``lens``), with the slot map of
+    the last step."""
+
+    def __init__(self, num_reqs, num_rows, num_blocks, block_size, max_kv_len, world_size, rank, interleave, dev):
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.num_rows, self.block_size, self.num_blocks = num_rows, block_size, num_blocks
+        self.shard = dict(world_size=world_size, rank=rank, interleave=interleave)
+        self.block_table = torch.full((num_reqs, max(1, -(-max_kv_len // block_size))), -1, **i32)
+        self.free_ring = torch.arange(num_blocks, **i32)
+        # {head, count} of the free blocks and the tokens whose blocks each request holds; before the last append
+        self._now = torch.zeros(2 + num_reqs, **i32)
+        self._now[1] = num_blocks
+        self._before = self._now.clone()
+        self.ring, self.lens = self._now[:2], self._now[2:]
+        self.slot_map = torch.empty(num_rows, **i32)
+
+    def _append(self, seq_lens, qo_indptr, stream, write):
+        """Tables and slot map for the step, then write(stream); as before if either call is refused."""
+        s = torch.cuda.current_stream() if stream is None else stream
+        if seq_lens.shape != self.lens.shape:
+            raise ValueError("seq_lens must have num_reqs entries")
+        with torch.cuda.stream(s):
+            self._before.copy_(self._now)
+        if seq_lens.data_ptr() == self.lens.data_ptr():   # lengths as they are: the table call writes them
+            seq_lens = self._before[2:]
+        try:
+            mla.update_block_tables(self._before[2:], seq_lens, qo_indptr, self.block_table, self.free_ring,
+                                    self._before[:2], self.block_size, self.num_rows, ring_out=self.ring,
+                                    slot_map=self.slot_map, stream=s, lens_out=self.lens, **self.shard)
+            write(s)
+        except Exception:
+            self.undo(s)
+            raise
+
+    def undo(self, stream=None):
+        """Blocks and lengths as before the last append: after one that the free blocks did not
+        suffice for (MLA_DEV_NO_FREE_BLOCK), before appending less.  An append that is left so
+        counts the blocks that were not there as held, and they go back to the free ones as -1.
+        The rows that an undone append wrote stay written, so a request's next new tokens start
+        no later than they did in it."""
+        s = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(s):
+            self._now.copy_(self._before)
+
+
+class PagedLatentCache(_PagedBlocks):
     """An e4m3 latent cache with one scale per ``scale_block`` rows, for up to ``num_reqs``
     requests of up to ``max_kv_len`` tokens (on this shard) in ``num_blocks`` blocks.  Which
     blocks a request holds, which are free and how many tokens each request has are device
@@ -132,20 +179,10 @@ class PagedLatentCache:
         if scale_block not in (1, 2, 4, 8, 16, 32, 64) or block_size % scale_block:
             raise ValueError("scale_block must be a power of two up to 64 that divides block_size")
         dev = torch.device(device)
-        i32 = dict(dtype=torch.int32, device=dev)
-        self.num_rows, self.block_size, self.scale_block = num_rows, block_size, scale_block
-        self.num_blocks = num_blocks
-        self.shard = dict(world_size=world_size, rank=rank, interleave=interleave)
+        super().__init__(num_reqs, num_rows, num_blocks, block_size, max_kv_len, world_size, rank, interleave, dev)
+        self.scale_block = scale_block
         self.codes = torch.zeros((num_blocks * block_size, mla.D_QK), dtype=torch.uint8, device=dev)
         self.scales = torch.ones(num_blocks * block_size // scale_block, dtype=torch.float32, device=dev)
-        self.block_table = torch.full((num_reqs, max(1, -(-max_kv_len // block_size))), -1, **i32)
-        self.free_ring = torch.arange(num_blocks, **i32)
-        # {head, count} of the free blocks and the tokens whose blocks each request holds; before the last append
-        self._now = torch.zeros(2 + num_reqs, **i32)
-        self._now[1] = num_blocks
-        self._before = self._now.clone()
-        self.ring, self.lens = self._now[:2], self._now[2:]
-        self.slot_map = torch.empty(num_rows, **i32)
 
     def append(self, kv_new: torch.Tensor, seq_lens: torch.Tensor, qo_indptr: torch.Tensor, stream=None):
         """The step's new tokens: request b grows (or, drafts taken back, shrinks) to seq_lens[b]
@@ -154,32 +191,86 @@ class PagedLatentCache:
         (MLA_DEV_BAD_INDPTR, MLA_DEV_BAD_FREE_RING) changes nothing.  Returns the slot map."""
         if kv_new.shape[0] != self.num_rows:
             raise ValueError("kv_new must have num_rows rows")
-        s = torch.cuda.current_stream() if stream is None else stream
-        if seq_lens.shape != self.lens.shape:
-            raise ValueError("seq_lens must have num_reqs entries")
-        with torch.cuda.stream(s):
-            self._before.copy_(self._now)
-        if seq_lens.data_ptr() == self.lens.data_ptr():   # lengths as they are: the table call writes them
-            seq_lens = self._before[2:]
-        try:
-            mla.update_block_tables(self._before[2:], seq_lens, qo_indptr, self.block_table, self.free_ring,
-                                    self._before[:2], self.block_size, self.num_rows, ring_out=self.ring,
-                                    slot_map=self.slot_map, stream=s, lens_out=self.lens, **self.shard)
-            mla.write_kv_scaled(kv_new, self.slot_map, self.codes, self.scales, self.scale_block, stream=s)
-        except Exception:
-            self.undo(s)
-            raise
+        self._append(seq_lens, qo_indptr, stream,
+                     lambda s: mla.write_kv_scaled(kv_new, self.slot_map, self.codes, self.scales, self.scale_block,
+                                                   stream=s))
         return self.slot_map
 
-    def undo(self, stream=None):
-        """Blocks and lengths as before the last append: after one that the free blocks did not
-        suffice for (MLA_DEV_NO_FREE_BLOCK), before appending less.  An append that is left so
-        counts the blocks that were not there as held, and they go back to the free ones as -1.
-        The rows that an undone append wrote stay written, so a request's next new tokens start
-        no later than they did in it."""
-        s = torch.cuda.current_stream() if stream is None else stream
-        with torch.cuda.stream(s):
-            self._now.copy_(self._before)
+
+class PagedKVCache(_PagedBlocks):
+    """Keys and values of ``num_kv_heads`` groups, bf16, in the paged form of PagedLatentCache
+    (blocks, lengths and capture alike): ``k`` [N, num_kv_heads, head_dim] and ``v``, or with
+    ``differential`` two keys of head_dim and one value of 2 head_dim per group."""
+
+    def __init__(self, *, num_reqs: int, num_rows: int, num_blocks: int, block_size: int, max_kv_len: int,
+                 num_kv_heads: int, head_dim: int, differential: bool = False, world_size: int = 1, rank: int = 0,
+                 interleave: int = 1, device="cuda"):
+        dev = torch.device(device)
+        super().__init__(num_reqs, num_rows, num_blocks, block_size, max_kv_len, world_size, rank, interleave, dev)
+        rows, maps = num_blocks * block_size, 2 if differential else 1
+        self.differential = differential
+        self.k = torch.zeros((rows, num_kv_heads) + (2,) * differential + (head_dim,), dtype=torch.bfloat16, device=dev)
+        self.v = torch.zeros((rows, num_kv_heads, maps * head_dim), dtype=torch.bfloat16, device=dev)
+
+    def append(self, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+               turns: torch.Tensor, seq_lens: torch.Tensor, qo_indptr: torch.Tensor, axes=None,
+               neighbours: bool = False, q_out: Optional[torch.Tensor] = None, stream=None):
+        """The step's new tokens, as PagedLatentCache.append: rows of k_new and v_new [num_rows,
+        ...] of the cache's head shapes, the keys and the queries q [num_rows, H, ...] rotated by
+        positions, turns and axes (mla_rotary_write).  Returns the rotated queries, in q_out or in
+        place of q."""
+        if q.shape[0] != self.num_rows or k_new.shape[0] != self.num_rows or v_new.shape[0] != self.num_rows:
+            raise ValueError("q, k_new and v_new must have num_rows rows")
+        q_out = q if q_out is None else q_out
+        flat = (lambda x: x.flatten(1, 2)) if self.differential else (lambda x: x)   # a key of its own per map
+        if self.differential and flat(q_out).data_ptr() != q_out.data_ptr():
+            raise ValueError("the two queries of a head must lie together")
+        self._append(seq_lens, qo_indptr, stream,
+                     lambda s: mla.rotary_write(flat(q), flat(k_new), v_new, positions, turns, self.slot_map,
+                                                flat(self.k), self.v, axes, neighbours, q_out=flat(q_out), stream=s))
+        return q_out
+
+
+class GroupedStep:
+    """One attention of the model that drafts over a paged K/V cache: row plan and sub-page table
+    (mla_plan_rows), then mla_decode_grouped, or mla_decode_differential with ``differential``.
+    Buffers are allocated once, by static bounds; a call launches kernels only and can be captured
+    in a CUDA graph."""
+
+    def __init__(self, *, num_reqs: int, num_rows: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                 max_qlen: int, block_size: int, num_blocks: int, max_kv_len: int, window: int = 0,
+                 differential: bool = False, device="cuda"):
+        dev = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.max_qlen, self.block_size, self.num_blocks, self.window = max_qlen, block_size, num_blocks, window
+        self.differential = differential
+        self.P = mla.page_size(block_size)
+        self.sp_stride = max(1, -(-max_kv_len // self.P))
+        self.row_len, self.row_req = torch.empty(num_rows, **i32), torch.empty(num_rows, **i32)
+        self.subpage = torch.empty((num_reqs, self.sp_stride), **i32)
+        width, maps = (2 * head_dim, (2,)) if differential else (head_dim, ())
+        self.out = torch.empty((num_rows, num_heads, width), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((num_rows, num_heads) + maps, dtype=torch.float32, device=dev)
+        self.workspace = torch.empty(
+            max(1, mla.decode_grouped_workspace_bytes(num_heads, num_kv_heads, max_qlen, head_dim, differential)),
+            dtype=torch.uint8, device=dev)
+
+    def __call__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_lens: torch.Tensor,
+                 qo_indptr: torch.Tensor, block_table: torch.Tensor, sm_scale: float, lam=None, gain=None,
+                 eps: float = 1e-5, stream=None):
+        """lam, gain, eps: the differential form's weights.  Returns (out, lse)."""
+        if (lam is not None) != self.differential:
+            raise ValueError("lam goes with a step made with differential")
+        mla.plan_rows(seq_lens, qo_indptr, self.row_len.shape[0], block_table, self.num_blocks, self.block_size,
+                      self.sp_stride, row_len=self.row_len, row_req=self.row_req, subpage_table=self.subpage,
+                      stream=stream)
+        common = (qo_indptr, self.row_len, self.subpage, self.P, self.max_qlen, sm_scale)
+        buffers = dict(window=self.window, out=self.out, lse=self.lse, workspace=self.workspace, stream=stream)
+        if self.differential:
+            mla.decode_differential(q, k_cache, v_cache, lam, *common, gain=gain, eps=eps, **buffers)
+        else:
+            mla.decode_grouped(q, k_cache, v_cache, *common, **buffers)
+        return self.out, self.lse
 
 
 class StepIO:
