@@ -1,109 +1,145 @@
 // mla_grouped.cu -- grouped-query and differential decode / causal verify over
-// a paged K/V cache.
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
+// a paged K/V cache: argument checks, tensor maps, launches, and the merge of
+// the units that the split cuts.  The decode kernel is in mla_grouped.cuh.
+#include <atomic>
 
-#include <cstdint>
-
-#include "mla_internal.h"
+#include "mla_grouped.cuh"
 
 namespace mla {
+namespace grouped {
 namespace {
 
-struct Params {
-  mla_grouped_args a;
-  const float *lambda, *gain;
-  float eps;
-  int maps, group;
-  int *err;
-};
+// Merge of one cut unit: its parts are record 1 of the chunk with its first
+// tile and record 0 of the chunks after it.  A warp takes a row (both maps of
+// it): statistics with a lane per part, then the parts' outputs, 64 W values
+// over 32 lanes, weighted by 2^(m - M) / L.
+constexpr int kMergeRows = 4;
 
-// One block per (row, head); the 256 threads go over the tokens in turn.
-__global__ void __launch_bounds__(256) grouped_simple(const __grid_constant__ Params p) {
+template <int kW, int kMaps, int kNC>
+__global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_constant__ Params p) {
+  constexpr int kNR = kNC / kMaps, kDv = 64 * kW, kV = kDv / 32;
+  __shared__ float weight[kMergeRows][kMaps][kMaxCtas];
   grid_dep_wait();
   grid_dep_launch();
-  const mla_grouped_args &a = p.a;
-  const int r = blockIdx.x, h = blockIdx.y, g = h / p.group, D = a.head_dim, Dv = p.maps * D;
-  __shared__ float q[512], part[256], o[2][512], red[8];
-  int b = -1;
-  for (int i = 0; i < a.num_reqs; ++i)
-    if (a.qo_indptr[i] <= r && r < a.qo_indptr[i + 1]) b = i;
-  if (b < 0) return;
-  const int q0 = a.qo_indptr[b], q1 = a.qo_indptr[b + 1];
-  if (q0 < 0 || q1 > a.num_rows || q1 - q0 > a.max_qlen) {
-    if (threadIdx.x == 0) atomicCAS(p.err, 0, MLA_DEV_BAD_INDPTR);
-    return;
-  }
-  const int bound = a.subpage_stride * a.page_size;
-  int n = a.row_len[r];
-  if (n > bound) {
-    if (threadIdx.x == 0) atomicCAS(p.err, 0, MLA_DEV_LEN_BOUND);
-    n = bound;
-  }
-  const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
-  const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + r * a.q_row + h * Dv;
-  const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(a.k_cache), *V = static_cast<const __nv_bfloat16 *>(a.v_cache);
-  for (int d = threadIdx.x; d < Dv; d += 256) q[d] = __bfloat162float(Q[d]);
-  for (int m = 0; m < p.maps; ++m) {
-    float top = -INFINITY, total = 0.0f, acc[2] = {0.0f, 0.0f};
-    for (int j0 = lo; j0 < n; j0 += 256) {
-      __syncthreads();
-      const int j = j0 + threadIdx.x;
-      float s = -INFINITY;
-      int64_t row = -1;
-      if (j < n) {
-        const int id = a.subpage_table[static_cast<int64_t>(b) * a.subpage_stride + j / a.page_size];
-        if (id < 0 || (id + 1LL) * a.page_size > a.num_cache_rows) atomicCAS(p.err, 0, MLA_DEV_BAD_SUBPAGE);
-        else row = static_cast<int64_t>(id) * a.page_size + j % a.page_size;
-        s = 0.0f;
-        if (row >= 0)
-          for (int d = 0; d < D; ++d) s += q[m * D + d] * __bfloat162float(K[row * a.k_row + g * Dv + m * D + d]);
-        s *= a.sm_scale;
-      }
-      float t = s;
-      for (int x = 16; x > 0; x >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, x));
-      if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = t;
-      __syncthreads();
-      float best = top;
-      for (int x = 0; x < 8; ++x) best = fmaxf(best, red[x]);
-      const float shrink = top == -INFINITY ? 0.0f : expf(top - best);
-      part[threadIdx.x] = j < n ? (best == -INFINITY ? s - s : expf(s - best)) : 0.0f;
-      __syncthreads();
-      total *= shrink;
-      acc[0] *= shrink;
-      acc[1] *= shrink;
-      const int take = min(256, n - j0);
-      for (int i = 0; i < take; ++i) {
-        const int id = a.subpage_table[static_cast<int64_t>(b) * a.subpage_stride + (j0 + i) / a.page_size];
-        const bool bad = id < 0 || (id + 1LL) * a.page_size > a.num_cache_rows;
-        const int64_t vr = static_cast<int64_t>(id) * a.page_size + (j0 + i) % a.page_size;
-        total += part[i];
-        for (int k = 0; k < 2; ++k) {
-          const int d = threadIdx.x + 256 * k;
-          if (d < Dv && !bad) acc[k] += part[i] * __bfloat162float(V[vr * a.v_row + g * Dv + d]);
-        }
-      }
-      top = best;
+  const Meta u = p.meta[blockIdx.x];
+  if (u.last < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = static_cast<int>(blockIdx.x), parts = u.last - first + 1;
+  const int c = static_cast<int>(blockIdx.y) * kMergeRows + warp;
+  const int q0 = p.qo_indptr[u.b], qlen = p.qo_indptr[u.b + 1] - q0;
+  int t, h;
+  if (c >= kNR || !column_row(p, u.rb, c, qlen, t, h)) return;
+  const int64_t row = (static_cast<int64_t>(q0) + t) * p.num_heads + u.g * p.group + h;
+  auto record = [&](int i) { return (static_cast<int64_t>(first) + i) * 2 + (i == 0 ? 1 : 0); };
+  float total[kMaps];
+#pragma unroll
+  for (int m = 0; m < kMaps; ++m) {
+    const int col = m * kNR + c;
+    float top = kLowest;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_stat[record(i) * 2 * kNC + col]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.0f;
+    for (int i = lane; i < parts; i += 32) {
+      const float *stat = p.part_stat + record(i) * 2 * kNC + col;
+      const float l = stat[kNC], w = l == 0.0f ? 0.0f : exp2f(stat[0] - top);
+      weight[warp][m][i] = w;
+      sum += w * l;
     }
-    for (int k = 0; k < 2; ++k) {
-      const int d = threadIdx.x + 256 * k;
-      if (d < Dv) o[m][d] = lo < n ? acc[k] / total : 0.0f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    total[m] = sum;
+    if (lane == 0) p.lse[row * kMaps + m] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+  __syncwarp();
+  float y[kV];
+#pragma unroll
+  for (int m = 0; m < kMaps; ++m) {
+    float acc[kV];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) acc[k] = 0.0f;
+    const float *src = p.part_o + (m * kNR + c) * kDv + lane * kV;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float w = weight[warp][m][i];
+      const float *o = src + record(i) * kNC * kDv;
+      float v[kV];
+      if constexpr (kV == 2) {
+        *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kV; k += 4) *reinterpret_cast<float4 *>(v + k) = *reinterpret_cast<const float4 *>(o + k);
+      }
+#pragma unroll
+      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * v[k];
     }
-    if (threadIdx.x == 0) a.lse[(static_cast<int64_t>(r) * a.num_heads + h) * p.maps + m] = lo < n ? top + logf(total) : -INFINITY;
+    const float inv = total[m] == 0.0f ? 0.0f : 1.0f / total[m];
+    const float by = m == 0 ? inv : -inv * p.lambda[u.g * p.group + h];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) y[k] = m == 0 ? acc[k] * by : y[k] + acc[k] * by;
   }
-  __syncthreads();
-  const float lam = p.maps == 2 ? p.lambda[h] : 0.0f;
-  float square = 0.0f;
-  for (int d = 0; d < Dv; ++d) {
-    const float y = p.maps == 2 ? o[0][d] - lam * o[1][d] : o[0][d];
-    square += y * y;
+  if (kMaps == 2 && p.gain != nullptr) {
+    float sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) sq += y[k] * y[k];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    const float norm = total[0] == 0.0f ? 0.0f : rsqrtf(sq * (1.0f / kDv) + p.eps);
+#pragma unroll
+    for (int k = 0; k < kV; ++k) y[k] = total[0] == 0.0f ? 0.0f : y[k] * norm * p.gain[lane * kV + k];
   }
-  const float norm = p.gain != nullptr ? rsqrtf(square / Dv + p.eps) : 1.0f;
-  for (int d = threadIdx.x; d < Dv; d += 256) {
-    const float y = p.maps == 2 ? o[0][d] - lam * o[1][d] : o[0][d];
-    static_cast<__nv_bfloat16 *>(a.out)[(static_cast<int64_t>(r) * a.num_heads + h) * Dv + d] =
-        __float2bfloat16_rn(p.gain != nullptr ? y * norm * p.gain[d] : y);
+  uint32_t packed[kV / 2];
+#pragma unroll
+  for (int k = 0; k < kV; k += 2) packed[k / 2] = pack_bf16(y[k], y[k + 1]);
+  __nv_bfloat16 *dst = p.out + row * kDv + lane * kV;
+  if constexpr (kV == 2) *reinterpret_cast<uint32_t *>(dst) = packed[0];
+  else if constexpr (kV == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(packed[0], packed[1]);
+  else *reinterpret_cast<uint4 *>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+}
+
+// Columns of the products: the fewest of 16, 32, 64 that hold a request's rows
+// of a group (differential: 16 or 32 of each map).
+int columns_of(const mla_grouped_args &a, bool differential) {
+  const int64_t rows = static_cast<int64_t>(a.max_qlen) * (a.num_heads / a.num_kv_heads);
+  if (differential) return rows <= 16 ? 32 : 64;
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+}
+
+struct Layout {
+  size_t part_o, part_stat, meta, total;
+};
+Layout layout_of(const mla_grouped_args &a, bool differential) {
+  const size_t nc = columns_of(a, differential), dv = static_cast<size_t>(a.head_dim) * (differential ? 2 : 1);
+  Layout l{};
+  size_t off = 0;
+  l.part_o = off;
+  off += align256(kMaxCtas * 2 * nc * dv * sizeof(float));
+  l.part_stat = off;
+  off += align256(kMaxCtas * 2 * 2 * nc * sizeof(float));
+  l.meta = off;
+  off += align256(kMaxCtas * sizeof(Meta));
+  l.total = off;
+  return l;
+}
+
+template <int kW, int kMaps, int kNC>
+mla_status launch_as(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const Params &p, int grid, bool merge,
+                     cudaStream_t stream) {
+  using C = Config<kW, kMaps, kNC>;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (!((ready.load(std::memory_order_relaxed) >> (dev & 63)) & 1u)) {
+    e = cudaFuncSetAttribute(grouped_kernel<kW, kMaps, kNC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "grouped kernel shared memory");
+    ready.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
   }
+  e = launch_pdl(grouped_kernel<kW, kMaps, kNC>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, q, k, v, p);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped launch");
+  if (!merge) return MLA_OK;
+  e = launch_pdl(grouped_merge<kW, kMaps, kNC>, dim3(grid, C::kNR / kMergeRows), dim3(32 * kMergeRows), 0, stream, p);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "grouped merge launch");
 }
 
 bool sizes_ok(const mla_grouped_args &a, bool differential) {
@@ -193,29 +229,111 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
   }
   int *err = device_error_word();
   if (err == nullptr) return MLA_ERR_CUDA;
-  Params p{*a, lambda, gain, eps, differential ? 2 : 1, a->num_heads / a->num_kv_heads, err};
-  const cudaError_t e = launch_pdl(grouped_simple, dim3(a->num_rows, a->num_heads), dim3(256), 0,
-                                   reinterpret_cast<cudaStream_t>(stream), p);
-  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "grouped launch");
+  const Layout lay = layout_of(*a, differential);
+  char *ws = static_cast<char *>(workspace);
+  const int maps = differential ? 2 : 1, W = a->head_dim * maps / 64, nc = columns_of(*a, differential), nr = nc / maps;
+  const int G = a->num_heads / a->num_kv_heads, P = a->page_size;
+  Params p{};
+  p.row_len = a->row_len;
+  p.out = static_cast<__nv_bfloat16 *>(a->out);
+  p.lse = a->lse;
+  p.lambda = lambda;
+  p.gain = gain;
+  p.eps = eps;
+  p.part_o = reinterpret_cast<float *>(ws + lay.part_o);
+  p.part_stat = reinterpret_cast<float *>(ws + lay.part_stat);
+  p.meta = reinterpret_cast<Meta *>(ws + lay.meta);
+  p.err = err;
+  p.wait_budget = a->wait_cycles > 0 ? a->wait_cycles : 4000000000LL;
+  p.drain_budget = 4000000000LL;
+  p.scale_log2 = a->sm_scale * 1.44269504088896340736f;
+  p.num_rows = a->num_rows;
+  p.num_heads = a->num_heads;
+  p.num_kv_heads = a->num_kv_heads;
+  p.group = G;
+  p.max_qlen = a->max_qlen;
+  p.max_len = a->subpage_stride * P;
+  p.window = a->window;
+  p.subpage_stride = a->subpage_stride;
+  p.page_size = P;
+  p.page_groups = static_cast<int>(a->num_cache_rows / 8);
+  p.head_blocks = (G + nr - 1) / nr;
+  p.heads_per_block = p.head_blocks == 1 ? G : nr;
+  p.rows_per_block = p.head_blocks == 1 ? (nr / G < a->max_qlen ? nr / G : a->max_qlen) : 1;
+
+  // Requests of one launch: as many as the kernel tabulates and as int32
+  // positions hold at the static bound.
+  const int64_t tiles = (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile + 1;
+  const int64_t blocks = p.head_blocks == 1 ? (a->max_qlen + p.rows_per_block - 1) / p.rows_per_block
+                                            : static_cast<int64_t>(a->max_qlen) * p.head_blocks;
+  const int64_t units = blocks * a->num_kv_heads, most = units * (tiles + kOverhead);
+  if (units > INT32_MAX || most > INT32_MAX) {
+    set_error("%s: one request of %d tokens and %d rows is too large", what, p.max_len, a->max_qlen);
+    return MLA_ERR_UNSUPPORTED;
+  }
+  const int64_t by_range = INT32_MAX / most;
+  const int reqs = static_cast<int>(by_range < kMaxReqs ? by_range : kMaxReqs);
+
+  CUtensorMap tq, tk, tv;
+  const uint64_t w64 = static_cast<uint64_t>(W), hkv = static_cast<uint64_t>(a->num_kv_heads), g64 = static_cast<uint64_t>(G);
+  {
+    const cuuint64_t dims[5] = {64, g64, static_cast<uint64_t>(a->num_rows), w64, hkv};
+    const cuuint64_t strides[4] = {w64 * 128, static_cast<uint64_t>(a->q_row) * 2, 128, g64 * w64 * 128};
+    const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.heads_per_block), static_cast<cuuint32_t>(p.rows_per_block), 1, 1};
+    const mla_status s = make_tmap_5d(&tq, a->q, dims, strides, box);
+    if (s != MLA_OK) return s;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t row = static_cast<uint64_t>(i == 0 ? a->k_row : a->v_row) * 2;
+    const cuuint64_t dims[5] = {64, 8, w64, static_cast<uint64_t>(p.page_groups), hkv};
+    const cuuint64_t strides[4] = {row, 128, row * 8, w64 * 128};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(W < 2 ? W : 2), static_cast<cuuint32_t>(P / 8), 1};
+    const mla_status s = make_tmap_5d(i == 0 ? &tk : &tv, i == 0 ? a->k_cache : a->v_cache, dims, strides, box);
+    if (s != MLA_OK) return s;
+  }
+  for (int b0 = 0; b0 < a->num_reqs; b0 += reqs) {
+    p.num_reqs = a->num_reqs - b0 < reqs ? a->num_reqs - b0 : reqs;
+    p.qo_indptr = a->qo_indptr + b0;
+    p.subpage_table = a->subpage_table + static_cast<int64_t>(b0) * a->subpage_stride;
+    // CTAs that can get a chunk at the static bound; with one unit to each no unit is cut
+    const int64_t want = most * p.num_reqs / kMinChunk;
+    const int grid = static_cast<int>(want < 1 ? 1 : (want < kMaxCtas ? want : kMaxCtas));
+    const bool merge = grid > 1 && tiles + kOverhead > 1;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    mla_status s = MLA_ERR_UNSUPPORTED;
+    if (!differential) {
+      if (W == 1) s = nc == 16 ? launch_as<1, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<1, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<1, 1, 64>(tq, tk, tv, p, grid, merge, cs);
+      else if (W == 2) s = nc == 16 ? launch_as<2, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<2, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<2, 1, 64>(tq, tk, tv, p, grid, merge, cs);
+      else s = nc == 16 ? launch_as<4, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<4, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<4, 1, 64>(tq, tk, tv, p, grid, merge, cs);
+    } else {
+      if (W == 2) s = nc == 32 ? launch_as<2, 2, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<2, 2, 64>(tq, tk, tv, p, grid, merge, cs);
+      else s = nc == 32 ? launch_as<4, 2, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<4, 2, 64>(tq, tk, tv, p, grid, merge, cs);
+    }
+    if (s != MLA_OK) return s;
+  }
+  return MLA_OK;
 }
 
 }  // namespace
+}  // namespace grouped
 }  // namespace mla
+
+using namespace mla;
 
 extern "C" {
 
 size_t mla_decode_grouped_workspace(const mla_grouped_args *a, int differential) {
-  if (a == nullptr || !mla::sizes_ok(*a, differential != 0)) return 0;
-  return 256;
+  if (a == nullptr || !grouped::sizes_ok(*a, differential != 0)) return 0;
+  return grouped::layout_of(*a, differential != 0).total;
 }
 
 mla_status mla_decode_grouped(const mla_grouped_args *a, void *workspace, size_t workspace_bytes, mla_stream_t stream) {
-  return mla::run("mla_decode_grouped", a, false, nullptr, nullptr, 0.0f, workspace, workspace_bytes, stream);
+  return grouped::run("mla_decode_grouped", a, false, nullptr, nullptr, 0.0f, workspace, workspace_bytes, stream);
 }
 
 mla_status mla_decode_differential(const mla_grouped_args *a, const float *lambda, const float *gain, float eps,
                                    void *workspace, size_t workspace_bytes, mla_stream_t stream) {
-  return mla::run("mla_decode_differential", a, true, lambda, gain, eps, workspace, workspace_bytes, stream);
+  return grouped::run("mla_decode_differential", a, true, lambda, gain, eps, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
