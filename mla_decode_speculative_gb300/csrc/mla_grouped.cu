@@ -98,11 +98,12 @@ __global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_co
 }
 
 // Columns of the products: the fewest of 16, 32, 64 that hold a request's rows
-// of a group (differential: 16 or 32 of each map).
+// of a group (differential: 16 or 32 of each map).  64 columns of 256 dims leave
+// no room for the ring: such rows go in blocks of 32.
 int columns_of(const mla_grouped_args &a, bool differential) {
   const int64_t rows = static_cast<int64_t>(a.max_qlen) * (a.num_heads / a.num_kv_heads);
   if (differential) return rows <= 16 ? 32 : 64;
-  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
+  return rows <= 16 ? 16 : (rows <= 32 || a.head_dim == 256 ? 32 : 64);
 }
 
 struct Layout {
@@ -259,6 +260,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
   p.page_groups = static_cast<int>(a->num_cache_rows / 8);
   p.head_blocks = (G + nr - 1) / nr;
   p.heads_per_block = p.head_blocks == 1 ? G : nr;
+  p.one_block = p.head_blocks == 1 && nr / G >= a->max_qlen;
   p.rows_per_block = p.head_blocks == 1 ? (nr / G < a->max_qlen ? nr / G : a->max_qlen) : 1;
 
   // Requests of one launch: as many as the kernel tabulates and as int32
@@ -304,7 +306,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     if (!differential) {
       if (W == 1) s = nc == 16 ? launch_as<1, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<1, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<1, 1, 64>(tq, tk, tv, p, grid, merge, cs);
       else if (W == 2) s = nc == 16 ? launch_as<2, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<2, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<2, 1, 64>(tq, tk, tv, p, grid, merge, cs);
-      else s = nc == 16 ? launch_as<4, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<4, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<4, 1, 64>(tq, tk, tv, p, grid, merge, cs);
+      else s = nc == 16 ? launch_as<4, 1, 16>(tq, tk, tv, p, grid, merge, cs) : launch_as<4, 1, 32>(tq, tk, tv, p, grid, merge, cs);
     } else {
       if (W == 2) s = nc == 32 ? launch_as<2, 2, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<2, 2, 64>(tq, tk, tv, p, grid, merge, cs);
       else s = nc == 32 ? launch_as<4, 2, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<4, 2, 64>(tq, tk, tv, p, grid, merge, cs);

@@ -21,8 +21,9 @@
 //    that one box brings a page as [8 rows][chunk][row][128 bytes]: the same
 //    uniform strides for pages of 8 as of 128, read by both products as they
 //    are (128-byte swizzle).
-//  * Copies in the order of use, K(t + 1) before V(t), through a ring of slots
-//    of at most 32 KB (two chunks); the stream of tiles runs on from part to part.
+//  * Copies through a ring of slots of at most 32 KB (two chunks) for the keys
+//    and one for the values, which wait for the softmax; a warp copies into each,
+//    a warp issues each product, and the stream of tiles runs on from part to part.
 //  * Balanced split: a unit (request, group, row block) is kOverhead positions
 //    and then its tiles; the positions of all units, laid end to end, are cut
 //    into equal chunks, one per SM.  A chunk holds at most two units that it
@@ -30,7 +31,9 @@
 //    records per SM, whatever the batch, and the merge looks at 152 chunks.
 //  * Softmax: a thread has one token and all columns of its group of warps (32
 //    at most), in registers.  The reference maximum moves only when a score
-//    passes it by 2^8; sums are float32 per thread and column.
+//    passes it by 2^8; sums are float32 per thread and column.  A probability goes
+//    to the product as two bf16 terms (2^-16 of itself), the second as further
+//    columns of N, which cost the tensor cores nothing up to N = 64.
 //  * Tokens that no row sees are neither loaded (whole pages) nor multiplied:
 //    their values in shared memory are set to zero.  A token that some rows see
 //    is looked at, and a value in it that is not finite is zeroed too and
@@ -49,7 +52,7 @@ namespace mla {
 namespace grouped {
 
 constexpr int kTile = 128;
-constexpr int kMaxReqs = 1024;    // requests of one launch (tabulated in shared memory)
+constexpr int kMaxReqs = 512;     // requests of one launch (tabulated in shared memory)
 constexpr int kOverhead = 2;      // positions a unit counts beside its tiles
 constexpr int kMinChunk = 6;      // positions a chunk has at least
 constexpr int kMaxCtas = 152;
@@ -76,6 +79,7 @@ struct Params {
   int subpage_stride, page_size, page_groups;  // page_groups: num_cache_rows / 8
   int rows_per_block;   // verify rows of a row block (group <= NR)
   int heads_per_block;  // query heads of a row block: group, or NR if group > NR
+  int one_block;        // every request has one row block
   int head_blocks;      // row blocks a verify row's group is cut into (1 if group <= NR)
 };
 
@@ -106,38 +110,46 @@ struct Config {
   static constexpr int kQChunkBytes = kNR * 128;
   static constexpr int kQBytes = kW * kQChunkBytes;
   static constexpr int kQBufs = kQBytes <= 8192 ? 2 : 1;
-  static constexpr int kPBytes = kTile * 128;
-  static constexpr int kMiscBytes = 16 * 1024;
+  static constexpr int kPN = 2 * kNC;               // columns of P^T: both terms
+  static constexpr int kPAtoms = kPN <= 64 ? 1 : 2; // of 64 columns
+  static constexpr int kPBytes = kPAtoms * kTile * 128;
+  static constexpr int kMiscBytes = 14 * 1024;
   static constexpr int kFit = (232448 - 1024 - kMiscBytes - kQBufs * kQBytes - 2 * kPBytes) / kSlotBytes;
   static constexpr int kSlots = kFit > 10 ? 10 : kFit;
+  static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;  // values wait for the softmax
   static constexpr int kGroups = kNC > 32 ? 2 : 1;  // groups of four softmax warps
   static constexpr int kCols = kNC / kGroups;       // columns of a group
   static constexpr int kSoftmaxWarps = 4 * kGroups;
-  static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kBlocks = kW < 2 ? 1 : kW / 2;  // blocks of O^T: 128 dims each (64 if W = 1)
-  static constexpr int kTmemUsed = kNC * (2 + kBlocks);
-  static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : (kTmemUsed <= 128 ? 128 : 256);
+  static constexpr int kTmemO = 2 * kNC;             // behind the two S^T: blocks of kPN columns
+  static constexpr int kTmemUsed = kTmemO + kPN * kBlocks;
+  static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : (kTmemUsed <= 128 ? 128 : (kTmemUsed <= 256 ? 256 : 512));
   static constexpr int kOffQ = kSlots * kSlotBytes;
   static constexpr int kOffP = kOffQ + kQBufs * kQBytes;
   static constexpr int kOffMisc = kOffP + 2 * kPBytes;
   static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;
-  static_assert(kTmemUsed <= 256 && kNR % 16 == 0 && kSlots >= 2 * kNS + (kNS == 1) && kSmem <= 232448, "configuration");
+  static_assert(kTmemUsed <= 512 && kNR % 16 == 0 && kKSlots >= kNS && kSmem <= 232448, "configuration");
 };
 
 struct Misc {
   uint64_t full[10], empty[10];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], o_done[2], fin;
+  uint64_t s_full[2], p_full[2], o_done[2], fin[2];
   uint32_t tmem_base;
   int abort, stop[2];
+  uint32_t armed[10], q_armed[2];         // 1 + the parity of the last use of a slot (or Q buffer) that a copy was issued for
   int start[kMaxReqs + 1];                // positions before request b
   int lo[kMaxReqs], hi[kMaxReqs];         // tokens that some row of the request sees: lo .. hi - 1
+  int q0[kMaxReqs], qlen[kMaxReqs];
   alignas(16) float red[2][4][32];        // [group of warps][warp][column]
-  alignas(16) float stat_m[64], stat_l[64];
+  alignas(16) float stat_m[64], stat_l[64], inv[64];
   int col_lo[64], col_hi[64];             // what a column of this part sees
+  int col_row[64];                        // its row of out (row * H + head), -1: none
+  float col_lam[64];
   unsigned bad[2];                        // columns of a group that see a value that is not finite
 };
-static_assert(sizeof(Misc) <= 16 * 1024, "misc");
+static_assert(sizeof(Misc) <= 14 * 1024, "misc");
 
 // A part: the tiles a .. b - 1 (of n) of a unit that lie in this chunk.
 struct Part {
@@ -154,8 +166,8 @@ struct Walk {
   const Params &p;
   const Misc &m;
   int pos_a, pos_e;     // the chunk
-  int b, j, per, units;
-  __device__ Walk(const Params &p_, const Misc &m_, int a, int e) : p(p_), m(m_), pos_a(a), pos_e(e) {
+  int b, g, rb, s, per, blocks;
+  __device__ __forceinline__ Walk(const Params &p_, const Misc &m_, int a, int e) : p(p_), m(m_), pos_a(a), pos_e(e) {
     int lo = 0, hi = p.num_reqs;  // first request that ends behind a
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -163,32 +175,35 @@ struct Walk {
       else hi = mid;
     }
     b = lo;
-    j = 0;
     enter();
-    if (b < p.num_reqs && a < e) j = (a - m.start[b]) / per;
+    if (b < p.num_reqs && a < e) {
+      const int j = (a - s) / per;
+      g = blocks == 1 ? j : j / blocks;
+      rb = j - g * blocks;
+      s += j * per;
+    }
   }
-  __device__ void enter() {
+  __device__ __forceinline__ void enter() {
     while (b < p.num_reqs && m.start[b + 1] == m.start[b]) ++b;
     if (b >= p.num_reqs) return;
     const int tiles = m.hi[b] > m.lo[b] ? (m.hi[b] + kTile - 1) / kTile - m.lo[b] / kTile : 0;
+    s = m.start[b];
     per = tiles + kOverhead;
-    units = (m.start[b + 1] - m.start[b]) / per;
+    blocks = p.one_block ? 1 : blocks_of(p, m.qlen[b]);
+    g = rb = 0;
   }
-  __device__ bool next(Part &o) {
-    while (b < p.num_reqs) {
-      const int s = m.start[b] + j * per;
-      if (s >= pos_e) return false;
+  __device__ __forceinline__ bool next(Part &o) {
+    while (b < p.num_reqs && s < pos_e) {
       const int first = s + kOverhead, n = per - kOverhead;
       o.a = max(pos_a, first) - first;
       o.e = min(pos_e, first + n) - first;
       const bool take = n > 0 ? o.e > o.a : s >= pos_a;
       if (take) {
         o.b = b;
-        o.q0 = p.qo_indptr[b];
-        o.qlen = p.qo_indptr[b + 1] - o.q0;
-        const int blocks = units / p.num_kv_heads;
-        o.g = j / blocks;
-        o.rb = j - o.g * blocks;
+        o.q0 = m.q0[b];
+        o.qlen = m.qlen[b];
+        o.g = g;
+        o.rb = rb;
         o.lo = m.lo[b];
         o.hi = m.hi[b];
         o.tile0 = o.lo / kTile;
@@ -196,10 +211,13 @@ struct Walk {
         o.start = s;
         if (n == 0) o.a = o.e = 0;
       }
-      if (++j == units) {
-        ++b;
-        j = 0;
-        enter();
+      s += per;
+      if (++rb == blocks) {
+        rb = 0;
+        if (++g == p.num_kv_heads) {
+          ++b;
+          enter();
+        }
       }
       if (take) return true;
     }
@@ -207,13 +225,16 @@ struct Walk {
   }
 };
 
-// Slot of the i-th slot use of the stream, and the parity of its full barrier.
-// K(t) is use kNS (2 t - 1) (0 for t = 0), V(t) use kNS (2 t + 2); the use that
-// would be K of the tile behind the last stays empty.
+// Slot of the u-th use of the keys' ring, or of the values' ring behind it (each
+// in order of its own copies and products), and the parity of that use.
 template <class C>
-__device__ __forceinline__ uint32_t k_use(uint32_t t) { return t == 0 ? 0 : C::kNS * (2 * t - 1); }
+__device__ __forceinline__ uint32_t k_slot(uint32_t u) { return u % C::kKSlots; }
 template <class C>
-__device__ __forceinline__ uint32_t v_use(uint32_t t) { return C::kNS * (2 * t + 2); }
+__device__ __forceinline__ uint32_t v_slot(uint32_t u) { return C::kKSlots + u % C::kVSlots; }
+template <class C>
+__device__ __forceinline__ uint32_t k_par(uint32_t u) { return (u / C::kKSlots) & 1u; }
+template <class C>
+__device__ __forceinline__ uint32_t v_par(uint32_t u) { return (u / C::kVSlots) & 1u; }
 
 __device__ __forceinline__ void record_error(int *err, int code) { atomicCAS(err, 0, code); }
 
@@ -233,6 +254,20 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 r;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
   return r;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t y;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(y));
+  return y != 0;
+}
+// D(tmem) = A B^T, or += if acc.
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
 }
 
 // One 5-D box -> shared memory, completing on an mbarrier.
@@ -319,10 +354,11 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   Misc &misc = *reinterpret_cast<Misc *>(smem + C::kOffMisc);
   const uint32_t s_slots = smem_u32(smem), s_q = s_slots + C::kOffQ, s_p = s_slots + C::kOffP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kProducer = C::kSoftmaxWarps, kMma = C::kSoftmaxWarps + 1;
+  // warps behind the softmax: copies of K and Q, copies of V, products with K, products with V
+  constexpr int kCopyK = C::kSoftmaxWarps, kCopyV = kCopyK + 1, kMmaK = kCopyK + 2, kMmaV = kCopyK + 3;
   constexpr int kSoftmaxThreads = 32 * C::kSoftmaxWarps;
 
-  if (warp == kMma) {
+  if (warp == kMmaK) {
     tmem_alloc(smem_u32(&misc.tmem_base), C::kTmemCols);
     tmem_relinquish();
   }
@@ -330,6 +366,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(smem_u32(&misc.full[i]), 1);
       mbar_init(smem_u32(&misc.empty[i]), 1);
+      misc.armed[i] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&misc.q_full[i]), 1);
@@ -337,9 +374,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       mbar_init(smem_u32(&misc.s_full[i]), 1);
       mbar_init(smem_u32(&misc.p_full[i]), C::kSoftmaxWarps);
       mbar_init(smem_u32(&misc.o_done[i]), 1);
+      mbar_init(smem_u32(&misc.fin[i]), 1);
+      misc.q_armed[i] = 0;
       misc.bad[i] = 0;
     }
-    mbar_init(smem_u32(&misc.fin), 1);
     misc.abort = 0;
     fence_mbar_init();
   }
@@ -374,10 +412,12 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         }
       }
       const int tiles = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile : 0;
-      cost = blocks_of(p, q1 - q0) * p.num_kv_heads * (tiles + kOverhead);
+      cost = (p.one_block ? 1 : blocks_of(p, q1 - q0)) * p.num_kv_heads * (tiles + kOverhead);
     }
     misc.lo[b] = hi > 0 ? lo : 0;
     misc.hi[b] = hi;
+    misc.q0[b] = q0;
+    misc.qlen[b] = q1 - q0;
     misc.start[b + 1] = cost;
   }
   if (threadIdx.x == 0) misc.start[0] = 0;
@@ -401,62 +441,47 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   tc_fence_after();
 
   const uint32_t tmem = misc.tmem_base;
-  const int total = misc.start[p.num_reqs];
-  const int chunks = max(1, min(static_cast<int>(gridDim.x), total / kMinChunk));
-  const int chunk = static_cast<int>(blockIdx.x);
-  auto cut = [&](int c) { return static_cast<int>(static_cast<long long>(c) * total / chunks); };
-  auto chunk_of = [&](int x) { return static_cast<int>((static_cast<long long>(x + 1) * chunks - 1) / total); };
+  // chunks 0 .. rest - 1 have size + 1 positions, the others size
+  const unsigned total = misc.start[p.num_reqs];
+  const unsigned chunks = max(1u, min(gridDim.x, total / kMinChunk)), size = total / chunks, rest = total - size * chunks;
+  const unsigned chunk = blockIdx.x;
+  auto cut = [&](unsigned c) { return static_cast<int>(c * size + min(c, rest)); };
+  auto chunk_of = [&](int x) {
+    const unsigned big = rest * (size + 1), u = static_cast<unsigned>(x);
+    return static_cast<int>(u < big ? u / (size + 1) : rest + (u - big) / size);
+  };
   const int pos_a = chunk < chunks ? cut(chunk) : total, pos_e = chunk < chunks ? cut(chunk + 1) : total;
   volatile int *abort_flag = &misc.abort;
   const long long budget = p.wait_budget;
-  auto fail = [&]() {
-    *abort_flag = 1;
-    record_error(p.err, MLA_DEV_WAIT_TIMEOUT);
+  bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    if (ok && !mbar_wait(bar, par, abort_flag, budget)) {
+      *abort_flag = 1;
+      record_error(p.err, MLA_DEV_WAIT_TIMEOUT);
+      ok = false;
+    }
+    return ok;
   };
-  auto full_bar = [&](uint32_t use) { return smem_u32(&misc.full[use % C::kSlots]); };
-  auto full_par = [&](uint32_t use) { return (use / C::kSlots) & 1u; };
+  auto full_bar = [&](uint32_t slot) { return smem_u32(&misc.full[slot]); };
+  auto empty_bar = [&](uint32_t slot) { return smem_u32(&misc.empty[slot]); };
 
-  if (warp == kProducer) {
+  if (warp == kCopyK || warp == kCopyV) {
     // ======================================================== copies
-    const uint64_t pol_kv = l2_policy_evict_first();
-    const uint64_t pol_q = l2_policy_evict_last();
+    const bool keys = warp == kCopyK;
+    const CUtensorMap *tm = keys ? &tm_k : &tm_v;
+    const uint64_t pol_kv = l2_policy_evict_first(), pol_q = l2_policy_evict_last();
     if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(tm);
+      if (keys) tma_prefetch_desc(&tm_q);
     }
     const int P = p.page_size, pages = kTile / P;
     const uint32_t page_bytes = static_cast<uint32_t>(P) * 128 * C::kCW;
-    uint32_t armed = 0, armed_par = 0;  // the latest copy into each slot
-    uint32_t q_armed = 0, q_armed_par = 0;
-    bool ok = true;
-    // page of this lane: row group, or the one behind the cache (zeros) if the id is bad
-    auto load_tile = [&](const CUtensorMap *tm, uint32_t use, int group8, bool mine, int n_pages, int g) {
-#pragma unroll
-      for (int s = 0; s < C::kNS; ++s) {
-        const uint32_t u = use + s, slot = u % C::kSlots;
-        if (lane == 0 && ok && !mbar_wait(smem_u32(&misc.empty[slot]), ((u / C::kSlots) & 1u) ^ 1u, abort_flag, budget)) {
-          fail();
-          ok = false;
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) return;
-        const uint32_t bar = smem_u32(&misc.full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, page_bytes * n_pages);
-        __syncwarp();
-        if (mine)
-          tma_load_5d(s_slots + slot * C::kSlotBytes + lane * page_bytes, tm, bar, 0, 0, s * C::kCW, group8, g, pol_kv);
-        armed |= 1u << slot;
-        armed_par = (armed_par & ~(1u << slot)) | (((u / C::kSlots) & 1u) << slot);
-      }
-    };
     Walk walk(p, misc, pos_a, pos_e);
     Part w;
     uint32_t t = 0, kq = 0;
-    int prev_group = 0, prev_pages = 0, prev_g = 0;
-    bool prev_mine = false;
     while (ok && walk.next(w)) {
       if (w.e == w.a) continue;
+      // a lane holds a page of the tile, and reads the next tile's ahead of the waits
       const int32_t *ids = p.subpage_table + static_cast<int64_t>(w.b) * p.subpage_stride;
       const int page_lo = w.lo / P, page_hi = (w.hi + P - 1) / P;
       auto id_of = [&](int tile) {
@@ -464,95 +489,59 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         return lane < pages && page >= page_lo && page < page_hi ? ids[page] : -1;
       };
       int id = id_of(w.a);
-      // Q of this part
-      const uint32_t qb = kq % C::kQBufs;
-      if (lane == 0 && !mbar_wait(smem_u32(&misc.q_empty[qb]), ((kq / C::kQBufs) & 1u) ^ 1u, abort_flag, budget)) {
-        fail();
-        ok = false;
-      }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
-      {
+      if (keys) {
+        const uint32_t qb = kq % C::kQBufs;
+        if (lane == 0) wait(smem_u32(&misc.q_empty[qb]), ((kq / C::kQBufs) & 1u) ^ 1u);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
         const uint32_t bar = smem_u32(&misc.q_full[qb]);
         const int rows = p.head_blocks == 1 ? p.rows_per_block : 1;
-        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kW * p.heads_per_block * rows * 128));
+        if (lane == 0) {
+          misc.q_armed[qb] = 1 + ((kq / C::kQBufs) & 1u);
+          mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kW * p.heads_per_block * rows * 128));
+        }
         __syncwarp();
         const int row = w.q0 + (p.head_blocks == 1 ? w.rb * rows : w.rb / p.head_blocks);
         const int head = p.head_blocks == 1 ? 0 : (w.rb % p.head_blocks) * p.heads_per_block;
         if (lane < kW)
           tma_load_5d(s_q + qb * C::kQBytes + lane * C::kQChunkBytes, &tm_q, bar, 0, head, row, lane, w.g, pol_q);
-        q_armed |= 1u << qb;
-        q_armed_par = (q_armed_par & ~(1u << qb)) | (((kq / C::kQBufs) & 1u) << qb);
         ++kq;
       }
       for (int i = w.a; i < w.e && ok; ++i, ++t) {
         const int first = (w.tile0 + i) * pages;
         const int p0 = max(page_lo, first), p1 = min(page_hi, first + pages);
-        const int page = first + lane;
-        const bool mine = page >= p0 && page < p1;
-        int group8 = p.page_groups;
+        const bool mine = first + lane >= p0 && first + lane < p1;
+        int group8 = p.page_groups;  // behind the cache: zeros
         if (mine) {
           if (id < 0 || (static_cast<int64_t>(id) + 1) * (P / 8) > p.page_groups) record_error(p.err, MLA_DEV_BAD_SUBPAGE);
           else group8 = id * (P / 8);
         }
         if (i + 1 < w.e) id = id_of(i + 1);
-        load_tile(&tm_k, k_use<C>(t), group8, mine, p1 - p0, w.g);
-        if (t > 0 && ok) load_tile(&tm_v, v_use<C>(t - 1), prev_group, prev_mine, prev_pages, prev_g);
-        prev_group = group8;
-        prev_mine = mine;
-        prev_pages = p1 - p0;
-        prev_g = w.g;
+#pragma unroll
+        for (int s = 0; s < C::kNS; ++s) {
+          const uint32_t use = C::kNS * t + s;
+          const uint32_t slot = keys ? k_slot<C>(use) : v_slot<C>(use), par = keys ? k_par<C>(use) : v_par<C>(use);
+          if (lane == 0) wait(empty_bar(slot), par ^ 1u);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane == 0) {
+            misc.armed[slot] = 1 + par;
+            mbar_arrive_expect_tx(full_bar(slot), page_bytes * (p1 - p0));
+          }
+          __syncwarp();
+          if (mine)
+            tma_load_5d(s_slots + slot * C::kSlotBytes + lane * page_bytes, tm, full_bar(slot), 0, 0, s * C::kCW, group8, w.g,
+                        pol_kv);
+        }
       }
     }
-    if (ok && t > 0) load_tile(&tm_v, v_use<C>(t - 1), prev_group, prev_mine, prev_pages, prev_g);
-    if (lane == 0 && (!ok || *abort_flag)) {
-      // copies in flight land before the memory is given up
-      const volatile int never = 0;
-      for (int s = 0; s < C::kSlots; ++s)
-        if (armed & (1u << s)) mbar_wait(smem_u32(&misc.full[s]), (armed_par >> s) & 1u, &never, p.drain_budget);
-      for (int s = 0; s < C::kQBufs; ++s)
-        if (q_armed & (1u << s)) mbar_wait(smem_u32(&misc.q_full[s]), (q_armed_par >> s) & 1u, &never, p.drain_budget);
-    }
-  } else if (warp == kMma) {
-    // ======================================================== products
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, C::kNR, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(kW < 2 ? 64 : 128, kNC, 1, 1);
-      const uint64_t d_k = sdesc_sw128(s_slots, 0, C::kCW * 1024);        // tokens: groups of 8
-      const uint64_t d_v = sdesc_sw128(s_slots, 1024, C::kCW * 1024);     // dims: chunks; tokens: groups of 8
+    __syncwarp();
+  } else if (warp == kMmaK) {
+    // ======================================================== S^T = K Q^T
+    if (elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, C::kNR, 0, 0);
+      const uint64_t d_k = sdesc_sw128(s_slots, 0, C::kCW * 1024);  // tokens: groups of 8
       const uint64_t d_q = sdesc_sw128(s_q, 0, 1024);
-      const uint64_t d_p = sdesc_sw128(s_p, 1024, 1024);
-      bool ok = true;
-      auto wait = [&](uint32_t bar, uint32_t par) {
-        if (ok && !mbar_wait(bar, par, abort_flag, budget)) {
-          fail();
-          ok = false;
-        }
-        return ok;
-      };
-      int prev_k0 = 0, prev_k1 = 0;
-      bool prev_first = false;
-      auto pv = [&](uint32_t t) {
-        if (!wait(smem_u32(&misc.p_full[t & 1u]), (t >> 1) & 1u)) return;
-        const uint32_t use = v_use<C>(t);
-#pragma unroll
-        for (int s = 0; s < C::kNS; ++s)
-          if (!wait(full_bar(use + s), full_par(use + s))) return;
-        tc_fence_after();
-        const uint64_t dp = d_p + (t & 1u) * (C::kPBytes >> 4);
-#pragma unroll
-        for (int s = 0; s < C::kBlocks; ++s) {
-          const uint64_t dv = d_v + ((use + s) % C::kSlots) * (C::kSlotBytes >> 4);
-          const uint32_t o = tmem + kNC * (2 + s);
-          for (int k = prev_k0; k < prev_k1; ++k) {
-            const uint64_t a = dv + k * (2 * C::kCW * 1024 >> 4), b = dp + k * (2048 >> 4);
-            if (prev_first && k == prev_k0) umma_bf16_ss_first(o, a, b, idesc_pv);
-            else umma_bf16_ss_acc(o, a, b, idesc_pv);
-          }
-          umma_commit(smem_u32(&misc.empty[(use + s) % C::kSlots]));
-        }
-        umma_commit(smem_u32(&misc.o_done[t & 1u]));
-      };
       Walk walk(p, misc, pos_a, pos_e);
       Part w;
       uint32_t t = 0, kq = 0;
@@ -560,44 +549,77 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         if (w.e == w.a) continue;
         const uint32_t qb = kq % C::kQBufs;
         if (!wait(smem_u32(&misc.q_full[qb]), (kq / C::kQBufs) & 1u)) break;
-        for (int i = w.a; i < w.e && ok; ++i, ++t) {
-          const uint32_t use = k_use<C>(t);
-          const uint32_t s_t = tmem + (t & 1u) * kNC;
+        ++kq;
+        for (int i = w.a; i < w.e; ++i, ++t) {
+          // S^T of tile t - 2 has been read
+          if (t >= 2 && !wait(smem_u32(&misc.p_full[t & 1u]), ((t - 2) >> 1) & 1u)) break;
 #pragma unroll
           for (int s = 0; s < C::kNS; ++s) {
-            if (!wait(full_bar(use + s), full_par(use + s))) break;
+            const uint32_t use = C::kNS * t + s, slot = k_slot<C>(use);
+            if (!wait(full_bar(slot), k_par<C>(use))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < C::kCW; ++c) {
-              const int chunk_i = s * C::kCW + c;             // of the token's row of keys
-              const int map = chunk_i / (kW / kMaps);
-              const bool fresh = chunk_i % (kW / kMaps) == 0;  // first chunk of its map
-              const uint64_t a = d_k + ((use + s) % C::kSlots) * (C::kSlotBytes >> 4) + c * (1024 >> 4);
-              const uint64_t b = d_q + qb * (C::kQBytes >> 4) + chunk_i * (C::kQChunkBytes >> 4);
-              const uint32_t d = s_t + map * C::kNR;
-              if (fresh) umma_bf16_ss_first(d, a, b, idesc_qk);
-              else umma_bf16_ss_acc(d, a, b, idesc_qk);
-              umma_bf16_ss_acc(d, a + 2, b + 2, idesc_qk);
-              umma_bf16_ss_acc(d, a + 4, b + 4, idesc_qk);
-              umma_bf16_ss_acc(d, a + 6, b + 6, idesc_qk);
+              const int ci = s * C::kCW + c;  // chunk of the token's row of keys
+              const uint64_t a = d_k + slot * (C::kSlotBytes >> 4) + c * (1024 >> 4);
+              const uint64_t b = d_q + qb * (C::kQBytes >> 4) + ci * (C::kQChunkBytes >> 4);
+              const uint32_t d = tmem + (t & 1u) * kNC + ci / (kW / kMaps) * C::kNR;
+              umma(d, a, b, idesc, ci % (kW / kMaps) != 0);
+              umma(d, a + 2, b + 2, idesc, 1);
+              umma(d, a + 4, b + 4, idesc, 1);
+              umma(d, a + 6, b + 6, idesc, 1);
             }
-            umma_commit(smem_u32(&misc.empty[(use + s) % C::kSlots]));
+            umma_commit(empty_bar(slot));
           }
           if (!ok) break;
           if (i + 1 == w.e) umma_commit(smem_u32(&misc.q_empty[qb]));
           umma_commit(smem_u32(&misc.s_full[t & 1u]));
-          if (t > 0) pv(t - 1);
-          const int tok = (w.tile0 + i) * kTile;
-          prev_k0 = max(w.lo - tok, 0) / 16;
-          prev_k1 = (min(w.hi - tok, kTile) + 15) / 16;
-          prev_first = i == w.a;
         }
-        ++kq;
       }
-      if (ok && t > 0) pv(t - 1);
-      umma_commit(smem_u32(&misc.fin));
+      umma_commit(smem_u32(&misc.fin[0]));
       const volatile int never = 0;
-      mbar_wait(smem_u32(&misc.fin), 0, &never, p.drain_budget);
+      mbar_wait(smem_u32(&misc.fin[0]), 0, &never, p.drain_budget);
+    }
+    __syncwarp();
+  } else if (warp == kMmaV) {
+    // ======================================================== O^T += V^T P^T
+    if (elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kW < 2 ? 64 : 128, C::kPN, 1, 1);
+      const uint64_t d_v = sdesc_sw128(s_slots, 1024, C::kCW * 1024);      // dims: chunks; tokens: groups of 8
+      const uint64_t d_p = sdesc_sw128(s_p, C::kPBytes / C::kPAtoms, 1024);  // columns: atoms of 64
+      Walk walk(p, misc, pos_a, pos_e);
+      Part w;
+      uint32_t t = 0;
+      while (ok && walk.next(w)) {
+        for (int i = w.a; i < w.e; ++i, ++t) {
+          if (!wait(smem_u32(&misc.p_full[t & 1u]), (t >> 1) & 1u)) break;
+          const int tok = (w.tile0 + i) * kTile;
+          const int k0 = max(w.lo - tok, 0) / 16, k1 = (min(w.hi - tok, kTile) + 15) / 16;
+          const uint64_t dp = d_p + (t & 1u) * (C::kPBytes >> 4);
+#pragma unroll
+          for (int s = 0; s < C::kBlocks; ++s) {
+            const uint32_t use = C::kNS * t + s, slot = v_slot<C>(use);
+            if (!wait(full_bar(slot), v_par<C>(use))) break;
+            tc_fence_after();
+            const uint64_t dv = d_v + slot * (C::kSlotBytes >> 4);
+            const uint32_t o = tmem + C::kTmemO + C::kPN * s;
+            if (k1 - k0 == kTile / 16) {
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                umma(o, dv + k * (2 * C::kCW * 1024 >> 4), dp + k * (2048 >> 4), idesc, k > 0 || i > w.a);
+            } else {
+              for (int k = k0; k < k1; ++k)
+                umma(o, dv + k * (2 * C::kCW * 1024 >> 4), dp + k * (2048 >> 4), idesc, k > k0 || i > w.a);
+            }
+            umma_commit(empty_bar(slot));
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&misc.o_done[t & 1u]));
+        }
+      }
+      umma_commit(smem_u32(&misc.fin[1]));
+      const volatile int never = 0;
+      mbar_wait(smem_u32(&misc.fin[1]), 0, &never, p.drain_budget);
     }
     __syncwarp();
   } else {
@@ -608,13 +630,6 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
     const int row = wq * 32 + lane;                // token of the tile; lane of TMEM
     const uint32_t grp_bar = 1 + grp, all_bar = 3;
-    bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t par) {
-      if (ok && !mbar_wait(bar, par, abort_flag, budget)) {
-        fail();
-        ok = false;
-      }
-    };
     uint32_t t = 0;
     int n_part = 0;
     Meta meta{0, 0, 0, -1};
@@ -632,6 +647,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       if (wq == 0 && lane < N) {
         misc.col_lo[my_col] = my_lo;
         misc.col_hi[my_col] = my_hi;
+        misc.col_row[my_col] = valid ? (w.q0 + ct) * p.num_heads + w.g * p.group + ch : -1;
+        if (kMaps == 2) misc.col_lam[my_col] = valid ? p.lambda[w.g * p.group + ch] : 0.0f;
       }
       named_bar_sync(all_bar, kSoftmaxThreads);
       if (threadIdx.x == 0) misc.stop[n_part & 1] = *abort_flag;
@@ -690,51 +707,66 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           const float r = reduce_columns<true, N>(v, lane);
           if (lane < N) misc.red[grp][wq][lane] = r;
           named_bar_sync(grp_bar, 128);
-          float f[N];
-#pragma unroll
-          for (int c = 0; c < N; ++c) {
-            const float best = fmaxf(fmaxf(misc.red[grp][0][c], misc.red[grp][1][c]), fmaxf(misc.red[grp][2][c], misc.red[grp][3][c]));
-            const float now = fmaxf(m[c], best);
-            f[c] = fast_exp2(m[c] - now);
-            m[c] = now;
-            sum[c] *= f[c];
-          }
-          if (i > w.a) {
+          const bool rescale = i > w.a;
+          if (rescale) {
             wait(smem_u32(&misc.o_done[sb ^ 1u]), ((t - 1) >> 1) & 1u);
             tc_fence_after();
+          }
 #pragma unroll
-            for (int s = 0; s < C::kBlocks; ++s) {
-              float o[N];
-              tmem_load<N>(tmem + lane_addr + kNC * (2 + s) + col0, o);
+          for (int h = 0; h < N; h += 16) {
+            float f[16];
 #pragma unroll
-              for (int c = 0; c < N; ++c) o[c] *= f[c];
-              tmem_store<N>(tmem + lane_addr + kNC * (2 + s) + col0, o);
+            for (int c = 0; c < 16; ++c) {
+              const float best = fmaxf(fmaxf(misc.red[grp][0][h + c], misc.red[grp][1][h + c]),
+                                       fmaxf(misc.red[grp][2][h + c], misc.red[grp][3][h + c]));
+              const float now = fmaxf(m[h + c], best);
+              f[c] = fast_exp2(m[h + c] - now);
+              m[h + c] = now;
+              sum[h + c] *= f[c];
             }
+            if (rescale)
+#pragma unroll
+              for (int s = 0; s < 2 * C::kBlocks; ++s) {  // both terms of every block
+                const uint32_t addr = tmem + lane_addr + C::kTmemO + kNC * s + col0 + h;
+                float o[16];
+                tmem_load<16>(addr, o);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) o[c] *= f[c];
+                tmem_store<16>(addr, o);
+              }
           }
         }
-        uint32_t pk[N / 2];
+        // a probability as two bf16 terms: its rounding, and the rounding of what that left
+        uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
         for (int c = 0; c < N; c += 2) {
           const float p0 = fast_exp2(x[c] - m[c]), p1 = fast_exp2(x[c + 1] - m[c + 1]);
           sum[c] += p0;
           sum[c + 1] += p1;
-          pk[c / 2] = pack_bf16(p0, p1);
+          const uint32_t u = pack_bf16(p0, p1);
+          hi[c / 2] = u;
+          lo[c / 2] = pack_bf16(p0 - __uint_as_float(u << 16), p1 - __uint_as_float(u & 0xffff0000u));
         }
         if (t >= 2) wait(smem_u32(&misc.o_done[sb]), ((t - 2) >> 1) & 1u);  // P of tile t - 2 has been read
         const uint32_t prow = s_p + sb * C::kPBytes + row * 128;
 #pragma unroll
-        for (int j = 0; j < N / 8; ++j)
-          st_shared_v4(prow + (((col0 / 8 + j) ^ (row & 7)) * 16), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        for (int j = 0; j < N / 8; ++j) {
+          st_shared_v4(prow + (((col0 / 8 + j) ^ (row & 7)) * 16), hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+          // the second terms: columns kNC on, of this atom of 64 or the next
+          const int at = (kNC + col0) / 8 + j;
+          st_shared_v4(prow + at / 8 * (kTile * 128) + (((at % 8) ^ (row & 7)) * 16), lo[4 * j], lo[4 * j + 1], lo[4 * j + 2],
+                       lo[4 * j + 3]);
+        }
         if (grp == 0 && (tok0 < edge_lo || tok0 + kTile > edge_hi)) {
           const bool dead = tok < w.lo || tok >= w.hi;
           const bool mixed = !dead && (tok < edge_lo || tok >= edge_hi);
           if (__any_sync(0xffffffffu, dead || mixed)) {
-            const uint32_t use = v_use<C>(t);
+            const uint32_t use = C::kNS * t;
 #pragma unroll
-            for (int s = 0; s < C::kNS; ++s) wait(full_bar(use + s), full_par(use + s));
+            for (int s = 0; s < C::kNS; ++s) wait(full_bar(v_slot<C>(use + s)), v_par<C>(use + s));
             bool zero = dead;
             auto piece = [&](int s, int c, int j) {
-              return s_slots + ((use + s) % C::kSlots) * C::kSlotBytes + (row >> 3) * (C::kCW * 1024) + c * 1024 +
+              return s_slots + v_slot<C>(use + s) * C::kSlotBytes + (row >> 3) * (C::kCW * 1024) + c * 1024 +
                      (row & 7) * 128 + j * 16;
             };
             if (mixed) {
@@ -783,79 +815,84 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           if (lane == c) misc.stat_m[col0 + c] = m[c];
       }
       named_bar_sync(grp_bar, 128);
-      if (wq == 0 && lane < N)
-        misc.stat_l[col0 + lane] = misc.red[grp][0][lane] + misc.red[grp][1][lane] + misc.red[grp][2][lane] + misc.red[grp][3][lane];
+      if (wq == 0 && lane < N) {
+        const float l = misc.red[grp][0][lane] + misc.red[grp][1][lane] + misc.red[grp][2][lane] + misc.red[grp][3][lane];
+        const bool bad = (misc.bad[grp] >> lane) & 1u;
+        misc.stat_l[my_col] = l;
+        // 0: the row saw nothing, and what its column of O^T holds is not looked at
+        misc.inv[my_col] = l == 0.0f ? 0.0f : (bad ? __int_as_float(0x7fffffff) : 1.0f / l);
+        if (w.a == 0 && w.e == w.n && valid) {
+          const int64_t at = static_cast<int64_t>(misc.col_row[my_col]) * kMaps + my_col / C::kNR;
+          p.lse[at] = l == 0.0f ? -INFINITY : (misc.stat_m[my_col] + log2f(l)) * kLn2;
+        }
+      }
       named_bar_sync(all_bar, kSoftmaxThreads);
       tc_fence_after();
       const bool whole = w.a == 0 && w.e == w.n;
-      const unsigned bad0 = misc.bad[0], bad1 = misc.bad[1];
-      auto is_bad = [&](int c) { return ((c < N ? bad0 >> c : bad1 >> (c - N)) & 1u) != 0; };
       // dim of this thread in block s of O^T: an M = 64 result has its rows in lanes 0-15 of each warp
       const bool has_dim = kW >= 2 || lane < 16;
       const int dim = kW >= 2 ? row : wq * 16 + lane;
+      // columns c .. c + 15 of block s: the sum of both terms
+      auto load_o = [&](int s, int c, float (&o)[16]) {
+        float u[16];
+        const uint32_t addr = tmem + lane_addr + C::kTmemO + C::kPN * s + c;
+        tmem_load<16>(addr, o);
+        tmem_load<16>(addr + kNC, u);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] += u[k];
+      };
       if (!whole) {
         const int64_t rec = static_cast<int64_t>(chunk) * 2 + (w.a == 0 ? 1 : 0);
         if (wq == 0 && lane < N) {
-          p.part_stat[rec * 2 * kNC + col0 + lane] = misc.stat_m[col0 + lane];
-          p.part_stat[rec * 2 * kNC + kNC + col0 + lane] = misc.stat_l[col0 + lane];
+          p.part_stat[rec * 2 * kNC + my_col] = misc.stat_m[my_col];
+          p.part_stat[rec * 2 * kNC + kNC + my_col] = misc.stat_l[my_col];
         }
         float *po = p.part_o + rec * kNC * C::kDv;
 #pragma unroll
-        for (int s = 0; s < C::kBlocks; ++s) {
-          float o[N];
-          tmem_load<N>(tmem + lane_addr + kNC * (2 + s) + col0, o);
-          if (has_dim)
+        for (int s = 0; s < C::kBlocks; ++s)
 #pragma unroll
-            for (int c = 0; c < N; ++c)
-              po[(col0 + c) * C::kDv + 128 * s + dim] = is_bad(col0 + c) ? __int_as_float(0x7fffffff) : o[c];
-        }
+          for (int h = 0; h < N; h += 16) {
+            float o[16];
+            load_o(s, col0 + h, o);
+            if (has_dim)
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float y = misc.inv[col0 + h + c];
+                if (misc.col_row[col0 + h + c] >= 0) po[(col0 + h + c) * C::kDv + 128 * s + dim] = isnan(y) ? y : o[c];
+              }
+          }
         if (w.a == 0) meta = Meta{w.b, w.g, w.rb, chunk_of(w.start + kOverhead + w.n - 1)};
       } else if (kMaps == 1) {
-        if (wq == 0 && valid && lane < N) {
-          const float l = misc.stat_l[my_col];
-          p.lse[(static_cast<int64_t>(w.q0) + ct) * p.num_heads + w.g * p.group + ch] =
-              l == 0.0f ? -INFINITY : (misc.stat_m[my_col] + log2f(l)) * kLn2;
-        }
 #pragma unroll
-        for (int s = 0; s < C::kBlocks; ++s) {
-          float o[N];
-          tmem_load<N>(tmem + lane_addr + kNC * (2 + s) + col0, o);
+        for (int s = 0; s < C::kBlocks; ++s)
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
-            int rt, rh;
-            if (column_row(p, w.rb, col0 + c, w.qlen, rt, rh) && has_dim) {
-              const float l = misc.stat_l[col0 + c];
-              const float y = l == 0.0f ? 0.0f : (is_bad(col0 + c) ? __int_as_float(0x7fffffff) : o[c] / l);
-              p.out[((static_cast<int64_t>(w.q0) + rt) * p.num_heads + w.g * p.group + rh) * C::kDv + 128 * s + dim] =
-                  __float2bfloat16_rn(y);
+          for (int h = 0; h < N; h += 16) {
+            float o[16];
+            load_o(s, col0 + h, o);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const int at = misc.col_row[col0 + h + c];
+              const float by = misc.inv[col0 + h + c];
+              if (at >= 0 && has_dim)
+                p.out[static_cast<int64_t>(at) * C::kDv + 128 * s + dim] = __float2bfloat16_rn(by == 0.0f ? 0.0f : o[c] * by);
             }
           }
-        }
       } else {
         // 16 rows of both maps per group of warps
         constexpr int R = 16;
         const int r0 = grp * R;
-        if (wq == 0 && valid && lane < N) {
-          const float l = misc.stat_l[my_col];
-          p.lse[((static_cast<int64_t>(w.q0) + ct) * p.num_heads + w.g * p.group + ch) * 2 + my_col / C::kNR] =
-              l == 0.0f ? -INFINITY : (misc.stat_m[my_col] + log2f(l)) * kLn2;
-        }
         float y[C::kBlocks][R], sq[R];
 #pragma unroll
         for (int c = 0; c < R; ++c) sq[c] = 0.0f;
 #pragma unroll
         for (int s = 0; s < C::kBlocks; ++s) {
           float o[R];
-          tmem_load<R>(tmem + lane_addr + kNC * (2 + s) + r0, y[s]);
-          tmem_load<R>(tmem + lane_addr + kNC * (2 + s) + C::kNR + r0, o);
+          load_o(s, r0, y[s]);
+          load_o(s, C::kNR + r0, o);
 #pragma unroll
           for (int c = 0; c < R; ++c) {
-            int rt, rh;
-            const bool there = column_row(p, w.rb, r0 + c, w.qlen, rt, rh);
-            const float lam = there ? p.lambda[w.g * p.group + rh] : 0.0f;
-            const float l0 = misc.stat_l[r0 + c], l1 = misc.stat_l[C::kNR + r0 + c];
-            const float u0 = l0 == 0.0f ? 0.0f : y[s][c] / l0, u1 = l1 == 0.0f ? 0.0f : o[c] / l1;
-            y[s][c] = is_bad(r0 + c) ? __int_as_float(0x7fffffff) : u0 - lam * u1;
+            const float i0 = misc.inv[r0 + c], i1 = misc.inv[C::kNR + r0 + c];
+            y[s][c] = (i0 == 0.0f ? 0.0f : y[s][c] * i0) - misc.col_lam[r0 + c] * (i1 == 0.0f ? 0.0f : o[c] * i1);
             sq[c] += y[s][c] * y[s][c];
           }
         }
@@ -864,7 +901,6 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         for (int c = 0; c < R; ++c) norm[c] = 1.0f;
         if (p.gain != nullptr) {
           const float r = reduce_columns<false, R>(sq, lane);
-          named_bar_sync(grp_bar, 128);
           if (lane < R) misc.red[grp][wq][lane] = r;
           named_bar_sync(grp_bar, 128);
 #pragma unroll
@@ -878,12 +914,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           const float gain = p.gain != nullptr ? p.gain[128 * s + dim] : 1.0f;
 #pragma unroll
           for (int c = 0; c < R; ++c) {
-            int rt, rh;
-            if (column_row(p, w.rb, r0 + c, w.qlen, rt, rh)) {
-              const float z = misc.stat_l[r0 + c] == 0.0f ? 0.0f : y[s][c] * norm[c] * gain;
-              p.out[((static_cast<int64_t>(w.q0) + rt) * p.num_heads + w.g * p.group + rh) * C::kDv + 128 * s + dim] =
-                  __float2bfloat16_rn(z);
-            }
+            const int at = misc.col_row[r0 + c];
+            if (at >= 0)
+              p.out[static_cast<int64_t>(at) * C::kDv + 128 * s + dim] =
+                  __float2bfloat16_rn(misc.inv[r0 + c] == 0.0f ? 0.0f : y[s][c] * norm[c] * gain);
           }
         }
       }
@@ -895,7 +929,15 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == kMmaK) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && misc.abort) {
+    // copies in flight land before the memory is given up
+    const volatile int never = 0;
+    for (int i = 0; i < C::kSlots; ++i)
+      if (misc.armed[i]) mbar_wait(smem_u32(&misc.full[i]), misc.armed[i] - 1, &never, p.drain_budget);
+    for (int i = 0; i < C::kQBufs; ++i)
+      if (misc.q_armed[i]) mbar_wait(smem_u32(&misc.q_full[i]), misc.q_armed[i] - 1, &never, p.drain_budget);
+  }
 }
 
 }  // namespace grouped
