@@ -254,13 +254,13 @@ mla_status make_tmap_tile3d(CUtensorMap *map, const void *base, CUtensorMapDataT
 }
 
 mla_status make_tmap_5d(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4],
-                        const cuuint32_t (&box)[5]) {
+                        const cuuint32_t (&box)[5], CUtensorMapL2promotion promotion) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return MLA_ERR_CUDA;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                             promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     set_error("cuTensorMapEncodeTiled (5-D) failed (CUresult %d)", (int)r);
     return MLA_ERR_CUDA;

@@ -3,6 +3,7 @@
 // the units that the split cuts.  The decode kernel is in mla_grouped.cuh.
 #include <atomic>
 
+
 #include "mla_grouped.cuh"
 
 namespace mla {
@@ -256,7 +257,8 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
   p.max_len = a->subpage_stride * P;
   p.window = a->window;
   p.subpage_stride = a->subpage_stride;
-  p.page_size = P;
+  while ((8 << p.page_shift) < P) ++p.page_shift;
+  p.page_shift += 3;
   p.page_groups = static_cast<int>(a->num_cache_rows / 8);
   p.head_blocks = (G + nr - 1) / nr;
   p.heads_per_block = p.head_blocks == 1 ? G : nr;
@@ -282,7 +284,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     const cuuint64_t dims[5] = {64, g64, static_cast<uint64_t>(a->num_rows), w64, hkv};
     const cuuint64_t strides[4] = {w64 * 128, static_cast<uint64_t>(a->q_row) * 2, 128, g64 * w64 * 128};
     const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.heads_per_block), static_cast<cuuint32_t>(p.rows_per_block), 1, 1};
-    const mla_status s = make_tmap_5d(&tq, a->q, dims, strides, box);
+    const mla_status s = make_tmap_5d(&tq, a->q, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (s != MLA_OK) return s;
   }
   for (int i = 0; i < 2; ++i) {
@@ -290,7 +292,9 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     const cuuint64_t dims[5] = {64, 8, w64, static_cast<uint64_t>(p.page_groups), hkv};
     const cuuint64_t strides[4] = {row, 128, row * 8, w64 * 128};
     const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(W < 2 ? W : 2), static_cast<cuuint32_t>(P / 8), 1};
-    const mla_status s = make_tmap_5d(i == 0 ? &tk : &tv, i == 0 ? a->k_cache : a->v_cache, dims, strides, box);
+    // a fetch of 256 bytes would bring another group's 128 bytes of a token along
+    const mla_status s = make_tmap_5d(i == 0 ? &tk : &tv, i == 0 ? a->k_cache : a->v_cache, dims, strides, box,
+                                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
     if (s != MLA_OK) return s;
   }
   for (int b0 = 0; b0 < a->num_reqs; b0 += reqs) {

@@ -76,7 +76,7 @@ struct Params {
   long long wait_budget, drain_budget;
   float scale_log2;
   int num_reqs, num_rows, num_heads, num_kv_heads, group, max_qlen, max_len, window;
-  int subpage_stride, page_size, page_groups;  // page_groups: num_cache_rows / 8
+  int subpage_stride, page_shift, page_groups;  // pages of 2^page_shift; page_groups: num_cache_rows / 8
   int rows_per_block;   // verify rows of a row block (group <= NR)
   int heads_per_block;  // query heads of a row block: group, or NR if group > NR
   int one_block;        // every request has one row block
@@ -132,6 +132,17 @@ struct Config {
   static_assert(kTmemUsed <= 512 && kNR % 16 == 0 && kKSlots >= kNS && kSmem <= 232448, "configuration");
 };
 
+// The first unit that a chunk meets: its request, group and row block, its
+// position, its positions, and the request's row blocks.
+struct Place {
+  int b, g, rb, s, per, blocks;
+};
+
+// Tiles of a request's units, from the tokens that its rows see.
+__device__ __forceinline__ int tiles_of(const int4 &req) {
+  return req.y > req.x ? (req.y + kTile - 1) / kTile - req.x / kTile : 0;
+}
+
 struct Misc {
   uint64_t full[10], empty[10];
   uint64_t q_full[2], q_empty[2];
@@ -140,8 +151,8 @@ struct Misc {
   int abort, stop[2];
   uint32_t armed[10], q_armed[2];         // 1 + the parity of the last use of a slot (or Q buffer) that a copy was issued for
   int start[kMaxReqs + 1];                // positions before request b
-  int lo[kMaxReqs], hi[kMaxReqs];         // tokens that some row of the request sees: lo .. hi - 1
-  int q0[kMaxReqs], qlen[kMaxReqs];
+  int4 req[kMaxReqs];                     // tokens that some row of the request sees (x .. y - 1), first row, rows
+  Place place;                            // where this chunk begins
   alignas(16) float red[2][4][32];        // [group of warps][warp][column]
   alignas(16) float stat_m[64], stat_l[64], inv[64];
   int col_lo[64], col_hi[64];             // what a column of this part sees
@@ -151,7 +162,7 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 14 * 1024, "misc");
 
-// A part: the tiles a .. b - 1 (of n) of a unit that lie in this chunk.
+// A part: the tiles a .. e - 1 (of n) of a unit that lie in this chunk.
 struct Part {
   int b, g, rb;   // request, group, row block
   int q0, qlen;
@@ -165,58 +176,45 @@ struct Part {
 struct Walk {
   const Params &p;
   const Misc &m;
-  int pos_a, pos_e;     // the chunk
+  int pos_a, pos_e;  // the chunk
   int b, g, rb, s, per, blocks;
+  int4 req;
   __device__ __forceinline__ Walk(const Params &p_, const Misc &m_, int a, int e) : p(p_), m(m_), pos_a(a), pos_e(e) {
-    int lo = 0, hi = p.num_reqs;  // first request that ends behind a
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (m.start[mid + 1] <= a) lo = mid + 1;
-      else hi = mid;
-    }
-    b = lo;
-    enter();
-    if (b < p.num_reqs && a < e) {
-      const int j = (a - s) / per;
-      g = blocks == 1 ? j : j / blocks;
-      rb = j - g * blocks;
-      s += j * per;
-    }
-  }
-  __device__ __forceinline__ void enter() {
-    while (b < p.num_reqs && m.start[b + 1] == m.start[b]) ++b;
-    if (b >= p.num_reqs) return;
-    const int tiles = m.hi[b] > m.lo[b] ? (m.hi[b] + kTile - 1) / kTile - m.lo[b] / kTile : 0;
-    s = m.start[b];
-    per = tiles + kOverhead;
-    blocks = p.one_block ? 1 : blocks_of(p, m.qlen[b]);
-    g = rb = 0;
+    b = m.place.b;
+    g = m.place.g;
+    rb = m.place.rb;
+    s = m.place.s;
+    per = m.place.per;
+    blocks = m.place.blocks;
+    req = m.req[b];
   }
   __device__ __forceinline__ bool next(Part &o) {
-    while (b < p.num_reqs && s < pos_e) {
+    while (s < pos_e) {
       const int first = s + kOverhead, n = per - kOverhead;
-      o.a = max(pos_a, first) - first;
-      o.e = min(pos_e, first + n) - first;
+      o.a = max(pos_a - first, 0);
+      o.e = min(pos_e - first, n);
       const bool take = n > 0 ? o.e > o.a : s >= pos_a;
-      if (take) {
-        o.b = b;
-        o.q0 = m.q0[b];
-        o.qlen = m.qlen[b];
-        o.g = g;
-        o.rb = rb;
-        o.lo = m.lo[b];
-        o.hi = m.hi[b];
-        o.tile0 = o.lo / kTile;
-        o.n = n;
-        o.start = s;
-        if (n == 0) o.a = o.e = 0;
-      }
+      o.b = b;
+      o.g = g;
+      o.rb = rb;
+      o.lo = req.x;
+      o.hi = req.y;
+      o.q0 = req.z;
+      o.qlen = req.w;
+      o.tile0 = o.lo / kTile;
+      o.n = n;
+      o.start = s;
+      if (n == 0) o.a = o.e = 0;
       s += per;
       if (++rb == blocks) {
         rb = 0;
-        if (++g == p.num_kv_heads) {
-          ++b;
-          enter();
+        if (++g == p.num_kv_heads && s < pos_e) {  // the next request that has rows
+          g = 0;
+          do ++b;
+          while (m.start[b + 1] <= s);
+          req = m.req[b];
+          blocks = p.one_block ? 1 : blocks_of(p, req.w);
+          per = tiles_of(req) + kOverhead;
         }
       }
       if (take) return true;
@@ -278,6 +276,20 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void *tmap, uint
       " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(w), "r"(bar), "l"(policy)
       : "memory");
+}
+
+// Stores of threads for which `there` holds (a predicate: 16 branches in a row
+// cost 120 cycles each).
+__device__ __forceinline__ void store_if(bool there, float *p, float v) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q st.global.f32 [%0], %1;\n\t}" ::"l"(p), "f"(v),
+               "r"(static_cast<uint32_t>(there))
+               : "memory");
+}
+__device__ __forceinline__ void store_if(bool there, __nv_bfloat16 *p, float v) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q st.global.b16 [%0], %1;\n\t}" ::"l"(p),
+               "h"(*reinterpret_cast<const uint16_t *>(&h)), "r"(static_cast<uint32_t>(there))
+               : "memory");
 }
 
 // 32 TMEM lanes x N columns per warp (thread i <- lane base + i), N = 16 or 32.
@@ -379,6 +391,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       misc.bad[i] = 0;
     }
     misc.abort = 0;
+    misc.place = Place{0, 0, 0, INT32_MAX, 0, 0};  // a chunk without positions
     fence_mbar_init();
   }
   // Query rows that no copy fills (a group that does not divide the columns) stay zero.
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   // What each request's rows see, and its positions.
   for (int b = threadIdx.x; b < p.num_reqs; b += C::kThreads) {
     const int q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
-    int lo = INT32_MAX, hi = 0, cost = 0;
+    int lo = INT32_MAX, hi = 0, cost = 0;  // of the rows that see anything
     if (q0 < 0 || q1 < q0 || q1 > p.num_rows || q1 - q0 > p.max_qlen) {
       record_error(p.err, MLA_DEV_BAD_INDPTR);
     } else if (q1 > q0) {
@@ -411,13 +424,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           }
         }
       }
-      const int tiles = hi > 0 ? (hi + kTile - 1) / kTile - lo / kTile : 0;
-      cost = (p.one_block ? 1 : blocks_of(p, q1 - q0)) * p.num_kv_heads * (tiles + kOverhead);
+      if (hi == 0) lo = 0;
+      cost = (p.one_block ? 1 : blocks_of(p, q1 - q0)) * p.num_kv_heads * (tiles_of(make_int4(lo, hi, 0, 0)) + kOverhead);
     }
-    misc.lo[b] = hi > 0 ? lo : 0;
-    misc.hi[b] = hi;
-    misc.q0[b] = q0;
-    misc.qlen[b] = q1 - q0;
+    misc.req[b] = make_int4(lo, hi, q0, q1 - q0);
     misc.start[b + 1] = cost;
   }
   if (threadIdx.x == 0) misc.start[0] = 0;
@@ -436,11 +446,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       carry += __shfl_sync(0xffffffffu, x, 31);
     }
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-
-  const uint32_t tmem = misc.tmem_base;
   // chunks 0 .. rest - 1 have size + 1 positions, the others size
   const unsigned total = misc.start[p.num_reqs];
   const unsigned chunks = max(1u, min(gridDim.x, total / kMinChunk)), size = total / chunks, rest = total - size * chunks;
@@ -451,6 +457,20 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     return static_cast<int>(u < big ? u / (size + 1) : rest + (u - big) / size);
   };
   const int pos_a = chunk < chunks ? cut(chunk) : total, pos_e = chunk < chunks ? cut(chunk + 1) : total;
+  for (int b = threadIdx.x; b < p.num_reqs; b += C::kThreads) {
+    const int from = misc.start[b];
+    if (from <= pos_a && pos_a < misc.start[b + 1]) {  // one request at most
+      const int4 req = misc.req[b];
+      const int per = tiles_of(req) + kOverhead, blocks = p.one_block ? 1 : blocks_of(p, req.w);
+      const int j = (pos_a - from) / per, g = blocks == 1 ? j : j / blocks;
+      misc.place = Place{b, g, j - g * blocks, from + j * per, per, blocks};
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem = misc.tmem_base;
   volatile int *abort_flag = &misc.abort;
   const long long budget = p.wait_budget;
   bool ok = true;
@@ -474,8 +494,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       tma_prefetch_desc(tm);
       if (keys) tma_prefetch_desc(&tm_q);
     }
-    const int P = p.page_size, pages = kTile / P;
-    const uint32_t page_bytes = static_cast<uint32_t>(P) * 128 * C::kCW;
+    const int shift = p.page_shift, pages = kTile >> shift, groups = 1 << (shift - 3);
+    const uint32_t page_bytes = (128u * C::kCW) << shift;
     Walk walk(p, misc, pos_a, pos_e);
     Part w;
     uint32_t t = 0, kq = 0;
@@ -483,7 +503,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       if (w.e == w.a) continue;
       // a lane holds a page of the tile, and reads the next tile's ahead of the waits
       const int32_t *ids = p.subpage_table + static_cast<int64_t>(w.b) * p.subpage_stride;
-      const int page_lo = w.lo / P, page_hi = (w.hi + P - 1) / P;
+      const int page_lo = w.lo >> shift, page_hi = ((w.hi - 1) >> shift) + 1;
       auto id_of = [&](int tile) {
         const int page = (w.tile0 + tile) * pages + lane;
         return lane < pages && page >= page_lo && page < page_hi ? ids[page] : -1;
@@ -513,8 +533,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         const bool mine = first + lane >= p0 && first + lane < p1;
         int group8 = p.page_groups;  // behind the cache: zeros
         if (mine) {
-          if (id < 0 || (static_cast<int64_t>(id) + 1) * (P / 8) > p.page_groups) record_error(p.err, MLA_DEV_BAD_SUBPAGE);
-          else group8 = id * (P / 8);
+          if (id < 0 || (static_cast<int64_t>(id) + 1) * groups > p.page_groups) record_error(p.err, MLA_DEV_BAD_SUBPAGE);
+          else group8 = id * groups;
         }
         if (i + 1 < w.e) id = id_of(i + 1);
 #pragma unroll
@@ -809,10 +829,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         const float r = reduce_columns<false, N>(v, lane);
         if (lane < N) misc.red[grp][wq][lane] = r;
       }
-      if (wq == 0) {
+      if (wq == 0 && lane == 0) {
 #pragma unroll
-        for (int c = 0; c < N; ++c)
-          if (lane == c) misc.stat_m[col0 + c] = m[c];
+        for (int c = 0; c < N; c += 4)
+          *reinterpret_cast<float4 *>(misc.stat_m + col0 + c) = make_float4(m[c], m[c + 1], m[c + 2], m[c + 3]);
       }
       named_bar_sync(grp_bar, 128);
       if (wq == 0 && lane < N) {
@@ -854,12 +874,12 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           for (int h = 0; h < N; h += 16) {
             float o[16];
             load_o(s, col0 + h, o);
-            if (has_dim)
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const float y = misc.inv[col0 + h + c];
-                if (misc.col_row[col0 + h + c] >= 0) po[(col0 + h + c) * C::kDv + 128 * s + dim] = isnan(y) ? y : o[c];
-              }
+            for (int c = 0; c < 16; ++c) {
+              const float y = misc.inv[col0 + h + c];
+              store_if(has_dim && misc.col_row[col0 + h + c] >= 0, po + (col0 + h + c) * C::kDv + 128 * s + dim,
+                       isnan(y) ? y : o[c]);
+            }
           }
         if (w.a == 0) meta = Meta{w.b, w.g, w.rb, chunk_of(w.start + kOverhead + w.n - 1)};
       } else if (kMaps == 1) {
@@ -873,8 +893,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
             for (int c = 0; c < 16; ++c) {
               const int at = misc.col_row[col0 + h + c];
               const float by = misc.inv[col0 + h + c];
-              if (at >= 0 && has_dim)
-                p.out[static_cast<int64_t>(at) * C::kDv + 128 * s + dim] = __float2bfloat16_rn(by == 0.0f ? 0.0f : o[c] * by);
+              store_if(at >= 0 && has_dim, p.out + static_cast<int64_t>(at) * C::kDv + 128 * s + dim,
+                       by == 0.0f ? 0.0f : o[c] * by);
             }
           }
       } else {
@@ -915,9 +935,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < R; ++c) {
             const int at = misc.col_row[r0 + c];
-            if (at >= 0)
-              p.out[static_cast<int64_t>(at) * C::kDv + 128 * s + dim] =
-                  __float2bfloat16_rn(misc.inv[r0 + c] == 0.0f ? 0.0f : y[s][c] * norm[c] * gain);
+            store_if(at >= 0, p.out + static_cast<int64_t>(at) * C::kDv + 128 * s + dim,
+                     misc.inv[r0 + c] == 0.0f ? 0.0f : y[s][c] * norm[c] * gain);
           }
         }
       }

@@ -31,7 +31,7 @@ mla_status make_tmap_tile3d(CUtensorMap *map, const void *base, CUtensorMapDataT
 
 // 5-D view (bf16, 128-byte swizzle); strides in bytes, of dims 1 to 4.
 mla_status make_tmap_5d(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4],
-                        const cuuint32_t (&box)[5]);
+                        const cuuint32_t (&box)[5], CUtensorMapL2promotion promotion);
 
 // Programmatic dependent launch.  Every kernel of the library is launched
 // with programmatic stream serialization: its CTAs may be scheduled while the
