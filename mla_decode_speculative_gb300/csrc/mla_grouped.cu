@@ -13,8 +13,20 @@ namespace {
 // Merge of one cut unit: its parts are record 1 of the chunk with its first
 // tile and record 0 of the chunks after it.  A warp takes a row (both maps of
 // it): statistics with a lane per part, then the parts' outputs, 64 W values
-// over 32 lanes, weighted by 2^(m - M) / L.
+// over 32 lanes, weighted by 2^(m - M) / L.  Bound by latency: the first four
+// parts' outputs are read beside the statistics.
 constexpr int kMergeRows = 4;
+constexpr int kAhead = 4;
+
+template <int kV>
+__device__ __forceinline__ void load_row(const float *o, float (&v)[kV]) {
+  if constexpr (kV == 2) {
+    *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kV; k += 4) *reinterpret_cast<float4 *>(v + k) = *reinterpret_cast<const float4 *>(o + k);
+  }
+}
 
 template <int kW, int kMaps, int kNC>
 __global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_constant__ Params p) {
@@ -22,35 +34,45 @@ __global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_co
   __shared__ float weight[kMergeRows][kMaps][kMaxCtas];
   grid_dep_wait();
   grid_dep_launch();
-  const Meta u = p.meta[blockIdx.x];
-  if (u.last < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int first = static_cast<int>(blockIdx.x), parts = u.last - first + 1;
-  const int c = static_cast<int>(blockIdx.y) * kMergeRows + warp;
-  const int q0 = p.qo_indptr[u.b], qlen = p.qo_indptr[u.b + 1] - q0;
+  const int first = static_cast<int>(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 u = *reinterpret_cast<const int4 *>(p.meta + first);  // q0, qlen, g, rb
+  const int last = p.meta[first].last;
+  if (last < 0) return;
+  const int parts = last - first + 1, c = static_cast<int>(blockIdx.y) * kMergeRows + warp;
   int t, h;
-  if (c >= kNR || !column_row(p, u.rb, c, qlen, t, h)) return;
-  const int64_t row = (static_cast<int64_t>(q0) + t) * p.num_heads + u.g * p.group + h;
+  if (c >= kNR || !column_row(p, u.w, c, u.y, t, h)) return;
+  h += u.z * p.group;
+  const int64_t row = (static_cast<int64_t>(u.x) + t) * p.num_heads + h;
   auto record = [&](int i) { return (static_cast<int64_t>(first) + i) * 2 + (i == 0 ? 1 : 0); };
-  float total[kMaps];
+  float ahead[kMaps][kAhead][kV], top[kMaps], sum[kMaps], m0[kMaps], l0[kMaps];
 #pragma unroll
   for (int m = 0; m < kMaps; ++m) {
-    const int col = m * kNR + c;
-    float top = kLowest;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_stat[record(i) * 2 * kNC + col]);
+    const float *stat = p.part_stat + record(lane) * 2 * kNC + m * kNR + c;
+    m0[m] = lane < parts ? stat[0] : kLowest;
+    l0[m] = lane < parts ? stat[kNC] : 0.0f;
+  }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.0f;
+  for (int m = 0; m < kMaps; ++m)
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < parts) load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, ahead[m][i]);
+#pragma unroll
+  for (int m = 0; m < kMaps; ++m) {
+    top[m] = m0[m];
+    for (int i = lane + 32; i < parts; i += 32) top[m] = fmaxf(top[m], p.part_stat[record(i) * 2 * kNC + m * kNR + c]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top[m] = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], o));
+    sum[m] = 0.0f;
     for (int i = lane; i < parts; i += 32) {
-      const float *stat = p.part_stat + record(i) * 2 * kNC + col;
-      const float l = stat[kNC], w = l == 0.0f ? 0.0f : exp2f(stat[0] - top);
+      const float *stat = p.part_stat + record(i) * 2 * kNC + m * kNR + c;
+      const float mi = i < 32 ? m0[m] : stat[0], li = i < 32 ? l0[m] : stat[kNC];
+      const float w = li == 0.0f ? 0.0f : exp2f(mi - top[m]);
       weight[warp][m][i] = w;
-      sum += w * l;
+      sum[m] += w * li;
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    total[m] = sum;
-    if (lane == 0) p.lse[row * kMaps + m] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    for (int o = 16; o >= 1; o >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], o);
+    if (lane == 0) p.lse[row * kMaps + m] = sum[m] == 0.0f ? -INFINITY : (top[m] + log2f(sum[m])) * kLn2;
   }
   __syncwarp();
   float y[kV];
@@ -59,23 +81,23 @@ __global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_co
     float acc[kV];
 #pragma unroll
     for (int k = 0; k < kV; ++k) acc[k] = 0.0f;
-    const float *src = p.part_o + (m * kNR + c) * kDv + lane * kV;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float w = weight[warp][m][i];
-      const float *o = src + record(i) * kNC * kDv;
-      float v[kV];
-      if constexpr (kV == 2) {
-        *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
-      } else {
+    // a part in which the row saw nothing holds no numbers
 #pragma unroll
-        for (int k = 0; k < kV; k += 4) *reinterpret_cast<float4 *>(v + k) = *reinterpret_cast<const float4 *>(o + k);
-      }
+    for (int i = 0; i < kAhead; ++i) {
+      const float w = i < parts ? weight[warp][m][i] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * ahead[m][i][k];
+    }
+#pragma unroll 4
+    for (int i = kAhead; i < parts; ++i) {
+      const float w = weight[warp][m][i];
+      float v[kV];
+      load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, v);
 #pragma unroll
       for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * v[k];
     }
-    const float inv = total[m] == 0.0f ? 0.0f : 1.0f / total[m];
-    const float by = m == 0 ? inv : -inv * p.lambda[u.g * p.group + h];
+    const float inv = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
+    const float by = m == 0 ? inv : -inv * p.lambda[h];
 #pragma unroll
     for (int k = 0; k < kV; ++k) y[k] = m == 0 ? acc[k] * by : y[k] + acc[k] * by;
   }
@@ -85,9 +107,9 @@ __global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_co
     for (int k = 0; k < kV; ++k) sq += y[k] * y[k];
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    const float norm = total[0] == 0.0f ? 0.0f : rsqrtf(sq * (1.0f / kDv) + p.eps);
+    const float norm = rsqrtf(sq * (1.0f / kDv) + p.eps);
 #pragma unroll
-    for (int k = 0; k < kV; ++k) y[k] = total[0] == 0.0f ? 0.0f : y[k] * norm * p.gain[lane * kV + k];
+    for (int k = 0; k < kV; ++k) y[k] = sum[0] == 0.0f ? 0.0f : y[k] * norm * p.gain[lane * kV + k];
   }
   uint32_t packed[kV / 2];
 #pragma unroll
@@ -304,7 +326,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     // CTAs that can get a chunk at the static bound; with one unit to each no unit is cut
     const int64_t want = most * p.num_reqs / kMinChunk;
     const int grid = static_cast<int>(want < 1 ? 1 : (want < kMaxCtas ? want : kMaxCtas));
-    const bool merge = grid > 1 && tiles + kOverhead > 1;
+    const bool merge = grid > 1;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     mla_status s = MLA_ERR_UNSUPPORTED;
     if (!differential) {

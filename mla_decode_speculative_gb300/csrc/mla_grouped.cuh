@@ -54,13 +54,14 @@ namespace grouped {
 constexpr int kTile = 128;
 constexpr int kMaxReqs = 512;     // requests of one launch (tabulated in shared memory)
 constexpr int kOverhead = 2;      // positions a unit counts beside its tiles
-constexpr int kMinChunk = 6;      // positions a chunk has at least
+constexpr int kMinChunk = 4;      // positions a chunk has at least
 constexpr int kMaxCtas = 152;
 
 // A unit that is cut across chunks: written by the chunk with its first tile.
 struct Meta {
-  int b, g, rb;
+  int q0, qlen, g, rb;
   int last;  // chunk of its last tile; -1: no such unit starts in this chunk
+  int pad[3];
 };
 
 struct Params {
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     const uint32_t grp_bar = 1 + grp, all_bar = 3;
     uint32_t t = 0;
     int n_part = 0;
-    Meta meta{0, 0, 0, -1};
+    Meta meta{0, 0, 0, 0, -1, {}};
     Walk walk(p, misc, pos_a, pos_e);
     Part w;
     while (walk.next(w)) {
@@ -881,7 +882,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
                        isnan(y) ? y : o[c]);
             }
           }
-        if (w.a == 0) meta = Meta{w.b, w.g, w.rb, chunk_of(w.start + kOverhead + w.n - 1)};
+        if (w.a == 0) meta = Meta{w.q0, w.qlen, w.g, w.rb, chunk_of(w.start + kOverhead + w.n - 1), {}};
       } else if (kMaps == 1) {
 #pragma unroll
         for (int s = 0; s < C::kBlocks; ++s)

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -588,15 +589,33 @@ def decode_verify_scaled(q, kv_cache, kv_scales, scale_block, qo_indptr, row_len
     return out, lse, workspace
 
 
-def _view_ptr(t: torch.Tensor, dev: int, name: str) -> int:
-    """Address of a bf16 tensor on the current device whose last dimension is contiguous."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: the values of a head must be contiguous")
-    return t.data_ptr()
+def _packer(cls):
+    """pack(...) of a ctypes structure's fields in order, nested ones in line: bytes of its layout.  Making
+    the structure itself takes longer than the launch (23 fields 0.9 us, with nested ones 3)."""
+    code = {ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_int64: "q", ctypes.c_void_p: "P"}
+    flat = lambda c: "".join(code[t] if t in code else flat(t) for _, t in c._fields_)   # noqa: E731
+    st = struct.Struct("@" + flat(cls) + "0q")
+    assert st.size == ctypes.sizeof(cls)
+    return st.pack
+
+
+_pack_rotary, _pack_grouped = _packer(RotaryArgs), _packer(GroupedArgs)
+_NO_HEADS = (0, 0, 0, 0, 0, 0, 0, 0)
+
+
+def _packed(name, *argtypes):
+    """The library's function `name` taking its argument structure as packed bytes."""
+    return ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, *argtypes)((name, lib()))
+
+
+_calls = {}
+
+
+def _call(name, *argtypes):
+    f = _calls.get(name)
+    if f is None:
+        f = _calls[name] = _packed(name, *argtypes)
+    return f
 
 
 def rotary_turns(freq, device="cuda") -> torch.Tensor:
@@ -614,26 +633,47 @@ def rotary_turns(freq, device="cuda") -> torch.Tensor:
     return torch.tensor(units, dtype=torch.int64, device=device)
 
 
-def _heads(x, out, rows, dev, name) -> Heads:
-    """x [T, heads, dim] to out [.., heads, dim]."""
-    shape = x.shape
-    if len(shape) != 3 or shape[0] != rows or out.dim() != 3 or out.shape[1:] != shape[1:]:
-        raise ValueError(f"{name} must be [{rows}, heads, dim] and its output hold as many heads and dims")
-    xs, os_ = x.stride(), out.stride()
-    return Heads(shape[1], shape[2], _view_ptr(x, dev, name), xs[0], xs[1], _view_ptr(out, dev, f"{name}'s output"),
-                 os_[0], os_[1])
+def _refuse_view(t, dev, name):
+    """The error for a tensor that is not bf16, on the current device, with contiguous heads."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    raise ValueError(f"{name}: the values of a head must be contiguous")
 
 
-def _rotary_args(positions, turns, axes, neighbours, dev):
-    i64, i32 = torch.int64, torch.int32
-    A, T = positions.shape if positions.dim() == 2 else (1, positions.shape[0])
-    if positions.dtype is not i32 or positions.get_device() != dev or (T > 1 and positions.stride(-1) != 1):
+def _heads(x, out, rows, dev, name, out_rows=None):
+    """mla_heads of x [rows, heads, dim] to out [out_rows, heads, dim] (out None: in place)."""
+    shape, step = x.shape, x.stride()
+    bf = torch.bfloat16
+    if len(shape) != 3 or shape[0] != rows:
+        raise ValueError(f"{name} must be [{rows}, heads, dim]")
+    if x.dtype is not bf or x.get_device() != dev or step[2] != 1 and shape[2] != 1:
+        _refuse_view(x, dev, name)
+    n, heads, dim = shape
+    if out is None:
+        ptr = x.data_ptr()
+        return heads, dim, ptr, step[0], step[1], ptr, step[0], step[1]
+    to, at = out.shape, out.stride()
+    if len(to) != 3 or to[1] != heads or to[2] != dim or to[0] != (n if out_rows is None else out_rows):
+        raise ValueError(f"the output of {name} must be [{n if out_rows is None else out_rows}, {heads}, {dim}]")
+    if out.dtype is not bf or out.get_device() != dev or at[2] != 1 and dim != 1:
+        _refuse_view(out, dev, f"the output of {name}")
+    return heads, dim, x.data_ptr(), step[0], step[1], out.data_ptr(), at[0], at[1]
+
+
+def _angles(positions, turns, axes, neighbours, dev):
+    """The arguments before q, k and v: rows, axes, R, pairing and the tables."""
+    shape, step = positions.shape, positions.stride()
+    T = shape[-1]
+    if positions.dtype is not torch.int32 or positions.get_device() != dev or len(shape) > 2 or T > 1 and step[-1] != 1:
         raise ValueError(f"positions must be [T] or [axes, T] int32 on cuda:{dev}, an axis's contiguous")
-    if axes is not None and axes.numel() != turns.numel():
+    pairs = turns.shape[0]
+    if axes is not None and axes.shape[0] != pairs:
         raise ValueError("axes must name one axis per entry of turns")
-    return RotaryArgs(T, A, 2 * turns.numel(), int(neighbours), positions.data_ptr(),
-                      positions.stride(0) if positions.dim() == 2 else 0, _dev_ptr(turns, i64, dev, "turns"),
-                      None if axes is None else _dev_ptr(axes, i32, dev, "axes"))
+    two = len(shape) == 2
+    return (T, shape[0] if two else 1, 2 * pairs, 1 if neighbours else 0, positions.data_ptr(), step[0] if two else 0,
+            _dev_ptr(turns, torch.int64, dev, "turns"), 0 if axes is None else _dev_ptr(axes, torch.int32, dev, "axes"))
 
 
 def rotary(q, k, positions, turns, axes=None, neighbours=False, q_out=None, k_out=None, stream=None):
@@ -642,22 +682,14 @@ def rotary(q, k, positions, turns, axes=None, neighbours=False, q_out=None, k_ou
     int32; turns from rotary_turns; axes [R / 2] int32: which axis turns a pair (None: the first).
     neighbours: pairs are (2i, 2i + 1) instead of (i, i + R / 2).  In place without q_out / k_out;
     any strides, the values of a head contiguous.  Returns (q_out, k_out)."""
-    L, dev, raw = _current(stream)
-    a = _rotary_args(positions, turns, axes, neighbours, dev)
-    if q is not None:
-        q_out = q if q_out is None else q_out
-        a.q = _heads(q, q_out, a.num_rows, dev, "q")
-        if q_out.shape[0] != a.num_rows:
-            raise ValueError("q_out must have q's rows")
-    if k is not None:
-        k_out = k if k_out is None else k_out
-        a.k = _heads(k, k_out, a.num_rows, dev, "k")
-        if k_out.shape[0] != a.num_rows:
-            raise ValueError("k_out must have k's rows")
-    st = L.mla_rotary(ctypes.byref(a), raw)
+    _, dev, raw = _current(stream)
+    head = _angles(positions, turns, axes, neighbours, dev)
+    a = _pack_rotary(*head, *(_NO_HEADS if q is None else _heads(q, q_out, head[0], dev, "q")),
+                     *(_NO_HEADS if k is None else _heads(k, k_out, head[0], dev, "k")), *_NO_HEADS, 0, 0)
+    st = _call("mla_rotary", ctypes.c_void_p)(a, raw)
     if st:
         _check(st, "mla_rotary")
-    return q_out, k_out
+    return q if q_out is None else q_out, k if k_out is None else k_out
 
 
 def rotary_write(q, k, v, positions, turns, slot_map, k_cache, v_cache, axes=None, neighbours=False, q_out=None,
@@ -665,23 +697,18 @@ def rotary_write(q, k, v, positions, turns, slot_map, k_cache, v_cache, axes=Non
     """mla_rotary_write: rotary on q [T, H, dim] (may be None) and k [T, Hk, dim], and row r of k
     (rotated) and of v [T, Hv, dim_v] written to row slot_map[r] (int32, -1: nowhere) of k_cache
     [N, Hk, dim] and v_cache [N, Hv, dim_v].  The other arguments are rotary's.  Returns q_out."""
-    L, dev, raw = _current(stream)
-    a = _rotary_args(positions, turns, axes, neighbours, dev)
-    T = a.num_rows
-    if q is not None:
-        q_out = q if q_out is None else q_out
-        a.q = _heads(q, q_out, T, dev, "q")
-        if q_out.shape[0] != T:
-            raise ValueError("q_out must have q's rows")
-    a.k, a.v = _heads(k, k_cache, T, dev, "k"), _heads(v, v_cache, T, dev, "v")
-    if slot_map.numel() < T or k_cache.shape[0] != v_cache.shape[0]:
-        raise ValueError("slot_map must hold T entries, and k_cache and v_cache as many rows as each other")
-    a.slot_map = _dev_ptr(slot_map, torch.int32, dev, "slot_map")
-    a.num_cache_rows = k_cache.shape[0]
-    st = L.mla_rotary_write(ctypes.byref(a), raw)
+    _, dev, raw = _current(stream)
+    head = _angles(positions, turns, axes, neighbours, dev)
+    T, N = head[0], k_cache.shape[0]
+    if slot_map.shape[0] < T:
+        raise ValueError("slot_map must hold T entries")
+    a = _pack_rotary(*head, *(_NO_HEADS if q is None else _heads(q, q_out, T, dev, "q")),
+                     *_heads(k, k_cache, T, dev, "k", N), *_heads(v, v_cache, T, dev, "v", N),
+                     _dev_ptr(slot_map, torch.int32, dev, "slot_map"), N)
+    st = _call("mla_rotary_write", ctypes.c_void_p)(a, raw)
     if st:
         _check(st, "mla_rotary_write")
-    return q_out
+    return q if q_out is None else q_out
 
 
 def decode_grouped_workspace_bytes(num_heads, num_kv_heads, max_qlen, head_dim, differential=False) -> int:
@@ -690,51 +717,60 @@ def decode_grouped_workspace_bytes(num_heads, num_kv_heads, max_qlen, head_dim, 
     return int(lib().mla_decode_grouped_workspace(ctypes.byref(a), int(differential)))
 
 
+def _rows_of(t, heads, width, dev, name):
+    """(address, row stride) of a bf16 tensor whose rows hold `heads` x `width` values without gaps."""
+    step = t.stride()
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or step[-1] != 1:
+        _refuse_view(t, dev, name)
+    if heads > 1 and step[1] != width or len(step) == 4 and 2 * step[2] != width:
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), step[0]
+
+
 def _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale, window, out, lse,
-             workspace, wait_cycles, dev, maps):
-    """(arguments, out, lse, workspace, its size needed) of a grouped call of 1 or 2 maps."""
-    T, H, D = q.shape[0], q.shape[1], q.shape[-1]
-    N, Hkv = k_cache.shape[:2]
-    pair = (2,) if maps == 2 else ()
-    if q.shape != (T, H, *pair, D) or k_cache.shape != (N, Hkv, *pair, D) or v_cache.shape != (N, Hkv, maps * D):
+             wait_cycles, dev, maps):
+    """(packed arguments, out, lse, (H, Hkv, D)) of a grouped call of 1 or 2 maps."""
+    qs, ks, vs = q.shape, k_cache.shape, v_cache.shape
+    T, H, D = qs[0], qs[1], qs[-1]
+    N, Hkv = ks[0], ks[1]
+    width = maps * D
+    if len(qs) != 2 + maps or len(ks) != 2 + maps or len(vs) != 3 or ks[-1] != D or vs[0] != N or vs[1] != Hkv or \
+            vs[2] != width or maps == 2 and (qs[2] != 2 or ks[2] != 2):
         raise ValueError("q must be [T, H, D], k_cache and v_cache [N, Hkv, D]" if maps == 1 else
                          "q must be [T, H, 2, D], k_cache [N, Hkv, 2, D] and v_cache [N, Hkv, 2 D]")
-    B, width = qo_indptr.numel() - 1, subpage_table.shape[-1]
-    if row_len.numel() != T or subpage_table.numel() != B * width:
+    B, pages = qo_indptr.shape[0] - 1, subpage_table.shape[-1]
+    if row_len.numel() != T or subpage_table.numel() != B * pages:
         raise ValueError("row_len must be [T] and subpage_table [B, width]")
-    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
-        step = D if name != "v_cache" else maps * D
-        if t.stride(1) != maps * D and t.shape[1] > 1 or maps == 2 and t.dim() == 4 and t.stride(2) != step:
-            raise ValueError(f"{name}: the heads of a row must be contiguous")
     if out is None:
-        out = torch.empty((T, H, maps * D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, H, width), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((T, H, *pair), dtype=torch.float32, device=q.device)
-    if out.numel() != T * H * maps * D or lse.numel() != T * H * maps:
+        lse = torch.empty((T, H) if maps == 1 else (T, H, 2), dtype=torch.float32, device=q.device)
+    if out.numel() != T * H * width or lse.numel() != T * H * maps:
         raise ValueError("out must hold a value vector and lse a number per row and head (and map)")
     i32 = torch.int32
-    a = GroupedArgs(B, T, H, Hkv, max_qlen, D, window, sm_scale, _view_ptr(q, dev, "q"), q.stride(0),
-                    _view_ptr(k_cache, dev, "k_cache"), k_cache.stride(0), _view_ptr(v_cache, dev, "v_cache"),
-                    v_cache.stride(0), N, _dev_ptr(qo_indptr, i32, dev, "qo_indptr"),
-                    _dev_ptr(row_len, i32, dev, "row_len"), _dev_ptr(subpage_table, i32, dev, "subpage_table"), width,
-                    page_size_, _dev_ptr(out, torch.bfloat16, dev, "out"), _dev_ptr(lse, torch.float32, dev, "lse"),
-                    wait_cycles)
-    need = lib().mla_decode_grouped_workspace(ctypes.byref(a), maps - 1)
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    return a, out, lse, workspace, need
+    a = _pack_grouped(B, T, H, Hkv, max_qlen, D, window, sm_scale, *_rows_of(q, H, width, dev, "q"),
+                      *_rows_of(k_cache, Hkv, width, dev, "k_cache"), *_rows_of(v_cache, Hkv, width, dev, "v_cache"), N,
+                      _dev_ptr(qo_indptr, i32, dev, "qo_indptr"), _dev_ptr(row_len, i32, dev, "row_len"),
+                      _dev_ptr(subpage_table, i32, dev, "subpage_table"), pages, page_size_,
+                      _dev_ptr(out, torch.bfloat16, dev, "out"), _dev_ptr(lse, torch.float32, dev, "lse"), wait_cycles)
+    return a, out, lse, (H, Hkv, D)
 
 
 def decode_grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale, window=0,
                    out=None, lse=None, workspace=None, stream=None, wait_cycles=0):
     """mla_decode_grouped: q [T, H, D] bf16 over k_cache, v_cache [N, Hkv, D] bf16 (D 64, 128 or
     256), each of any row stride; qo_indptr, row_len, subpage_table, page_size_ as decode_verify's.
-    window: a row sees its last `window` tokens only (0: all).  Returns (out [T, H, D] bf16,
-    lse [T, H] f32, workspace)."""
-    L, dev, raw = _current(stream)
-    a, out, lse, workspace, need = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen,
-                                            sm_scale, window, out, lse, workspace, wait_cycles, dev, 1)
-    st = L.mla_decode_grouped(ctypes.byref(a), _dev_ptr(workspace, torch.uint8, dev, "workspace"), need, raw)
+    window: a row sees its last `window` tokens only (0: all).  workspace: uint8, at least
+    decode_grouped_workspace_bytes (None: allocated).  Returns (out [T, H, D] bf16, lse [T, H]
+    f32, workspace)."""
+    _, dev, raw = _current(stream)
+    a, out, lse, sizes = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale,
+                                  window, out, lse, wait_cycles, dev, 1)
+    if workspace is None:
+        need = decode_grouped_workspace_bytes(sizes[0], sizes[1], max_qlen, sizes[2])
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = _call("mla_decode_grouped", ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)(
+        a, _dev_ptr(workspace, torch.uint8, dev, "workspace"), workspace.numel(), raw)
     if st:
         _check(st, "mla_decode_grouped")
     return out, lse, workspace
@@ -746,15 +782,18 @@ def decode_differential(q, k_cache, v_cache, lam, qo_indptr, row_len, subpage_ta
     bf16 (D 64 or 128): map 0 minus lam[h] (float32 [H]) times map 1, then, with gain (float32
     [2 D]), the norm over the head's 2 D values.  Returns (out [T, H, 2 D] bf16, lse [T, H, 2]
     f32, workspace)."""
-    L, dev, raw = _current(stream)
-    a, out, lse, workspace, need = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen,
-                                            sm_scale, window, out, lse, workspace, wait_cycles, dev, 2)
-    f32 = torch.float32
-    if lam.numel() != a.num_heads or (gain is not None and gain.numel() != 2 * a.head_dim):
+    _, dev, raw = _current(stream)
+    a, out, lse, sizes = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale,
+                                  window, out, lse, wait_cycles, dev, 2)
+    if lam.numel() != sizes[0] or gain is not None and gain.numel() != 2 * sizes[2]:
         raise ValueError("lam must be [H] and gain [2 D]")
-    st = L.mla_decode_differential(ctypes.byref(a), _dev_ptr(lam, f32, dev, "lam"),
-                                   None if gain is None else _dev_ptr(gain, f32, dev, "gain"), eps,
-                                   _dev_ptr(workspace, torch.uint8, dev, "workspace"), need, raw)
+    if workspace is None:
+        need = decode_grouped_workspace_bytes(sizes[0], sizes[1], max_qlen, sizes[2], True)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    f32, vp = torch.float32, ctypes.c_void_p
+    st = _call("mla_decode_differential", vp, vp, ctypes.c_float, vp, ctypes.c_size_t, vp)(
+        a, _dev_ptr(lam, f32, dev, "lam"), None if gain is None else _dev_ptr(gain, f32, dev, "gain"), eps,
+        _dev_ptr(workspace, torch.uint8, dev, "workspace"), workspace.numel(), raw)
     if st:
         _check(st, "mla_decode_differential")
     return out, lse, workspace

@@ -160,14 +160,23 @@ def test_turns_are_the_frequencies_to_half_a_unit():
 def test_wrapper_refusals_on_the_host():
     """Shapes and strides that the binding itself refuses, before it looks at devices."""
     x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
-    for src, dst in ((x[0], x), (x, x[:, :, :32]), (x, x[:, :1]), (x[:3], x)):
+    for src, dst in ((x[0], x), (x, x[:, :, :32]), (x, x[:, :1]), (x[:3], x), (x, x[:3]), (x, x[0]), (x, x[:, :, ::2])):
         with pytest.raises(ValueError):
-            mla._heads(src, dst, 4, 0, "q")
+            mla._heads(src, dst, 4, -1, "q")
+    with pytest.raises(ValueError, match="contiguous"):
+        mla._heads(x.transpose(1, 2), None, 4, -1, "q")
     with pytest.raises(TypeError):
-        mla._heads(x.float(), x.float(), 4, 0, "q")
+        mla._heads(x.float(), None, 4, -1, "q")
+    with pytest.raises(ValueError, match="device"):
+        mla._heads(x, None, 4, 0, "q")
+    assert mla._heads(x, None, 4, -1, "q")[:2] == (2, 64) and mla._heads(x, x[..., :], 4, -1, "q")[6:] == (128, 64)
+    pos, turns = torch.zeros((3, 4), dtype=torch.int32), mla.rotary_turns([1.0, 0.5], device="cpu")
+    for bad in ((pos.long(), turns, None), (pos.T, turns, None), (pos[None], turns, None), (pos, turns, torch.zeros(3, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            mla._angles(*bad, False, -1)
     ind, lens, sub = torch.zeros(2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros((1, 4), dtype=torch.int32)
     cache = torch.zeros((64, 2, 64), dtype=torch.bfloat16)
-    call = lambda q, k, v, lens=lens, maps=1: mla._grouped(q, k, v, ind, lens, sub, 16, 4, 0.1, 0, None, None, None, 0, 0, maps)  # noqa: E731
+    call = lambda q, k, v, lens=lens, maps=1: mla._grouped(q, k, v, ind, lens, sub, 16, 4, 0.1, 0, None, None, 0, -1, maps)  # noqa: E731
     for bad in ((x, cache, cache[:, :1]), (x, cache[:, :, :32], cache), (x[:, :, :32], cache, cache), (x, cache, cache[:32])):
         with pytest.raises(ValueError):
             call(*bad)
@@ -180,6 +189,15 @@ def test_wrapper_refusals_on_the_host():
     with pytest.raises(ValueError, match="contiguous"):
         call(torch.zeros((4, 4, 2, 64), dtype=torch.bfloat16)[:, ::2], cache.unflatten(1, (2, 1)).expand(-1, -1, 2, -1),
              torch.zeros((64, 2, 128), dtype=torch.bfloat16), maps=2)
+
+
+def test_packed_arguments_are_the_structures_bytes():
+    """The bytes that the binding packs are those of the ctypes structure with the same fields."""
+    values = list(range(1, 8)) + [0.5] + list(range(9, 24))
+    assert mla._pack_grouped(*values) == bytes(mla.GroupedArgs(*values))
+    heads = [mla.Heads(*range(8 * i, 8 * i + 8)) for i in (1, 2, 3)]
+    a = mla.RotaryArgs(1, 2, 3, 4, 5, 6, 7, 8, *heads, 9, 10)
+    assert mla._pack_rotary(1, 2, 3, 4, 5, 6, 7, 8, *range(8, 32), 9, 10) == bytes(a)
 
 
 def test_step_and_cache_refusals():
