@@ -8,11 +8,16 @@
 // 10^6 * 0.9 is off by 0.03 radians).  Its top 32 bits, as a signed fraction
 // in [-1/2, 1/2) turns, go to sincospi in float32.
 //
-// Memory bound: 4 bytes per value for about 3 operations.  A thread holds the
-// sines of up to 8 pairs of one row and goes over several heads with them (16
-// bytes a load, two loads a head, four heads in flight), so a row's sines are
-// made once per 8 heads.  Values that are only copied (v, the dims past R) are
-// blocks of the same launch.
+// Memory bound: 4 bytes per value for about 3 operations, once the sines are
+// shared: a block takes whole rows (or part of one), makes their sines once in
+// shared memory, and its threads go over the rows' heads in stretches of 16
+// bytes, so that what a warp touches is one run of memory.  A thread's first
+// stretch is read before the sines are made.  Values that are only copied (v,
+// the dims past R) are blocks of the same launch.  Large calls live from many
+// blocks an SM (8 of 32 registers a thread, four stretches a thread), small ones
+// from short code (4 blocks): 16,400 rows of 32 + 8 heads of 128 and 8 of values
+// 63.3 us against 75.0 with 4 blocks an SM, 620 rows of the same 3.7 against 5.2
+// with 8; four stretches in flight a thread, at two blocks an SM, 91 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,24 +29,36 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kJobs = 5;       // q, k rotated; q, k behind the rotated part; v
-constexpr int kMaxHeads = 16;  // heads a thread takes at most
+constexpr int kJobs = 5;        // q, k rotated; q, k behind the rotated part; v
+constexpr int kEach = 4;        // items a thread has at most
+constexpr int kTable = 1024;    // sines of a block
 
+// Division by a fixed d: n / d for n * d < 2^32 (n < rows x width <= 1024 by the
+// width, n < width by the lanes, which the host checks).
+struct Div {
+  uint32_t d, m;
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return m == 0 ? n : __umulhi(n, m); }
+};
+Div divisor(uint32_t d) { return Div{d, d == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + d - 1) / d)}; }
+
+// Items of a job: (row, head, lane), lane fastest; `width` items a row.
 struct Job {
   const uint16_t *src;
   uint16_t *dst;
   int64_t src_row, src_head, dst_row, dst_head;
   int first_block;  // of the launch
-  int heads, chunks, per;  // heads in all; head chunks; heads a chunk
-  int lanes;        // threads a row
-  int units;        // copies: vectors a head
-  int vec;          // pairs (rotation) or values (copy) a thread takes at once: 8, 4 or 1
+  int width;        // heads x lanes
+  int rows;         // rows a block
+  int blocks_row;   // blocks a row (1 if rows > 1)
+  int items;        // items a block
+  Div by_width, by_lanes;
+  int vec;          // pairs (rotation) or values (copy) of an item: 8, 4 or 1
   int rotate, by_slot;
 };
 
 struct Params {
   Job job[kJobs];
-  int num_jobs, num_rows, num_axes, pairs, neighbours;
+  int num_jobs, num_rows, num_axes, pairs;
   const int32_t *positions;
   int64_t axis_stride;
   const int64_t *turns;
@@ -76,116 +93,113 @@ __device__ __forceinline__ int64_t slot_of(const Params &p, int r) {
   return s;
 }
 
-// Pairs V * lane .. V * lane + V - 1 of the heads h0 .. h1 - 1 of one row.
-template <int V>
-__device__ __forceinline__ void rotate_heads(const Params &p, const Job &j, int r, int lane, int h0, int h1) {
-  int64_t out_row = r;
-  if (j.by_slot) {
-    out_row = slot_of(p, r);
-    if (out_row < 0) return;
+// cos, sin of pair q of row r.
+__device__ __forceinline__ float2 turn_of(const Params &p, int r, int q) {
+  int a = p.axes != nullptr ? p.axes[q] : 0;
+  if (a < 0 || a >= p.num_axes) {
+    atomicCAS(p.err, 0, MLA_DEV_BAD_AXIS);
+    a = 0;
   }
-  const int i0 = V * lane;
-  float c[V], s[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    int a = p.axes != nullptr ? p.axes[i0 + i] : 0;
-    if (a < 0 || a >= p.num_axes) {
-      atomicCAS(p.err, 0, MLA_DEV_BAD_AXIS);
-      a = 0;
+  const int64_t pos = p.positions[a * p.axis_stride + r];
+  const uint64_t turn = static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.turns[q]);
+  float2 cs;
+  sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &cs.y, &cs.x);
+  return cs;
+}
+
+// A block's rows [r0, r1), items [at, end) of them (counted from row r0).
+// kV: values a load has; rotation: an item is kV pairs, read as two of them.
+template <int kV, bool kRotate, bool kNeighbours>
+__device__ __forceinline__ void run_job(const Params &p, const Job &j, int r0, int r1, uint32_t at, uint32_t end, float *table) {
+  using T = typename Vec<kV>::T;
+  const int lanes = static_cast<int>(j.by_lanes.d);
+  Pack<kV> a, b;
+  int row = 0, at_a = 0, at_b = 0, lane = 0;
+  int64_t to = -1;
+  auto load = [&](uint32_t i) {
+    to = -1;
+    if (i >= end) return;
+    const uint32_t r = j.rows > 1 ? j.by_width(i) : 0, hl = i - r * j.width, h = j.by_lanes(hl);
+    row = static_cast<int>(r);
+    lane = static_cast<int>(hl - h * lanes);
+    at_a = (kRotate && kNeighbours ? 2 * kV : kV) * lane;
+    at_b = kNeighbours ? at_a + kV : p.pairs + at_a;
+    const uint16_t *x = j.src + (r0 + static_cast<int64_t>(r)) * j.src_row + h * j.src_head;
+    a.raw = *reinterpret_cast<const T *>(x + at_a);
+    if (kRotate) b.raw = *reinterpret_cast<const T *>(x + at_b);
+    const int64_t out = j.by_slot ? slot_of(p, r0 + row) : r0 + row;
+    to = out < 0 ? -1 : out * j.dst_row + h * j.dst_head;
+  };
+  uint32_t i = at + threadIdx.x;
+  load(i);
+  if (kRotate) {
+    // row by row: the (cos, sin) of pairs kV l + 2 k, + 1 of lane l at 16-byte place k * lanes + l
+    for (int u = threadIdx.x; u < (r1 - r0) * p.pairs; u += kThreads) {
+      const int r = u / p.pairs, q = u - r * p.pairs;
+      const int place = kV == 1 ? q : ((q % kV) / 2 * lanes + q / kV) * 2 + q % 2;
+      reinterpret_cast<float2 *>(table)[r * p.pairs + place] = turn_of(p, r0 + r, q);
     }
-    const int64_t pos = p.positions[a * p.axis_stride + r];
-    const uint64_t turn = static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.turns[i0 + i]);
-    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s[i], &c[i]);
+    __syncthreads();
   }
-  // the pairs' values: a run in each half of the rotated part, or one run of twice the length
-  const int at_a = p.neighbours ? 2 * i0 : i0;
-  const int at_b = p.neighbours ? 2 * i0 + V : p.pairs + i0;
-  const uint16_t *src = j.src + static_cast<int64_t>(r) * j.src_row;
-  uint16_t *dst = j.dst + out_row * j.dst_row;
-  using T = typename Vec<V>::T;
-  for (int h = h0; h < h1; h += 4) {
-    Pack<V> a[4], b[4];
+  while (true) {
+    if (to >= 0) {
+      uint16_t *y = j.dst + to;
+      if (kRotate) {
+        const float *t = table + 2 * row * p.pairs;
+        Pack<kV> oa, ob;
+        auto turn = [&](int e, float c, float s) {  // pair e of the item
+          // neighbours: values 2e, 2e + 1 of the run a, b
+          Pack<kV> &pu = kNeighbours && 2 * e >= kV ? b : a, &pv = kNeighbours && 2 * e + 1 < kV ? a : b;
+          Pack<kV> &ou = kNeighbours && 2 * e >= kV ? ob : oa, &ov = kNeighbours && 2 * e + 1 < kV ? oa : ob;
+          const int iu = kNeighbours ? (2 * e) % kV : e, iv = kNeighbours ? (2 * e + 1) % kV : e;
+          const float u = __bfloat162float(pu.h[iu]), v = __bfloat162float(pv.h[iv]);
+          ou.h[iu] = __float2bfloat16_rn(u * c - v * s);
+          ov.h[iv] = __float2bfloat16_rn(v * c + u * s);
+        };
+        if constexpr (kV == 1) {
+          const float2 cs = reinterpret_cast<const float2 *>(t)[lane];
+          turn(0, cs.x, cs.y);
+        } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (h + k < h1) {
-        const uint16_t *x = src + (h + k) * j.src_head;
-        a[k].raw = *reinterpret_cast<const T *>(x + at_a);
-        b[k].raw = *reinterpret_cast<const T *>(x + at_b);
-      }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (h + k < h1) {
-        Pack<V> oa, ob;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float x, y;
-          if (p.neighbours) {  // values 2i, 2i + 1 of the run a, b
-            x = __bfloat162float(2 * i < V ? a[k].h[(2 * i) % V] : b[k].h[(2 * i) % V]);
-            y = __bfloat162float(2 * i + 1 < V ? a[k].h[(2 * i + 1) % V] : b[k].h[(2 * i + 1) % V]);
-          } else {
-            x = __bfloat162float(a[k].h[i]);
-            y = __bfloat162float(b[k].h[i]);
-          }
-          const __nv_bfloat16 u = __float2bfloat16_rn(x * c[i] - y * s[i]);
-          const __nv_bfloat16 w = __float2bfloat16_rn(y * c[i] + x * s[i]);
-          if (p.neighbours) {
-            (2 * i < V ? oa : ob).h[(2 * i) % V] = u;
-            (2 * i + 1 < V ? oa : ob).h[(2 * i + 1) % V] = w;
-          } else {
-            oa.h[i] = u;
-            ob.h[i] = w;
+          for (int e = 0; e < kV; e += 2) {
+            const float4 cs = reinterpret_cast<const float4 *>(t)[e / 2 * lanes + lane];
+            turn(e, cs.x, cs.y);
+            turn(e + 1, cs.z, cs.w);
           }
         }
-        uint16_t *y = dst + (h + k) * j.dst_head;
         *reinterpret_cast<T *>(y + at_a) = oa.raw;
         *reinterpret_cast<T *>(y + at_b) = ob.raw;
+      } else {
+        *reinterpret_cast<T *>(y + at_a) = a.raw;
       }
-  }
-}
-
-// Vectors lane, lane + lanes, .. of the heads h0 .. h1 - 1 of one row, copied.
-template <int V>
-__device__ __forceinline__ void copy_heads(const Params &p, const Job &j, int r, int lane, int h0, int h1) {
-  int64_t out_row = r;
-  if (j.by_slot) {
-    out_row = slot_of(p, r);
-    if (out_row < 0) return;
-  }
-  const uint16_t *src = j.src + static_cast<int64_t>(r) * j.src_row;
-  uint16_t *dst = j.dst + out_row * j.dst_row;
-  using T = typename Vec<V>::T;
-  for (int u = lane; u < j.units; u += j.lanes)
-    for (int h = h0; h < h1; h += 4) {
-      T x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (h + k < h1) x[k] = *reinterpret_cast<const T *>(src + (h + k) * j.src_head + u * V);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (h + k < h1) *reinterpret_cast<T *>(dst + (h + k) * j.dst_head + u * V) = x[k];
     }
+    i += kThreads;
+    if (i >= end) break;
+    load(i);
+  }
 }
 
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params p) {
+template <bool kNeighbours, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) rotary_kernel(const __grid_constant__ Params p) {
+  __shared__ alignas(16) float table[2 * kTable];
   grid_dep_wait();
   grid_dep_launch();
   int n = 0;
   while (n + 1 < p.num_jobs && static_cast<int>(blockIdx.x) >= p.job[n + 1].first_block) ++n;
   const Job &j = p.job[n];
   const int block = static_cast<int>(blockIdx.x) - j.first_block;
-  const int rows = kThreads / j.lanes;  // rows a block
-  const int r = (block / j.chunks) * rows + static_cast<int>(threadIdx.x) / j.lanes;
-  const int lane = static_cast<int>(threadIdx.x) % j.lanes;
-  if (static_cast<int>(threadIdx.x) >= rows * j.lanes || r >= p.num_rows) return;
-  const int h0 = (block % j.chunks) * j.per, h1 = min(h0 + j.per, j.heads);
+  const int group = block / j.blocks_row, part = block - group * j.blocks_row;
+  const int r0 = group * j.rows, r1 = min(r0 + j.rows, p.num_rows);
+  const uint32_t at = static_cast<uint32_t>(part) * j.items;
+  const uint32_t end = min(at + j.items, static_cast<uint32_t>(r1 - r0) * j.width);
   if (j.rotate) {
-    if (j.vec == 8) rotate_heads<8>(p, j, r, lane, h0, h1);
-    else if (j.vec == 4) rotate_heads<4>(p, j, r, lane, h0, h1);
-    else rotate_heads<1>(p, j, r, lane, h0, h1);
+    if (j.vec == 8) run_job<8, true, kNeighbours>(p, j, r0, r1, at, end, table);
+    else if (j.vec == 4) run_job<4, true, kNeighbours>(p, j, r0, r1, at, end, table);
+    else run_job<1, true, kNeighbours>(p, j, r0, r1, at, end, table);
   } else {
-    if (j.vec == 8) copy_heads<8>(p, j, r, lane, h0, h1);
-    else if (j.vec == 4) copy_heads<4>(p, j, r, lane, h0, h1);
-    else copy_heads<1>(p, j, r, lane, h0, h1);
+    if (j.vec == 8) run_job<8, false, false>(p, j, r0, r1, at, end, table);
+    else if (j.vec == 4) run_job<4, false, false>(p, j, r0, r1, at, end, table);
+    else run_job<1, false, false>(p, j, r0, r1, at, end, table);
   }
 }
 
@@ -288,7 +302,6 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
   p.num_rows = a->num_rows;
   p.num_axes = a->num_axes;
   p.pairs = a->rot_dim / 2;
-  p.neighbours = a->neighbours != 0;
   p.positions = a->positions;
   p.axis_stride = a->axis_stride;
   p.turns = a->turns;
@@ -297,6 +310,7 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
   p.num_cache_rows = a->num_cache_rows;
   p.err = err;
   int64_t blocks = 0;
+  bool too_wide = false, large = false;
   auto add = [&](const mla_heads &t, bool rotate, int at, int dim, bool by_slot) {
     Job &j = p.job[p.num_jobs++];
     j.src = static_cast<const uint16_t *>(t.src) + at;
@@ -305,22 +319,24 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
     j.src_head = t.src_head;
     j.dst_row = t.dst_row;
     j.dst_head = t.dst_head;
-    j.heads = t.heads;
     j.rotate = rotate;
     j.by_slot = by_slot;
     j.vec = vector_of(t, at, rotate ? p.pairs : dim);
-    j.units = (rotate ? p.pairs : dim) / j.vec;
-    j.lanes = j.units < kThreads ? j.units : kThreads;
-    // Heads a thread goes over with its sines: as many as leave the GPU 152 x
-    // 1024 threads, 16 at most.
-    const int64_t threads = static_cast<int64_t>(p.num_rows) * j.lanes * t.heads;
-    int64_t per = threads / (152 * 1024);
-    per = per < 1 ? 1 : (per > kMaxHeads ? kMaxHeads : per);
-    j.per = static_cast<int>(per);
-    j.chunks = (t.heads + j.per - 1) / j.per;
+    const int lanes = (rotate ? p.pairs : dim) / j.vec;
+    if (static_cast<int64_t>(t.heads) * lanes * lanes > UINT32_MAX) too_wide = true;
+    j.width = t.heads * lanes;
+    // Items a thread has: four, or what leaves the GPU two blocks an SM.
+    const int64_t share = static_cast<int64_t>(p.num_rows) * j.width / (304 * kThreads);
+    large |= share >= kEach;
+    const int each = static_cast<int>(share < 1 ? 1 : (share > kEach ? kEach : share)) * kThreads;
+    const int most = rotate ? kTable / p.pairs : 65536;
+    j.rows = each / j.width < 1 ? 1 : (each / j.width > most ? most : each / j.width);
+    j.blocks_row = j.rows > 1 || j.width <= each ? 1 : (j.width + each - 1) / each;
+    j.items = j.blocks_row > 1 ? each : j.rows * j.width;
+    j.by_width = divisor(static_cast<uint32_t>(j.width));
+    j.by_lanes = divisor(static_cast<uint32_t>(lanes));
     j.first_block = static_cast<int>(blocks);
-    const int rows = kThreads / j.lanes;
-    blocks += static_cast<int64_t>((p.num_rows + rows - 1) / rows) * j.chunks;
+    blocks += static_cast<int64_t>((p.num_rows + j.rows - 1) / j.rows) * j.blocks_row;
   };
   const int R = a->rot_dim;
   if (a->q.heads > 0) add(a->q, true, 0, R, false);
@@ -328,12 +344,15 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
   if (a->v.heads > 0) add(a->v, false, 0, a->v.dim, true);
   if (a->q.heads > 0 && a->q.dim > R && a->q.src != a->q.dst) add(a->q, false, R, a->q.dim - R, false);
   if (a->k.heads > 0 && a->k.dim > R && a->k.src != a->k.dst) add(a->k, false, R, a->k.dim - R, write);
-  if (blocks > INT32_MAX) {
-    set_error("%s: %d rows need too many blocks", what, a->num_rows);
+  if (too_wide || blocks > INT32_MAX) {
+    set_error("%s: %d rows of these heads are too many", what, a->num_rows);
     return MLA_ERR_UNSUPPORTED;
   }
-  const cudaError_t e = launch_pdl(rotary_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
-                                   reinterpret_cast<cudaStream_t>(stream), p);
+  const dim3 grid(static_cast<unsigned>(blocks)), threads(kThreads);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      a->neighbours ? (large ? launch_pdl(rotary_kernel<true, 8>, grid, threads, 0, s, p) : launch_pdl(rotary_kernel<true, 4>, grid, threads, 0, s, p))
+                    : (large ? launch_pdl(rotary_kernel<false, 8>, grid, threads, 0, s, p) : launch_pdl(rotary_kernel<false, 4>, grid, threads, 0, s, p));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "rotary launch");
 }
 
