@@ -1,7 +1,6 @@
 // mla_grouped.cu -- grouped-query and differential decode / causal verify over
-// a paged K/V cache: argument checks, tensor maps, launches, and the merge of
-// the units that the split cuts.  The decode kernel is in mla_grouped.cuh.
-#include <atomic>
+// a paged K/V cache: argument checks, tensor maps and the choice of the
+// configuration.  The kernels are in mla_grouped.cuh and mla_grouped_launch.cuh.
 
 
 #include "mla_grouped.cuh"
@@ -9,116 +8,6 @@
 namespace mla {
 namespace grouped {
 namespace {
-
-// Merge of one cut unit: its parts are record 1 of the chunk with its first
-// tile and record 0 of the chunks after it.  A warp takes a row (both maps of
-// it): statistics with a lane per part, then the parts' outputs, 64 W values
-// over 32 lanes, weighted by 2^(m - M) / L.  Bound by latency: the first four
-// parts' outputs are read beside the statistics.
-constexpr int kMergeRows = 4;
-constexpr int kAhead = 4;
-
-template <int kV>
-__device__ __forceinline__ void load_row(const float *o, float (&v)[kV]) {
-  if constexpr (kV == 2) {
-    *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
-  } else {
-#pragma unroll
-    for (int k = 0; k < kV; k += 4) *reinterpret_cast<float4 *>(v + k) = *reinterpret_cast<const float4 *>(o + k);
-  }
-}
-
-template <int kW, int kMaps, int kNC>
-__global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_constant__ Params p) {
-  constexpr int kNR = kNC / kMaps, kDv = 64 * kW, kV = kDv / 32;
-  __shared__ float weight[kMergeRows][kMaps][kMaxCtas];
-  grid_dep_wait();
-  grid_dep_launch();
-  const int first = static_cast<int>(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 u = *reinterpret_cast<const int4 *>(p.meta + first);  // q0, qlen, g, rb
-  const int last = p.meta[first].last;
-  if (last < 0) return;
-  const int parts = last - first + 1, c = static_cast<int>(blockIdx.y) * kMergeRows + warp;
-  int t, h;
-  if (c >= kNR || !column_row(p, u.w, c, u.y, t, h)) return;
-  h += u.z * p.group;
-  const int64_t row = (static_cast<int64_t>(u.x) + t) * p.num_heads + h;
-  auto record = [&](int i) { return (static_cast<int64_t>(first) + i) * 2 + (i == 0 ? 1 : 0); };
-  float ahead[kMaps][kAhead][kV], top[kMaps], sum[kMaps], m0[kMaps], l0[kMaps];
-#pragma unroll
-  for (int m = 0; m < kMaps; ++m) {
-    const float *stat = p.part_stat + record(lane) * 2 * kNC + m * kNR + c;
-    m0[m] = lane < parts ? stat[0] : kLowest;
-    l0[m] = lane < parts ? stat[kNC] : 0.0f;
-  }
-#pragma unroll
-  for (int m = 0; m < kMaps; ++m)
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i < parts) load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, ahead[m][i]);
-#pragma unroll
-  for (int m = 0; m < kMaps; ++m) {
-    top[m] = m0[m];
-    for (int i = lane + 32; i < parts; i += 32) top[m] = fmaxf(top[m], p.part_stat[record(i) * 2 * kNC + m * kNR + c]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top[m] = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], o));
-    sum[m] = 0.0f;
-    for (int i = lane; i < parts; i += 32) {
-      const float *stat = p.part_stat + record(i) * 2 * kNC + m * kNR + c;
-      const float mi = i < 32 ? m0[m] : stat[0], li = i < 32 ? l0[m] : stat[kNC];
-      const float w = li == 0.0f ? 0.0f : exp2f(mi - top[m]);
-      weight[warp][m][i] = w;
-      sum[m] += w * li;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], o);
-    if (lane == 0) p.lse[row * kMaps + m] = sum[m] == 0.0f ? -INFINITY : (top[m] + log2f(sum[m])) * kLn2;
-  }
-  __syncwarp();
-  float y[kV];
-#pragma unroll
-  for (int m = 0; m < kMaps; ++m) {
-    float acc[kV];
-#pragma unroll
-    for (int k = 0; k < kV; ++k) acc[k] = 0.0f;
-    // a part in which the row saw nothing holds no numbers
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const float w = i < parts ? weight[warp][m][i] : 0.0f;
-#pragma unroll
-      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * ahead[m][i][k];
-    }
-#pragma unroll 4
-    for (int i = kAhead; i < parts; ++i) {
-      const float w = weight[warp][m][i];
-      float v[kV];
-      load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, v);
-#pragma unroll
-      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * v[k];
-    }
-    const float inv = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
-    const float by = m == 0 ? inv : -inv * p.lambda[h];
-#pragma unroll
-    for (int k = 0; k < kV; ++k) y[k] = m == 0 ? acc[k] * by : y[k] + acc[k] * by;
-  }
-  if (kMaps == 2 && p.gain != nullptr) {
-    float sq = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kV; ++k) sq += y[k] * y[k];
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    const float norm = rsqrtf(sq * (1.0f / kDv) + p.eps);
-#pragma unroll
-    for (int k = 0; k < kV; ++k) y[k] = sum[0] == 0.0f ? 0.0f : y[k] * norm * p.gain[lane * kV + k];
-  }
-  uint32_t packed[kV / 2];
-#pragma unroll
-  for (int k = 0; k < kV; k += 2) packed[k / 2] = pack_bf16(y[k], y[k + 1]);
-  __nv_bfloat16 *dst = p.out + row * kDv + lane * kV;
-  if constexpr (kV == 2) *reinterpret_cast<uint32_t *>(dst) = packed[0];
-  else if constexpr (kV == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(packed[0], packed[1]);
-  else *reinterpret_cast<uint4 *>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-}
 
 // Columns of the products: the fewest of 16, 32, 64 that hold a request's rows
 // of a group (differential: 16 or 32 of each map).  64 columns of 256 dims leave
@@ -144,26 +33,6 @@ Layout layout_of(const mla_grouped_args &a, bool differential) {
   off += align256(kMaxCtas * sizeof(Meta));
   l.total = off;
   return l;
-}
-
-template <int kW, int kMaps, int kNC>
-mla_status launch_as(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const Params &p, int grid, bool merge,
-                     cudaStream_t stream) {
-  using C = Config<kW, kMaps, kNC>;
-  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (!((ready.load(std::memory_order_relaxed) >> (dev & 63)) & 1u)) {
-    e = cudaFuncSetAttribute(grouped_kernel<kW, kMaps, kNC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return cuda_fail(e, "grouped kernel shared memory");
-    ready.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
-  }
-  e = launch_pdl(grouped_kernel<kW, kMaps, kNC>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, q, k, v, p);
-  if (e != cudaSuccess) return cuda_fail(e, "grouped launch");
-  if (!merge) return MLA_OK;
-  e = launch_pdl(grouped_merge<kW, kMaps, kNC>, dim3(grid, C::kNR / kMergeRows), dim3(32 * kMergeRows), 0, stream, p);
-  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "grouped merge launch");
 }
 
 bool sizes_ok(const mla_grouped_args &a, bool differential) {
@@ -323,20 +192,13 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     p.num_reqs = a->num_reqs - b0 < reqs ? a->num_reqs - b0 : reqs;
     p.qo_indptr = a->qo_indptr + b0;
     p.subpage_table = a->subpage_table + static_cast<int64_t>(b0) * a->subpage_stride;
-    // CTAs that can get a chunk at the static bound; with one unit to each no unit is cut
+    // no more CTAs than there are chunks at the static bound; one chunk cuts no unit
     const int64_t want = most * p.num_reqs / kMinChunk;
     const int grid = static_cast<int>(want < 1 ? 1 : (want < kMaxCtas ? want : kMaxCtas));
     const bool merge = grid > 1;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    mla_status s = MLA_ERR_UNSUPPORTED;
-    if (!differential) {
-      if (W == 1) s = nc == 16 ? launch_as<1, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<1, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<1, 1, 64>(tq, tk, tv, p, grid, merge, cs);
-      else if (W == 2) s = nc == 16 ? launch_as<2, 1, 16>(tq, tk, tv, p, grid, merge, cs) : nc == 32 ? launch_as<2, 1, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<2, 1, 64>(tq, tk, tv, p, grid, merge, cs);
-      else s = nc == 16 ? launch_as<4, 1, 16>(tq, tk, tv, p, grid, merge, cs) : launch_as<4, 1, 32>(tq, tk, tv, p, grid, merge, cs);
-    } else {
-      if (W == 2) s = nc == 32 ? launch_as<2, 2, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<2, 2, 64>(tq, tk, tv, p, grid, merge, cs);
-      else s = nc == 32 ? launch_as<4, 2, 32>(tq, tk, tv, p, grid, merge, cs) : launch_as<4, 2, 64>(tq, tk, tv, p, grid, merge, cs);
-    }
+    const mla_status s =
+        differential ? launch_differential(W, nc, tq, tk, tv, p, grid, merge, cs) : launch_grouped(W, nc, tq, tk, tv, p, grid, merge, cs);
     if (s != MLA_OK) return s;
   }
   return MLA_OK;

@@ -960,5 +960,12 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   }
 }
 
+// The launches of a call: W chunks a token, nc columns (mla_grouped_plain.cu,
+// mla_grouped_differential.cu).
+mla_status launch_grouped(int W, int nc, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const Params &p,
+                          int grid, bool merge, cudaStream_t stream);
+mla_status launch_differential(int W, int nc, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const Params &p,
+                               int grid, bool merge, cudaStream_t stream);
+
 }  // namespace grouped
 }  // namespace mla

@@ -1,0 +1,143 @@
+// mla_grouped_launch.cuh -- the merge of the units that the split cuts, and the
+// two launches of a call, for one configuration.  Included by the translation
+// units that instantiate them.
+#pragma once
+#include <atomic>
+
+#include "mla_grouped.cuh"
+
+namespace mla {
+namespace grouped {
+
+// Merge of one cut unit: its parts are record 1 of the chunk with its first
+// tile and record 0 of the chunks after it.  A warp takes a row (both maps of
+// it): statistics with a lane per part, then the parts' outputs, 64 W values
+// over 32 lanes, weighted by 2^(m - M) / L.  Bound by latency: the first four
+// parts' outputs are read beside the statistics.
+constexpr int kMergeRows = 4;
+constexpr int kAhead = 4;
+
+template <int kV>
+__device__ __forceinline__ void load_row(const float *o, float (&v)[kV]) {
+  if constexpr (kV == 2) {
+    *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kV; k += 4) *reinterpret_cast<float4 *>(v + k) = *reinterpret_cast<const float4 *>(o + k);
+  }
+}
+
+template <int kW, int kMaps, int kNC>
+__global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_constant__ Params p) {
+  constexpr int kNR = kNC / kMaps, kDv = 64 * kW, kV = kDv / 32;
+  __shared__ float weight[kMergeRows][kMaps][kMaxCtas];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int first = static_cast<int>(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 u = *reinterpret_cast<const int4 *>(p.meta + first);  // q0, qlen, g, rb
+  const int last = p.meta[first].last;
+  if (last < 0) return;
+  const int parts = last - first + 1, c = static_cast<int>(blockIdx.y) * kMergeRows + warp;
+  int t, h;
+  if (c >= kNR || !column_row(p, u.w, c, u.y, t, h)) return;
+  h += u.z * p.group;
+  const int64_t row = (static_cast<int64_t>(u.x) + t) * p.num_heads + h;
+  auto record = [&](int i) { return (static_cast<int64_t>(first) + i) * 2 + (i == 0 ? 1 : 0); };
+  float ahead[kMaps][kAhead][kV], top[kMaps], sum[kMaps], m0[kMaps], l0[kMaps];
+#pragma unroll
+  for (int m = 0; m < kMaps; ++m) {
+    const float *stat = p.part_stat + record(lane) * 2 * kNC + m * kNR + c;
+    m0[m] = lane < parts ? stat[0] : kLowest;
+    l0[m] = lane < parts ? stat[kNC] : 0.0f;
+  }
+#pragma unroll
+  for (int m = 0; m < kMaps; ++m)
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < parts) load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, ahead[m][i]);
+#pragma unroll
+  for (int m = 0; m < kMaps; ++m) {
+    top[m] = m0[m];
+    for (int i = lane + 32; i < parts; i += 32) top[m] = fmaxf(top[m], p.part_stat[record(i) * 2 * kNC + m * kNR + c]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top[m] = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], o));
+    sum[m] = 0.0f;
+    for (int i = lane; i < parts; i += 32) {
+      const float *stat = p.part_stat + record(i) * 2 * kNC + m * kNR + c;
+      const float mi = i < 32 ? m0[m] : stat[0], li = i < 32 ? l0[m] : stat[kNC];
+      const float w = li == 0.0f ? 0.0f : exp2f(mi - top[m]);
+      weight[warp][m][i] = w;
+      sum[m] += w * li;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], o);
+    if (lane == 0) p.lse[row * kMaps + m] = sum[m] == 0.0f ? -INFINITY : (top[m] + log2f(sum[m])) * kLn2;
+  }
+  __syncwarp();
+  float y[kV];
+#pragma unroll
+  for (int m = 0; m < kMaps; ++m) {
+    float acc[kV];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) acc[k] = 0.0f;
+    // a part in which the row saw nothing holds no numbers
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float w = i < parts ? weight[warp][m][i] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * ahead[m][i][k];
+    }
+#pragma unroll 4
+    for (int i = kAhead; i < parts; ++i) {
+      const float w = weight[warp][m][i];
+      float v[kV];
+      load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, v);
+#pragma unroll
+      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * v[k];
+    }
+    const float inv = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
+    const float by = m == 0 ? inv : -inv * p.lambda[h];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) y[k] = m == 0 ? acc[k] * by : y[k] + acc[k] * by;
+  }
+  if (kMaps == 2 && p.gain != nullptr) {
+    float sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) sq += y[k] * y[k];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    const float norm = rsqrtf(sq * (1.0f / kDv) + p.eps);
+#pragma unroll
+    for (int k = 0; k < kV; ++k) y[k] = sum[0] == 0.0f ? 0.0f : y[k] * norm * p.gain[lane * kV + k];
+  }
+  uint32_t packed[kV / 2];
+#pragma unroll
+  for (int k = 0; k < kV; k += 2) packed[k / 2] = pack_bf16(y[k], y[k + 1]);
+  __nv_bfloat16 *dst = p.out + row * kDv + lane * kV;
+  if constexpr (kV == 2) *reinterpret_cast<uint32_t *>(dst) = packed[0];
+  else if constexpr (kV == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(packed[0], packed[1]);
+  else *reinterpret_cast<uint4 *>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+}
+
+template <int kW, int kMaps, int kNC>
+mla_status launch_as(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const Params &p, int grid, bool merge,
+                     cudaStream_t stream) {
+  using C = Config<kW, kMaps, kNC>;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (!((ready.load(std::memory_order_relaxed) >> (dev & 63)) & 1u)) {
+    e = cudaFuncSetAttribute(grouped_kernel<kW, kMaps, kNC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "grouped kernel shared memory");
+    ready.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  e = launch_pdl(grouped_kernel<kW, kMaps, kNC>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, q, k, v, p);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped launch");
+  if (!merge) return MLA_OK;
+  e = launch_pdl(grouped_merge<kW, kMaps, kNC>, dim3(grid, C::kNR / kMergeRows), dim3(32 * kMergeRows), 0, stream, p);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e, "grouped merge launch");
+}
+
+}  // namespace grouped
+}  // namespace mla

@@ -416,6 +416,100 @@ def test_another_stream_and_its_own_workspace():
     assert torch.equal(out, want) and torch.equal(l, lse)
 
 
+@pytest.mark.parametrize("maps", [1, 2])
+def test_more_requests_than_one_launch_tabulates(maps):
+    """1,300 requests, some without rows, some that see nothing."""
+    r = np.random.default_rng(14)
+    L, ql = r.integers(3, 40, 1300), r.integers(0, 4, 1300)
+    L[::100], ql[::100] = 400, 2
+    s = State(L, ql, 4, 2, 64, 8, maps=maps, seed=14)
+    s.row_len[::37] = 0
+    s.check()
+
+
+@pytest.mark.parametrize("maps,H,Hkv,window", [(1, 6, 2, 0), (1, 6, 2, 70), (2, 4, 1, 0), (1, 40, 1, 0)])
+def test_many_rows_per_request(maps, H, Hkv, window):
+    """Prompts as one causal call: many row blocks, tiles that only some rows see."""
+    State([300, 77, 140], [300, 77, 9], H, Hkv, 64, 16, maps=maps, seed=15).check(window)
+
+
+@pytest.mark.parametrize("bs", [8, 64, 128])
+def test_cache_of_one_block_and_of_less_than_a_page(bs):
+    s = State([5], [2], 4, 2, 128, bs, seed=16)
+    s.check()
+    s.table[:] = 0
+    s.k, s.v = s.k[:8].clone(), s.v[:8].clone()   # eight rows: no whole page of 64 or 128
+    s.k[:], s.v[:] = 1, 1
+    out, lse = s.run()
+    if bs == 8:
+        assert (out == 1).all() and mla.get_device_error() == 0
+    else:
+        assert (out == 0).all() and mla.get_device_error() == 5
+
+
+def test_window_does_not_read_pages_before_it():
+    """Pages that have left every row's window may have gone back to the pool; a table wider than the
+    requests need."""
+    s = State([1500, 300], [3, 2], 8, 2, 128, 16, seed=17)
+    want, lse = s.check(window=200)
+    wide = np.full((2, 4 * s.table.shape[1]), -1, np.int32)
+    wide[:, :s.table.shape[1]] = s.table
+    wide[0, :(1500 - 3 + 1 - 200) // 16] = -1
+    wide[1, :(300 - 2 + 1 - 200) // 16] = 10 ** 8
+    s.table = wide
+    out, l = s.run(200)
+    assert torch.equal(out, want) and torch.equal(l, lse) and mla.get_device_error() == 0
+
+
+@pytest.mark.parametrize("maps,D", [(1, 64), (1, 128), (1, 256), (2, 64), (2, 128)])
+def test_waits_that_run_out_are_recorded(maps, D):
+    """A budget that no copy can meet: every CTA gives up, the next call is right."""
+    s = State([3000, 200, 1000], [4, 1, 2], 16, 4, D, 16, maps=maps, seed=18)
+    want, lse = s.run()
+    for _ in range(2):
+        s.run(wait_cycles=1)
+        assert mla.get_device_error() == 6
+    out, l = s.run()
+    assert torch.equal(out, want) and torch.equal(l, lse) and mla.get_device_error() == 0
+
+
+def test_two_captured_graphs_with_a_workspace_each():
+    """Two calls captured apart, replayed at the same time on two streams, over and over."""
+    states = [State([4000, 700], [2, 2], 16, 4, 128, 32, seed=20), State([3000, 2500, 10], [1, 1, 1], 8, 2, 64, 16, maps=2, seed=21)]
+    want = [s.run() for s in states]
+    graphs = []
+    for s in states:
+        args = (i32(s.ind), i32(s.row_len), i32(s.table), s.P, s.qmax, s.scale)
+        H, D = s.q.shape[1], s.q.shape[-1]
+        ws = torch.empty(mla.decode_grouped_workspace_bytes(H, s.k.shape[1], s.qmax, D, s.maps == 2), dtype=torch.uint8).cuda()
+        out = torch.zeros((s.T, H, s.maps * D), dtype=BF).cuda()
+        lse = torch.zeros((s.T, H) + (2,) * (s.maps - 1)).cuda()
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            if s.maps == 1:
+                mla.decode_grouped(s.q, s.k, s.v, *args, out=out, lse=lse, workspace=ws)
+            else:
+                mla.decode_differential(s.q, s.k, s.v, s.lam, *args, out=out, lse=lse, workspace=ws)
+        graphs.append((g, out, lse, args))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(30):
+        for (g, *_), stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, out, lse, _), (o, l) in zip(graphs, want):
+        assert torch.equal(out, o) and torch.equal(lse, l)
+    assert mla.get_device_error() == 0
+
+
+def test_workspace_that_is_too_small_is_refused():
+    s = State([100], [1], 4, 2, 64, 16, seed=22)
+    with pytest.raises(mla.MLAError) as e:
+        s.run(workspace=torch.empty(64, dtype=torch.uint8).cuda())
+    assert e.value.status == mla.MLA_ERR_WORKSPACE
+
+
 def test_cache_past_32_bit_offsets():
     """A pool of more than 2^31 elements, the request's pages at its end."""
     bs, Hkv, D = 64, 8, 128
