@@ -783,6 +783,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           const bool mixed = !dead && (tok < edge_lo || tok >= edge_hi);
           if (__any_sync(0xffffffffu, dead || mixed)) {
             const uint32_t use = C::kNS * t;
+            // the slots' last values have been read: until then the parity could be theirs
+            if (t > 0) wait(smem_u32(&misc.o_done[sb ^ 1u]), ((t - 1) >> 1) & 1u);
 #pragma unroll
             for (int s = 0; s < C::kNS; ++s) wait(full_bar(v_slot<C>(use + s)), v_par<C>(use + s));
             bool zero = dead;
