@@ -190,6 +190,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
   }
   for (int b0 = 0; b0 < a->num_reqs; b0 += reqs) {
     p.num_reqs = a->num_reqs - b0 < reqs ? a->num_reqs - b0 : reqs;
+    p.first_req = b0;
     p.qo_indptr = a->qo_indptr + b0;
     p.subpage_table = a->subpage_table + static_cast<int64_t>(b0) * a->subpage_stride;
     // no more CTAs than there are chunks at the static bound; one chunk cuts no unit

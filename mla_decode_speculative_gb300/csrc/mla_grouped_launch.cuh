@@ -10,12 +10,13 @@ namespace mla {
 namespace grouped {
 
 // Merge of one cut unit: its parts are record 1 of the chunk with its first
-// tile and record 0 of the chunks after it.  A warp takes a row (both maps of
-// it): statistics with a lane per part, then the parts' outputs, 64 W values
-// over 32 lanes, weighted by 2^(m - M) / L.  Bound by latency: the first four
-// parts' outputs are read beside the statistics.
+// tile and record 0 of the chunks after it.  A warp takes a row's map:
+// statistics with a lane per part, then the parts' outputs, 64 W values over 32
+// lanes, weighted by 2^(m - M) / L; the difference of the maps and its norm go
+// through shared memory.  Bound by round trips, so the first parts' outputs are
+// read beside the statistics: with four of them and a warp per row 16 units of
+// ten parts took 5 us more than no merge, 24 differential ones of seven 6 us.
 constexpr int kMergeRows = 4;
-constexpr int kAhead = 4;
 
 template <int kV>
 __device__ __forceinline__ void load_row(const float *o, float (&v)[kV]) {
@@ -28,87 +29,95 @@ __device__ __forceinline__ void load_row(const float *o, float (&v)[kV]) {
 }
 
 template <int kW, int kMaps, int kNC>
-__global__ void __launch_bounds__(32 * kMergeRows) grouped_merge(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __grid_constant__ Params p) {
   constexpr int kNR = kNC / kMaps, kDv = 64 * kW, kV = kDv / 32;
-  __shared__ float weight[kMergeRows][kMaps][kMaxCtas];
+  constexpr int kAhead = kW == 4 ? 8 : 12;
+  __shared__ float weight[kMergeRows * kMaps][kMaxCtas];
+  __shared__ alignas(16) float other[kMergeRows][kMaps == 2 ? kDv : 4];
   grid_dep_wait();
   grid_dep_launch();
   const int first = static_cast<int>(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 u = *reinterpret_cast<const int4 *>(p.meta + first);  // q0, qlen, g, rb
   const int last = p.meta[first].last;
   if (last < 0) return;
-  const int parts = last - first + 1, c = static_cast<int>(blockIdx.y) * kMergeRows + warp;
+  const int m = kMaps == 2 ? warp & 1 : 0, slot = warp / kMaps;  // the warps of a row lie together
+  const int parts = last - first + 1, c = static_cast<int>(blockIdx.y) * kMergeRows + slot;
   int t, h;
-  if (c >= kNR || !column_row(p, u.w, c, u.y, t, h)) return;
+  const bool there = column_row(p, u.w, c, u.y, t, h);
+  if (!there) {
+    if (kMaps == 2) __syncthreads();
+    return;
+  }
   h += u.z * p.group;
   const int64_t row = (static_cast<int64_t>(u.x) + t) * p.num_heads + h;
   auto record = [&](int i) { return (static_cast<int64_t>(first) + i) * 2 + (i == 0 ? 1 : 0); };
-  float ahead[kMaps][kAhead][kV], top[kMaps], sum[kMaps], m0[kMaps], l0[kMaps];
+  const float *stats = p.part_stat + m * kNR + c;
+  const float *outs = p.part_o + (m * kNR + c) * kDv + lane * kV;
+  const float m0 = lane < parts ? stats[record(lane) * 2 * kNC] : kLowest;
+  const float l0 = lane < parts ? stats[record(lane) * 2 * kNC + kNC] : 0.0f;
+  float ahead[kAhead][kV], gain[kV], lam = 0.0f;
 #pragma unroll
-  for (int m = 0; m < kMaps; ++m) {
-    const float *stat = p.part_stat + record(lane) * 2 * kNC + m * kNR + c;
-    m0[m] = lane < parts ? stat[0] : kLowest;
-    l0[m] = lane < parts ? stat[kNC] : 0.0f;
+  for (int i = 0; i < kAhead; ++i)
+    if (i < parts) load_row<kV>(outs + record(i) * kNC * kDv, ahead[i]);
+  if (kMaps == 2) {
+    lam = p.lambda[h];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) gain[k] = p.gain != nullptr ? p.gain[lane * kV + k] : 1.0f;
+  }
+  float top = m0;
+  for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, stats[record(i) * 2 * kNC]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.0f;
+  for (int i = lane; i < parts; i += 32) {
+    const float mi = i < 32 ? m0 : stats[record(i) * 2 * kNC], li = i < 32 ? l0 : stats[record(i) * 2 * kNC + kNC];
+    const float w = li == 0.0f ? 0.0f : exp2f(mi - top);
+    weight[warp][i] = w;
+    sum += w * li;
   }
 #pragma unroll
-  for (int m = 0; m < kMaps; ++m)
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (i < parts) load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, ahead[m][i]);
-#pragma unroll
-  for (int m = 0; m < kMaps; ++m) {
-    top[m] = m0[m];
-    for (int i = lane + 32; i < parts; i += 32) top[m] = fmaxf(top[m], p.part_stat[record(i) * 2 * kNC + m * kNR + c]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top[m] = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], o));
-    sum[m] = 0.0f;
-    for (int i = lane; i < parts; i += 32) {
-      const float *stat = p.part_stat + record(i) * 2 * kNC + m * kNR + c;
-      const float mi = i < 32 ? m0[m] : stat[0], li = i < 32 ? l0[m] : stat[kNC];
-      const float w = li == 0.0f ? 0.0f : exp2f(mi - top[m]);
-      weight[warp][m][i] = w;
-      sum[m] += w * li;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], o);
-    if (lane == 0) p.lse[row * kMaps + m] = sum[m] == 0.0f ? -INFINITY : (top[m] + log2f(sum[m])) * kLn2;
-  }
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) p.lse[row * kMaps + m] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
   __syncwarp();
   float y[kV];
 #pragma unroll
-  for (int m = 0; m < kMaps; ++m) {
-    float acc[kV];
+  for (int k = 0; k < kV; ++k) y[k] = 0.0f;
+  // a part in which the row saw nothing holds no numbers
 #pragma unroll
-    for (int k = 0; k < kV; ++k) acc[k] = 0.0f;
-    // a part in which the row saw nothing holds no numbers
+  for (int i = 0; i < kAhead; ++i) {
+    const float w = i < parts ? weight[warp][i] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const float w = i < parts ? weight[warp][m][i] : 0.0f;
-#pragma unroll
-      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * ahead[m][i][k];
-    }
-#pragma unroll 4
-    for (int i = kAhead; i < parts; ++i) {
-      const float w = weight[warp][m][i];
-      float v[kV];
-      load_row<kV>(p.part_o + (record(i) * kNC + m * kNR + c) * kDv + lane * kV, v);
-#pragma unroll
-      for (int k = 0; k < kV; ++k) acc[k] += w == 0.0f ? 0.0f : w * v[k];
-    }
-    const float inv = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
-    const float by = m == 0 ? inv : -inv * p.lambda[h];
-#pragma unroll
-    for (int k = 0; k < kV; ++k) y[k] = m == 0 ? acc[k] * by : y[k] + acc[k] * by;
+    for (int k = 0; k < kV; ++k) y[k] += w == 0.0f ? 0.0f : w * ahead[i][k];
   }
-  if (kMaps == 2 && p.gain != nullptr) {
-    float sq = 0.0f;
+#pragma unroll 4
+  for (int i = kAhead; i < parts; ++i) {
+    const float w = weight[warp][i];
+    float v[kV];
+    load_row<kV>(outs + record(i) * kNC * kDv, v);
 #pragma unroll
-    for (int k = 0; k < kV; ++k) sq += y[k] * y[k];
+    for (int k = 0; k < kV; ++k) y[k] += w == 0.0f ? 0.0f : w * v[k];
+  }
+  const float by = (sum == 0.0f ? 0.0f : 1.0f / sum) * (m == 1 ? lam : 1.0f);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    const float norm = rsqrtf(sq * (1.0f / kDv) + p.eps);
+  for (int k = 0; k < kV; ++k) y[k] *= by;
+  if (kMaps == 2) {
+    if (m == 1)
 #pragma unroll
-    for (int k = 0; k < kV; ++k) y[k] = sum[0] == 0.0f ? 0.0f : y[k] * norm * p.gain[lane * kV + k];
+      for (int k = 0; k < kV; ++k) other[slot][lane * kV + k] = y[k];
+    __syncthreads();
+    if (m == 1) return;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) y[k] -= other[slot][lane * kV + k];
+    if (p.gain != nullptr) {
+      float sq = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) sq += y[k] * y[k];
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      const float norm = rsqrtf(sq * (1.0f / kDv) + p.eps);
+#pragma unroll
+      for (int k = 0; k < kV; ++k) y[k] = sum == 0.0f ? 0.0f : y[k] * norm * gain[k];
+    }
   }
   uint32_t packed[kV / 2];
 #pragma unroll
@@ -135,7 +144,7 @@ mla_status launch_as(const CUtensorMap &q, const CUtensorMap &k, const CUtensorM
   e = launch_pdl(grouped_kernel<kW, kMaps, kNC>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, q, k, v, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped launch");
   if (!merge) return MLA_OK;
-  e = launch_pdl(grouped_merge<kW, kMaps, kNC>, dim3(grid, C::kNR / kMergeRows), dim3(32 * kMergeRows), 0, stream, p);
+  e = launch_pdl(grouped_merge<kW, kMaps, kNC>, dim3(grid, C::kNR / kMergeRows), dim3(32 * kMergeRows * kMaps), 0, stream, p);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "grouped merge launch");
 }
 
