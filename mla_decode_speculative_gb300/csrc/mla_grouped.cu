@@ -10,12 +10,11 @@ namespace grouped {
 namespace {
 
 // Columns of the products: the fewest of 16, 32, 64 that hold a request's rows
-// of a group (differential: 16 or 32 of each map).  64 columns of 256 dims leave
-// no room for the ring: such rows go in blocks of 32.
+// of a group (differential: 16 or 32 of each map).
 int columns_of(const mla_grouped_args &a, bool differential) {
   const int64_t rows = static_cast<int64_t>(a.max_qlen) * (a.num_heads / a.num_kv_heads);
   if (differential) return rows <= 16 ? 32 : 64;
-  return rows <= 16 ? 16 : (rows <= 32 || a.head_dim == 256 ? 32 : 64);
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
 }
 
 struct Layout {

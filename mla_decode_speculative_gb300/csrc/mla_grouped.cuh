@@ -116,7 +116,8 @@ struct Config {
   static constexpr int kPAtoms = kPN <= 64 ? 1 : 2; // of 64 columns
   static constexpr int kPBytes = kPAtoms * kTile * 128;
   static constexpr int kMiscBytes = 14 * 1024;
-  static constexpr int kFit = (232448 - 1024 - kMiscBytes - kQBufs * kQBytes - 2 * kPBytes) / kSlotBytes;
+  static constexpr int kPBufs = kW == 4 && kNR == 64 ? 1 : 2;  // where two leave no room for a key and a value tile
+  static constexpr int kFit = (232448 - 1024 - kMiscBytes - kQBufs * kQBytes - kPBufs * kPBytes) / kSlotBytes;
   static constexpr int kSlots = kFit > 10 ? 10 : kFit;
   static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;  // values wait for the softmax
   static constexpr int kGroups = kNC > 32 ? 2 : 1;  // groups of four softmax warps
@@ -129,7 +130,7 @@ struct Config {
   static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : (kTmemUsed <= 128 ? 128 : (kTmemUsed <= 256 ? 256 : 512));
   static constexpr int kOffQ = kSlots * kSlotBytes;
   static constexpr int kOffP = kOffQ + kQBufs * kQBytes;
-  static constexpr int kOffMisc = kOffP + 2 * kPBytes;
+  static constexpr int kOffMisc = kOffP + kPBufs * kPBytes;
   static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;
   static_assert(kTmemUsed <= 512 && kNR % 16 == 0 && kKSlots >= kNS && kSmem <= 232448, "configuration");
 };
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           if (!wait(smem_u32(&misc.p_full[t & 1u]), (t >> 1) & 1u)) break;
           const int tok = (w.tile0 + i) * kTile;
           const int k0 = max(w.lo - tok, 0) / 16, k1 = (min(w.hi - tok, kTile) + 15) / 16;
-          const uint64_t dp = d_p + (t & 1u) * (C::kPBytes >> 4);
+          const uint64_t dp = d_p + (t % C::kPBufs) * (C::kPBytes >> 4);
 #pragma unroll
           for (int s = 0; s < C::kBlocks; ++s) {
             const uint32_t use = C::kNS * t + s, slot = v_slot<C>(use);
@@ -776,8 +777,9 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           hi[c / 2] = u;
           lo[c / 2] = pack_bf16(p0 - __uint_as_float(u << 16), p1 - __uint_as_float(u & 0xffff0000u));
         }
-        if (t >= 2) wait(smem_u32(&misc.o_done[sb]), ((t - 2) >> 1) & 1u);  // P of tile t - 2 has been read
-        const uint32_t prow = s_p + sb * C::kPBytes + row * 128;
+        // the P^T that this one overwrites has been read
+        if (t >= C::kPBufs) wait(smem_u32(&misc.o_done[(t - C::kPBufs) & 1u]), ((t - C::kPBufs) >> 1) & 1u);
+        const uint32_t prow = s_p + (t % C::kPBufs) * C::kPBytes + row * 128;
 #pragma unroll
         for (int j = 0; j < N / 8; ++j) {
           st_shared_v4(prow + (((col0 / 8 + j) ^ (row & 7)) * 16), hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);

@@ -18,7 +18,8 @@ mla_status launch_grouped(int W, int nc, const CUtensorMap &q, const CUtensorMap
     return launch_as<2, 1, 64>(q, k, v, p, grid, merge, stream);
   }
   if (nc == 16) return launch_as<4, 1, 16>(q, k, v, p, grid, merge, stream);
-  return launch_as<4, 1, 32>(q, k, v, p, grid, merge, stream);
+  if (nc == 32) return launch_as<4, 1, 32>(q, k, v, p, grid, merge, stream);
+  return launch_as<4, 1, 64>(q, k, v, p, grid, merge, stream);
 }
 
 }  // namespace grouped

@@ -374,7 +374,7 @@ def test_strides_of_queries_and_caches():
 
 @pytest.mark.parametrize("maps,D,H,Hkv,L,n", [
     (1, 64, 16, 4, [5000, 120, 1, 2222], 2), (2, 64, 16, 4, [5000, 120, 1, 2222], 2), (1, 256, 12, 4, [623] * 60, 1),
-    (1, 256, 40, 4, [562] * 35, 4), (2, 128, 56, 8, [562] * 35, 4), (2, 128, 7, 1, [100 + 37 * i for i in range(60)], 3),
+    (1, 256, 24, 4, [562] * 35, 4), (1, 256, 40, 4, [562] * 35, 4), (2, 128, 56, 8, [562] * 35, 4), (2, 128, 7, 1, [100 + 37 * i for i in range(60)], 3),
     (1, 128, 64, 2, [300 + 11 * i for i in range(40)], 2)])
 def test_repeats_itself_bit_by_bit(maps, D, H, Hkv, L, n):
     """Many units that end inside a tile, so that their last values are cleared while the tile before is still
