@@ -115,7 +115,7 @@ struct Config {
   static constexpr int kPN = 2 * kNC;               // columns of P^T: both terms
   static constexpr int kPAtoms = kPN <= 64 ? 1 : 2; // of 64 columns
   static constexpr int kPBytes = kPAtoms * kTile * 128;
-  static constexpr int kMiscBytes = 14 * 1024;
+  static constexpr int kMiscBytes = 15 * 1024;
   static constexpr int kPBufs = kW == 4 && kNR == 64 ? 1 : 2;  // where two leave no room for a key and a value tile
   static constexpr int kFit = (232448 - 1024 - kMiscBytes - kQBufs * kQBytes - kPBufs * kPBytes) / kSlotBytes;
   static constexpr int kSlots = kFit > 10 ? 10 : kFit;
@@ -146,24 +146,30 @@ __device__ __forceinline__ int tiles_of(const int4 &req) {
   return req.y > req.x ? (req.y + kTile - 1) / kTile - req.x / kTile : 0;
 }
 
+// What the softmax warps share about a part's columns.
+struct Columns {
+  alignas(16) float stat_m[64], stat_l[64], inv[64];
+  int lo[64], hi[64];  // tokens that a column sees
+  int row[64];         // its row of out (row * H + head), -1: none
+  float lam[64];
+  unsigned bad[2];     // columns of a group of warps that see a value that is not finite
+  int stop;            // the role ends here (a wait ran out)
+};
+
 struct Misc {
   uint64_t full[10], empty[10];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2], fin[2];
   uint32_t tmem_base;
-  int abort, stop[2];
+  int abort;
   uint32_t armed[10], q_armed[2];         // 1 + the parity of the last use of a slot (or Q buffer) that a copy was issued for
   int start[kMaxReqs + 1];                // positions before request b
   int4 req[kMaxReqs];                     // tokens that some row of the request sees (x .. y - 1), first row, rows
   Place place;                            // where this chunk begins
   alignas(16) float red[2][4][32];        // [group of warps][warp][column]
-  alignas(16) float stat_m[64], stat_l[64], inv[64];
-  int col_lo[64], col_hi[64];             // what a column of this part sees
-  int col_row[64];                        // its row of out (row * H + head), -1: none
-  float col_lam[64];
-  unsigned bad[2];                        // columns of a group that see a value that is not finite
+  Columns cols[2];                        // of the even and odd parts
 };
-static_assert(sizeof(Misc) <= 14 * 1024, "misc");
+static_assert(sizeof(Misc) <= 15 * 1024, "misc");
 
 // A part: the tiles a .. e - 1 (of n) of a unit that lie in this chunk.
 struct Part {
@@ -391,7 +397,6 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       mbar_init(smem_u32(&misc.o_done[i]), 1);
       mbar_init(smem_u32(&misc.fin[i]), 1);
       misc.q_armed[i] = 0;
-      misc.bad[i] = 0;
     }
     misc.abort = 0;
     misc.place = Place{0, 0, 0, INT32_MAX, 0, 0};  // a chunk without positions
@@ -665,34 +670,42 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     Meta meta{0, 0, 0, 0, -1, {}};
     Walk walk(p, misc, pos_a, pos_e);
     Part w;
+    const int my_col = col0 + lane % N;
+    bool valid = false;
+    int my_lo = 0, my_hi = 0, ct = 0, ch = 0, cur_b = -1, cur_rb = -1;
     while (walk.next(w)) {
-      // what this lane's column sees
-      int my_lo = 0, my_hi = 0, ct, ch;
-      const int my_col = col0 + lane % N;
-      const bool valid = column_row(p, w.rb, my_col % C::kNR, w.qlen, ct, ch);
-      if (valid) {
-        my_hi = min(max(p.row_len[w.q0 + ct], 0), p.max_len);
+      Columns &cols = misc.cols[n_part & 1];
+      ++n_part;
+      // what this lane's column sees; the groups of a request see the same
+      if (w.b != cur_b || w.rb != cur_rb) {
+        cur_b = w.b;
+        cur_rb = w.rb;
+        valid = column_row(p, w.rb, my_col % C::kNR, w.qlen, ct, ch);
+        my_hi = valid ? min(max(p.row_len[w.q0 + ct], 0), p.max_len) : 0;
         my_lo = p.window > 0 ? max(0, my_hi - p.window) : 0;
       }
       if (wq == 0 && lane < N) {
-        misc.col_lo[my_col] = my_lo;
-        misc.col_hi[my_col] = my_hi;
-        misc.col_row[my_col] = valid ? (w.q0 + ct) * p.num_heads + w.g * p.group + ch : -1;
-        if (kMaps == 2) misc.col_lam[my_col] = valid ? p.lambda[w.g * p.group + ch] : 0.0f;
+        cols.lo[my_col] = my_lo;
+        cols.hi[my_col] = my_hi;
+        cols.row[my_col] = valid ? (w.q0 + ct) * p.num_heads + w.g * p.group + ch : -1;
+        if (kMaps == 2) cols.lam[my_col] = valid ? p.lambda[w.g * p.group + ch] : 0.0f;
+      }
+      // What the columns hold is one buffer for the even parts and one for the
+      // odd: a part's is written again only behind the next part's barrier here.
+      if (threadIdx.x == 0) {
+        cols.bad[0] = cols.bad[1] = 0;
+        cols.stop = *abort_flag;
       }
       named_bar_sync(all_bar, kSoftmaxThreads);
-      if (threadIdx.x == 0) misc.stop[n_part & 1] = *abort_flag;
-      named_bar_sync(all_bar, kSoftmaxThreads);
-      if (misc.stop[n_part & 1]) break;
-      ++n_part;
+      if (cols.stop) break;
       // tokens that this group's columns all see (all_lo .. all_hi - 1), and
       // that all columns see that see anything (edge_lo .. edge_hi - 1)
       int all_lo = valid ? my_lo : 0, all_hi = valid ? my_hi : INT32_MAX;
       int edge_lo = 0, edge_hi = INT32_MAX;
       for (int c = lane; c < kNC; c += 32)
-        if (misc.col_hi[c] > 0) {
-          edge_lo = max(edge_lo, misc.col_lo[c]);
-          edge_hi = min(edge_hi, misc.col_hi[c]);
+        if (cols.hi[c] > 0) {
+          edge_lo = max(edge_lo, cols.lo[c]);
+          edge_hi = min(edge_hi, cols.hi[c]);
         }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) {
@@ -817,7 +830,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
               if (odd) {
                 zero = true;
                 for (int c = 0; c < kNC; ++c)
-                  if (tok >= misc.col_lo[c] && tok < misc.col_hi[c]) atomicOr(&misc.bad[c / N], 1u << (c % N));
+                  if (tok >= cols.lo[c] && tok < cols.hi[c]) atomicOr(&cols.bad[c / N], 1u << (c % N));
               }
             }
             if (zero)
@@ -845,18 +858,18 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       if (wq == 0 && lane == 0) {
 #pragma unroll
         for (int c = 0; c < N; c += 4)
-          *reinterpret_cast<float4 *>(misc.stat_m + col0 + c) = make_float4(m[c], m[c + 1], m[c + 2], m[c + 3]);
+          *reinterpret_cast<float4 *>(cols.stat_m + col0 + c) = make_float4(m[c], m[c + 1], m[c + 2], m[c + 3]);
       }
       named_bar_sync(grp_bar, 128);
       if (wq == 0 && lane < N) {
         const float l = misc.red[grp][0][lane] + misc.red[grp][1][lane] + misc.red[grp][2][lane] + misc.red[grp][3][lane];
-        const bool bad = (misc.bad[grp] >> lane) & 1u;
-        misc.stat_l[my_col] = l;
+        const bool bad = (cols.bad[grp] >> lane) & 1u;
+        cols.stat_l[my_col] = l;
         // 0: the row saw nothing, and what its column of O^T holds is not looked at
-        misc.inv[my_col] = l == 0.0f ? 0.0f : (bad ? __int_as_float(0x7fffffff) : 1.0f / l);
+        cols.inv[my_col] = l == 0.0f ? 0.0f : (bad ? __int_as_float(0x7fffffff) : 1.0f / l);
         if (w.a == 0 && w.e == w.n && valid) {
-          const int64_t at = static_cast<int64_t>(misc.col_row[my_col]) * kMaps + my_col / C::kNR;
-          p.lse[at] = l == 0.0f ? -INFINITY : (misc.stat_m[my_col] + log2f(l)) * kLn2;
+          const int64_t at = static_cast<int64_t>(cols.row[my_col]) * kMaps + my_col / C::kNR;
+          p.lse[at] = l == 0.0f ? -INFINITY : (cols.stat_m[my_col] + log2f(l)) * kLn2;
         }
       }
       named_bar_sync(all_bar, kSoftmaxThreads);
@@ -877,8 +890,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       if (!whole) {
         const int64_t rec = static_cast<int64_t>(chunk) * 2 + (w.a == 0 ? 1 : 0);
         if (wq == 0 && lane < N) {
-          p.part_stat[rec * 2 * kNC + my_col] = misc.stat_m[my_col];
-          p.part_stat[rec * 2 * kNC + kNC + my_col] = misc.stat_l[my_col];
+          p.part_stat[rec * 2 * kNC + my_col] = cols.stat_m[my_col];
+          p.part_stat[rec * 2 * kNC + kNC + my_col] = cols.stat_l[my_col];
         }
         float *po = p.part_o + rec * kNC * C::kDv;
 #pragma unroll
@@ -889,8 +902,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
             load_o(s, col0 + h, o);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const float y = misc.inv[col0 + h + c];
-              store_if(has_dim && misc.col_row[col0 + h + c] >= 0, po + (col0 + h + c) * C::kDv + 128 * s + dim,
+              const float y = cols.inv[col0 + h + c];
+              store_if(has_dim && cols.row[col0 + h + c] >= 0, po + (col0 + h + c) * C::kDv + 128 * s + dim,
                        isnan(y) ? y : o[c]);
             }
           }
@@ -904,8 +917,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
             load_o(s, col0 + h, o);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const int at = misc.col_row[col0 + h + c];
-              const float by = misc.inv[col0 + h + c];
+              const int at = cols.row[col0 + h + c];
+              const float by = cols.inv[col0 + h + c];
               store_if(at >= 0 && has_dim, p.out + static_cast<int64_t>(at) * C::kDv + 128 * s + dim,
                        by == 0.0f ? 0.0f : o[c] * by);
             }
@@ -924,8 +937,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           load_o(s, C::kNR + r0, o);
 #pragma unroll
           for (int c = 0; c < R; ++c) {
-            const float i0 = misc.inv[r0 + c], i1 = misc.inv[C::kNR + r0 + c];
-            y[s][c] = (i0 == 0.0f ? 0.0f : y[s][c] * i0) - misc.col_lam[r0 + c] * (i1 == 0.0f ? 0.0f : o[c] * i1);
+            const float i0 = cols.inv[r0 + c], i1 = cols.inv[C::kNR + r0 + c];
+            y[s][c] = (i0 == 0.0f ? 0.0f : y[s][c] * i0) - cols.lam[r0 + c] * (i1 == 0.0f ? 0.0f : o[c] * i1);
             sq[c] += y[s][c] * y[s][c];
           }
         }
@@ -947,15 +960,13 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           const float gain = p.gain != nullptr ? p.gain[128 * s + dim] : 1.0f;
 #pragma unroll
           for (int c = 0; c < R; ++c) {
-            const int at = misc.col_row[r0 + c];
+            const int at = cols.row[r0 + c];
             store_if(at >= 0, p.out + static_cast<int64_t>(at) * C::kDv + 128 * s + dim,
-                     misc.inv[r0 + c] == 0.0f ? 0.0f : y[s][c] * norm[c] * gain);
+                     cols.inv[r0 + c] == 0.0f ? 0.0f : y[s][c] * norm[c] * gain);
           }
         }
       }
       tc_fence_before();
-      named_bar_sync(all_bar, kSoftmaxThreads);  // statistics and flags have been read
-      if (threadIdx.x < 2) misc.bad[threadIdx.x] = 0;
     }
     if (threadIdx.x == 0) p.meta[chunk] = meta;
   }
