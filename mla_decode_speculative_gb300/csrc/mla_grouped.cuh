@@ -29,8 +29,8 @@
 //    into equal chunks, one per SM.  A chunk holds at most two units that it
 //    does not hold whole: its first and its last.  So there are two partial
 //    records per SM, whatever the batch, and the merge looks at 152 chunks.
-//  * Softmax: a thread has one token and all columns of its group of warps (32
-//    at most), in registers.  The reference maximum moves only when a score
+//  * Softmax: a thread has one token and the 16 columns of its group of warps (32
+//    of 64), in registers.  The reference maximum moves only when a score
 //    passes it by 2^8; sums are float32 per thread and column.  A probability goes
 //    to the product as two bf16 terms (2^-16 of itself), the second as further
 //    columns of N, which cost the tensor cores nothing up to N = 64.
@@ -115,13 +115,13 @@ struct Config {
   static constexpr int kPN = 2 * kNC;               // columns of P^T: both terms
   static constexpr int kPAtoms = kPN <= 64 ? 1 : 2; // of 64 columns
   static constexpr int kPBytes = kPAtoms * kTile * 128;
-  static constexpr int kMiscBytes = 15 * 1024;
+  static constexpr int kMiscBytes = 16 * 1024;
   static constexpr int kPBufs = kW == 4 && kNR == 64 ? 1 : 2;  // where two leave no room for a key and a value tile
   static constexpr int kFit = (232448 - 1024 - kMiscBytes - kQBufs * kQBytes - kPBufs * kPBytes) / kSlotBytes;
   static constexpr int kSlots = kFit > 10 ? 10 : kFit;
   static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;  // values wait for the softmax
-  static constexpr int kGroups = kNC > 32 ? 2 : 1;  // groups of four softmax warps
-  static constexpr int kCols = kNC / kGroups;       // columns of a group
+  static constexpr int kCols = kNC < 64 ? 16 : 32;  // columns of a group of four softmax warps
+  static constexpr int kGroups = kNC / kCols;
   static constexpr int kSoftmaxWarps = 4 * kGroups;
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kBlocks = kW < 2 ? 1 : kW / 2;  // blocks of O^T: 128 dims each (64 if W = 1)
@@ -146,6 +146,28 @@ __device__ __forceinline__ int tiles_of(const int4 &req) {
   return req.y > req.x ? (req.y + kTile - 1) / kTile - req.x / kTile : 0;
 }
 
+// A part: the tiles a .. e - 1 (of n) of a unit that lie in this chunk.
+struct Part {
+  int b, g, rb;   // request, group, row block
+  int q0, qlen;
+  int lo, hi;     // tokens the request sees
+  int tile0;      // tile index of the unit's tile 0
+  int a, e, n;
+  int start;      // position of the unit
+};
+
+struct Misc;
+
+// Goes over a chunk's parts in order.  The issuing roles have one each; the
+// softmax warps' is in shared memory (in registers it made them spill).
+struct Walk {
+  int pos_a, pos_e;  // the chunk
+  int b, g, rb, s, per, blocks;
+  int4 req;
+  __device__ __forceinline__ void begin(const Misc &m, int a, int e);
+  __device__ __forceinline__ bool next(const Params &p, const Misc &m, Part &o);
+};
+
 // What the softmax warps share about a part's columns.
 struct Columns {
   alignas(16) float stat_m[64], stat_l[64], inv[64];
@@ -153,6 +175,8 @@ struct Columns {
   int row[64];         // its row of out (row * H + head), -1: none
   float lam[64];
   unsigned bad[2];     // columns of a group of warps that see a value that is not finite
+  Part part;           // the part itself
+  int more;            // there is one
   int stop;            // the role ends here (a wait ran out)
 };
 
@@ -165,72 +189,47 @@ struct Misc {
   uint32_t armed[10], q_armed[2];         // 1 + the parity of the last use of a slot (or Q buffer) that a copy was issued for
   int start[kMaxReqs + 1];                // positions before request b
   int4 req[kMaxReqs];                     // tokens that some row of the request sees (x .. y - 1), first row, rows
+  Walk walk;                              // the softmax warps'
   Place place;                            // where this chunk begins
   alignas(16) float red[2][4][32];        // [group of warps][warp][column]
   Columns cols[2];                        // of the even and odd parts
 };
-static_assert(sizeof(Misc) <= 15 * 1024, "misc");
+static_assert(sizeof(Misc) <= 16 * 1024, "misc");
 
-// A part: the tiles a .. e - 1 (of n) of a unit that lie in this chunk.
-struct Part {
-  int b, g, rb;   // request, group, row block
-  int q0, qlen;
-  int lo, hi;     // tokens the request sees
-  int tile0;      // tile index of the unit's tile 0
-  int a, e, n;
-  int start;      // position of the unit
-};
+__device__ __forceinline__ void Walk::begin(const Misc &m, int a, int e) {
+  pos_a = a;
+  pos_e = e;
+  b = m.place.b;
+  g = m.place.g;
+  rb = m.place.rb;
+  s = m.place.s;
+  per = m.place.per;
+  blocks = m.place.blocks;
+  req = m.req[b];
+}
 
-// Goes over a chunk's parts in order; every role has its own.
-struct Walk {
-  const Params &p;
-  const Misc &m;
-  int pos_a, pos_e;  // the chunk
-  int b, g, rb, s, per, blocks;
-  int4 req;
-  __device__ __forceinline__ Walk(const Params &p_, const Misc &m_, int a, int e) : p(p_), m(m_), pos_a(a), pos_e(e) {
-    b = m.place.b;
-    g = m.place.g;
-    rb = m.place.rb;
-    s = m.place.s;
-    per = m.place.per;
-    blocks = m.place.blocks;
-    req = m.req[b];
-  }
-  __device__ __forceinline__ bool next(Part &o) {
-    while (s < pos_e) {
-      const int first = s + kOverhead, n = per - kOverhead;
-      o.a = max(pos_a - first, 0);
-      o.e = min(pos_e - first, n);
-      const bool take = n > 0 ? o.e > o.a : s >= pos_a;
-      o.b = b;
-      o.g = g;
-      o.rb = rb;
-      o.lo = req.x;
-      o.hi = req.y;
-      o.q0 = req.z;
-      o.qlen = req.w;
-      o.tile0 = o.lo / kTile;
-      o.n = n;
-      o.start = s;
-      if (n == 0) o.a = o.e = 0;
-      s += per;
-      if (++rb == blocks) {
-        rb = 0;
-        if (++g == p.num_kv_heads && s < pos_e) {  // the next request that has rows
-          g = 0;
-          do ++b;
-          while (m.start[b + 1] <= s);
-          req = m.req[b];
-          blocks = p.one_block ? 1 : blocks_of(p, req.w);
-          per = tiles_of(req) + kOverhead;
-        }
+__device__ __forceinline__ bool Walk::next(const Params &p, const Misc &m, Part &o) {
+  while (s < pos_e) {
+    const int first = s + kOverhead, n = per - kOverhead;
+    const int a = max(pos_a - first, 0), e = min(pos_e - first, n);
+    const bool take = n > 0 ? e > a : s >= pos_a;
+    if (take) o = Part{b, g, rb, req.z, req.w, req.x, req.y, req.x / kTile, n == 0 ? 0 : a, n == 0 ? 0 : e, n, s};
+    s += per;
+    if (++rb == blocks) {
+      rb = 0;
+      if (++g == p.num_kv_heads && s < pos_e) {  // the next request that has rows
+        g = 0;
+        do ++b;
+        while (m.start[b + 1] <= s);
+        req = m.req[b];
+        blocks = p.one_block ? 1 : blocks_of(p, req.w);
+        per = tiles_of(req) + kOverhead;
       }
-      if (take) return true;
     }
-    return false;
+    if (take) return true;
   }
-};
+  return false;
+}
 
 // Slot of the u-th use of the keys' ring, or of the values' ring behind it (each
 // in order of its own copies and products), and the parity of that use.
@@ -511,10 +510,11 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     }
     const int shift = p.page_shift, pages = kTile >> shift, groups = 1 << (shift - 3);
     const uint32_t page_bytes = (128u * C::kCW) << shift;
-    Walk walk(p, misc, pos_a, pos_e);
+    Walk walk;
+    walk.begin(misc, pos_a, pos_e);
     Part w;
     uint32_t t = 0, kq = 0;
-    while (ok && walk.next(w)) {
+    while (ok && walk.next(p, misc, w)) {
       if (w.e == w.a) continue;
       // a lane holds a page of the tile, and reads the next tile's ahead of the waits
       const int32_t *ids = p.subpage_table + static_cast<int64_t>(w.b) * p.subpage_stride;
@@ -577,10 +577,11 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       constexpr uint32_t idesc = idesc_bf16_f32(128, C::kNR, 0, 0);
       const uint64_t d_k = sdesc_sw128(s_slots, 0, C::kCW * 1024);  // tokens: groups of 8
       const uint64_t d_q = sdesc_sw128(s_q, 0, 1024);
-      Walk walk(p, misc, pos_a, pos_e);
+      Walk walk;
+      walk.begin(misc, pos_a, pos_e);
       Part w;
       uint32_t t = 0, kq = 0;
-      while (ok && walk.next(w)) {
+      while (ok && walk.next(p, misc, w)) {
         if (w.e == w.a) continue;
         const uint32_t qb = kq % C::kQBufs;
         if (!wait(smem_u32(&misc.q_full[qb]), (kq / C::kQBufs) & 1u)) break;
@@ -622,10 +623,11 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       constexpr uint32_t idesc = idesc_bf16_f32(kW < 2 ? 64 : 128, C::kPN, 1, 1);
       const uint64_t d_v = sdesc_sw128(s_slots, 1024, C::kCW * 1024);      // dims: chunks; tokens: groups of 8
       const uint64_t d_p = sdesc_sw128(s_p, C::kPBytes / C::kPAtoms, 1024);  // columns: atoms of 64
-      Walk walk(p, misc, pos_a, pos_e);
+      Walk walk;
+      walk.begin(misc, pos_a, pos_e);
       Part w;
       uint32_t t = 0;
-      while (ok && walk.next(w)) {
+      while (ok && walk.next(p, misc, w)) {
         for (int i = w.a; i < w.e; ++i, ++t) {
           if (!wait(smem_u32(&misc.p_full[t & 1u]), (t >> 1) & 1u)) break;
           const int tok = (w.tile0 + i) * kTile;
@@ -666,16 +668,19 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     const int row = wq * 32 + lane;                // token of the tile; lane of TMEM
     const uint32_t grp_bar = 1 + grp, all_bar = 3;
     uint32_t t = 0;
-    int n_part = 0;
     Meta meta{0, 0, 0, 0, -1, {}};
-    Walk walk(p, misc, pos_a, pos_e);
-    Part w;
     const int my_col = col0 + lane % N;
     bool valid = false;
     int my_lo = 0, my_hi = 0, ct = 0, ch = 0, cur_b = -1, cur_rb = -1;
-    while (walk.next(w)) {
+    if (threadIdx.x == 0) {
+      misc.walk.begin(misc, pos_a, pos_e);
+      misc.cols[0].more = misc.walk.next(p, misc, misc.cols[0].part);
+    }
+    named_bar_sync(all_bar, kSoftmaxThreads);
+    for (int n_part = 0;; ++n_part) {
       Columns &cols = misc.cols[n_part & 1];
-      ++n_part;
+      if (!cols.more) break;
+      const Part &w = cols.part;
       // what this lane's column sees; the groups of a request see the same
       if (w.b != cur_b || w.rb != cur_rb) {
         cur_b = w.b;
@@ -690,14 +695,18 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         cols.row[my_col] = valid ? (w.q0 + ct) * p.num_heads + w.g * p.group + ch : -1;
         if (kMaps == 2) cols.lam[my_col] = valid ? p.lambda[w.g * p.group + ch] : 0.0f;
       }
-      // What the columns hold is one buffer for the even parts and one for the
-      // odd: a part's is written again only behind the next part's barrier here.
+      // The even parts have one buffer and the odd parts the other: a part's is
+      // written again only behind the next part's barrier here.
       if (threadIdx.x == 0) {
         cols.bad[0] = cols.bad[1] = 0;
         cols.stop = *abort_flag;
       }
       named_bar_sync(all_bar, kSoftmaxThreads);
       if (cols.stop) break;
+      if (threadIdx.x == 0) {  // read behind the barrier of this part's result
+        Columns &then = misc.cols[(n_part + 1) & 1];
+        then.more = misc.walk.next(p, misc, then.part);
+      }
       // tokens that this group's columns all see (all_lo .. all_hi - 1), and
       // that all columns see that see anything (edge_lo .. edge_hi - 1)
       int all_lo = valid ? my_lo : 0, all_hi = valid ? my_hi : INT32_MAX;
@@ -923,8 +932,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
                        by == 0.0f ? 0.0f : o[c] * by);
             }
           }
-      } else {
-        // 16 rows of both maps per group of warps
+      } else if (grp * 16 < C::kNR) {
+        // 16 rows of both maps per group of warps, of the first half of them
         constexpr int R = 16;
         const int r0 = grp * R;
         float y[C::kBlocks][R], sq[R];
