@@ -546,8 +546,8 @@ size_t mla_decode_grouped_workspace(const mla_grouped_args *a, int differential)
  *   out[r,h,:] = sum_j softmax(s)_j v[j,g,:],  lse[r,h] = ln sum_j e^{s_j}.
  * A row that sees nothing gives out = 0 and lse = -inf.  Rows from
  * qo_indptr[B] on are left as they were.  Scores, softmax sums and outputs are
- * held in float32; probabilities are rounded to bf16 for the product with the
- * values (2^-9 relative each, 2^-8 at most), and so is the result.
+ * held in float32; a probability goes to the product with the values as two
+ * bf16 terms (2^-16 of itself), the result is rounded to bf16.
  * q, k_cache and v_cache are 16-byte aligned with rows a multiple of 8
  * elements apart; num_cache_rows is a multiple of 8.
  * Keys and values that no row of a request sees are never used as numbers.  A

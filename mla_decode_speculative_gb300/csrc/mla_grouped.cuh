@@ -171,7 +171,7 @@ struct Walk {
 // What the softmax warps share about a part's columns.
 struct Columns {
   alignas(16) float stat_m[64], stat_l[64], inv[64];
-  int lo[64], hi[64];  // tokens that a column sees
+  alignas(16) int lo[64], hi[64];  // tokens that a column sees
   int row[64];         // its row of out (row * H + head), -1: none
   float lam[64];
   unsigned bad[2];     // columns of a group of warps that see a value that is not finite
@@ -358,6 +358,24 @@ __device__ __forceinline__ float reduce_columns(float (&v)[N], int lane) {
     v[0] = kMax ? fmaxf(v[0], recv) : v[0] + recv;
   }
   return v[0];
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 constexpr float kLowest = -3.402823466e38f;  // a column that has seen nothing yet
@@ -723,43 +741,62 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         edge_lo = max(edge_lo, __shfl_xor_sync(0xffffffffu, edge_lo, o));
         edge_hi = min(edge_hi, __shfl_xor_sync(0xffffffffu, edge_hi, o));
       }
-      float m[N], sum[N];
+      uint64_t less[N / 2], sum[N / 2];  // minus the reference maximum, and this thread's sum, of two columns each
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        m[c] = kLowest;
-        sum[c] = 0.0f;
+      for (int c = 0; c < N / 2; ++c) {
+        less[c] = pair(-kLowest, -kLowest);
+        sum[c] = 0;
       }
+      const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), minus2 = pair(-1.0f, -1.0f);
       for (int i = w.a; i < w.e; ++i, ++t) {
         const uint32_t sb = t & 1u;
         const int tok0 = (w.tile0 + i) * kTile, tok = tok0 + row;
         wait(smem_u32(&misc.s_full[sb]), (t >> 1) & 1u);
         tc_fence_after();
-        float x[N];
-        tmem_load<N>(tmem + lane_addr + sb * kNC + col0, x);
-        const bool masked = tok0 < all_lo || tok0 + kTile > all_hi;
-        float top = -INFINITY;
-        if (!masked) {
+        float x[N];  // scores, base 2, less the reference maximum
+        const uint32_t s_addr = tmem + lane_addr + sb * kNC + col0;
+        tmem_load<N>(s_addr, x);
+        uint32_t sees = 0xffffffffu;  // columns that see this thread's token
+        if (tok0 < all_lo || tok0 + kTile > all_hi) {
+          sees = 0;
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
-            x[c] *= p.scale_log2;
-            top = fmaxf(top, x[c] - m[c]);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < N; ++c) {
-            const int lo = __shfl_sync(0xffffffffu, my_lo, c), hi = __shfl_sync(0xffffffffu, my_hi, c);
-            x[c] = tok >= lo && tok < hi ? x[c] * p.scale_log2 : -INFINITY;
-            top = fmaxf(top, x[c] - m[c]);
+          for (int c = 0; c < N; c += 4) {
+            const int4 lo = *reinterpret_cast<const int4 *>(cols.lo + col0 + c), hi = *reinterpret_cast<const int4 *>(cols.hi + col0 + c);
+            sees |= (tok >= lo.x && tok < hi.x ? 1u << c : 0u) | (tok >= lo.y && tok < hi.y ? 2u << c : 0u) |
+                    (tok >= lo.z && tok < hi.z ? 4u << c : 0u) | (tok >= lo.w && tok < hi.w ? 8u << c : 0u);
           }
         }
-        if (named_bar_red_or(grp_bar, 128, top > kLag)) {
+        auto relate = [&](float &top) {
+#pragma unroll
+          for (int c = 0; c < N; c += 2) {
+            unpair(fma2(pair(x[c], x[c + 1]), scale2, less[c / 2]), x[c], x[c + 1]);
+            top = fmaxf(top, fmaxf(x[c], x[c + 1]));
+          }
+        };
+        auto hide = [&]() {  // what a column does not see is minus infinity
+          if (sees == 0xffffffffu) return;
+#pragma unroll
+          for (int c = 0; c < N; ++c) x[c] = (sees >> c) & 1u ? x[c] : -INFINITY;
+        };
+        float top = -INFINITY;
+        const bool rescale = i > w.a;  // there are outputs already
+        hide();
+        bool move = true;
+        if (rescale) {
+          relate(top);
+          move = named_bar_red_or(grp_bar, 128, top > kLag);
+          if (move) {
+            tmem_load<N>(s_addr, x);
+            hide();
+          }
+        }
+        if (move) {
           float v[N];
 #pragma unroll
-          for (int c = 0; c < N; ++c) v[c] = x[c];
+          for (int c = 0; c < N; ++c) v[c] = x[c] * p.scale_log2;
           const float r = reduce_columns<true, N>(v, lane);
           if (lane < N) misc.red[grp][wq][lane] = r;
           named_bar_sync(grp_bar, 128);
-          const bool rescale = i > w.a;
           if (rescale) {
             wait(smem_u32(&misc.o_done[sb ^ 1u]), ((t - 1) >> 1) & 1u);
             tc_fence_after();
@@ -768,13 +805,21 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           for (int h = 0; h < N; h += 16) {
             float f[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float best = fmaxf(fmaxf(misc.red[grp][0][h + c], misc.red[grp][1][h + c]),
-                                       fmaxf(misc.red[grp][2][h + c], misc.red[grp][3][h + c]));
-              const float now = fmaxf(m[h + c], best);
-              f[c] = fast_exp2(m[h + c] - now);
-              m[h + c] = now;
-              sum[h + c] *= f[c];
+            for (int c = 0; c < 16; c += 2) {
+              float l[2], now[2];
+              unpair(less[(h + c) / 2], l[0], l[1]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int at = h + c + k;
+                const float best = fmaxf(fmaxf(misc.red[grp][0][at], misc.red[grp][1][at]),
+                                         fmaxf(misc.red[grp][2][at], misc.red[grp][3][at]));
+                now[k] = fmaxf(-l[k], best);
+                f[c + k] = fast_exp2(-l[k] - now[k]);
+              }
+              less[(h + c) / 2] = pair(-now[0], -now[1]);
+              float s0, s1;
+              unpair(sum[(h + c) / 2], s0, s1);
+              sum[(h + c) / 2] = pair(s0 * f[c], s1 * f[c + 1]);
             }
             if (rescale)
 #pragma unroll
@@ -787,17 +832,20 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
                 tmem_store<16>(addr, o);
               }
           }
+          relate(top);
         }
         // a probability as two bf16 terms: its rounding, and the rounding of what that left
         uint32_t hi[N / 2], lo[N / 2];
 #pragma unroll
         for (int c = 0; c < N; c += 2) {
-          const float p0 = fast_exp2(x[c] - m[c]), p1 = fast_exp2(x[c + 1] - m[c + 1]);
-          sum[c] += p0;
-          sum[c + 1] += p1;
+          const uint64_t pp = pair(fast_exp2(x[c]), fast_exp2(x[c + 1]));
+          sum[c / 2] = add2(sum[c / 2], pp);
+          float p0, p1;
+          unpair(pp, p0, p1);
           const uint32_t u = pack_bf16(p0, p1);
+          unpair(fma2(pair(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), minus2, pp), p0, p1);
           hi[c / 2] = u;
-          lo[c / 2] = pack_bf16(p0 - __uint_as_float(u << 16), p1 - __uint_as_float(u & 0xffff0000u));
+          lo[c / 2] = pack_bf16(p0, p1);
         }
         // the P^T that this one overwrites has been read
         if (t >= C::kPBufs) wait(smem_u32(&misc.o_done[(t - C::kPBufs) & 1u]), ((t - C::kPBufs) >> 1) & 1u);
@@ -860,14 +908,17 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       {
         float v[N];
 #pragma unroll
-        for (int c = 0; c < N; ++c) v[c] = sum[c];
+        for (int c = 0; c < N; c += 2) unpair(sum[c / 2], v[c], v[c + 1]);
         const float r = reduce_columns<false, N>(v, lane);
         if (lane < N) misc.red[grp][wq][lane] = r;
       }
       if (wq == 0 && lane == 0) {
 #pragma unroll
-        for (int c = 0; c < N; c += 4)
-          *reinterpret_cast<float4 *>(cols.stat_m + col0 + c) = make_float4(m[c], m[c + 1], m[c + 2], m[c + 3]);
+        for (int c = 0; c < N; c += 2) {
+          float l0, l1;
+          unpair(less[c / 2], l0, l1);
+          *reinterpret_cast<float2 *>(cols.stat_m + col0 + c) = make_float2(-l0, -l1);
+        }
       }
       named_bar_sync(grp_bar, 128);
       if (wq == 0 && lane < N) {

@@ -10,9 +10,10 @@ float32 operations by 3 2^-24 of |x| + |y|: all below 2^-20 (|x| + |y|), then on
 Attention: a score's float32 dot product of D bf16 products (exact) is off by at most D 2^-23 of the sum
 of their magnitudes (the tensor cores may cut instead of rounding), its scaling, the subtraction of the
 maximum and exp2 by a few float32 roundings of numbers no larger than |s| + |max|: together d_j.  A
-probability is rounded to bf16 once: 2^-8.  Sums over n tokens in float32, in any order: n 2^-23.  So
-with weights w_j = softmax(s)_j, each off by (2^-8 + 2 d + n 2^-23) of itself,
-    |out - ref| <= (2^-8 + 2 d + 2 n 2^-23) sum_j w_j |v_j| + 2^-8 |ref|,   |lse - ref| <= d + n 2^-23 + 2^-22 |ref|.
+probability goes to the product as its rounding to bf16 and the rounding of what that left: 2^-16.
+Sums over n tokens in float32, in any order: n 2^-23.  So with weights w_j = softmax(s)_j, each off by
+(2^-16 + 2 d + n 2^-23) of itself,
+    |out - ref| <= (2^-16 + 2 d + 2 n 2^-23) sum_j w_j |v_j| + 2^-8 |ref|,   |lse - ref| <= d + n 2^-23 + 2^-22 |ref|.
 The difference of two maps adds their bounds; the norm divides by the root mean square, itself off by at
 most the root mean square of the bound."""
 import math
@@ -54,7 +55,7 @@ def attend(q, k, v, scale, lo, hi):
     out, lse = w @ v, (m + np.log(total))[:, 0]
     d = (D * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(k).T) + 4 * EPS32 * (np.abs(s) + np.abs(m)) + 2.0 ** -22).max(1)
     sums = n * 2.0 ** -23
-    tol = (HALF_BF16 + 2 * d + 2 * sums)[:, None] * (w @ np.abs(v)) + HALF_BF16 * np.abs(out)
+    tol = (HALF_BF16 ** 2 + 2 * d + 2 * sums)[:, None] * (w @ np.abs(v)) + HALF_BF16 * np.abs(out)
     return out, tol, lse, d + sums + 2.0 ** -22 * np.abs(lse)
 
 
