@@ -10,6 +10,7 @@ fallback path.  Call ``mla_decode_speculative_gb300.build.build()`` first (or
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 import threading
@@ -618,18 +619,23 @@ def _call(name, *argtypes):
     return f
 
 
+_TURN = 2 ** 192 * 10 ** 60 // (2 * 3141592653589793238462643383279502884197169399375105820974944)  # 2^192 / (2 pi)
+
+
 def rotary_turns(freq, device="cuda") -> torch.Tensor:
-    """The table mla_rotary takes for pairs of `freq` radians per position (float64 [R / 2]): the
-    turns per position in units of 2^-64, modulo 1, as int64 [R / 2] on `device`."""
-    f = torch.as_tensor(freq, dtype=torch.float64).cpu()
-    if f.dim() != 1 or not torch.isfinite(f).all():
-        raise ValueError("freq must be [R / 2] finite radians per position")
-    pi = 3141592653589793238462643383279502884197  # pi * 10^39: the quotient in whole numbers, rounded once
+    """The table mla_rotary takes for pairs of `freq` radians per position (float64 [R / 2], below
+    2^32): the turns per position in units of 2^-64, modulo 1, rounded once, as int64 [R / 2] on
+    `device`."""
+    f = torch.as_tensor(freq, dtype=torch.float64)
+    if f.dim() != 1:
+        raise ValueError("freq must be [R / 2]")
     units = []
     for x in f.tolist():
-        n, d = x.as_integer_ratio()
-        n, d = n * 2 ** 64 * 10 ** 39, 2 * d * pi
-        units.append(((2 * n + d) // (2 * d) + 2 ** 63) % 2 ** 64 - 2 ** 63)
+        if not abs(x) < 2.0 ** 32:
+            raise ValueError(f"freq must be finite radians per position below 2^32, got {x}")
+        m, e = math.frexp(x)   # x = m * 2^e, in whole numbers (m * 2^53) * 2^(e - 53)
+        shift = 128 + 53 - e
+        units.append(((int(m * 2 ** 53) * _TURN + (1 << shift - 1) >> shift) + 2 ** 63) % 2 ** 64 - 2 ** 63)
     return torch.tensor(units, dtype=torch.int64, device=device)
 
 

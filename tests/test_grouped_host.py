@@ -145,14 +145,14 @@ def test_structs_match_the_header(tmp_path):
 def test_turns_are_the_frequencies_to_half_a_unit():
     """|turns / 2^64 - freq / (2 pi)| <= 2^-65 modulo 1, against a longer pi (to 60 digits)."""
     pi = Fraction(314159265358979323846264338327950288419716939937510582097494, 10 ** 59)
-    f = [1.0, 0.9, 1e-4, 10000.0 ** -0.37, 3.0, -0.25, 0.0, 1e5]
+    f = [1.0, 0.9, 1e-4, 10000.0 ** -0.37, 3.0, -0.25, 0.0, 1e5, 1e-300, -4e9]
     got = mla.rotary_turns(f, device="cpu")
     assert got.dtype == torch.int64 and got.shape == (len(f),)
     for x, t in zip(f, got.tolist()):
         off = Fraction(t, 2 ** 64) - Fraction(x) / (2 * pi)
         off -= round(off)
         assert abs(off) <= Fraction(1, 2 ** 65) * Fraction(1001, 1000)
-    for bad in ([[1.0]], [math.inf], [math.nan]):
+    for bad in ([[1.0]], [math.inf], [math.nan], [2.0 ** 32], [-1e300]):
         with pytest.raises(ValueError):
             mla.rotary_turns(bad, device="cpu")
 
