@@ -157,7 +157,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
 
   // Requests of one launch: as many as the kernel tabulates and as int32
   // positions hold at the static bound.
-  const int64_t tiles = (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile + 1;
+  const int64_t tiles = (static_cast<int64_t>(p.max_len) + kTile - 1) / kTile + (p.window > 0 ? 1 : 0);
   const int64_t blocks = p.head_blocks == 1 ? (a->max_qlen + p.rows_per_block - 1) / p.rows_per_block
                                             : static_cast<int64_t>(a->max_qlen) * p.head_blocks;
   const int64_t units = blocks * a->num_kv_heads, most = units * (tiles + kOverhead);
@@ -192,10 +192,11 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     p.first_req = b0;
     p.qo_indptr = a->qo_indptr + b0;
     p.subpage_table = a->subpage_table + static_cast<int64_t>(b0) * a->subpage_stride;
-    // no more CTAs than there are chunks at the static bound; one chunk cuts no unit
-    const int64_t want = most * p.num_reqs / kMinChunk;
-    const int grid = static_cast<int>(want < 1 ? 1 : (want < kMaxCtas ? want : kMaxCtas));
-    const bool merge = grid > 1;
+    // no more CTAs than there are chunks at the static bound
+    const int64_t all = units * p.num_reqs, want = most * p.num_reqs / kMinChunk > all ? most * p.num_reqs / kMinChunk : all;
+    const int grid = static_cast<int>(want < kMaxCtas ? want : kMaxCtas);
+    p.few = all <= grid;
+    const bool merge = grid > 1 && !(p.few && tiles <= whole_tiles(W));  // units may be cut
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const mla_status s =
         differential ? launch_differential(W, nc, tq, tk, tv, p, grid, merge, cs) : launch_grouped(W, nc, tq, tk, tv, p, grid, merge, cs);

@@ -6,7 +6,7 @@
 //   s_j = sm_scale <q_m, k_{j,g,m}>,  o_m = sum_j softmax(s)_j v_{j,g}
 // with an online base-2 softmax.  The rows of a group (heads x verify rows) go
 // over their keys and values together, so the cache is read once per group:
-// 2 R flops a byte for R rows, so memory decides (282 flops a byte is the ridge)
+// R flops a byte for R rows, so memory decides (282 flops a byte is the ridge)
 // as long as the tensor cores, the softmax and the copies run beside each other.
 //
 //  * Tile = 128 tokens of one group.  Both products have the tokens' or the
@@ -26,7 +26,7 @@
 //    a warp issues each product, and the stream of tiles runs on from part to part.
 //  * Balanced split: a unit (request, group, row block) is kOverhead positions
 //    and then its tiles; the positions of all units, laid end to end, are cut
-//    into equal chunks, one per SM.  A chunk holds at most two units that it
+//    into equal chunks, one per SM (a few short units: a chunk each).  A chunk holds at most two units that it
 //    does not hold whole: its first and its last.  So there are two partial
 //    records per SM, whatever the batch, and the merge looks at 152 chunks.
 //  * Softmax: a thread has one token and the 16 columns of its group of warps (32
@@ -68,6 +68,12 @@ constexpr int kOverhead = 2;      // positions a unit counts beside its tiles (1
 constexpr int kMinChunk = 4;      // positions a chunk has at least (6: two requests of two tiles 8.0 -> 12.3 us)
 constexpr int kMaxCtas = 152;
 
+// Tiles up to which units are not cut, when there are no more units than SMs: a
+// tile more takes 0.3-0.6 us, parts and their merge 2 to 4 (units of 4 tiles of 128
+// dims 13.3 -> 9.4 us for 16 requests, of 8 tiles 15.8 -> 12.6 for 16, 9.8 -> 10.0
+// for one; of 256 dims 4 tiles 12.7 -> 10.4, 8 tiles 12.7 -> 15.1).
+__host__ __device__ constexpr int whole_tiles(int W) { return W == 4 ? 4 : 8; }
+
 // A unit that is cut across chunks: written by the chunk with its first tile.
 struct Meta {
   int q0, qlen, g, rb;
@@ -93,6 +99,7 @@ struct Params {
   int rows_per_block;   // verify rows of a row block (group <= NR)
   int heads_per_block;  // query heads of a row block: group, or NR if group > NR
   int one_block;        // every request has one row block
+  int few;              // no more units than CTAs
   int head_blocks;      // row blocks a verify row's group is cut into (1 if group <= NR)
 };
 
@@ -173,7 +180,7 @@ struct Misc;
 // softmax warps' is in shared memory (in registers it made them spill).
 struct Walk {
   int pos_a, pos_e;  // the chunk
-  int b, g, rb, s, per, blocks;
+  int b, g, rb, s, per, blocks, tiles;
   int4 req;
   __device__ __forceinline__ void begin(const Misc &m, int a, int e);
   __device__ __forceinline__ bool next(const Params &p, const Misc &m, Part &o);
@@ -202,6 +209,7 @@ struct Misc {
   int4 req[kMaxReqs];                     // tokens that some row of the request sees (x .. y - 1), first row, rows
   Walk walk;                              // the softmax warps'
   Place place;                            // where this chunk begins
+  int whole;                              // a chunk is a unit: one position each
   alignas(16) float red[2][4][32];        // [group of warps][warp][column]
   Columns cols[2];                        // of the even and odd parts
 };
@@ -217,12 +225,13 @@ __device__ __forceinline__ void Walk::begin(const Misc &m, int a, int e) {
   per = m.place.per;
   blocks = m.place.blocks;
   req = m.req[b];
+  tiles = tiles_of(req);
 }
 
 __device__ __forceinline__ bool Walk::next(const Params &p, const Misc &m, Part &o) {
   while (s < pos_e) {
-    const int first = s + kOverhead, n = per - kOverhead;
-    const int a = max(pos_a - first, 0), e = min(pos_e - first, n);
+    const int first = s + kOverhead, n = tiles;
+    const int a = m.whole ? 0 : max(pos_a - first, 0), e = m.whole ? n : min(pos_e - first, n);
     const bool take = n > 0 ? e > a : s >= pos_a;
     if (take) o = Part{b, g, rb, req.z, req.w, req.x, req.y, req.x / kTile, n == 0 ? 0 : a, n == 0 ? 0 : e, n, s};
     s += per;
@@ -234,7 +243,8 @@ __device__ __forceinline__ bool Walk::next(const Params &p, const Misc &m, Part 
         while (m.start[b + 1] <= s);
         req = m.req[b];
         blocks = p.one_block ? 1 : blocks_of(p, req.w);
-        per = tiles_of(req) + kOverhead;
+        tiles = tiles_of(req);
+        per = m.whole ? 1 : tiles + kOverhead;
       }
     }
     if (take) return true;
@@ -438,6 +448,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   grid_dep_launch();
 
   // What each request's rows see, and its positions.
+  bool low = true;  // units are not worth a cut
   for (int b = threadIdx.x; b < p.num_reqs; b += C::kThreads) {
     // the first row lengths where a batch of equal requests has them, read beside the offsets
     int ahead[4];
@@ -468,18 +479,21 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         }
       }
       if (hi == 0) lo = 0;
-      cost = (p.one_block ? 1 : blocks_of(p, q1 - q0)) * p.num_kv_heads * (tiles_of(make_int4(lo, hi, 0, 0)) + kOverhead);
+      const int tiles = tiles_of(make_int4(lo, hi, 0, 0));
+      low &= tiles <= whole_tiles(kW);
+      cost = (p.one_block ? 1 : blocks_of(p, q1 - q0)) * p.num_kv_heads * (tiles + kOverhead);
     }
     misc.req[b] = make_int4(lo, hi, q0, q1 - q0);
     misc.start[b + 1] = cost;
   }
   if (threadIdx.x == 0) misc.start[0] = 0;
-  __syncthreads();
+  const bool whole = __syncthreads_and(low) != 0 && p.few;
   if (warp == 0) {  // running sum, in place
     int carry = 0;
     for (int base = 0; base < p.num_reqs; base += 32) {
       const int b = base + lane;
       int x = b < p.num_reqs ? misc.start[b + 1] : 0;
+      if (whole && x > 0) x = blocks_of(p, misc.req[b].w) * p.num_kv_heads;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   __syncthreads();
   // chunks 0 .. rest - 1 have size + 1 positions, the others size
   const unsigned total = misc.start[p.num_reqs];
-  const unsigned chunks = max(1u, min(gridDim.x, total / kMinChunk)), size = total / chunks, rest = total - size * chunks;
+  const unsigned chunks = max(1u, min(gridDim.x, whole ? total : total / kMinChunk)), size = total / chunks, rest = total - size * chunks;
   const unsigned chunk = blockIdx.x;
   auto cut = [&](unsigned c) { return static_cast<int>(c * size + min(c, rest)); };
   auto chunk_of = [&](int x) {
@@ -500,11 +514,12 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     return static_cast<int>(u < big ? u / (size + 1) : rest + (u - big) / size);
   };
   const int pos_a = chunk < chunks ? cut(chunk) : total, pos_e = chunk < chunks ? cut(chunk + 1) : total;
+  if (threadIdx.x == 0) misc.whole = whole;
   for (int b = threadIdx.x; b < p.num_reqs; b += C::kThreads) {
     const int from = misc.start[b];
     if (from <= pos_a && pos_a < misc.start[b + 1]) {  // one request at most
       const int4 req = misc.req[b];
-      const int per = tiles_of(req) + kOverhead, blocks = p.one_block ? 1 : blocks_of(p, req.w);
+      const int per = whole ? 1 : tiles_of(req) + kOverhead, blocks = p.one_block ? 1 : blocks_of(p, req.w);
       const int j = (pos_a - from) / per, g = blocks == 1 ? j : j / blocks;
       misc.place = Place{b, g, j - g * blocks, from + j * per, per, blocks};
     }
