@@ -149,6 +149,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
   p.subpage_stride = a->subpage_stride;
   while ((8 << p.page_shift) < P) ++p.page_shift;
   p.page_shift += 3;
+  p.box_shift = p.page_shift < 5 ? p.page_shift : 5;
   p.page_groups = static_cast<int>(a->num_cache_rows / 8);
   p.head_blocks = (G + nr - 1) / nr;
   p.heads_per_block = p.head_blocks == 1 ? G : nr;
@@ -181,7 +182,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     const uint64_t row = static_cast<uint64_t>(i == 0 ? a->k_row : a->v_row) * 2;
     const cuuint64_t dims[5] = {64, 8, w64, static_cast<uint64_t>(p.page_groups), hkv};
     const cuuint64_t strides[4] = {row, 128, row * 8, w64 * 128};
-    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(W < 2 ? W : 2), static_cast<cuuint32_t>(P / 8), 1};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(W < 2 ? W : 2), 1u << (p.box_shift - 3), 1};
     // a fetch of 256 bytes would bring another group's 128 bytes of a token along
     const mla_status s = make_tmap_5d(i == 0 ? &tk : &tv, i == 0 ? a->k_cache : a->v_cache, dims, strides, box,
                                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B);

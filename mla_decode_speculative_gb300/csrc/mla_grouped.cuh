@@ -18,9 +18,10 @@
 //    of one product with the values, which are thus read once.
 //  * A token's row of a group is W chunks of 64 values (W = 1, 2, 4: the keys of
 //    all maps, or the values).  The tensor map splits cache rows in eights, so
-//    that one box brings a page as [8 rows][chunk][row][128 bytes]: the same
-//    uniform strides for pages of 8 as of 128, read by both products as they
-//    are (128-byte swizzle).
+//    that one box brings a page (32 tokens of a larger one: what lies outside a
+//    window or behind the end is not read) as [8 rows][chunk][row][128 bytes]:
+//    the same uniform strides for pages of 8 as of 128, read by both products as
+//    they are (128-byte swizzle).
 //  * Copies through a ring of slots of at most 32 KB (two chunks) for the keys
 //    and one for the values, which wait for the softmax; a warp copies into each,
 //    a warp issues each product, and the stream of tiles runs on from part to part.
@@ -96,6 +97,7 @@ struct Params {
   int first_req;  // of the call, where it takes several launches
   int num_reqs, num_rows, num_heads, num_kv_heads, group, max_qlen, max_len, window;
   int subpage_stride, page_shift, page_groups;  // pages of 2^page_shift; page_groups: num_cache_rows / 8
+  int box_shift;        // a copy's box has 2^box_shift tokens: a page, or 32 of a larger one
   int rows_per_block;   // verify rows of a row block (group <= NR)
   int heads_per_block;  // query heads of a row block: group, or NR if group > NR
   int one_block;        // every request has one row block
@@ -552,20 +554,21 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       tma_prefetch_desc(tm);
       if (keys) tma_prefetch_desc(&tm_q);
     }
-    const int shift = p.page_shift, pages = kTile >> shift, groups = 1 << (shift - 3);
-    const uint32_t page_bytes = (128u * C::kCW) << shift;
+    // boxes of a tile, row groups of a page, boxes of a page
+    const int shift = p.box_shift, boxes = kTile >> shift, groups = 1 << (p.page_shift - 3), split = p.page_shift - shift;
+    const uint32_t box_bytes = (128u * C::kCW) << shift;
     Walk walk;
     walk.begin(misc, pos_a, pos_e);
     Part w;
     uint32_t t = 0, kq = 0;
     while (ok && walk.next(p, misc, w)) {
       if (w.e == w.a) continue;
-      // a lane holds a page of the tile, and reads the next tile's ahead of the waits
+      // a lane holds a box of the tile, and reads the next tile's page id ahead of the waits
       const int32_t *ids = p.subpage_table + static_cast<int64_t>(w.b) * p.subpage_stride;
-      const int page_lo = w.lo >> shift, page_hi = ((w.hi - 1) >> shift) + 1;
+      const int box_lo = w.lo >> shift, box_hi = ((w.hi - 1) >> shift) + 1;
       auto id_of = [&](int tile) {
-        const int page = (w.tile0 + tile) * pages + lane;
-        return lane < pages && page >= page_lo && page < page_hi ? ids[page] : -1;
+        const int box = (w.tile0 + tile) * boxes + lane;
+        return lane < boxes && box >= box_lo && box < box_hi ? ids[box >> split] : -1;
       };
       int id = id_of(w.a);
       if (keys) {
@@ -587,13 +590,13 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         ++kq;
       }
       for (int i = w.a; i < w.e && ok; ++i, ++t) {
-        const int first = (w.tile0 + i) * pages;
-        const int p0 = max(page_lo, first), p1 = min(page_hi, first + pages);
-        const bool mine = first + lane >= p0 && first + lane < p1;
+        const int first = (w.tile0 + i) * boxes;
+        const int b0 = max(box_lo, first), b1 = min(box_hi, first + boxes);
+        const bool mine = first + lane >= b0 && first + lane < b1;
         int group8 = p.page_groups;  // behind the cache: zeros
         if (mine) {
           if (id < 0 || (static_cast<int64_t>(id) + 1) * groups > p.page_groups) record_error(p.err, MLA_DEV_BAD_SUBPAGE);
-          else group8 = id * groups;
+          else group8 = id * groups + (((first + lane) & ((1 << split) - 1)) << (shift - 3));
         }
         if (i + 1 < w.e) id = id_of(i + 1);
 #pragma unroll
@@ -605,11 +608,11 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           if (!ok) break;
           if (lane == 0) {
             misc.armed[slot] = 1 + par;
-            mbar_arrive_expect_tx(full_bar(slot), page_bytes * (p1 - p0));
+            mbar_arrive_expect_tx(full_bar(slot), box_bytes * (b1 - b0));
           }
           __syncwarp();
           if (mine)
-            tma_load_5d(s_slots + slot * C::kSlotBytes + lane * page_bytes, tm, full_bar(slot), 0, 0, s * C::kCW, group8, w.g,
+            tma_load_5d(s_slots + slot * C::kSlotBytes + lane * box_bytes, tm, full_bar(slot), 0, 0, s * C::kCW, group8, w.g,
                         pol_kv);
         }
       }
@@ -747,10 +750,6 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       }
       named_bar_sync(all_bar, kSoftmaxThreads);
       if (cols.stop) break;
-      if (threadIdx.x == 0) {  // read behind the barrier of this part's result
-        Columns &then = misc.cols[(n_part + 1) & 1];
-        then.more = misc.walk.next(p, misc, then.part);
-      }
       // tokens that this group's columns all see (all_lo .. all_hi - 1), and
       // that all columns see that see anything (edge_lo .. edge_hi - 1)
       int all_lo = valid ? my_lo : 0, all_hi = valid ? my_hi : INT32_MAX;
@@ -930,6 +929,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       }
 
       // ---- the part's result
+      if (threadIdx.x == 0) {  // the next part, beside the last product; read behind this result's barrier
+        Columns &then = misc.cols[(n_part + 1) & 1];
+        then.more = misc.walk.next(p, misc, then.part);
+      }
       if (w.e > w.a) wait(smem_u32(&misc.o_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u);
       {
         float v[N];
