@@ -14,8 +14,10 @@ namespace grouped {
 // statistics with a lane per part, then the parts' outputs, 64 W values over 32
 // lanes, weighted by 2^(m - M) / L; the difference of the maps and its norm go
 // through shared memory.  Bound by round trips, so the first parts' outputs are
-// read beside the statistics: with four of them and a warp per row 16 units of
-// ten parts took 5 us more than no merge, 24 differential ones of seven 6 us.
+// read beside the statistics, 8 or 12 at a time: with four of them and a warp per
+// row 16 units of ten parts took 5 us more than no merge, 24 differential ones of
+// seven 6 us (now 4.3 each).  Four warps per row and map were slower but for units
+// of a hundred parts (48 window units 28.7 -> 32.6).
 constexpr int kMergeRows = 4;
 
 template <int kV>
@@ -82,20 +84,18 @@ __global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __
   float y[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) y[k] = 0.0f;
-  // a part in which the row saw nothing holds no numbers
+  for (int base = 0;;) {  // a part in which the row saw nothing holds no numbers
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const float w = i < parts ? weight[warp][i] : 0.0f;
+    for (int i = 0; i < kAhead; ++i) {
+      const float w = base + i < parts ? weight[warp][base + i] : 0.0f;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) y[k] += w == 0.0f ? 0.0f : w * ahead[i][k];
-  }
-#pragma unroll 4
-  for (int i = kAhead; i < parts; ++i) {
-    const float w = weight[warp][i];
-    float v[kV];
-    load_row<kV>(outs + record(i) * kNC * kDv, v);
+      for (int k = 0; k < kV; ++k) y[k] += w == 0.0f ? 0.0f : w * ahead[i][k];
+    }
+    base += kAhead;
+    if (base >= parts) break;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) y[k] += w == 0.0f ? 0.0f : w * v[k];
+    for (int i = 0; i < kAhead; ++i)
+      if (base + i < parts) load_row<kV>(outs + record(base + i) * kNC * kDv, ahead[i]);
   }
   const float by = (sum == 0.0f ? 0.0f : 1.0f / sum) * (m == 1 ? lam : 1.0f);
 #pragma unroll
@@ -144,7 +144,8 @@ mla_status launch_as(const CUtensorMap &q, const CUtensorMap &k, const CUtensorM
   e = launch_pdl(grouped_kernel<kW, kMaps, kNC>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, q, k, v, p);
   if (e != cudaSuccess) return cuda_fail(e, "grouped launch");
   if (!merge) return MLA_OK;
-  e = launch_pdl(grouped_merge<kW, kMaps, kNC>, dim3(grid, C::kNR / kMergeRows), dim3(32 * kMergeRows * kMaps), 0, stream, p);
+  const int rows = p.rows_per_block * p.heads_per_block;  // of a unit
+  e = launch_pdl(grouped_merge<kW, kMaps, kNC>, dim3(grid, (rows + kMergeRows - 1) / kMergeRows), dim3(32 * kMergeRows * kMaps), 0, stream, p);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e, "grouped merge launch");
 }
 
