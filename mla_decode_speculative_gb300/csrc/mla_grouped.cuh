@@ -454,11 +454,9 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   for (int b = threadIdx.x; b < p.num_reqs; b += C::kThreads) {
     // the first row lengths where a batch of equal requests has them, read beside the offsets
     int ahead[4];
+    const int64_t guess = static_cast<int64_t>(p.first_req + b) * p.max_qlen;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t r = static_cast<int64_t>(p.first_req + b) * p.max_qlen + k;
-      ahead[k] = k < p.max_qlen && r < p.num_rows ? p.row_len[r] : 0;
-    }
+    for (int k = 0; k < 4; ++k) ahead[k] = k < p.max_qlen && guess + k < p.num_rows ? p.row_len[guess + k] : 0;
     const int q0 = p.qo_indptr[b], q1 = p.qo_indptr[b + 1];
     int lo = INT32_MAX, hi = 0, cost = 0;  // of the rows that see anything
     if (q0 < 0 || q1 < q0 || q1 > p.num_rows || q1 - q0 > p.max_qlen) {
@@ -467,7 +465,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       for (int r0 = q0; r0 < q1; r0 += 4) {
         int n[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) n[k] = r0 + k >= q1 ? 0 : (q0 == (p.first_req + b) * p.max_qlen && r0 == q0 ? ahead[k] : p.row_len[r0 + k]);
+        for (int k = 0; k < 4; ++k) n[k] = r0 + k >= q1 ? 0 : (q0 == guess && r0 == q0 ? ahead[k] : p.row_len[r0 + k]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (n[k] > p.max_len) {

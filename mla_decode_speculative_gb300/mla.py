@@ -723,6 +723,14 @@ def decode_grouped_workspace_bytes(num_heads, num_kv_heads, max_qlen, head_dim, 
     return int(lib().mla_decode_grouped_workspace(ctypes.byref(a), int(differential)))
 
 
+def _empty(shape, dtype, device, stream):
+    """An output or workspace of the call's own: memory of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows_of(t, heads, width, dev, name):
     """(address, row stride) of a bf16 tensor whose rows hold `heads` x `width` values without gaps."""
     step = t.stride()
@@ -734,7 +742,7 @@ def _rows_of(t, heads, width, dev, name):
 
 
 def _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale, window, out, lse,
-             wait_cycles, dev, maps):
+             wait_cycles, dev, maps, stream=None):
     """(packed arguments, out, lse, (H, Hkv, D)) of a grouped call of 1 or 2 maps."""
     qs, ks, vs = q.shape, k_cache.shape, v_cache.shape
     T, H, D = qs[0], qs[1], qs[-1]
@@ -748,9 +756,9 @@ def _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_,
     if row_len.numel() != T or subpage_table.numel() != B * pages:
         raise ValueError("row_len must be [T] and subpage_table [B, width]")
     if out is None:
-        out = torch.empty((T, H, width), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, H, width), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H) if maps == 1 else (T, H, 2), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H) if maps == 1 else (T, H, 2), torch.float32, q.device, stream)
     if out.numel() != T * H * width or lse.numel() != T * H * maps:
         raise ValueError("out must hold a value vector and lse a number per row and head (and map)")
     i32 = torch.int32
@@ -771,10 +779,10 @@ def decode_grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_
     f32, workspace)."""
     _, dev, raw = _current(stream)
     a, out, lse, sizes = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale,
-                                  window, out, lse, wait_cycles, dev, 1)
+                                  window, out, lse, wait_cycles, dev, 1, stream)
     if workspace is None:
         need = decode_grouped_workspace_bytes(sizes[0], sizes[1], max_qlen, sizes[2])
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     st = _call("mla_decode_grouped", ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)(
         a, _dev_ptr(workspace, torch.uint8, dev, "workspace"), workspace.numel(), raw)
     if st:
@@ -790,12 +798,12 @@ def decode_differential(q, k_cache, v_cache, lam, qo_indptr, row_len, subpage_ta
     f32, workspace)."""
     _, dev, raw = _current(stream)
     a, out, lse, sizes = _grouped(q, k_cache, v_cache, qo_indptr, row_len, subpage_table, page_size_, max_qlen, sm_scale,
-                                  window, out, lse, wait_cycles, dev, 2)
+                                  window, out, lse, wait_cycles, dev, 2, stream)
     if lam.numel() != sizes[0] or gain is not None and gain.numel() != 2 * sizes[2]:
         raise ValueError("lam must be [H] and gain [2 D]")
     if workspace is None:
         need = decode_grouped_workspace_bytes(sizes[0], sizes[1], max_qlen, sizes[2], True)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     f32, vp = torch.float32, ctypes.c_void_p
     st = _call("mla_decode_differential", vp, vp, ctypes.c_float, vp, ctypes.c_size_t, vp)(
         a, _dev_ptr(lam, f32, dev, "lam"), None if gain is None else _dev_ptr(gain, f32, dev, "gain"), eps,

@@ -222,9 +222,8 @@ class PagedKVCache(_PagedBlocks):
         if q.shape[0] != self.num_rows or k_new.shape[0] != self.num_rows or v_new.shape[0] != self.num_rows:
             raise ValueError("q, k_new and v_new must have num_rows rows")
         q_out = q if q_out is None else q_out
-        flat = (lambda x: x.flatten(1, 2)) if self.differential else (lambda x: x)   # a key of its own per map
-        if self.differential and flat(q_out).data_ptr() != q_out.data_ptr():
-            raise ValueError("the two queries of a head must lie together")
+        # a query or key of its own per map (a view: strides that allow none are refused)
+        flat = (lambda x: x.view(x.shape[0], -1, x.shape[-1])) if self.differential else (lambda x: x)
         self._append(seq_lens, qo_indptr, stream,
                      lambda s: mla.rotary_write(flat(q), flat(k_new), v_new, positions, turns, self.slot_map,
                                                 flat(self.k), self.v, axes, neighbours, q_out=flat(q_out), stream=s))
