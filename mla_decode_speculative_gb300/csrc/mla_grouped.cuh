@@ -882,8 +882,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
                        lo[4 * j + 3]);
         }
         if (grp == 0 && (tok0 < edge_lo || tok0 + kTile > edge_hi)) {
-          const bool dead = tok < w.lo || tok >= w.hi;
-          const bool mixed = !dead && (tok < edge_lo || tok >= edge_hi);
+          const bool unseen = tok < w.lo || tok >= w.hi;
+          // of these only the ones in a step of 16 that the product takes
+          const bool dead = unseen && (tok | 15) >= w.lo && (tok & ~15) < w.hi;
+          const bool mixed = !unseen && (tok < edge_lo || tok >= edge_hi);
           if (__any_sync(0xffffffffu, dead || mixed)) {
             const uint32_t use = C::kNS * t;
             // the slots' last values have been read: until then the parity could be theirs
@@ -891,9 +893,9 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
 #pragma unroll
             for (int s = 0; s < C::kNS; ++s) wait(full_bar(v_slot<C>(use + s)), v_par<C>(use + s));
             bool zero = dead;
-            auto piece = [&](int s, int c, int j) {
+            auto piece = [&](int s, int c, int j) {  // lanes in different columns of 16 bytes: no bank twice
               return s_slots + v_slot<C>(use + s) * C::kSlotBytes + (row >> 3) * (C::kCW * 1024) + c * 1024 +
-                     (row & 7) * 128 + j * 16;
+                     (row & 7) * 128 + ((j + lane) & 7) * 16;
             };
             if (mixed) {
               bool odd = false;
