@@ -118,6 +118,61 @@ def test_rotary_angles_add_up_and_far_positions_are_exact():
     close(mla.rotary(near.clone(), None, i32(7 * pos), turns)[0], want, tol)
 
 
+@pytest.mark.parametrize("T,H,Hk,D,Dk,R,neighbours,inplace", [
+    (130, 200, 9, 128, 128, 128, False, False),   # a row is more than a block
+    (700, 65, 1, 64, 64, 64, True, False),        # a row is a little more than a round of threads
+    (5001, 1, 1, 128, 128, 128, True, True),      # sines enough for half a block
+    (900, 24, 3, 70, 128, 64, False, False),      # q and k of different alignment
+    (3001, 130, 6, 128, 128, 64, False, False),   # larger than L2: the values past R with the rotated ones
+    (5003, 96, 8, 80, 80, 40, True, False), (3001, 190, 10, 70, 70, 6, False, False),
+    (3001, 150, 6, 128, 96, 32, True, False),     # the same of q and k with unequal tails
+    (3001, 140, 10, 72, 72, 64, False, False)])   # that do not divide so
+def test_rotary_in_one_call_is_rotary_in_many(T, H, Hk, D, Dk, R, neighbours, inplace):
+    """q and k together, in whichever way they share their blocks, are q and k by themselves some rows at a
+    time, bit for bit; and that is the reference."""
+    r = np.random.default_rng(T + H)
+    q, k = rand((T, H, D), 1), rand((T, Hk, Dk), 2)
+    pos, axes, f = r.integers(0, 1 << 20, (3, T)), r.integers(0, 3, R // 2), freqs(R // 2)
+    turns, ax = mla.rotary_turns(f), i32(axes)
+    some = [0, T // 3, T - 1]
+    parts = []
+    for x in (q, k):
+        out = torch.zeros_like(x)
+        for t in range(0, T, 97):
+            rows = slice(t, min(t + 97, T))
+            mla.rotary(x[rows], None, i32(pos[:, rows]), turns, ax, neighbours=neighbours, q_out=out[rows])
+        want, tol = ref.rotate(f64(x[some]), pos[:, some], f, axes, neighbours)
+        close(out[some], want, tol)
+        parts.append(out)
+    if inplace:
+        got = mla.rotary(q, k, i32(pos), turns, ax, neighbours=neighbours)
+    else:
+        got = mla.rotary(q, k, i32(pos), turns, ax, neighbours=neighbours, q_out=torch.zeros_like(q), k_out=torch.zeros_like(k))
+    assert torch.equal(got[0], parts[0]) and torch.equal(got[1], parts[1])
+    assert mla.get_device_error() == 0
+
+
+@pytest.mark.parametrize("T,H,Hkv,D,R", [(4100, 64, 8, 80, 40), (2500, 90, 6, 128, 64), (6000, 2, 2, 128, 128)])
+def test_rotary_write_of_many_rows(T, H, Hkv, D, R):
+    """The keys and values of a call are the rotary's, in the rows that the slots name; the others stay."""
+    r = np.random.default_rng(T)
+    q, k, v = rand((T, H, D), 1), rand((T, Hkv, D), 2), rand((T, Hkv, D), 3)
+    pos, turns = i32(r.integers(0, 1 << 17, T)), mla.rotary_turns(freqs(R // 2))
+    slots = r.permutation(2 * T)[:T].astype(np.int32)
+    slots[::7] = -1
+    kc, vc = (torch.full((2 * T, Hkv, D), 7.0, dtype=BF).cuda() for _ in range(2))
+    want_q, want_k = mla.rotary(q.clone(), k.clone(), pos, turns)
+    got = mla.rotary_write(q, k, v, pos, turns, i32(slots), kc, vc, q_out=torch.zeros_like(q))
+    at = torch.as_tensor(slots[slots >= 0].astype(np.int64)).cuda()
+    there = torch.as_tensor(slots >= 0).cuda()
+    assert torch.equal(got, want_q)
+    assert torch.equal(kc[at], want_k[there]) and torch.equal(vc[at], v[there])
+    rest = torch.ones(2 * T, dtype=torch.bool).cuda()
+    rest[at] = False
+    assert (kc[rest] == 7).all() and (vc[rest] == 7).all()
+    assert mla.get_device_error() == 0
+
+
 def test_rotary_bad_axis_is_recorded():
     x, f = rand((3, 1, 8), 1), freqs(4)
     mla.rotary(x, None, i32(np.zeros((2, 3))), mla.rotary_turns(f), i32([0, 1, 2, -1]))
