@@ -197,6 +197,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
     const int64_t all = units * p.num_reqs, want = most * p.num_reqs / kMinChunk > all ? most * p.num_reqs / kMinChunk : all;
     const int grid = static_cast<int>(want < kMaxCtas ? want : kMaxCtas);
     p.few = all <= grid;
+    p.may_twin = blocks > 1 && grid > 1;
     const bool merge = grid > 1 && !(p.few && tiles <= whole_tiles(W));  // units may be cut
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const mla_status s =

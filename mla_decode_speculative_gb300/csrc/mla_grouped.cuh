@@ -27,7 +27,8 @@
 //    a warp issues each product, and the stream of tiles runs on from part to part.
 //  * Balanced split: a unit (request, group, row block) is kOverhead positions
 //    and then its tiles; the positions of all units, laid end to end, are cut
-//    into equal chunks, one per SM (a few short units: a chunk each).  A chunk holds at most two units that it
+//    into equal chunks, one per SM, or per two that have a group's row blocks between
+//    them (a few short units: a chunk each).  A chunk holds at most two units that it
 //    does not hold whole: its first and its last.  So there are two partial
 //    records per SM, whatever the batch, and the merge looks at 152 chunks.
 //  * Softmax: a thread has one token and the 16 columns of its group of warps (32
@@ -78,8 +79,9 @@ __host__ __device__ constexpr int whole_tiles(int W) { return W == 4 ? 4 : 8; }
 // A unit that is cut across chunks: written by the chunk with its first tile.
 struct Meta {
   int q0, qlen, g, rb;
-  int last;  // chunk of its last tile; -1: no such unit starts in this chunk
-  int pad[3];
+  int last;  // CTA that has its last tile; -1: no such unit starts in this one's chunk
+  int step;  // from a CTA with a part to the next
+  int pad[2];
 };
 
 struct Params {
@@ -88,9 +90,9 @@ struct Params {
   float *lse;
   const float *lambda, *gain;
   float eps;
-  float *part_o;     // [chunk][2][NC][64 W] unnormalised outputs
-  float *part_stat;  // [chunk][2][2][NC] base-2 maxima, sums
-  Meta *meta;        // [chunk]
+  float *part_o;     // [CTA][2][NC][64 W] unnormalised outputs
+  float *part_stat;  // [CTA][2][2][NC] base-2 maxima, sums
+  Meta *meta;        // [CTA]
   int *err;
   long long wait_budget, drain_budget;
   float scale_log2;
@@ -102,6 +104,7 @@ struct Params {
   int heads_per_block;  // query heads of a row block: group, or NR if group > NR
   int one_block;        // every request has one row block
   int few;              // no more units than CTAs
+  int may_twin;         // a request may have several row blocks
   int head_blocks;      // row blocks a verify row's group is cut into (1 if group <= NR)
 };
 
@@ -155,8 +158,13 @@ struct Config {
   static_assert(kTmemUsed <= 512 && kNR % 16 == 0 && kKSlots >= kNS && kSmem <= 232448, "configuration");
 };
 
-// The first unit that a chunk meets: its request, group and row block, its
-// position, its positions, and the request's row blocks.
+// Row blocks of the CTAs of a chunk: of two, one has the even and one the odd ones.
+__device__ __forceinline__ int rounds_of(const Params &p, int qlen, int twin) {
+  return p.one_block ? 1 : (blocks_of(p, qlen) + twin) >> twin;
+}
+
+// The first unit that a chunk meets: its request, group and round of row blocks,
+// its position, its positions, and the request's rounds.
 struct Place {
   int b, g, rb, s, per, blocks;
 };
@@ -185,6 +193,7 @@ struct Walk {
   int b, g, rb, s, per, blocks, tiles;
   int4 req;
   __device__ __forceinline__ void begin(const Misc &m, int a, int e);
+  template <bool kTwin>  // there may be several row blocks
   __device__ __forceinline__ bool next(const Params &p, const Misc &m, Part &o);
 };
 
@@ -212,6 +221,7 @@ struct Misc {
   Walk walk;                              // the softmax warps'
   Place place;                            // where this chunk begins
   int whole;                              // a chunk is a unit: one position each
+  int twin;                               // 1: two CTAs share a chunk, each with its row blocks
   alignas(16) float red[2][4][32];        // [group of warps][warp][column]
   Columns cols[2];                        // of the even and odd parts
 };
@@ -230,12 +240,19 @@ __device__ __forceinline__ void Walk::begin(const Misc &m, int a, int e) {
   tiles = tiles_of(req);
 }
 
+template <bool kTwin>
 __device__ __forceinline__ bool Walk::next(const Params &p, const Misc &m, Part &o) {
+  const int twin = kTwin && p.may_twin ? m.twin : 0;
   while (s < pos_e) {
     const int first = s + kOverhead, n = tiles;
     const int a = m.whole ? 0 : max(pos_a - first, 0), e = m.whole ? n : min(pos_e - first, n);
-    const bool take = n > 0 ? e > a : s >= pos_a;
-    if (take) o = Part{b, g, rb, req.z, req.w, req.x, req.y, req.x / kTile, n == 0 ? 0 : a, n == 0 ? 0 : e, n, s};
+    int block = kTwin ? rb : 0;
+    bool take = n > 0 ? e > a : s >= pos_a;
+    if (twin) {
+      block = 2 * rb + static_cast<int>(blockIdx.x & 1);
+      take = take && block < blocks_of(p, req.w);
+    }
+    if (take) o = Part{b, g, block, req.z, req.w, req.x, req.y, req.x / kTile, n == 0 ? 0 : a, n == 0 ? 0 : e, n, s};
     s += per;
     if (++rb == blocks) {
       rb = 0;
@@ -244,7 +261,7 @@ __device__ __forceinline__ bool Walk::next(const Params &p, const Misc &m, Part 
         do ++b;
         while (m.start[b + 1] <= s);
         req = m.req[b];
-        blocks = p.one_block ? 1 : blocks_of(p, req.w);
+        blocks = kTwin ? rounds_of(p, req.w, twin) : 1;
         tiles = tiles_of(req);
         per = m.whole ? 1 : tiles + kOverhead;
       }
@@ -418,6 +435,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   // warps behind the softmax: copies of K and Q, copies of V, products with K, products with V
   constexpr int kCopyK = C::kSoftmaxWarps, kCopyV = kCopyK + 1, kMmaK = kCopyK + 2, kMmaV = kCopyK + 3;
   constexpr int kSoftmaxThreads = 32 * C::kSoftmaxWarps;
+  constexpr bool kTwin = kNC == 64;  // fewer columns hold all rows of a group
 
   if (warp == kMmaK) {
     tmem_alloc(smem_u32(&misc.tmem_base), C::kTmemCols);
@@ -483,17 +501,41 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       low &= tiles <= whole_tiles(kW);
       cost = (p.one_block ? 1 : blocks_of(p, q1 - q0)) * p.num_kv_heads * (tiles + kOverhead);
     }
-    misc.req[b] = make_int4(lo, hi, q0, q1 - q0);
+    misc.req[b] = make_int4(lo, hi, q0, cost > 0 ? q1 - q0 : 0);
     misc.start[b + 1] = cost;
   }
   if (threadIdx.x == 0) misc.start[0] = 0;
   const bool whole = __syncthreads_and(low) != 0 && p.few;
-  if (warp == 0) {  // running sum, in place
-    int carry = 0;
+  if (warp == 0) {
+    int twin = 0, carry = 0;
+    // Row blocks of a group read the same keys and values.  Two CTAs share a chunk, one
+    // with the even and one with the odd blocks, where these are about as many (the odd
+    // block of a request leaves one idle): they go over the tokens together, and the
+    // second read is L2's.  16 requests of 16,384 tokens, 128 rows of 4 groups of 128 dims
+    // 172 -> 126 us, of two maps 324 -> 232; at 1.25 instead of 1.1 64 requests of 3-8 x 16
+    // rows 146 -> 139, but 24 ragged ones of 1-8 x 16 78 -> 87.
+    if (kTwin && p.may_twin) {
+      float single = 0.0f, pairs = 0.0f;
+      for (int b = lane; b < p.num_reqs; b += 32) {
+        const int4 req = misc.req[b];
+        const int blocks = blocks_of(p, req.w), positions = req.w > 0 ? tiles_of(req) + kOverhead : 0;
+        single += static_cast<float>(blocks) * positions;
+        pairs += static_cast<float>((blocks + 1) / 2) * positions;
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        single += __shfl_xor_sync(0xffffffffu, single, o);
+        pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+      }
+      twin = !whole && 2.0f * pairs <= 1.1f * single;
+      if (lane == 0) misc.twin = twin;
+    }
+    // running sum, in place
     for (int base = 0; base < p.num_reqs; base += 32) {
       const int b = base + lane;
       int x = b < p.num_reqs ? misc.start[b + 1] : 0;
       if (whole && x > 0) x = blocks_of(p, misc.req[b].w) * p.num_kv_heads;
+      if (twin && x > 0) x = rounds_of(p, misc.req[b].w, 1) * p.num_kv_heads * (tiles_of(misc.req[b]) + kOverhead);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -506,8 +548,9 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
   __syncthreads();
   // chunks 0 .. rest - 1 have size + 1 positions, the others size
   const unsigned total = misc.start[p.num_reqs];
-  const unsigned chunks = max(1u, min(gridDim.x, whole ? total : total / kMinChunk)), size = total / chunks, rest = total - size * chunks;
-  const unsigned chunk = blockIdx.x;
+  const int twin = kTwin && p.may_twin ? misc.twin : 0;
+  const unsigned chunks = max(1u, min(gridDim.x >> twin, whole ? total : total / kMinChunk)), size = total / chunks, rest = total - size * chunks;
+  const unsigned chunk = blockIdx.x >> twin;
   auto cut = [&](unsigned c) { return static_cast<int>(c * size + min(c, rest)); };
   auto chunk_of = [&](int x) {
     const unsigned big = rest * (size + 1), u = static_cast<unsigned>(x);
@@ -519,7 +562,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     const int from = misc.start[b];
     if (from <= pos_a && pos_a < misc.start[b + 1]) {  // one request at most
       const int4 req = misc.req[b];
-      const int per = whole ? 1 : tiles_of(req) + kOverhead, blocks = p.one_block ? 1 : blocks_of(p, req.w);
+      const int per = whole ? 1 : tiles_of(req) + kOverhead, blocks = rounds_of(p, req.w, twin);
       const int j = (pos_a - from) / per, g = blocks == 1 ? j : j / blocks;
       misc.place = Place{b, g, j - g * blocks, from + j * per, per, blocks};
     }
@@ -559,7 +602,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     walk.begin(misc, pos_a, pos_e);
     Part w;
     uint32_t t = 0, kq = 0;
-    while (ok && walk.next(p, misc, w)) {
+    while (ok && walk.next<kTwin>(p, misc, w)) {
       if (w.e == w.a) continue;
       // a lane holds a box of the tile, and reads the next tile's page id ahead of the waits
       const int32_t *ids = p.subpage_table + static_cast<int64_t>(w.b) * p.subpage_stride;
@@ -626,7 +669,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       walk.begin(misc, pos_a, pos_e);
       Part w;
       uint32_t t = 0, kq = 0;
-      while (ok && walk.next(p, misc, w)) {
+      while (ok && walk.next<kTwin>(p, misc, w)) {
         if (w.e == w.a) continue;
         const uint32_t qb = kq % C::kQBufs;
         if (!wait(smem_u32(&misc.q_full[qb]), (kq / C::kQBufs) & 1u)) break;
@@ -672,7 +715,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       walk.begin(misc, pos_a, pos_e);
       Part w;
       uint32_t t = 0;
-      while (ok && walk.next(p, misc, w)) {
+      while (ok && walk.next<kTwin>(p, misc, w)) {
         for (int i = w.a; i < w.e; ++i, ++t) {
           if (!wait(smem_u32(&misc.p_full[t & 1u]), (t >> 1) & 1u)) break;
           const int tok = (w.tile0 + i) * kTile;
@@ -713,13 +756,13 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     const int row = wq * 32 + lane;                // token of the tile; lane of TMEM
     const uint32_t grp_bar = 1 + grp, all_bar = 3;
     uint32_t t = 0;
-    Meta meta{0, 0, 0, 0, -1, {}};
+    Meta meta{0, 0, 0, 0, -1, 1, {}};
     const int my_col = col0 + lane % N;
     bool valid = false;
     int my_lo = 0, my_hi = 0, ct = 0, ch = 0, cur_b = -1, cur_rb = -1;
     if (threadIdx.x == 0) {
       misc.walk.begin(misc, pos_a, pos_e);
-      misc.cols[0].more = misc.walk.next(p, misc, misc.cols[0].part);
+      misc.cols[0].more = misc.walk.next<kTwin>(p, misc, misc.cols[0].part);
     }
     named_bar_sync(all_bar, kSoftmaxThreads);
     for (int n_part = 0;; ++n_part) {
@@ -931,7 +974,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       // ---- the part's result
       if (threadIdx.x == 0) {  // the next part, beside the last product; read behind this result's barrier
         Columns &then = misc.cols[(n_part + 1) & 1];
-        then.more = misc.walk.next(p, misc, then.part);
+        then.more = misc.walk.next<kTwin>(p, misc, then.part);
       }
       if (w.e > w.a) wait(smem_u32(&misc.o_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u);
       {
@@ -977,7 +1020,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         for (int k = 0; k < 16; ++k) o[k] += u[k];
       };
       if (!whole) {
-        const int64_t rec = static_cast<int64_t>(chunk) * 2 + (w.a == 0 ? 1 : 0);
+        const int64_t rec = static_cast<int64_t>(blockIdx.x) * 2 + (w.a == 0 ? 1 : 0);
         if (wq == 0 && lane < N) {
           p.part_stat[rec * 2 * kNC + my_col] = cols.stat_m[my_col];
           p.part_stat[rec * 2 * kNC + kNC + my_col] = cols.stat_l[my_col];
@@ -996,7 +1039,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
                        isnan(y) ? y : o[c]);
             }
           }
-        if (w.a == 0) meta = Meta{w.q0, w.qlen, w.g, w.rb, chunk_of(w.start + kOverhead + w.n - 1), {}};
+        if (w.a == 0) {
+          const int twin = kTwin && p.may_twin ? misc.twin : 0, last = chunk_of(w.start + kOverhead + w.n - 1);
+          meta = Meta{w.q0, w.qlen, w.g, w.rb, (last << twin) + static_cast<int>(blockIdx.x & twin), 1 + twin, {}};
+        }
       } else if (kMaps == 1) {
 #pragma unroll
         for (int s = 0; s < C::kBlocks; ++s)
@@ -1057,7 +1103,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       }
       tc_fence_before();
     }
-    if (threadIdx.x == 0) p.meta[chunk] = meta;
+    if (threadIdx.x == 0) p.meta[blockIdx.x] = meta;
   }
   tc_fence_before();
   __syncthreads();

@@ -40,10 +40,10 @@ __global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __
   grid_dep_launch();
   const int first = static_cast<int>(blockIdx.x), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 u = *reinterpret_cast<const int4 *>(p.meta + first);  // q0, qlen, g, rb
-  const int last = p.meta[first].last;
+  const int last = p.meta[first].last, step = p.meta[first].step;
   if (last < 0) return;
   const int m = kMaps == 2 ? warp & 1 : 0, slot = warp / kMaps;  // the warps of a row lie together
-  const int parts = last - first + 1, c = static_cast<int>(blockIdx.y) * kMergeRows + slot;
+  const int parts = (last - first) / step + 1, c = static_cast<int>(blockIdx.y) * kMergeRows + slot;
   int t, h;
   const bool there = column_row(p, u.w, c, u.y, t, h);
   if (!there) {
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __
   }
   h += u.z * p.group;
   const int64_t row = (static_cast<int64_t>(u.x) + t) * p.num_heads + h;
-  auto record = [&](int i) { return (static_cast<int64_t>(first) + i) * 2 + (i == 0 ? 1 : 0); };
+  auto record = [&](int i) { return (static_cast<int64_t>(first) + i * step) * 2 + (i == 0 ? 1 : 0); };
   const float *stats = p.part_stat + m * kNR + c;
   const float *outs = p.part_o + (m * kNR + c) * kDv + lane * kV;
   const float m0 = lane < parts ? stats[record(lane) * 2 * kNC] : kLowest;

@@ -427,6 +427,23 @@ def test_strides_of_queries_and_caches():
     assert torch.equal(out, want) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("maps,L,ql,H,Hkv,D,bs,window", [
+    (1, [700] * 6, [8] * 6, 64, 4, 128, 16, 0),                    # two row blocks each
+    (1, [9000, 20, 300, 5000, 64, 1], [8, 8, 8, 8, 8, 1], 64, 4, 64, 64, 0),   # and one with one
+    (1, [130, 1500] * 9, [8, 8] * 8 + [3, 8], 64, 4, 64, 32, 100),
+    (1, [2500] * 3, [1] * 3, 128, 1, 128, 128, 0),                 # a row's heads in two blocks
+    (1, [400] * 5, [3] * 5, 100, 1, 256, 8, 0),                    # in two of unequal size
+    (1, [3000] * 2, [11] * 2, 64, 1, 64, 16, 0),                   # eleven blocks: the last one alone
+    (1, [3000] * 3, [3] * 3, 64, 1, 64, 16, 0),                    # three: not in twos
+    (2, [1800] * 4, [8] * 4, 16, 2, 64, 64, 0), (2, [900, 4000, 77], [16, 16, 16], 8, 2, 128, 16, 300)])
+def test_row_blocks_that_share_their_keys(maps, L, ql, H, Hkv, D, bs, window):
+    """More rows of a group than a product holds, cut into several parts, with rows that see nothing."""
+    s = State(L, ql, H, Hkv, D, bs, maps=maps, joint=False, seed=len(L) + H, spare=2)
+    for k in range(0, s.ind[-1], 13):
+        s.row_len[k] = 0
+    s.check(window)
+
+
 @pytest.mark.parametrize("maps,D,H,Hkv,L,n", [
     (1, 64, 16, 4, [5000, 120, 1, 2222], 2), (2, 64, 16, 4, [5000, 120, 1, 2222], 2), (1, 256, 12, 4, [623] * 60, 1),
     (1, 256, 24, 4, [562] * 35, 4), (1, 256, 40, 4, [562] * 35, 4), (2, 128, 56, 8, [562] * 35, 4), (2, 128, 7, 1, [100 + 37 * i for i in range(60)], 3),
