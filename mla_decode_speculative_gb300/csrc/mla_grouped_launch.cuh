@@ -73,9 +73,11 @@ __global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __
   float sum = 0.0f;
   for (int i = lane; i < parts; i += 32) {
     const float mi = i < 32 ? m0 : stats[record(i) * 2 * kNC], li = i < 32 ? l0 : stats[record(i) * 2 * kNC + kNC];
-    const float w = li == 0.0f ? 0.0f : exp2f(mi - top);
+    // -1: the row saw nothing in this part, whose outputs are no numbers.  A weight of zero is one
+    // like any other: outputs that are not finite reach the row through it.
+    const float w = li == 0.0f ? -1.0f : exp2f(mi - top);
     weight[warp][i] = w;
-    sum += w * li;
+    sum += li == 0.0f ? 0.0f : w * li;
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -84,12 +86,12 @@ __global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __
   float y[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) y[k] = 0.0f;
-  for (int base = 0;;) {  // a part in which the row saw nothing holds no numbers
+  for (int base = 0;;) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const float w = base + i < parts ? weight[warp][base + i] : 0.0f;
+      const float w = base + i < parts ? weight[warp][base + i] : -1.0f;
 #pragma unroll
-      for (int k = 0; k < kV; ++k) y[k] += w == 0.0f ? 0.0f : w * ahead[i][k];
+      for (int k = 0; k < kV; ++k) y[k] += w < 0.0f ? 0.0f : w * ahead[i][k];
     }
     base += kAhead;
     if (base >= parts) break;

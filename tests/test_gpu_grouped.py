@@ -389,6 +389,42 @@ def test_nan_reaches_the_rows_that_see_its_token(what, window):
                 assert torch.equal(out[r, h], clean[r, h]) and torch.equal(lse[r, h], clean_lse[r, h]), (r, h)
 
 
+@pytest.mark.parametrize("what", ["seen_by_all", "seen_by_some", "infinite"])
+@pytest.mark.parametrize("copies", [1, 150])
+@pytest.mark.parametrize("maps", [1, 2])
+def test_value_that_is_not_finite_in_a_part_of_vanishing_weight(maps, copies, what):
+    """The later half of the keys scores 160 e-folds (230 powers of two) above the earlier one, whose parts'
+    weights are zero in float32; a value of the earlier half that is not finite still reaches the rows that see
+    it, wherever the split falls: one request (every unit cut), and 150 copies of it (most units whole)."""
+    n, j, D = 6000, 1000, 64
+    s = State([n], [2], 4, 2, D, 16, maps=maps, seed=30)
+    if what == "seen_by_some":
+        s.row_len[0] = 940                     # inside the token's tile
+    at = s.table[0][np.arange(n) // s.P].astype(np.int64) * s.P + np.arange(n) % s.P
+    rows = torch.as_tensor(at).cuda()
+    s.k[rows] = (0.1 * s.k[rows].float()).to(BF)
+    s.k[rows[3000:]] = 5.0
+    s.q[:] = 4.0                               # scores: 8^-1 * 64 * 4 * 5 = 160
+    s.table, s.row_len = np.repeat(s.table, copies, 0), np.tile(s.row_len, copies)
+    s.q, s.ind, s.T = s.q.repeat(copies, *([1] * (s.q.dim() - 1))), np.arange(copies + 1) * 2, 2 * copies
+    clean, clean_lse = s.run()
+    assert torch.isfinite(clean).all()
+    s.v[rows[j], 1, 5] = math.inf if what == "infinite" else math.nan
+    out, lse = s.run()
+    assert torch.equal(lse, clean_lse)
+    for r in range(s.T):
+        assert torch.equal(out[r, :2], clean[r, :2])
+        if s.row_len[r] <= j:
+            assert torch.equal(out[r], clean[r])
+        elif what == "seen_by_some":
+            assert torch.isnan(out[r, 2:]).all()
+        else:
+            assert not torch.isfinite(out[r, 2:, 5]).any()
+            keep = [d for d in range(maps * D) if d != 5]
+            assert torch.equal(out[r, 2:, keep], clean[r, 2:, keep])
+    assert mla.get_device_error() == 0
+
+
 def test_query_that_is_not_finite_spoils_its_own_row():
     s = State([300], [4], 8, 2, 128, 16, seed=8)
     clean, _ = s.run()
