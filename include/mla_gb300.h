@@ -556,7 +556,8 @@ size_t mla_decode_grouped_workspace(const mla_grouped_args *a, int differential)
  * those that see it become NaN in all of their dims.
  * Device checks: MLA_DEV_BAD_INDPTR (the request's rows are left as they were),
  * MLA_DEV_LEN_BOUND (row_len > subpage_stride * P: clipped),
- * MLA_DEV_BAD_SUBPAGE (the page is read as zeros), MLA_DEV_WAIT_TIMEOUT. */
+ * MLA_DEV_BAD_SUBPAGE (the page is read as zeros), MLA_DEV_WAIT_TIMEOUT (a row
+ * and head is right or left as it was, out and lse alike). */
 mla_status mla_decode_grouped(const mla_grouped_args *a, void *workspace, size_t workspace_bytes,
                               mla_stream_t stream);
 

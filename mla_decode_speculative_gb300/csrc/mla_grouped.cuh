@@ -41,7 +41,8 @@
 //    is looked at, and a value in it that is not finite is zeroed too and
 //    spoils the rows that see it (0 x NaN would spoil the others).
 //  * Every wait is bounded; one that runs out records MLA_DEV_WAIT_TIMEOUT, all
-//    roles end, copies in flight land, TMEM is freed.
+//    roles end, copies in flight land, TMEM is freed.  Neither the part at hand
+//    nor a unit with such a part is stored: its rows are left as they were.
 //
 // Measured (calls in a graph): 32 requests of 1,024-8,192 tokens, 8 key heads of
 // 128, 92-95 us (593 MB: 6.3 TB/s, 0.92-0.95 of a copy's rate); 4 x 131,072, 4 key
@@ -81,7 +82,8 @@ struct Meta {
   int q0, qlen, g, rb;
   int last;  // CTA that has its last tile; -1: no such unit starts in this one's chunk
   int step;  // from a CTA with a part to the next
-  int pad[2];
+  int sound; // of this CTA's chunk: all of its parts are there (0: a wait gave up before the last one)
+  int pad;
 };
 
 struct Params {
@@ -756,7 +758,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     const int row = wq * 32 + lane;                // token of the tile; lane of TMEM
     const uint32_t grp_bar = 1 + grp, all_bar = 3;
     uint32_t t = 0;
-    Meta meta{0, 0, 0, 0, -1, 1, {}};
+    Meta meta{0, 0, 0, 0, -1, 1, 0, 0};
     const int my_col = col0 + lane % N;
     bool valid = false;
     int my_lo = 0, my_hi = 0, ct = 0, ch = 0, cur_b = -1, cur_rb = -1;
@@ -767,7 +769,10 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     named_bar_sync(all_bar, kSoftmaxThreads);
     for (int n_part = 0;; ++n_part) {
       Columns &cols = misc.cols[n_part & 1];
-      if (!cols.more) break;
+      if (!cols.more) {
+        meta.sound = 1;
+        break;
+      }
       const Part &w = cols.part;
       // what this lane's column sees; the groups of a request see the same
       if (w.b != cur_b || w.rb != cur_rb) {
@@ -999,14 +1004,17 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         cols.stat_l[my_col] = l;
         // 0: the row saw nothing, and what its column of O^T holds is not looked at
         cols.inv[my_col] = l == 0.0f ? 0.0f : (bad ? __int_as_float(0x7fffffff) : 1.0f / l);
-        if (w.a == 0 && w.e == w.n && valid) {
-          const int64_t at = static_cast<int64_t>(cols.row[my_col]) * kMaps + my_col / C::kNR;
-          p.lse[at] = l == 0.0f ? -INFINITY : (cols.stat_m[my_col] + log2f(l)) * kLn2;
-        }
       }
-      named_bar_sync(all_bar, kSoftmaxThreads);
+      // A part that any of these threads gave up on is not stored, nor are those behind it: what a
+      // wait guarded is stale, and the warps whose own waits ended multiplied it like the rest.
+      if (named_bar_red_or(all_bar, kSoftmaxThreads, !ok)) break;
       tc_fence_after();
       const bool whole = w.a == 0 && w.e == w.n;
+      if (whole && valid && wq == 0 && lane < N) {
+        const int64_t at = static_cast<int64_t>(cols.row[my_col]) * kMaps + my_col / C::kNR;
+        const float l = cols.stat_l[my_col];
+        p.lse[at] = l == 0.0f ? -INFINITY : (cols.stat_m[my_col] + log2f(l)) * kLn2;
+      }
       // dim of this thread in block s of O^T: an M = 64 result has its rows in lanes 0-15 of each warp
       const bool has_dim = kW >= 2 || lane < 16;
       const int dim = kW >= 2 ? row : wq * 16 + lane;
@@ -1041,7 +1049,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           }
         if (w.a == 0) {
           const int twin = kTwin && p.may_twin ? misc.twin : 0, last = chunk_of(w.start + kOverhead + w.n - 1);
-          meta = Meta{w.q0, w.qlen, w.g, w.rb, (last << twin) + static_cast<int>(blockIdx.x & twin), 1 + twin, {}};
+          meta = Meta{w.q0, w.qlen, w.g, w.rb, (last << twin) + static_cast<int>(blockIdx.x & twin), 1 + twin, 0, 0};
         }
       } else if (kMaps == 1) {
 #pragma unroll

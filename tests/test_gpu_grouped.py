@@ -587,6 +587,33 @@ def test_waits_that_run_out_are_recorded(maps, D):
     assert torch.equal(out, want) and torch.equal(l, lse) and mla.get_device_error() == 0
 
 
+@pytest.mark.parametrize("maps,L,ql,H,Hkv,D", [
+    (1, [3000, 200, 1000], [4, 1, 2], 16, 4, 64), (1, [9000, 40, 300, 5000], [1, 2, 1, 1], 8, 4, 256),
+    (1, [2500] * 6, [8] * 6, 64, 4, 128), (1, [300 + 90 * i for i in range(64)], [1] * 64, 16, 8, 128),
+    (2, [3000, 200, 1000], [4, 1, 2], 16, 4, 64), (2, [120 + 90 * i for i in range(64)], [2] * 64, 16, 8, 64),
+    (2, [20000, 900], [4, 4], 32, 4, 128)])
+def test_waits_that_run_out_leave_rows_as_they_were_or_right(maps, L, ql, H, Hkv, D):
+    """Wait budgets from one that no copy meets to one that some do: every row and head is what it was before
+    the call or what a call that ran through gives, output and sum alike."""
+    s = State(L, ql, H, Hkv, D, 16, maps=maps, seed=31)
+    want, want_lse = s.run()
+    gave_up = 0
+    for cycles in (1, 1, 500, 2000, 4000, 8000, 16000, 32000):
+        out = torch.full((s.T, H, maps * D), 3.0, dtype=BF).cuda()
+        lse = torch.full((s.T, H) + (2,) * (maps - 1), 5.0).cuda()
+        s.run(out=out, lse=lse, wait_cycles=cycles)
+        code = mla.get_device_error()
+        assert code in (0, 6)
+        same = (out == want).all(-1) & (lse == want_lse).reshape(s.T, H, -1).all(-1)
+        kept = (out == 3).all(-1) & (lse == 5).reshape(s.T, H, -1).all(-1)
+        assert (same | kept).all(), f"{cycles} cycles: {int((~(same | kept)).sum())} of {s.T * H} rows and heads"
+        assert code == 6 or same.all()
+        gave_up += code == 6
+    assert gave_up >= 2
+    out, lse = s.run()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and mla.get_device_error() == 0
+
+
 def test_two_captured_graphs_with_a_workspace_each():
     """Two calls captured apart, replayed at the same time on two streams, over and over."""
     states = [State([4000, 700], [2, 2], 16, 4, 128, 32, seed=20), State([3000, 2500, 10], [1, 1, 1], 8, 2, 64, 16, maps=2, seed=21)]
