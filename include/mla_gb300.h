@@ -551,9 +551,12 @@ size_t mla_decode_grouped_workspace(const mla_grouped_args *a, int differential)
  * q, k_cache and v_cache are 16-byte aligned with rows a multiple of 8
  * elements apart; num_cache_rows is a multiple of 8.
  * Keys and values that no row of a request sees are never used as numbers.  A
- * key that is not finite reaches the rows that see its token only; so does a
- * value, but where some rows of the request see its token and others do not,
- * those that see it become NaN in all of their dims.
+ * key that is not finite reaches the rows that see its token only (a row whose
+ * scores are all minus infinity counts as one that sees nothing); so does a
+ * value: its dim of those rows is not finite.  An infinite value gives infinity
+ * there, as the sum above does, or NaN if its probability rounds to zero.  Where
+ * some rows of the request see the token and others do not, those that see it
+ * may become NaN in all of their dims.
  * Device checks: MLA_DEV_BAD_INDPTR (the request's rows are left as they were),
  * MLA_DEV_LEN_BOUND (row_len > subpage_stride * P: clipped),
  * MLA_DEV_BAD_SUBPAGE (the page is read as zeros), MLA_DEV_WAIT_TIMEOUT (a row

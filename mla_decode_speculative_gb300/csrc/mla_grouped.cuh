@@ -1018,14 +1018,16 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       // dim of this thread in block s of O^T: an M = 64 result has its rows in lanes 0-15 of each warp
       const bool has_dim = kW >= 2 || lane < 16;
       const int dim = kW >= 2 ? row : wq * 16 + lane;
-      // columns c .. c + 15 of block s: the sum of both terms
+      // columns c .. c + 15 of block s: the sum of both terms.  Where the first is infinite the
+      // second is not looked at: a probability's second term may be zero or negative, and its
+      // product with an infinite value is not that value's.
       auto load_o = [&](int s, int c, float (&o)[16]) {
         float u[16];
         const uint32_t addr = tmem + lane_addr + C::kTmemO + C::kPN * s + c;
         tmem_load<16>(addr, o);
         tmem_load<16>(addr + kNC, u);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] += u[k];
+        for (int k = 0; k < 16; ++k) o[k] = fabsf(o[k]) == INFINITY ? o[k] : o[k] + u[k];
       };
       if (!whole) {
         const int64_t rec = static_cast<int64_t>(blockIdx.x) * 2 + (w.a == 0 ? 1 : 0);

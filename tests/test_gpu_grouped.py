@@ -425,6 +425,33 @@ def test_value_that_is_not_finite_in_a_part_of_vanishing_weight(maps, copies, wh
     assert mla.get_device_error() == 0
 
 
+@pytest.mark.parametrize("L,ql,H,Hkv,D,bs", [
+    ([700], [3], 8, 2, 64, 16), ([900, 30], [1, 4], 16, 4, 128, 64), ([400], [8], 64, 4, 128, 16),
+    ([500, 60], [2, 2], 8, 1, 256, 32), ([20000], [2], 8, 2, 128, 16)])
+def test_infinite_value_is_infinite_in_its_dim(L, ql, H, Hkv, D, bs):
+    """A value of plus or minus infinity at tokens that all rows of the request see: infinite in that dim, as the
+    weighted sum is; both in one dim: NaN; every other number as it was.  In units that are cut and whole ones."""
+    s = State(L, ql, H, Hkv, D, bs, seed=32)
+    s.q *= 0.5                                 # no weight that rounds to zero
+    clean, clean_lse = s.run()
+    at = lambda b, j: int(s.table[b][j // s.P]) * s.P + j % s.P  # noqa: E731
+    g = Hkv - 1
+    for j, d, x in ((3, 5, math.inf), (L[0] // 2, D - 1, -math.inf), (L[0] - ql[0] - 1, 5, math.inf),
+                    (7, 11, math.inf), (L[0] // 2 + 1, 11, -math.inf)):
+        s.v[at(0, j), g, d] = x
+    out, lse = s.run()
+    assert torch.equal(lse, clean_lse)
+    want, per = clean.clone(), H // Hkv
+    want[:ql[0], g * per:, 5], want[:ql[0], g * per:, D - 1] = math.inf, -math.inf
+    want[:ql[0], g * per:, 11] = math.nan
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(nan=0.0, posinf=1e9, neginf=-1e9), want.nan_to_num(nan=0.0, posinf=1e9, neginf=-1e9))
+    o, tol, l, ltol = s.want()
+    close(out, o, tol, "out")
+    close(lse, l.reshape(lse.shape), ltol.reshape(lse.shape), "lse")
+    assert mla.get_device_error() == 0
+
+
 def test_query_that_is_not_finite_spoils_its_own_row():
     s = State([300], [4], 8, 2, 128, 16, seed=8)
     clean, _ = s.run()
