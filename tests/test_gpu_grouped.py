@@ -547,6 +547,27 @@ def test_device_checks():
         assert mla.get_device_error() == 1
 
 
+@pytest.mark.parametrize("maps", [1, 2])
+@pytest.mark.parametrize("ind,good", [([0, 2, 1], None), ([0, 1, 9], 0), ([-1, 1, 2], 1), ([0, 1, 2], 1)])
+def test_requests_with_wrong_offsets_leave_their_rows(maps, ind, good):
+    """The rows of a request that the device checks refuse hold what they held, outputs and sums; the other
+    request's are right."""
+    s = State([100, 100], [1, 1], 4, 2, 64, 16, maps=maps, seed=33)
+    full, full_lse = s.run()
+    s.ind = np.array(ind)
+    out = torch.full((2, 4, maps * 64), 3.0, dtype=BF).cuda()
+    lse = torch.full((2, 4) + (2,) * (maps - 1), 5.0).cuda()
+    if ind == [0, 2, 1]:
+        s.qmax = 1                             # two rows are above the bound of one, and the next offset goes back
+    s.run(out=out, lse=lse)
+    assert mla.get_device_error() == (0 if ind == [0, 1, 2] else 1)
+    for r in range(2):
+        if ind == [0, 1, 2] or r == good:
+            assert torch.equal(out[r], full[r]) and torch.equal(lse[r], full_lse[r])
+        else:
+            assert (out[r] == 3).all() and (lse[r] == 5).all()
+
+
 def test_another_stream_and_its_own_workspace():
     s = State([900, 20], [2, 2], 8, 2, 128, 16, seed=13)
     want, lse = s.run()
