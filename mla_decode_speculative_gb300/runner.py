@@ -158,7 +158,8 @@ class _PagedBlocks:
         suffice for (MLA_DEV_NO_FREE_BLOCK), before appending less.  An append that is left so
         counts the blocks that were not there as held, and they go back to the free ones as -1.
         The rows that an undone append wrote stay written, so a request's next new tokens start
-        no later than they did in it."""
+        no later than they did in it; queries that it rotated in place stay rotated
+        (PagedKVCache.append's q_out)."""
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
             self._now.copy_(self._before)
@@ -218,7 +219,9 @@ class PagedKVCache(_PagedBlocks):
         """The step's new tokens, as PagedLatentCache.append: rows of k_new and v_new [num_rows,
         ...] of the cache's head shapes, the keys and the queries q [num_rows, H, ...] rotated by
         positions, turns and axes (mla_rotary_write).  Returns the rotated queries, in q_out or in
-        place of q."""
+        place of q.  In place, a step that the device checks refuse or that undo takes back has
+        turned q all the same: what is appended again needs queries that are not rotated yet, so a
+        step that may be made again goes to a q_out."""
         if q.shape[0] != self.num_rows or k_new.shape[0] != self.num_rows or v_new.shape[0] != self.num_rows:
             raise ValueError("q, k_new and v_new must have num_rows rows")
         q_out = q if q_out is None else q_out

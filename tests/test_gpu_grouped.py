@@ -788,3 +788,33 @@ def test_drafting_steps(differential):
                                                np.arange(160)[None], 1, 50, f64(lam), f64(gain) if differential else None)
             close(out[at[b]:at[b + 1]], want, tol, f"step {n}")
             close(lse[at[b]:at[b + 1]], l, ltol, f"step {n}")
+
+
+@pytest.mark.parametrize("differential", [False, True])
+def test_kv_append_that_ran_out_of_blocks_is_undone_and_made_again(differential):
+    """Too few free blocks, undone, then appended again with the same queries: with q_out they and the keys are
+    those of a step that never failed."""
+    maps, D = 2 if differential else 1, 64
+    make = lambda: runner.PagedKVCache(num_reqs=2, num_rows=64, num_blocks=6, block_size=16, max_kv_len=96,  # noqa: E731
+                                       num_kv_heads=2, head_dim=D, differential=differential)
+    pair = (2,) if differential else ()
+    q, k = rand((64, 4) + pair + (D,), 1), rand((64, 2) + pair + (D,), 2)
+    v, pos, turns = rand((64, 2, maps * D), 3), i32(np.arange(64) * 31), mla.rotary_turns(freqs(D // 2))
+    q0, rest = q.clone(), (k, v, pos, turns)
+    c, never = make(), make()
+    for x in (c, never):
+        x.append(q, *rest, i32([40, 10]), i32([0, 40, 50]), q_out=torch.empty_like(q))
+    assert mla.get_device_error() == 0
+    held = c.ring.clone(), c.lens.clone()
+    q_out = torch.empty_like(q)
+    c.append(q, *rest, i32([70, 40]), i32([0, 30, 60]), q_out=q_out)
+    assert mla.get_device_error() == 7
+    c.undo()
+    assert torch.equal(c.ring, held[0]) and torch.equal(c.lens, held[1]) and torch.equal(q, q0)
+    got = c.append(q, *rest, i32([41, 40]), i32([0, 1, 31]), q_out=q_out)
+    want = never.append(q, *rest, i32([41, 40]), i32([0, 1, 31]), q_out=torch.empty_like(q))
+    assert mla.get_device_error() == 0 and torch.equal(got, want) and torch.equal(q, q0)
+    for x, y in ((c.slot_map, never.slot_map), (c.lens, never.lens)):
+        assert torch.equal(x, y)
+    at = c.slot_map[:31].long()
+    assert torch.equal(c.k[at], never.k[at]) and torch.equal(c.v[at], never.v[at])
