@@ -201,7 +201,8 @@ class PagedLatentCache(_PagedBlocks):
 class PagedKVCache(_PagedBlocks):
     """Keys and values of ``num_kv_heads`` groups, bf16, in the paged form of PagedLatentCache
     (blocks, lengths and capture alike): ``k`` [N, num_kv_heads, head_dim] and ``v``, or with
-    ``differential`` two keys of head_dim and one value of 2 head_dim per group."""
+    ``differential`` two keys of head_dim and one value of 2 head_dim per group.  GroupedStep reads
+    one that is not sharded, of the head and block sizes that it names; the rotary write fills any."""
 
     def __init__(self, *, num_reqs: int, num_rows: int, num_blocks: int, block_size: int, max_kv_len: int,
                  num_kv_heads: int, head_dim: int, differential: bool = False, world_size: int = 1, rank: int = 0,
@@ -236,8 +237,9 @@ class PagedKVCache(_PagedBlocks):
 class GroupedStep:
     """One attention of the model that drafts over a paged K/V cache: row plan and sub-page table
     (mla_plan_rows), then mla_decode_grouped, or mla_decode_differential with ``differential``.
-    Buffers are allocated once, by static bounds; a call launches kernels only and can be captured
-    in a CUDA graph."""
+    Heads of 64, 128 or 256 (differential: 64 or 128), blocks a multiple of 8 tokens; the cache holds
+    whole requests (a shard's rows are not planned for).  Buffers are allocated once, by static
+    bounds; a call launches kernels only and can be captured in a CUDA graph."""
 
     def __init__(self, *, num_reqs: int, num_rows: int, num_heads: int, num_kv_heads: int, head_dim: int,
                  max_qlen: int, block_size: int, num_blocks: int, max_kv_len: int, window: int = 0,
@@ -247,15 +249,21 @@ class GroupedStep:
         self.max_qlen, self.block_size, self.num_blocks, self.window = max_qlen, block_size, num_blocks, window
         self.differential = differential
         self.P = mla.page_size(block_size)
+        need = mla.decode_grouped_workspace_bytes(num_heads, num_kv_heads, max_qlen, head_dim, differential)
+        if not need:
+            raise ValueError(f"no attention of {num_heads} heads over {num_kv_heads} of {head_dim} values"
+                             f"{', two maps' * differential}, rows of up to {max_qlen}")
+        if self.P < 8:
+            raise ValueError(f"block_size {block_size} is not a multiple of 8 tokens")
+        if max_qlen > num_rows or window < 0:
+            raise ValueError(f"max_qlen {max_qlen} above num_rows {num_rows}, or window {window} below 0")
         self.sp_stride = max(1, -(-max_kv_len // self.P))
         self.row_len, self.row_req = torch.empty(num_rows, **i32), torch.empty(num_rows, **i32)
         self.subpage = torch.empty((num_reqs, self.sp_stride), **i32)
         width, maps = (2 * head_dim, (2,)) if differential else (head_dim, ())
         self.out = torch.empty((num_rows, num_heads, width), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((num_rows, num_heads) + maps, dtype=torch.float32, device=dev)
-        self.workspace = torch.empty(
-            max(1, mla.decode_grouped_workspace_bytes(num_heads, num_kv_heads, max_qlen, head_dim, differential)),
-            dtype=torch.uint8, device=dev)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
 
     def __call__(self, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seq_lens: torch.Tensor,
                  qo_indptr: torch.Tensor, block_table: torch.Tensor, sm_scale: float, lam=None, gain=None,

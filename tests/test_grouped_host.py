@@ -212,3 +212,16 @@ def test_step_and_cache_refusals():
     with pytest.raises(ValueError, match="lam"):
         step(x, cache.k, cache.v, None, None, None, 0.1, lam=torch.ones(2))
     assert cache.k.shape == (64, 2, 64) and np.prod(cache.v.shape) == 64 * 2 * 64
+
+
+@pytest.mark.parametrize("change", [
+    dict(head_dim=80), dict(head_dim=256, differential=True), dict(num_heads=3), dict(num_kv_heads=0), dict(max_qlen=0),
+    dict(block_size=4), dict(block_size=12), dict(block_size=0), dict(max_qlen=5), dict(window=-1)])
+def test_step_that_no_call_could_take_is_not_made(change):
+    """Sizes that the attention refuses are refused where the step is made, not at its first call."""
+    sizes = dict(num_reqs=1, num_rows=4, num_heads=4, num_kv_heads=2, head_dim=64, max_qlen=4, block_size=16, num_blocks=4,
+                 max_kv_len=64, device="cpu")
+    for D, bs, differential in ((64, 8, False), (128, 24, True), (256, 256, False)):
+        assert runner.GroupedStep(**{**sizes, "head_dim": D, "block_size": bs}, differential=differential).workspace.numel() > 1
+    with pytest.raises((ValueError, mla.MLAError)):
+        runner.GroupedStep(**{**sizes, **change})
