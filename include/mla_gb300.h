@@ -512,7 +512,7 @@ typedef struct mla_grouped_args {
   int window;            /* row r sees its last `window` tokens only; 0: all of them */
   float sm_scale;
   const void *q;         /* [T, H, D] bf16, rows q_row elements apart (differential: [T, H, 2, D]) */
-  int64_t q_row;
+  int64_t q_row;         /* (T == 1: any) */
   const void *k_cache;   /* [num_cache_rows, Hkv, D] bf16, rows k_row elements apart ([.., Hkv, 2, D]) */
   int64_t k_row;
   const void *v_cache;   /* [num_cache_rows, Hkv, D] bf16, rows v_row elements apart ([.., Hkv, 2 D]) */

@@ -34,6 +34,11 @@ Layout layout_of(const mla_grouped_args &a, bool differential) {
   return l;
 }
 
+// From a row of q to the next (of a single one whatever the caller's stride is).
+int64_t q_stride(const mla_grouped_args &a, bool differential) {
+  return a.num_rows > 1 ? a.q_row : static_cast<int64_t>(differential ? 2 : 1) * a.head_dim * a.num_heads;
+}
+
 bool sizes_ok(const mla_grouped_args &a, bool differential) {
   return a.num_heads >= 1 && a.num_kv_heads >= 1 && a.num_heads % a.num_kv_heads == 0 && a.max_qlen >= 1 &&
          (a.head_dim == 64 || a.head_dim == 128 || (a.head_dim == 256 && !differential));
@@ -88,11 +93,12 @@ mla_status check(const char *what, const mla_grouped_args *a, bool differential)
       return MLA_ERR_INVALID_ARG;
     }
   const int64_t row = static_cast<int64_t>(differential ? 2 : 1) * a->head_dim;
-  if (a->q_row % 8 != 0 || a->k_row % 8 != 0 || a->v_row % 8 != 0 || a->q_row < row * a->num_heads ||
-      a->k_row < row * a->num_kv_heads || a->v_row < row * a->num_kv_heads || a->q_row > (1LL << 34) ||
+  const int64_t q_row = q_stride(*a, differential);
+  if (q_row % 8 != 0 || a->k_row % 8 != 0 || a->v_row % 8 != 0 || q_row < row * a->num_heads ||
+      a->k_row < row * a->num_kv_heads || a->v_row < row * a->num_kv_heads || q_row > (1LL << 34) ||
       a->k_row > (1LL << 34) || a->v_row > (1LL << 34)) {
     set_error("%s: rows must be a multiple of 8 elements apart and not overlap (q %lld, k %lld, v %lld)", what,
-              (long long)a->q_row, (long long)a->k_row, (long long)a->v_row);
+              (long long)q_row, (long long)a->k_row, (long long)a->v_row);
     return MLA_ERR_INVALID_ARG;
   }
   if (a->num_cache_rows % 8 != 0) {
@@ -173,7 +179,7 @@ mla_status run(const char *what, const mla_grouped_args *a, bool differential, c
   const uint64_t w64 = static_cast<uint64_t>(W), hkv = static_cast<uint64_t>(a->num_kv_heads), g64 = static_cast<uint64_t>(G);
   {
     const cuuint64_t dims[5] = {64, g64, static_cast<uint64_t>(a->num_rows), w64, hkv};
-    const cuuint64_t strides[4] = {w64 * 128, static_cast<uint64_t>(a->q_row) * 2, 128, g64 * w64 * 128};
+    const cuuint64_t strides[4] = {w64 * 128, static_cast<uint64_t>(q_stride(*a, differential)) * 2, 128, g64 * w64 * 128};
     const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.heads_per_block), static_cast<cuuint32_t>(p.rows_per_block), 1, 1};
     const mla_status s = make_tmap_5d(&tq, a->q, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (s != MLA_OK) return s;

@@ -490,6 +490,18 @@ def test_strides_of_queries_and_caches():
     assert torch.equal(out, want) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("maps", [1, 2])
+def test_single_row_of_any_stride(maps):
+    """One row of queries as it comes out of a transpose, a row stride of one head."""
+    s = State([300], [1], 8, 2, 64, 16, maps=maps, seed=34)
+    want, lse = s.check()
+    by_head = torch.empty((8, 1) + tuple(s.q.shape[2:]), dtype=BF).cuda()
+    s.q = by_head.copy_(s.q.transpose(0, 1)).transpose(0, 1)
+    assert s.q.stride(0) == maps * 64
+    out, lse2 = s.run()
+    assert torch.equal(out, want) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("maps,L,ql,H,Hkv,D,bs,window", [
     (1, [700] * 6, [8] * 6, 64, 4, 128, 16, 0),                    # two row blocks each
     (1, [9000, 20, 300, 5000, 64, 1], [8, 8, 8, 8, 8, 1], 64, 4, 64, 64, 0),   # and one with one

@@ -125,6 +125,16 @@ def test_workspace_refusals(L, differential):
     assert L.mla_decode_grouped_workspace(ctypes.byref(_grouped(head_dim=96)), differential) == 0
 
 
+@pytest.mark.parametrize("differential", [0, 1])
+def test_single_row_has_no_stride(L, differential):
+    """One row of queries: the distance to a next one is not looked at (what follows is the workspace's check)."""
+    for q_row in (0, 64, 513, -8, 1 << 40):
+        a = _grouped(num_rows=1, max_qlen=1, q_row=q_row)
+        status = L.mla_decode_differential(ctypes.byref(a), VP(256), None, 0.0, None, 0, None) if differential else \
+            L.mla_decode_grouped(ctypes.byref(a), None, 0, None)
+        assert status == WORKSPACE, L.mla_last_error_string()
+
+
 def test_structs_match_the_header(tmp_path):
     structs = {"mla_heads": mla.Heads, "mla_rotary_args": mla.RotaryArgs, "mla_grouped_args": mla.GroupedArgs}
     src = tmp_path / "t.c"
