@@ -320,8 +320,6 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
     return MLA_ERR_INVALID_ARG;
   }
   if (a->num_rows == 0 || (a->q.heads == 0 && a->k.heads == 0)) return MLA_OK;
-  int *err = device_error_word();
-  if (err == nullptr) return MLA_ERR_CUDA;
 
   Params p{};
   p.num_rows = a->num_rows;
@@ -334,7 +332,6 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
   p.axes = a->axes;
   p.slot_map = a->slot_map;
   p.num_cache_rows = a->num_cache_rows;
-  p.err = err;
   int64_t blocks = 0;
   int64_t all = 0;
   const int64_t wave = 4 * 152 * kThreads;  // threads of four blocks an SM
@@ -354,7 +351,10 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
     j.vec = vector_of(t, at, rotate ? p.pairs : dim);
     j.rot = (rotate ? p.pairs : dim) / j.vec;
     const int lanes = j.rot + tail / (2 * j.vec);
-    if (static_cast<int64_t>(heads) * lanes * lanes > UINT32_MAX) too_wide = true;
+    if (static_cast<int64_t>(heads) * lanes * lanes > UINT32_MAX) {  // heads x lanes may not be an int
+      too_wide = true;
+      return;
+    }
     j.width = heads * lanes;
     // Items a thread has: what the GPU takes at once with four blocks an SM, up to four
     // (with two an SM: 7,000 rows of 9 heads of 80 and 3 of values 10.1 -> 6.9 us).
@@ -409,6 +409,9 @@ mla_status run(const mla_rotary_args *a, bool write, mla_stream_t stream) {
     set_error("%s: %d rows of these heads are too many", what, a->num_rows);
     return MLA_ERR_UNSUPPORTED;
   }
+  int *err = device_error_word();
+  if (err == nullptr) return MLA_ERR_CUDA;
+  p.err = err;
   const bool large = all > 7 * wave, neighbours = a->neighbours != 0;
   const bool tail = with_q + with_k > 0;
   const dim3 grid(static_cast<unsigned>(blocks)), threads(kThreads);

@@ -64,6 +64,15 @@ def test_rotary_write_refusals(L, change, status):
     assert b"mla_rotary_write" in L.mla_last_error_string()
 
 
+@pytest.mark.parametrize("heads,dim,src", [(65536, 65536, 514), (65536, 65536, 512), (65535, 65535, 514), (40000, 60001, 514)])
+def test_rows_wider_than_an_int_are_refused(L, heads, dim, src):
+    """2^32 values a row, one at a time: refused before anything is divided by their number as an int, which is 0."""
+    a = _rotary(v={})
+    a.v = mla.Heads(heads, dim, src, heads * dim, dim, 4096, heads * dim, dim)
+    assert L.mla_rotary_write(ctypes.byref(a), None) == UNSUPPORTED
+    assert b"too many" in L.mla_last_error_string()
+
+
 def test_null_structs_and_nothing_to_do(L):
     assert L.mla_rotary(None, None) == INVALID and L.mla_rotary_write(None, None) == INVALID
     assert L.mla_decode_grouped(None, VP(256), 1 << 20, None) == INVALID
