@@ -82,8 +82,7 @@ struct Meta {
   int q0, qlen, g, rb;
   int last;  // CTA that has its last tile; -1: no such unit starts in this one's chunk
   int step;  // from a CTA with a part to the next
-  int sound; // of this CTA's chunk: all of its parts are there (0: a wait gave up before the last one)
-  int pad;
+  int pad[2];
 };
 
 struct Params {
@@ -93,7 +92,7 @@ struct Params {
   const float *lambda, *gain;
   float eps;
   float *part_o;     // [CTA][2][NC][64 W] unnormalised outputs
-  float *part_stat;  // [CTA][2][2][NC] base-2 maxima, sums
+  float *part_stat;  // [CTA][2][2][NC] base-2 maxima, sums (-1: a wait gave up)
   Meta *meta;        // [CTA]
   int *err;
   long long wait_budget, drain_budget;
@@ -758,9 +757,9 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     const int row = wq * 32 + lane;                // token of the tile; lane of TMEM
     const uint32_t grp_bar = 1 + grp, all_bar = 3;
     uint32_t t = 0;
-    Meta meta{0, 0, 0, 0, -1, 1, 0, 0};
+    Meta meta{0, 0, 0, 0, -1, 1, {}};
     const int my_col = col0 + lane % N;
-    bool valid = false;
+    bool valid = false, gave_up = false;
     int my_lo = 0, my_hi = 0, ct = 0, ch = 0, cur_b = -1, cur_rb = -1;
     if (threadIdx.x == 0) {
       misc.walk.begin(misc, pos_a, pos_e);
@@ -769,10 +768,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
     named_bar_sync(all_bar, kSoftmaxThreads);
     for (int n_part = 0;; ++n_part) {
       Columns &cols = misc.cols[n_part & 1];
-      if (!cols.more) {
-        meta.sound = 1;
-        break;
-      }
+      if (!cols.more) break;
       const Part &w = cols.part;
       // what this lane's column sees; the groups of a request see the same
       if (w.b != cur_b || w.rb != cur_rb) {
@@ -795,7 +791,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
         cols.stop = *abort_flag;
       }
       named_bar_sync(all_bar, kSoftmaxThreads);
-      if (cols.stop) break;
+      gave_up = cols.stop;
+      if (gave_up) break;
       // tokens that this group's columns all see (all_lo .. all_hi - 1), and
       // that all columns see that see anything (edge_lo .. edge_hi - 1)
       int all_lo = valid ? my_lo : 0, all_hi = valid ? my_hi : INT32_MAX;
@@ -1007,7 +1004,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       }
       // A part that any of these threads gave up on is not stored, nor are those behind it: what a
       // wait guarded is stale, and the warps whose own waits ended multiplied it like the rest.
-      if (named_bar_red_or(all_bar, kSoftmaxThreads, !ok)) break;
+      gave_up = named_bar_red_or(all_bar, kSoftmaxThreads, !ok);
+      if (gave_up) break;
       tc_fence_after();
       const bool whole = w.a == 0 && w.e == w.n;
       if (whole && valid && wq == 0 && lane < N) {
@@ -1051,7 +1049,7 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
           }
         if (w.a == 0) {
           const int twin = kTwin && p.may_twin ? misc.twin : 0, last = chunk_of(w.start + kOverhead + w.n - 1);
-          meta = Meta{w.q0, w.qlen, w.g, w.rb, (last << twin) + static_cast<int>(blockIdx.x & twin), 1 + twin, 0, 0};
+          meta = Meta{w.q0, w.qlen, w.g, w.rb, (last << twin) + static_cast<int>(blockIdx.x & twin), 1 + twin, {}};
         }
       } else if (kMaps == 1) {
 #pragma unroll
@@ -1114,6 +1112,8 @@ __global__ void __launch_bounds__(Config<kW, kMaps, kNC>::kThreads, 1)
       tc_fence_before();
     }
     if (threadIdx.x == 0) p.meta[blockIdx.x] = meta;
+    // a unit that reaches into this chunk is not merged: a negative sum tells
+    if (gave_up && wq == 0 && lane < N) p.part_stat[(static_cast<int64_t>(blockIdx.x) * 2 * 2 + 1) * kNC + my_col] = -1.0f;
   }
   tc_fence_before();
   __syncthreads();

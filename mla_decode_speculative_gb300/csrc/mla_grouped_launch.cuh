@@ -57,7 +57,6 @@ __global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __
   const float *outs = p.part_o + (m * kNR + c) * kDv + lane * kV;
   const float m0 = lane < parts ? stats[record(lane) * 2 * kNC] : kLowest;
   const float l0 = lane < parts ? stats[record(lane) * 2 * kNC + kNC] : 0.0f;
-  int sound = lane < parts ? p.meta[first + lane * step].sound : 1;
   float ahead[kAhead][kV], gain[kV], lam = 0.0f;
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
@@ -71,22 +70,23 @@ __global__ void __launch_bounds__(32 * kMergeRows *kMaps) grouped_merge(const __
   for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, stats[record(i) * 2 * kNC]);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  for (int i = lane + 32; i < parts; i += 32) sound &= p.meta[first + i * step].sound;
-  if (!__all_sync(0xffffffffu, sound)) {  // the same for all warps: a part is not there
-    if (kMaps == 2) __syncthreads();
-    return;
-  }
   float sum = 0.0f;
+  bool there_all = true;
   for (int i = lane; i < parts; i += 32) {
     const float mi = i < 32 ? m0 : stats[record(i) * 2 * kNC], li = i < 32 ? l0 : stats[record(i) * 2 * kNC + kNC];
     // -1: the row saw nothing in this part, whose outputs are no numbers.  A weight of zero is one
     // like any other: outputs that are not finite reach the row through it.
     const float w = li == 0.0f ? -1.0f : exp2f(mi - top);
     weight[warp][i] = w;
+    there_all = there_all && !(li < 0.0f);
     sum += li == 0.0f ? 0.0f : w * li;
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (!__all_sync(0xffffffffu, there_all)) {  // a wait gave up (both maps' warps see it): the row stays as it was
+    if (kMaps == 2) __syncthreads();
+    return;
+  }
   if (lane == 0) p.lse[row * kMaps + m] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
   __syncwarp();
   float y[kV];
