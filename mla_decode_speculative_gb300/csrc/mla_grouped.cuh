@@ -44,14 +44,16 @@
 //    roles end, copies in flight land, TMEM is freed.  Neither the part at hand
 //    nor a unit with such a part is stored: its rows are left as they were.
 //
-// Measured (calls in a graph): 32 requests of 1,024-8,192 tokens, 8 key heads of
-// 128, 92-95 us (593 MB: 6.3 TB/s, 0.92-0.95 of a copy's rate); 4 x 131,072, 4 key
-// heads, 64 rows 167 us (1.07 GB: 0.95); 40 requests of 8 groups with two maps of 64
-// 129-132 us (839 MB: 0.94-0.96); heads of 64 79-86 us (470 MB: 0.81-0.88). A tile
-// of 16 columns takes its softmax about 900 cycles, its products 400 and 420, beside
-// 2,800 for its copy; of 64 columns the softmax 1,500 (two warps a scheduler: exp2
-// 512, the rest instructions). What every call adds: 4 us until the first copies
-// (offsets, row lengths, sum, page ids in turn), 1 of epilogue, 1-4 of merge.
+// Measured (one call among others on fresh inputs; in brackets calls in a graph, by
+// box): 32 requests of 1,024-8,192 tokens, 8 key heads of 128, 96.5 us (593 MB: 6.1
+// TB/s, 0.91 of a copy's rate) [92-94]; 4 x 131,072, 4 key heads, 64 rows 169.5 us
+// (1.07 GB: 0.94) [167-170]; 40 requests of 8 groups with two maps of 64 134 us (839
+// MB: 0.93) [129-133]; ragged ones with heads of 64 89 us (470 MB: 0.78) [80-88]. A
+// tile of 16 columns takes its softmax about 900 cycles, its products 400 and 420,
+// beside 2,800 for its copy; of 64 columns the softmax 1,500 (two warps a scheduler:
+// exp2 512, the rest instructions and spills). What every call adds: 4 us until the
+// first copies (offsets, row lengths, sum, page ids in turn), 1 of epilogue, 1-4 of
+// merge.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

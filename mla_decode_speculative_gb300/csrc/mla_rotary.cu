@@ -12,15 +12,16 @@
 // shared: a block takes up to 1,024 items of 16 bytes of each half (or of two
 // neighbouring runs), from wherever they begin in a row, makes the sines of the rows
 // that it meets once in shared memory, and goes over them, so that what a warp touches
-// is one run of memory.  q and k are one sequence of heads, with the same sines: one
-// head of each, 39,000 rows of 128, 11.3 us against 26.6 apart.  A thread's first item
+// is one run of memory.  (Times here are calls in a graph on one state: no host time, and
+// what is smaller than L2 stays there.)  q and k are one sequence of heads, with the same
+// sines: one head of each, 39,000 rows of 128, 11.3 us against 26.6 apart.  A thread's first item
 // is read before the sines are made.  Values that are only copied (v, the dims past R
 // of a small call) are blocks of the same launch.  Large calls live from many blocks an
 // SM (8 of 32 registers a thread, four items a thread), small ones from short code
-// (4 blocks): 16,400 rows of 32 + 8 heads of 128 and 8 of values 63.3 us (6.6 TB/s,
-// 0.97 of a copy's rate) against 74 with 4 blocks an SM, 620 rows of the same 3.9
-// against 5.1 with 8; 9,001 rows of 64 + 1 heads of 64 26.6 (5.6 TB/s), 128 rows of
-// 16 + 1 2.2.  With one head the sines bound it: 160,000 rows of 96 37 us, half a
+// (4 blocks): 16,400 rows of 32 + 8 heads of 128 and 8 of values 63.9 us (6.5 TB/s,
+// 0.97 of a copy's rate; the same on fresh inputs) against 74 with 4 blocks an SM, 620
+// rows of the same 3.9 against 5.1 with 8; 9,001 rows of 64 + 1 heads of 64 26.6 (5.6
+// TB/s; on fresh inputs 28.1), 128 rows of 16 + 1 2.2.  With one head the sines bound it: 160,000 rows of 96 37 us, half a
 // copy's rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
